@@ -12,6 +12,10 @@ Names mirror the C entry points:
     puro_fp8_quant_transpose(x, t_out)    -> (q, s)   128-token blocks per column
     puro_fp8_quant_dual(x, t_out)         -> both of the above from one read of x
     puro_fp8_swiglu_quant_dual(gate, up)  -> h = bf16(silu(gate) * up) and its dual quantisation
+    puro_fp8_rmsnorm_quant_act(x, weight, residual)   -> residual sum, norm and its 1x128 blocks (serving)
+    puro_fp8_rmsnorm_quant_dual(x, weight, residual)  -> the same with both copies (training)
+    puro_fp8_rmsnorm_bwd_quant_dual(dy, z, rstd, weight, dres) -> dx, dw and dx's dual quantisation
+    puro_fp8_swiglu_bwd_quant_dual(dh, gate, up)      -> the gate and up gradients' dual quantisation
     puro_fp8_gemm(layout, A, sA, B, sB, bgran, out_dtype) -> C
     puro_fp8_gemm_workspace_size(layout, M, N, K, bgran)
     puro_fp8_gemm(..., mx=True)           -> puro_fp8_gemm_mx (power-of-two scales, scaled matrix cores)
@@ -68,6 +72,13 @@ class QuantWeightDesc(ctypes.Structure):
                 ("qt", ctypes.c_void_p), ("ldqt", ctypes.c_int64), ("st", ctypes.c_void_p)]
 
 
+class QuantDualOut(ctypes.Structure):
+    """puro_quant_dual_out_t: where one tensor's dual quantisation goes."""
+    _fields_ = [("q_row", ctypes.c_void_p), ("ldq_row", ctypes.c_int64), ("s_row", ctypes.c_void_p),
+                ("lds_row", ctypes.c_int64), ("q_tok", ctypes.c_void_p), ("ldq_tok", ctypes.c_int64),
+                ("s_tok", ctypes.c_void_p), ("lds_tok", ctypes.c_int64)]
+
+
 def gemm_desc(M, N, segments, C, ldc, accumulate=False):
     """GemmDesc from (K, A, lda, sA, B, ldb, sB) tuples of pointers and strides."""
     if not 1 <= len(segments) <= MAX_SEGMENTS:
@@ -105,6 +116,23 @@ def lib():
             f = getattr(L, name)
             f.restype = i32
             f.argtypes = [vp, i64, vp, i64, i64, i64, vp, i64, vp, i64, vp, i32, vp, i64, vp, vp]
+        f32 = ctypes.c_float
+        norm_args = [vp, i64, vp, i64, vp, i32, f32, i64, i64, vp, i64, vp, vp, i64, vp, i64, vp]
+        for suffix in ("", "_pow2"):
+            f = getattr(L, "puro_fp8_rmsnorm_quant_act" + suffix)
+            f.restype, f.argtypes = i32, norm_args + [vp]
+            f = getattr(L, "puro_fp8_rmsnorm_quant_dual" + suffix)
+            f.restype, f.argtypes = i32, norm_args + [i32, vp, i64, vp, vp]
+            f = getattr(L, "puro_fp8_rmsnorm_bwd_quant_dual" + suffix)
+            f.restype = i32
+            f.argtypes = [vp, i64, vp, i64, vp, vp, i32, vp, i64, i64, i64, vp, i64, vp, i32, vp, i64, vp, i32, vp,
+                          i64, vp, vp, ctypes.c_size_t, vp]
+            f = getattr(L, "puro_fp8_swiglu_bwd_quant_dual" + suffix)
+            f.restype = i32
+            f.argtypes = [vp, i64, vp, i64, vp, i64, i64, i64, i32, ctypes.POINTER(QuantDualOut),
+                          ctypes.POINTER(QuantDualOut), vp]
+        L.puro_fp8_rmsnorm_bwd_workspace_size.restype = ctypes.c_size_t
+        L.puro_fp8_rmsnorm_bwd_workspace_size.argtypes = [i64, i64]
         L.puro_fp8_gemm_workspace_size.restype = ctypes.c_size_t
         L.puro_fp8_gemm_workspace_size.argtypes = [i32, i64, i64, i64, i32]
         for name in ("puro_fp8_gemm", "puro_fp8_gemm_mx", "puro_fp8_gemm_native"):
@@ -389,6 +417,174 @@ def puro_fp8_swiglu_quant_dual(gate, up, transpose_out=True, h=None, store_h=Tru
               _ptr(q_row), _ld(q_row), _ptr(s_row), 1 if transpose_out else 0, _ptr(q_tok), _ld(q_tok),
               _ptr(s_tok), _stream(stream)), "puro_fp8_swiglu_quant_dual")
     return h, q_row, s_row, q_tok, s_tok
+
+
+def _need_in(t, shape, dtypes, name, device):
+    if tuple(t.shape) != tuple(shape) or t.dtype not in dtypes:
+        raise ValueError("%s: expected %s %s, got %s %s" % (name, tuple(shape), "/".join(str(d) for d in dtypes),
+                                                            tuple(t.shape), t.dtype))
+    if not t.is_cuda or t.device != device:
+        raise ValueError("%s: expected a tensor on the GPU that holds the other arguments (%s), got one on %s" % (
+            name, device, t.device))
+
+
+def _norm_weight(weight, cols, device):
+    _need_in(weight, (cols,), (torch.float32, torch.bfloat16), "weight", device)
+    if cols > 1 and weight.stride(0) != 1:
+        raise ValueError("weight must be dense")
+    return _dtype_code(weight)
+
+
+def _norm_forward(x, weight, residual, z, rstd, h, store_h):
+    """Checked and allocated arguments shared by the norm's two forms."""
+    tokens, cols = x.shape
+    dev = x.device
+    _need_in(x, (tokens, cols), (torch.bfloat16,), "x", dev)
+    wdt = _norm_weight(weight, cols, dev)
+    if residual is not None:
+        _need_in(residual, (tokens, cols), (torch.bfloat16,), "residual", dev)
+        if z is None:
+            z = empty_2d(tokens, cols, torch.bfloat16, dev)
+        _need_in(z, (tokens, cols), (torch.bfloat16,), "z", dev)
+    elif z is not None:
+        raise ValueError("z is written with a residual only (without one it is x)")
+    if rstd is None:
+        rstd = torch.empty((tokens,), dtype=torch.float32, device=dev)
+    _need_in(rstd, (tokens,), (torch.float32,), "rstd", dev)
+    if tokens > 1 and rstd.stride(0) != 1:
+        raise ValueError("rstd must be dense")
+    if store_h and h is None:
+        h = empty_2d(tokens, cols, torch.bfloat16, dev)
+    if h is not None:
+        _need_in(h, (tokens, cols), (torch.bfloat16,), "h", dev)
+    return tokens, cols, wdt, z, rstd, h
+
+
+def _opt(t):
+    """(pointer, row stride) of an optional tensor."""
+    return (_ptr(t), _ld(t)) if t is not None else (ctypes.c_void_p(0), 0)
+
+
+@_stream_allocs
+def puro_fp8_rmsnorm_quant_act(x, weight, residual=None, eps=1e-6, z=None, rstd=None, h=None, store_h=False, q=None,
+                               s=None, stream=None, pow2=False):
+    """z = bf16(x + residual) (x without one), n = z / sqrt(mean z^2 + eps) * weight, and n's 1x128 blocks
+    as puro_fp8_quant_act lays them out (n is quantised in FP32, not rounded to bfloat16 first).
+    x, residual: bfloat16 [tokens][cols]; weight: float32 / bfloat16 [cols].  h (given, or allocated with
+    store_h): bf16(n).  Returns (z, rstd, h or None, q, s)."""
+    tokens, cols, wdt, z, rstd, h = _norm_forward(x, weight, residual, z, rstd, h, store_h)
+    if q is None:
+        q = empty_2d(tokens, cols, torch.uint8, x.device)
+    if s is None:
+        s = torch.empty((tokens, _nblk(cols)), dtype=torch.float32, device=x.device)
+    _need(q, (tokens, cols), torch.uint8, "q")
+    _need_dense(s, (tokens, _nblk(cols)), "s")
+    fn = lib().puro_fp8_rmsnorm_quant_act_pow2 if pow2 else lib().puro_fp8_rmsnorm_quant_act
+    _check(fn(_ptr(x), _ld(x), *_opt(residual), _ptr(weight), wdt, eps, tokens, cols, *_opt(z), _ptr(rstd), *_opt(h),
+              _ptr(q), _ld(q), _ptr(s), _stream(stream)), "puro_fp8_rmsnorm_quant_act")
+    return (x if residual is None else z), rstd, h, q, s
+
+
+@_stream_allocs
+def puro_fp8_rmsnorm_quant_dual(x, weight, residual=None, eps=1e-6, transpose_out=True, z=None, rstd=None, h=None,
+                                store_h=False, q_row=None, s_row=None, q_tok=None, s_tok=None, stream=None,
+                                pow2=False):
+    """puro_fp8_rmsnorm_quant_act with both copies of n, as puro_fp8_quant_dual lays them out.
+    Returns (z, rstd, h or None, q_row, s_row, q_tok, s_tok); z and rstd are what the gradient takes."""
+    tokens, cols, wdt, z, rstd, h = _norm_forward(x, weight, residual, z, rstd, h, store_h)
+    q_row, s_row, q_tok, s_tok = _dual_outs(tokens, cols, transpose_out, x.device, q_row, s_row, q_tok, s_tok)
+    fn = lib().puro_fp8_rmsnorm_quant_dual_pow2 if pow2 else lib().puro_fp8_rmsnorm_quant_dual
+    _check(fn(_ptr(x), _ld(x), *_opt(residual), _ptr(weight), wdt, eps, tokens, cols, *_opt(z), _ptr(rstd), *_opt(h),
+              _ptr(q_row), _ld(q_row), _ptr(s_row), 1 if transpose_out else 0, _ptr(q_tok), _ld(q_tok), _ptr(s_tok),
+              _stream(stream)), "puro_fp8_rmsnorm_quant_dual")
+    return (x if residual is None else z), rstd, h, q_row, s_row, q_tok, s_tok
+
+
+def puro_fp8_rmsnorm_bwd_workspace_size(tokens, cols):
+    return int(lib().puro_fp8_rmsnorm_bwd_workspace_size(tokens, cols))
+
+
+@_stream_allocs
+def puro_fp8_rmsnorm_bwd_quant_dual(dy, z, rstd, weight, dres=None, transpose_out=True, dx=None, dw=None,
+                                    accumulate=False, q_row=None, s_row=None, q_tok=None, s_tok=None, workspace=None,
+                                    stream=None, pow2=False):
+    """Gradient of the norm: dx = dres + rstd (g - xh mean(g xh)), g = weight dy, xh = z rstd (dres: the
+    gradient along the residual stream), with dx's dual quantisation, and dw = sum over tokens of dy xh
+    (added to the given dw with accumulate).  dy, z, dres: bfloat16 [tokens][cols]; z, rstd: the forward's.
+    Returns (dx bfloat16, dw float32, q_row, s_row, q_tok, s_tok)."""
+    tokens, cols = dy.shape
+    dev = dy.device
+    _need_in(dy, (tokens, cols), (torch.bfloat16,), "dy", dev)
+    _need_in(z, (tokens, cols), (torch.bfloat16,), "z", dev)
+    _need_in(rstd, (tokens,), (torch.float32,), "rstd", dev)
+    if tokens > 1 and rstd.stride(0) != 1:
+        raise ValueError("rstd must be dense")
+    wdt = _norm_weight(weight, cols, dev)
+    if dres is not None:
+        _need_in(dres, (tokens, cols), (torch.bfloat16,), "dres", dev)
+    if dx is None:
+        dx = empty_2d(tokens, cols, torch.bfloat16, dev)
+    _need_in(dx, (tokens, cols), (torch.bfloat16,), "dx", dev)
+    if dw is None:
+        if accumulate:
+            raise ValueError("accumulate needs dw")
+        dw = torch.empty((cols,), dtype=torch.float32, device=dev)
+    _need_in(dw, (cols,), (torch.float32,), "dw", dev)
+    if cols > 1 and dw.stride(0) != 1:
+        raise ValueError("dw must be dense")
+    q_row, s_row, q_tok, s_tok = _dual_outs(tokens, cols, transpose_out, dev, q_row, s_row, q_tok, s_tok)
+    if workspace is None:
+        workspace = torch.empty(puro_fp8_rmsnorm_bwd_workspace_size(tokens, cols), dtype=torch.uint8, device=dev)
+    fn = lib().puro_fp8_rmsnorm_bwd_quant_dual_pow2 if pow2 else lib().puro_fp8_rmsnorm_bwd_quant_dual
+    _check(fn(_ptr(dy), _ld(dy), _ptr(z), _ld(z), _ptr(rstd), _ptr(weight), wdt, *_opt(dres), tokens, cols, _ptr(dx),
+              _ld(dx), _ptr(dw), 1 if accumulate else 0, _ptr(q_row), _ld(q_row), _ptr(s_row),
+              1 if transpose_out else 0, _ptr(q_tok), _ld(q_tok), _ptr(s_tok), _ptr(workspace), workspace.numel(),
+              _stream(stream)), "puro_fp8_rmsnorm_bwd_quant_dual")
+    return dx, dw, q_row, s_row, q_tok, s_tok
+
+
+def _sld(t):
+    """Row stride of a scale array that may be a column slice of a wider one."""
+    if t.numel() and t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError("expected unit stride along the last dimension of a scale array")
+    return t.stride(0) if t.numel() and t.shape[0] > 1 else t.shape[1]
+
+
+@_stream_allocs
+def puro_fp8_swiglu_bwd_quant_dual(dh, gate, up, transpose_out=True, joined=False, q_row=None, s_row=None, q_tok=None,
+                                   s_tok=None, stream=None, pow2=False):
+    """Gradient of h = silu(gate) * up: dup = dh silu(gate), dgate = dh up silu'(gate), each quantised both
+    ways in FP32 (not rounded to bfloat16 first).  dh, gate, up: bfloat16 [tokens][cols].
+
+    joined=False: returns two (q_row, s_row, q_tok, s_tok), dgate's and dup's, laid out as
+    puro_fp8_quant_dual's.  joined=True (cols a multiple of 128): one such tuple for the [tokens][2 cols]
+    tensor that holds dgate's columns, then dup's; q_row, s_row, q_tok and s_tok may then be given."""
+    tokens, cols = dh.shape
+    dev = dh.device
+    for t, name in ((dh, "dh"), (gate, "gate"), (up, "up")):
+        _need_in(t, (tokens, cols), (torch.bfloat16,), name, dev)
+    if joined:
+        if cols % 128:
+            raise ValueError("joined gradients need a multiple of 128 columns, got %d" % cols)
+        res = _dual_outs(tokens, 2 * cols, transpose_out, dev, q_row, s_row, q_tok, s_tok)
+        qr, sr, qt, st = res
+        nb = cols // 128
+        if transpose_out:
+            halves = [(qr[:, :cols], sr[:, :nb], qt[:cols], st[:cols]), (qr[:, cols:], sr[:, nb:], qt[cols:], st[cols:])]
+        else:
+            halves = [(qr[:, :cols], sr[:, :nb], qt[:, :cols], st[:, :cols]),
+                      (qr[:, cols:], sr[:, nb:], qt[:, cols:], st[:, cols:])]
+    else:
+        if any(t is not None for t in (q_row, s_row, q_tok, s_tok)):
+            raise ValueError("outputs can be given for joined gradients only")
+        halves = [_dual_outs(tokens, cols, transpose_out, dev, None, None, None, None) for _ in range(2)]
+        res = tuple(halves)
+    outs = [QuantDualOut(_ptr(qr), _ld(qr), _ptr(sr), _sld(sr), _ptr(qt), _ld(qt), _ptr(st), _sld(st))
+            for qr, sr, qt, st in halves]
+    fn = lib().puro_fp8_swiglu_bwd_quant_dual_pow2 if pow2 else lib().puro_fp8_swiglu_bwd_quant_dual
+    _check(fn(_ptr(dh), _ld(dh), _ptr(gate), _ld(gate), _ptr(up), _ld(up), tokens, cols, 1 if transpose_out else 0,
+              outs[0], outs[1], _stream(stream)), "puro_fp8_swiglu_bwd_quant_dual")
+    return res
 
 
 def gemm_dims(layout, A, B):

@@ -198,7 +198,268 @@ static puro_status_t swiglu_dual_impl(const void *gate, int64_t ldg, const void 
     }
 }
 
+// A BF16 tensor argument [rows][cols] beside the quantiser pair's own checks.
+static puro_status_t check_bf16(const void *p, int64_t ld, int64_t cols, bool empty)
+{
+    if (bad_ld(ld, cols))
+        return PURO_ERR_SHAPE;
+    if (!empty && !p)
+        return PURO_ERR_NULL;
+    if (ld % 16 || (p && !aligned(p, 16)))
+        return PURO_ERR_ALIGN;
+    return PURO_OK;
+}
+
+// Shared by the norm's forms: everything but the codes and scales.
+static puro_status_t check_norm(const puro::NormIn &in, int wdt, bool need_rstd)
+{
+    if (wdt != PURO_F32 && wdt != PURO_BF16)
+        return PURO_ERR_ENUM;
+    if (bad_extent(in.tokens) || bad_extent(in.cols))
+        return PURO_ERR_SHAPE;
+    const bool empty = in.tokens == 0 || in.cols == 0;
+    puro_status_t st = check_bf16(in.x, in.ldx, in.cols, empty);
+    if (st != PURO_OK)
+        return st;
+    if (in.res) {
+        st = check_bf16(in.res, in.ldres, in.cols, empty);
+        if (st == PURO_OK)
+            st = check_bf16(in.z, in.ldz, in.cols, empty);
+        if (st != PURO_OK)
+            return st;
+    }
+    if (in.h) {
+        st = check_bf16(in.h, in.ldh, in.cols, empty);
+        if (st != PURO_OK)
+            return st;
+    }
+    if (!empty && (!in.w || (need_rstd && !in.rstd)))
+        return PURO_ERR_NULL;
+    if ((in.w && !aligned(in.w, 16)) || (in.rstd && !aligned(in.rstd, 4)))
+        return PURO_ERR_ALIGN;
+    if (!(in.eps > 0.0f) || in.eps > 3.0e38f)
+        return PURO_ERR_VALUE;
+    return PURO_OK;
+}
+
+static puro::NormIn norm_in(const void *x, int64_t ldx, const void *residual, int64_t ldres, const void *weight,
+                            puro_dtype_t wdt, float eps, int64_t tokens, int64_t cols, void *z, int64_t ldz,
+                            float *rstd, void *h, int64_t ldh)
+{
+    return puro::NormIn{static_cast<const uint16_t *>(x), ldx, static_cast<const uint16_t *>(residual), ldres, weight,
+                        wdt == PURO_BF16, eps, tokens, cols, static_cast<uint16_t *>(z), ldz, rstd,
+                        static_cast<uint16_t *>(h), ldh};
+}
+
+static puro_status_t norm_act_impl(const puro::NormIn &in, int wdt, uint8_t *q, int64_t ldq, float *s, bool pow2,
+                                   hipStream_t stream)
+{
+    try {
+        puro_status_t st = check_norm(in, wdt, false);
+        if (st == PURO_OK)
+            st = check_quant(in.x, PURO_BF16, in.tokens, in.cols, in.ldx, q, ldq, in.cols, s);
+        if (st != PURO_OK)
+            return st;
+        if (in.tokens == 0 || in.cols == 0)
+            return PURO_OK;
+        return from_hip(puro::launch_norm_act(in, q, ldq, s, pow2, stream));
+    } catch (...) {
+        return PURO_ERR_INTERNAL;
+    }
+}
+
+static puro_status_t norm_dual_impl(const puro::NormIn &in, int wdt, uint8_t *q_row, int64_t ldq_row, float *s_row,
+                                    int transpose_out, uint8_t *q_tok, int64_t ldq_tok, float *s_tok, bool pow2,
+                                    hipStream_t stream)
+{
+    try {
+        if (transpose_out != 0 && transpose_out != 1)
+            return PURO_ERR_ENUM;
+        puro_status_t st = check_norm(in, wdt, true);
+        if (st == PURO_OK)
+            st = check_quant(in.x, PURO_BF16, in.tokens, in.cols, in.ldx, q_row, ldq_row, in.cols, s_row);
+        if (st == PURO_OK)
+            st = check_quant(in.x, PURO_BF16, in.tokens, in.cols, in.ldx, q_tok, ldq_tok,
+                             transpose_out ? in.tokens : in.cols, s_tok);
+        if (st != PURO_OK)
+            return st;
+        if (in.tokens == 0 || in.cols == 0)
+            return PURO_OK;
+        return from_hip(puro::launch_norm_dual(in, q_row, ldq_row, s_row, transpose_out == 1, q_tok, ldq_tok, s_tok,
+                                               pow2, stream));
+    } catch (...) {
+        return PURO_ERR_INTERNAL;
+    }
+}
+
+static puro_status_t norm_bwd_impl(const puro::NormBwd &b, int wdt, int accumulate, uint8_t *q_row, int64_t ldq_row,
+                                   float *s_row, int transpose_out, uint8_t *q_tok, int64_t ldq_tok, float *s_tok,
+                                   void *workspace, size_t ws_bytes, bool pow2, hipStream_t stream)
+{
+    try {
+        if (transpose_out != 0 && transpose_out != 1)
+            return PURO_ERR_ENUM;
+        if (wdt != PURO_F32 && wdt != PURO_BF16)
+            return PURO_ERR_ENUM;
+        if (accumulate != 0 && accumulate != 1)
+            return PURO_ERR_ENUM;
+        puro_status_t st = check_quant(b.dy, PURO_BF16, b.tokens, b.cols, b.lddy, q_row, ldq_row, b.cols, s_row);
+        if (st == PURO_OK)
+            st = check_quant(b.z, PURO_BF16, b.tokens, b.cols, b.ldz, q_tok, ldq_tok,
+                             transpose_out ? b.tokens : b.cols, s_tok);
+        const bool empty = b.tokens == 0 || b.cols == 0;
+        if (st == PURO_OK && b.dres)
+            st = check_bf16(b.dres, b.lddres, b.cols, empty);
+        if (st == PURO_OK)
+            st = check_bf16(b.dx, b.lddx, b.cols, empty);
+        if (st != PURO_OK)
+            return st;
+        if ((b.cols > 0 && !b.dw) || (!empty && (!b.w || !b.rstd)))
+            return PURO_ERR_NULL;
+        if ((b.w && !aligned(b.w, 16)) || (b.rstd && !aligned(b.rstd, 4)) || (b.dw && !aligned(b.dw, 4)))
+            return PURO_ERR_ALIGN;
+        const size_t need = puro::norm_bwd_workspace_bytes(b.tokens, b.cols);
+        if (!empty && (!workspace || ws_bytes < need || !aligned(workspace, 256)))
+            return PURO_ERR_WORKSPACE;
+        if (b.cols == 0)
+            return PURO_OK;
+        return from_hip(puro::launch_norm_bwd(b, q_row, ldq_row, s_row, transpose_out == 1, q_tok, ldq_tok, s_tok,
+                                              pow2, workspace, stream));
+    } catch (...) {
+        return PURO_ERR_INTERNAL;
+    }
+}
+
+static puro_status_t swiglu_bwd_impl(const void *dh, int64_t lddh, const void *gate, int64_t ldg, const void *up,
+                                     int64_t ldu, int64_t tokens, int64_t cols, int transpose_out,
+                                     const puro_quant_dual_out_t *dgate, const puro_quant_dual_out_t *dup, bool pow2,
+                                     hipStream_t stream)
+{
+    try {
+        if (transpose_out != 0 && transpose_out != 1)
+            return PURO_ERR_ENUM;
+        if (!dgate || !dup)
+            return PURO_ERR_NULL;
+        if (bad_extent(tokens) || bad_extent(cols))
+            return PURO_ERR_SHAPE;
+        const bool empty = tokens == 0 || cols == 0;
+        puro::SwigluBwd b{static_cast<const uint16_t *>(dh), lddh, static_cast<const uint16_t *>(gate), ldg,
+                          static_cast<const uint16_t *>(up), ldu, tokens, cols, {}, {}};
+        puro_status_t st = check_bf16(up, ldu, cols, empty);
+        if (st != PURO_OK)
+            return st;
+        const puro_quant_dual_out_t *outs[2] = {dgate, dup};
+        for (int i = 0; i < 2; i++) {
+            const puro_quant_dual_out_t &o = *outs[i];
+            st = check_quant(dh, PURO_BF16, tokens, cols, lddh, o.q_row, o.ldq_row, cols, o.s_row);
+            if (st == PURO_OK)
+                st = check_quant(gate, PURO_BF16, tokens, cols, ldg, o.q_tok, o.ldq_tok,
+                                 transpose_out ? tokens : cols, o.s_tok);
+            if (st != PURO_OK)
+                return st;
+            if (bad_ld(o.lds_row, (cols + 127) / 128) || bad_ld(o.lds_tok, transpose_out ? (tokens + 127) / 128 : cols))
+                return PURO_ERR_SHAPE;
+            (i == 0 ? b.dgate : b.dup) = puro::GradOut{o.q_row, o.ldq_row, o.s_row, o.lds_row,
+                                                       o.q_tok, o.ldq_tok, o.s_tok, o.lds_tok};
+        }
+        if (empty)
+            return PURO_OK;
+        return from_hip(puro::launch_swiglu_bwd(b, transpose_out == 1, pow2, stream));
+    } catch (...) {
+        return PURO_ERR_INTERNAL;
+    }
+}
+
 extern "C" {
+
+puro_status_t puro_fp8_rmsnorm_quant_act(const void *x, int64_t ldx, const void *residual, int64_t ldres,
+                                         const void *weight, puro_dtype_t wdt, float eps, int64_t tokens,
+                                         int64_t cols, void *z, int64_t ldz, float *rstd, void *h, int64_t ldh,
+                                         uint8_t *q, int64_t ldq, float *s, hipStream_t stream)
+{
+    return norm_act_impl(norm_in(x, ldx, residual, ldres, weight, wdt, eps, tokens, cols, z, ldz, rstd, h, ldh), wdt,
+                         q, ldq, s, false, stream);
+}
+
+puro_status_t puro_fp8_rmsnorm_quant_dual(const void *x, int64_t ldx, const void *residual, int64_t ldres,
+                                          const void *weight, puro_dtype_t wdt, float eps, int64_t tokens,
+                                          int64_t cols, void *z, int64_t ldz, float *rstd, void *h, int64_t ldh,
+                                          uint8_t *q_row, int64_t ldq_row, float *s_row, int transpose_out,
+                                          uint8_t *q_tok, int64_t ldq_tok, float *s_tok, hipStream_t stream)
+{
+    return norm_dual_impl(norm_in(x, ldx, residual, ldres, weight, wdt, eps, tokens, cols, z, ldz, rstd, h, ldh), wdt,
+                          q_row, ldq_row, s_row, transpose_out, q_tok, ldq_tok, s_tok, false, stream);
+}
+
+puro_status_t puro_fp8_rmsnorm_bwd_quant_dual(const void *dy, int64_t lddy, const void *z, int64_t ldz,
+                                              const float *rstd, const void *weight, puro_dtype_t wdt,
+                                              const void *dres, int64_t lddres, int64_t tokens, int64_t cols,
+                                              void *dx, int64_t lddx, float *dw, int accumulate, uint8_t *q_row,
+                                              int64_t ldq_row, float *s_row, int transpose_out, uint8_t *q_tok,
+                                              int64_t ldq_tok, float *s_tok, void *workspace, size_t ws_bytes,
+                                              hipStream_t stream)
+{
+    const puro::NormBwd b{static_cast<const uint16_t *>(dy), lddy, static_cast<const uint16_t *>(z), ldz, rstd,
+                          weight, wdt == PURO_BF16, static_cast<const uint16_t *>(dres), lddres, tokens, cols,
+                          static_cast<uint16_t *>(dx), lddx, dw, accumulate == 1};
+    return norm_bwd_impl(b, wdt, accumulate, q_row, ldq_row, s_row, transpose_out, q_tok, ldq_tok, s_tok, workspace,
+                         ws_bytes, false, stream);
+}
+
+puro_status_t puro_fp8_swiglu_bwd_quant_dual(const void *dh, int64_t lddh, const void *gate, int64_t ldg,
+                                             const void *up, int64_t ldu, int64_t tokens, int64_t cols,
+                                             int transpose_out, const puro_quant_dual_out_t *dgate,
+                                             const puro_quant_dual_out_t *dup, hipStream_t stream)
+{
+    return swiglu_bwd_impl(dh, lddh, gate, ldg, up, ldu, tokens, cols, transpose_out, dgate, dup, false, stream);
+}
+
+puro_status_t puro_fp8_rmsnorm_quant_act_pow2(const void *x, int64_t ldx, const void *residual, int64_t ldres,
+                                         const void *weight, puro_dtype_t wdt, float eps, int64_t tokens,
+                                         int64_t cols, void *z, int64_t ldz, float *rstd, void *h, int64_t ldh,
+                                         uint8_t *q, int64_t ldq, float *s, hipStream_t stream)
+{
+    return norm_act_impl(norm_in(x, ldx, residual, ldres, weight, wdt, eps, tokens, cols, z, ldz, rstd, h, ldh), wdt,
+                         q, ldq, s, true, stream);
+}
+
+puro_status_t puro_fp8_rmsnorm_quant_dual_pow2(const void *x, int64_t ldx, const void *residual, int64_t ldres,
+                                          const void *weight, puro_dtype_t wdt, float eps, int64_t tokens,
+                                          int64_t cols, void *z, int64_t ldz, float *rstd, void *h, int64_t ldh,
+                                          uint8_t *q_row, int64_t ldq_row, float *s_row, int transpose_out,
+                                          uint8_t *q_tok, int64_t ldq_tok, float *s_tok, hipStream_t stream)
+{
+    return norm_dual_impl(norm_in(x, ldx, residual, ldres, weight, wdt, eps, tokens, cols, z, ldz, rstd, h, ldh), wdt,
+                          q_row, ldq_row, s_row, transpose_out, q_tok, ldq_tok, s_tok, true, stream);
+}
+
+puro_status_t puro_fp8_rmsnorm_bwd_quant_dual_pow2(const void *dy, int64_t lddy, const void *z, int64_t ldz,
+                                              const float *rstd, const void *weight, puro_dtype_t wdt,
+                                              const void *dres, int64_t lddres, int64_t tokens, int64_t cols,
+                                              void *dx, int64_t lddx, float *dw, int accumulate, uint8_t *q_row,
+                                              int64_t ldq_row, float *s_row, int transpose_out, uint8_t *q_tok,
+                                              int64_t ldq_tok, float *s_tok, void *workspace, size_t ws_bytes,
+                                              hipStream_t stream)
+{
+    const puro::NormBwd b{static_cast<const uint16_t *>(dy), lddy, static_cast<const uint16_t *>(z), ldz, rstd,
+                          weight, wdt == PURO_BF16, static_cast<const uint16_t *>(dres), lddres, tokens, cols,
+                          static_cast<uint16_t *>(dx), lddx, dw, accumulate == 1};
+    return norm_bwd_impl(b, wdt, accumulate, q_row, ldq_row, s_row, transpose_out, q_tok, ldq_tok, s_tok, workspace,
+                         ws_bytes, true, stream);
+}
+
+puro_status_t puro_fp8_swiglu_bwd_quant_dual_pow2(const void *dh, int64_t lddh, const void *gate, int64_t ldg,
+                                             const void *up, int64_t ldu, int64_t tokens, int64_t cols,
+                                             int transpose_out, const puro_quant_dual_out_t *dgate,
+                                             const puro_quant_dual_out_t *dup, hipStream_t stream)
+{
+    return swiglu_bwd_impl(dh, lddh, gate, ldg, up, ldu, tokens, cols, transpose_out, dgate, dup, true, stream);
+}
+
+size_t puro_fp8_rmsnorm_bwd_workspace_size(int64_t tokens, int64_t cols)
+{
+    return bad_extent(tokens) || bad_extent(cols) ? 0 : puro::norm_bwd_workspace_bytes(tokens, cols);
+}
 
 puro_status_t puro_fp8_swiglu_quant_dual(const void *gate, int64_t ldg, const void *up, int64_t ldu,
                                          int64_t tokens, int64_t cols, void *h, int64_t ldh, uint8_t *q_row,
@@ -606,6 +867,7 @@ const char *puro_status_string(puro_status_t status)
     case PURO_ERR_WORKSPACE: return "workspace missing, too small or misaligned";
     case PURO_ERR_HIP: return "HIP runtime error at launch";
     case PURO_ERR_INTERNAL: return "internal error";
+    case PURO_ERR_VALUE: return "scalar argument out of range";
     }
     return "unknown status";
 }

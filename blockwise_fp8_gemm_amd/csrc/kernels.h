@@ -45,6 +45,72 @@ hipError_t launch_swiglu_dual(const uint16_t *g, int64_t ldg, const uint16_t *u,
                               bool transpose_out, uint8_t *qt, int64_t ldqt, float *st, bool pow2,
                               hipStream_t stream);
 
+// Norm: z = BF16(x + res) (x itself when res is NULL, and z unused), r = 1 /
+// sqrt(mean z^2 + eps) to rstd, n = z r w.  h: BF16(n) is stored there unless NULL.
+struct NormIn {
+    const uint16_t *x;
+    int64_t ldx;
+    const uint16_t *res;
+    int64_t ldres;
+    const void *w;
+    bool wbf16;
+    float eps;
+    int64_t tokens, cols;
+    uint16_t *z;
+    int64_t ldz;
+    float *rstd;   // may be NULL in launch_norm_act
+    uint16_t *h;
+    int64_t ldh;
+};
+hipError_t launch_norm_act(const NormIn &in, uint8_t *q, int64_t ldq, float *s, bool pow2, hipStream_t st);
+hipError_t launch_norm_dual(const NormIn &in, uint8_t *qr, int64_t ldqr, float *sr, bool transpose_out, uint8_t *qt,
+                            int64_t ldqt, float *stok, bool pow2, hipStream_t st);
+
+// Norm gradient: dx = dres + r (w dy - z r mean(w dy z r)) (dres may be NULL),
+// dw = (dw +) sum over tokens of dy z r.
+struct NormBwd {
+    const uint16_t *dy;
+    int64_t lddy;
+    const uint16_t *z;
+    int64_t ldz;
+    const float *rstd;
+    const void *w;
+    bool wbf16;
+    const uint16_t *dres;
+    int64_t lddres;
+    int64_t tokens, cols;
+    uint16_t *dx;
+    int64_t lddx;
+    float *dw;
+    bool accumulate;
+};
+size_t norm_bwd_workspace_bytes(int64_t tokens, int64_t cols);
+hipError_t launch_norm_bwd(const NormBwd &b, uint8_t *qr, int64_t ldqr, float *sr, bool transpose_out, uint8_t *qt,
+                           int64_t ldqt, float *stok, bool pow2, void *workspace, hipStream_t st);
+
+// Gradient of h = silu(g) u, both halves quantised both ways.
+struct GradOut {
+    uint8_t *q_row;
+    int64_t ldq_row;
+    float *s_row;
+    int64_t lds_row;   // row strides of the scale arrays
+    uint8_t *q_tok;
+    int64_t ldq_tok;
+    float *s_tok;
+    int64_t lds_tok;
+};
+struct SwigluBwd {
+    const uint16_t *dh;
+    int64_t lddh;
+    const uint16_t *g;
+    int64_t ldg;
+    const uint16_t *u;
+    int64_t ldu;
+    int64_t tokens, cols;
+    GradOut dgate, dup;
+};
+hipError_t launch_swiglu_bwd(const SwigluBwd &b, bool transpose_out, bool pow2, hipStream_t st);
+
 constexpr int kGemmMaxSeg = 4;
 
 // One K segment of a product: A, B and their block scales over K indices 0 .. K-1.

@@ -59,7 +59,8 @@ typedef enum {
     PURO_ERR_ENUM = 4,      /* unknown dtype / layout / granularity value          */
     PURO_ERR_WORKSPACE = 5, /* workspace missing or smaller than required          */
     PURO_ERR_HIP = 6,       /* the HIP runtime reported an error at launch         */
-    PURO_ERR_INTERNAL = 7   /* unexpected internal failure                         */
+    PURO_ERR_INTERNAL = 7,  /* unexpected internal failure                         */
+    PURO_ERR_VALUE = 8      /* a scalar argument outside its documented range      */
 } puro_status_t;
 
 typedef enum { PURO_F32 = 0, PURO_BF16 = 1 } puro_dtype_t;
@@ -197,6 +198,104 @@ puro_status_t puro_fp8_swiglu_quant_dual(const void *gate, int64_t ldg, const vo
                                          int64_t ldq_tok, float *s_tok, hipStream_t stream);
 
 /*
+ * Root-mean-square norm of the residual stream, quantised where it is formed:
+ * the input of the q/k/v and gate/up projections.
+ * Passage: the model card's configuration table (Qwen3-1.7B: a norm in front of
+ * every attention and feed-forward block, on the sum of the residual stream and
+ * the block before) and its setup paragraph (norms in BF16 or FP32, the GEMMs
+ * that read them in blockwise E4M3).  For x and residual BF16 [tokens][cols]:
+ *     z[t][c] = BF16_RNE( x + residual )            (z = x when residual is NULL)
+ *     r[t]    = 1 / sqrt( mean over c of z^2 + eps )
+ *     n[t][c] = z r w[c]                            in FP32, not rounded further
+ * z is stored (row stride ldz; required with a residual, ignored without: z is
+ * x then), r to rstd [tokens] FP32, and BF16_RNE(n) to h unless h is NULL.
+ * Codes and scales are of the FP32 n: s = amax|n| / 448 over each block, q =
+ * E4M3_RNE(n / s) with n / s formed within 2 ulps of FP32 (a zero s as in the
+ * quantisers above).  Quantising n before any rounding to BF16 is what sets
+ * them apart from quantising h.
+ *   weight  [cols], FP32 or BF16 (wdt), dense, 16-byte aligned
+ *   eps     finite and > 0, else PURO_ERR_VALUE
+ * The squares of a row must sum to a finite FP32 value.  The outputs must not
+ * overlap each other or the inputs.
+ *
+ * puro_fp8_rmsnorm_quant_act writes the 1x128 row blocks only (q, s as
+ * puro_fp8_quant_act): the form for serving, down to single tokens; rstd may
+ * be NULL.  puro_fp8_rmsnorm_quant_dual writes both copies (as
+ * puro_fp8_quant_dual); its rstd is what the gradient below reads.
+ */
+puro_status_t puro_fp8_rmsnorm_quant_act(const void *x, int64_t ldx, const void *residual, int64_t ldres,
+                                         const void *weight, puro_dtype_t wdt, float eps, int64_t tokens,
+                                         int64_t cols, void *z, int64_t ldz, float *rstd, void *h, int64_t ldh,
+                                         uint8_t *q, int64_t ldq, float *s, hipStream_t stream);
+puro_status_t puro_fp8_rmsnorm_quant_dual(const void *x, int64_t ldx, const void *residual, int64_t ldres,
+                                          const void *weight, puro_dtype_t wdt, float eps, int64_t tokens,
+                                          int64_t cols, void *z, int64_t ldz, float *rstd, void *h, int64_t ldh,
+                                          uint8_t *q_row, int64_t ldq_row, float *s_row, int transpose_out,
+                                          uint8_t *q_tok, int64_t ldq_tok, float *s_tok, hipStream_t stream);
+
+/*
+ * Gradient of the norm above, quantised as the output gradient dY of the
+ * linear layer whose output x was added to the residual stream.  For dy, z
+ * and dres BF16 [tokens][cols], rstd as the forward stored it, g = w dy and
+ * xh = z r:
+ *     dx[t][c] = dres + r ( g - xh mean over c of (g xh) )      (dres NULL: 0)
+ *     dw[c]    = (accumulate ? dw[c] : 0) + sum over t of dy xh
+ * dres is the gradient that reaches z past the norm, along the residual
+ * stream.  dx is stored as BF16 (the gradient of x and of the residual) and its
+ * FP32 value, unrounded, is quantised both ways as above.  dw is FP32 [cols];
+ * tokens are added in a fixed order (equal calls give equal bits).
+ * tokens = 0 leaves dw zero, or as it was with accumulate.  accumulate other
+ * than 0 or 1 is PURO_ERR_ENUM.
+ * workspace: at least puro_fp8_rmsnorm_bwd_workspace_size(tokens, cols) bytes
+ * (0 for invalid extents) of device memory, 256-byte aligned, not used by other
+ * work in flight (two captured graphs that replay at once need one each).
+ */
+size_t puro_fp8_rmsnorm_bwd_workspace_size(int64_t tokens, int64_t cols);
+puro_status_t puro_fp8_rmsnorm_bwd_quant_dual(const void *dy, int64_t lddy, const void *z, int64_t ldz,
+                                              const float *rstd, const void *weight, puro_dtype_t wdt,
+                                              const void *dres, int64_t lddres, int64_t tokens, int64_t cols,
+                                              void *dx, int64_t lddx, float *dw, int accumulate, uint8_t *q_row,
+                                              int64_t ldq_row, float *s_row, int transpose_out, uint8_t *q_tok,
+                                              int64_t ldq_tok, float *s_tok, void *workspace, size_t ws_bytes,
+                                              hipStream_t stream);
+
+/*
+ * Where one tensor's dual quantisation goes when its scales are part of a
+ * wider array: q_row [tokens][cols] (row stride ldq_row), s_row [tokens]
+ * [ceil(cols/128)] (row stride lds_row); q_tok and s_tok as
+ * puro_fp8_quant_dual's with transpose_out, s_tok with row stride lds_tok.
+ * The scale strides are at least the row lengths, any number of elements.
+ */
+typedef struct {
+    uint8_t *q_row;
+    int64_t ldq_row;
+    float *s_row;
+    int64_t lds_row;
+    uint8_t *q_tok;
+    int64_t ldq_tok;
+    float *s_tok;
+    int64_t lds_tok;
+} puro_quant_dual_out_t;
+
+/*
+ * Gradient of the gated activation h = silu(gate) up, both halves quantised as
+ * the output gradient of the gate and up projections: for dh, gate and up BF16
+ * [tokens][cols] (dh: the down projection's data gradient) and sg = 1 / (1 + e^-gate):
+ *     dup   = dh gate sg
+ *     dgate = dh up sg (1 + gate (1 - sg))
+ * in FP32, quantised unrounded both ways as above.  With cols a multiple of 128
+ * the two results may be the column halves of one [tokens][2 cols] tensor
+ * (q_row, s_row; and the row halves of q_tok, s_tok with transpose_out = 1): the
+ * operands of one data-gradient GEMM over the concatenated gate/up outputs.
+ * dgate and dup point to HOST structures, read before the call returns.  |dh up
+ * gate| must be finite in FP32.
+ */
+puro_status_t puro_fp8_swiglu_bwd_quant_dual(const void *dh, int64_t lddh, const void *gate, int64_t ldg,
+                                             const void *up, int64_t ldu, int64_t tokens, int64_t cols,
+                                             int transpose_out, const puro_quant_dual_out_t *dgate,
+                                             const puro_quant_dual_out_t *dup, hipStream_t stream);
+
+/*
  * Workspace bytes puro_fp8_gemm needs for this problem (0 = none).  Returns 0
  * for invalid arguments as well; puro_fp8_gemm reports those.
  */
@@ -318,6 +417,29 @@ puro_status_t puro_fp8_swiglu_quant_dual_pow2(const void *gate, int64_t ldg, con
                                               int64_t tokens, int64_t cols, void *h, int64_t ldh,
                                               uint8_t *q_row, int64_t ldq_row, float *s_row, int transpose_out,
                                               uint8_t *q_tok, int64_t ldq_tok, float *s_tok, hipStream_t stream);
+
+puro_status_t puro_fp8_rmsnorm_quant_act_pow2(const void *x, int64_t ldx, const void *residual, int64_t ldres,
+                                              const void *weight, puro_dtype_t wdt, float eps, int64_t tokens,
+                                              int64_t cols, void *z, int64_t ldz, float *rstd, void *h,
+                                              int64_t ldh, uint8_t *q, int64_t ldq, float *s, hipStream_t stream);
+puro_status_t puro_fp8_rmsnorm_quant_dual_pow2(const void *x, int64_t ldx, const void *residual, int64_t ldres,
+                                               const void *weight, puro_dtype_t wdt, float eps, int64_t tokens,
+                                               int64_t cols, void *z, int64_t ldz, float *rstd, void *h,
+                                               int64_t ldh, uint8_t *q_row, int64_t ldq_row, float *s_row,
+                                               int transpose_out, uint8_t *q_tok, int64_t ldq_tok, float *s_tok,
+                                               hipStream_t stream);
+puro_status_t puro_fp8_rmsnorm_bwd_quant_dual_pow2(const void *dy, int64_t lddy, const void *z, int64_t ldz,
+                                                   const float *rstd, const void *weight, puro_dtype_t wdt,
+                                                   const void *dres, int64_t lddres, int64_t tokens,
+                                                   int64_t cols, void *dx, int64_t lddx, float *dw,
+                                                   int accumulate, uint8_t *q_row, int64_t ldq_row, float *s_row,
+                                                   int transpose_out, uint8_t *q_tok, int64_t ldq_tok,
+                                                   float *s_tok, void *workspace, size_t ws_bytes,
+                                                   hipStream_t stream);
+puro_status_t puro_fp8_swiglu_bwd_quant_dual_pow2(const void *dh, int64_t lddh, const void *gate, int64_t ldg,
+                                                  const void *up, int64_t ldu, int64_t tokens, int64_t cols,
+                                                  int transpose_out, const puro_quant_dual_out_t *dgate,
+                                                  const puro_quant_dual_out_t *dup, hipStream_t stream);
 
 /*
  * GEMM on the scaled FP8 matrix cores: arguments, storage and result
