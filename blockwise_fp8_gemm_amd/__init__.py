@@ -21,6 +21,7 @@ Names mirror the C entry points:
     puro_fp8_gemm(..., mx=True)           -> puro_fp8_gemm_mx (power-of-two scales, scaled matrix cores)
     puro_fp8_gemm(..., native=True)       -> puro_fp8_gemm_native (partials on the FP8 matrix cores)
     puro_fp8_gemm_grouped(..., mx=True / native=True) -> the grouped forms of those two
+    puro_fp8_newton_schulz_grouped([grads])  -> their Newton-Schulz orthogonalised directions
     puro_status_string(status)
 Tensors are 2-D, row-major (stride(1) == 1), with a row stride that is a
 multiple of 16 elements and 16-byte aligned storage.
@@ -79,6 +80,12 @@ class QuantDualOut(ctypes.Structure):
                 ("s_tok", ctypes.c_void_p), ("lds_tok", ctypes.c_int64)]
 
 
+class NewtonSchulzDesc(ctypes.Structure):
+    """puro_newton_schulz_desc_t: one matrix of puro_fp8_newton_schulz_grouped."""
+    _fields_ = [("g", ctypes.c_void_p), ("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("ldg", ctypes.c_int64),
+                ("o", ctypes.c_void_p), ("ldo", ctypes.c_int64)]
+
+
 def gemm_desc(M, N, segments, C, ldc, accumulate=False):
     """GemmDesc from (K, A, lda, sA, B, ldb, sB) tuples of pointers and strides."""
     if not 1 <= len(segments) <= MAX_SEGMENTS:
@@ -133,6 +140,11 @@ def lib():
                           ctypes.POINTER(QuantDualOut), vp]
         L.puro_fp8_rmsnorm_bwd_workspace_size.restype = ctypes.c_size_t
         L.puro_fp8_rmsnorm_bwd_workspace_size.argtypes = [i64, i64]
+        L.puro_fp8_newton_schulz_workspace_size.restype = ctypes.c_size_t
+        L.puro_fp8_newton_schulz_workspace_size.argtypes = [ctypes.POINTER(NewtonSchulzDesc), i32]
+        L.puro_fp8_newton_schulz_grouped.restype = i32
+        L.puro_fp8_newton_schulz_grouped.argtypes = [i32, ctypes.POINTER(NewtonSchulzDesc), i32, i32,
+                                                     ctypes.POINTER(f32), f32, vp, ctypes.c_size_t, vp]
         L.puro_fp8_gemm_workspace_size.restype = ctypes.c_size_t
         L.puro_fp8_gemm_workspace_size.argtypes = [i32, i64, i64, i64, i32]
         for name in ("puro_fp8_gemm", "puro_fp8_gemm_mx", "puro_fp8_gemm_native"):
@@ -735,3 +747,47 @@ def puro_fp8_gemm_grouped(layout, problems, bgran="128x128", out_dtype=torch.bfl
     _check(getattr(lib(), name)(LAYOUTS[layout], BGRAN[bgran], PURO_BF16 if out_dtype == torch.bfloat16 else PURO_F32,
                                 descs, len(problems), _stream(stream)), name)
     return outs
+
+
+def puro_fp8_newton_schulz_workspace_size(shapes):
+    """Bytes puro_fp8_newton_schulz_grouped needs for matrices of these (rows, cols)."""
+    descs = (NewtonSchulzDesc * max(len(shapes), 1))(*[NewtonSchulzDesc(None, r, c, 0, None, 0) for r, c in shapes])
+    return int(lib().puro_fp8_newton_schulz_workspace_size(descs, len(shapes)))
+
+
+@_stream_allocs
+def puro_fp8_newton_schulz_grouped(grads, steps=5, coefficients=(3.4445, -4.7750, 2.0315), eps=1e-7, outs=None,
+                                   workspace=None, stream=None):
+    """Orthogonalised directions of several gradients (or momenta), one call: each matrix is divided by its
+    Frobenius norm + eps and `steps` times X <- a X + (b X X^T + c (X X^T)^2) X is formed (on the transpose of
+    a tall matrix).  grads: 2-D tensors of one dtype (float32 / bfloat16); coefficients: (a, b, c), or one
+    such triple per step.  Returns the list of bfloat16 results (written into outs when given)."""
+    if outs is None:
+        outs = [None] * len(grads)
+    if len(outs) != len(grads):
+        raise ValueError("outs must have one entry per gradient")
+    if not grads:
+        return []
+    triples = list(coefficients) if hasattr(coefficients[0], "__len__") else [coefficients] * steps
+    if len(triples) != steps or any(len(t) != 3 for t in triples):
+        raise ValueError("coefficients: one (a, b, c), or one per step")
+    dev, dtype = grads[0].device, grads[0].dtype
+    code = _dtype_code(grads[0])
+    descs = (NewtonSchulzDesc * len(grads))()
+    res = []
+    for i, (g, o) in enumerate(zip(grads, outs)):
+        _need_in(g, tuple(g.shape), (dtype,), "grads[%d]" % i, dev)
+        rows, cols = g.shape
+        if o is None:
+            o = empty_2d(rows, cols, torch.bfloat16, dev)
+        _need_in(o, (rows, cols), (torch.bfloat16,), "outs[%d]" % i, dev)
+        descs[i] = NewtonSchulzDesc(_ptr(g), rows, cols, _ld(g), _ptr(o), _ld(o))
+        res.append(o)
+    if workspace is None:
+        need = int(lib().puro_fp8_newton_schulz_workspace_size(descs, len(grads)))
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    coef = (ctypes.c_float * (3 * steps))(*[v for t in triples for v in t])
+    _check(lib().puro_fp8_newton_schulz_grouped(code, descs, len(grads), steps, coef, eps, _ptr(workspace),
+                                                workspace.numel() * workspace.element_size(), _stream(stream)),
+           "puro_fp8_newton_schulz_grouped")
+    return res

@@ -3,6 +3,7 @@
 #include "../../include/puro_fp8.h"
 #include "kernels.h"
 
+#include <cmath>
 #include <mutex>
 #include <vector>
 
@@ -854,6 +855,102 @@ puro_status_t puro_fp8_gemm_grouped_native(puro_layout_t layout, puro_bscale_t b
                                            const puro_gemm_desc_t *problems, int count, hipStream_t stream)
 {
     return gemm_grouped_impl(GROUP_NATIVE, layout, bgran, cdt, problems, count, stream);
+}
+
+// Whether the steps keep the FP16 products in range, from singular values in
+// [0, 1] on: f(s) = a s + b s^3 + c s^5 and B's eigenvalues b l + c l^2, l = s^2,
+// both taken at the ends of the interval and at their turning points.
+static bool newton_in_range(int steps, const float *coef)
+{
+    double top = 1.0;   // largest singular value
+    for (int k = 0; k < steps; k++) {
+        const double a = coef[3 * k], b = coef[3 * k + 1], c = coef[3 * k + 2];
+        if (!std::isfinite(a) || !std::isfinite(b) || !std::isfinite(c))
+            return false;
+        auto f = [&](double s) { return std::fabs(s * (a + s * s * (b + c * s * s))); };
+        auto p = [&](double l) { return std::fabs(l * (b + c * l)); };
+        double most = f(top), widest = p(top * top);
+        if (c != 0.0) {
+            const double turn = -b / (2.0 * c);
+            if (turn > 0.0 && turn < top * top)
+                widest = std::fmax(widest, p(turn));
+            const double disc = 9.0 * b * b - 20.0 * a * c;   // a + 3 b l + 5 c l^2 = 0
+            for (int sign = -1; sign <= 1 && disc >= 0.0; sign += 2) {
+                const double l = (-3.0 * b + sign * std::sqrt(disc)) / (10.0 * c);
+                if (l > 0.0 && l < top * top)
+                    most = std::fmax(most, f(std::sqrt(l)));
+            }
+        } else if (b != 0.0 && -a / (3.0 * b) > 0.0 && -a / (3.0 * b) < top * top) {
+            most = std::fmax(most, f(std::sqrt(-a / (3.0 * b))));
+        }
+        if (!(widest <= 32.0) || !(most <= 2.0))
+            return false;
+        top = most;
+    }
+    return true;
+}
+
+static bool newton_bad_dims(const puro_newton_schulz_desc_t &d)
+{
+    return d.rows < 0 || d.cols < 0 || d.rows > PURO_NS_MAX_DIM || d.cols > PURO_NS_MAX_DIM;
+}
+
+size_t puro_fp8_newton_schulz_workspace_size(const puro_newton_schulz_desc_t *items, int count)
+{
+    try {
+        if (count <= 0 || count > PURO_NS_MAX_GROUP || !items)
+            return 0;
+        std::vector<puro::NsMatrix> v;
+        for (int i = 0; i < count; i++) {
+            if (newton_bad_dims(items[i]))
+                return 0;
+            if (items[i].rows > 0 && items[i].cols > 0)
+                v.push_back({nullptr, items[i].rows, items[i].cols, 0, nullptr, 0});
+        }
+        return puro::newton_workspace_bytes(v.data(), (int)v.size());
+    } catch (...) {
+        return 0;
+    }
+}
+
+puro_status_t puro_fp8_newton_schulz_grouped(puro_dtype_t gdt, const puro_newton_schulz_desc_t *items, int count,
+                                             int steps, const float *coef, float eps, void *workspace,
+                                             size_t ws_bytes, hipStream_t stream)
+{
+    try {
+        if (gdt != PURO_F32 && gdt != PURO_BF16)
+            return PURO_ERR_ENUM;
+        if (count < 0 || count > PURO_NS_MAX_GROUP)
+            return PURO_ERR_SHAPE;
+        if ((count > 0 && !items) || !coef)
+            return PURO_ERR_NULL;
+        if (steps < 1 || steps > PURO_NS_MAX_STEPS || !(eps > 0.0f) || !std::isfinite(eps) ||
+            !newton_in_range(steps, coef))
+            return PURO_ERR_VALUE;
+        std::vector<puro::NsMatrix> v;
+        v.reserve((size_t)count);
+        for (int i = 0; i < count; i++) {
+            const puro_newton_schulz_desc_t &d = items[i];
+            if (newton_bad_dims(d) || bad_ld(d.ldg, d.cols) || bad_ld(d.ldo, d.cols))
+                return PURO_ERR_SHAPE;
+            const bool empty = d.rows == 0 || d.cols == 0;
+            if (!empty && (!d.g || !d.o))
+                return PURO_ERR_NULL;
+            if (d.ldg % 16 || d.ldo % 16 || (d.g && !aligned(d.g, 16)) || (d.o && !aligned(d.o, 16)))
+                return PURO_ERR_ALIGN;
+            if (!empty)
+                v.push_back({d.g, d.rows, d.cols, d.ldg, d.o, d.ldo});
+        }
+        if (v.empty())
+            return PURO_OK;
+        const size_t need = puro::newton_workspace_bytes(v.data(), (int)v.size());
+        if (!workspace || ws_bytes < need || !aligned(workspace, 256))
+            return PURO_ERR_WORKSPACE;
+        return from_hip(puro::launch_newton(v.data(), (int)v.size(), gdt == PURO_BF16, steps, coef, eps, workspace,
+                                            stream));
+    } catch (...) {
+        return PURO_ERR_INTERNAL;
+    }
 }
 
 const char *puro_status_string(puro_status_t status)

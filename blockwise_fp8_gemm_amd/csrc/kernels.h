@@ -111,6 +111,19 @@ struct SwigluBwd {
 };
 hipError_t launch_swiglu_bwd(const SwigluBwd &b, bool transpose_out, bool pow2, hipStream_t st);
 
+// Newton-Schulz orthogonalisation of `count` matrices [rows][cols] (FP32 or
+// BF16), results in BF16; coef holds a, b, c of every step.
+struct NsMatrix {
+    const void *g;
+    int64_t rows, cols, ldg;
+    void *o;
+    int64_t ldo;
+};
+constexpr int kNsGroupMax = 16;   // matrices per launch; more take several rounds
+size_t newton_workspace_bytes(const NsMatrix *ms, int count);
+hipError_t launch_newton(const NsMatrix *ms, int count, bool gbf16, int steps, const float *coef, float eps,
+                         void *workspace, hipStream_t st);
+
 constexpr int kGemmMaxSeg = 4;
 
 // One K segment of a product: A, B and their block scales over K indices 0 .. K-1.

@@ -1,0 +1,517 @@
+// Newton-Schulz orthogonalisation of weight gradients on the gfx950 matrix
+// cores: the update direction of the Muon-type optimiser that the Puro-2B
+// pages name for the recipe's matrix parameters.
+//
+// With M <= N (a tall matrix is handled as its transpose), X0 = G / (|G|_F +
+// eps) and per step
+//   A = X X^T,   B = b A + c A A,   X <- a X + B X
+// which maps every singular value s of X to a s + b s^3 + c s^5 and leaves the
+// singular vectors as they are.
+//
+// Number formats.  The products run on the FP16 matrix cores (BF16's rate,
+// three more significand bits).  X is kept as the sum of two FP16 numbers, hi +
+// lo (22 bits): the products read hi, the term a X reads both.  The diagonal
+// of B is kept apart in FP32 and joins a in that term, X <- (a + d_i) X +
+// (B - d) hi, so that the part of the step that is largest for well
+// conditioned rows carries no FP16 rounding at all.  X is held times a power
+// of two near sqrt(N) and A and B times 2^10, which keeps entries clear of
+// FP16's subnormals; with the singular values at most 2 and |b l + c l^2| at
+// most 32 (checked on the host) nothing overflows.  Simulated against 64 bits
+// on 64 x 64 to 1024 x 1024 gradients: 0.6e-3 to 1.6e-3 relative, the BF16
+// rounding of the result itself being 1.7e-3; with BF16 operands it would be
+// 0.5e-2 to 1.6e-2.
+//
+// A and B are symmetric: only the tiles on and above the diagonal are formed,
+// and each is stored twice.  B X reads X^T, which every step writes beside X,
+// so that all three products have both operands contiguous along K.
+#include "common.h"
+#include "kernels.h"
+
+#include <algorithm>
+#include <cmath>
+
+namespace puro {
+
+namespace {
+
+typedef _Float16 v8h __attribute__((ext_vector_type(8)));
+typedef _Float16 v4h __attribute__((ext_vector_type(4)));
+typedef int v4i __attribute__((ext_vector_type(4)));
+
+constexpr float kScaleA = 1024.0f;   // A and B are held times this
+constexpr int kNormBlocks = 128;     // partial sums of |G|^2 per matrix
+
+struct NsItem {
+    const void *g;
+    void *o;
+    int64_t ldg, ldo;
+    int M, N;      // M <= N after the transpose of a tall matrix
+    int Mp, Np;    // padded to whole tiles; the padding holds zeros
+    int tall;
+    float s;       // X is held times s
+    uint16_t *xh, *xl;      // [Mp][Np]
+    uint16_t *xt[2];        // [Np][Mp], hi, read and written in turn
+    uint16_t *a, *b;        // [Mp][Mp]
+    float *d;               // [Mp] diagonal of B
+    double *part;           // [kNormBlocks]
+};
+
+struct NsGroup {
+    NsItem it[kNsGroupMax];
+    int first[kNsGroupMax + 1];   // workgroups of item i: [first[i], first[i+1])
+    int count;
+    int gbf16;
+    int flip;                     // which xt is read
+    int last;                     // the step whose result is the output
+    float a, b, c, eps;
+};
+
+typedef __attribute__((address_space(4))) const NsGroup *KernargNs;
+
+__device__ __forceinline__ KernargNs kernarg()
+{
+    return (KernargNs)__builtin_amdgcn_kernarg_segment_ptr();
+}
+
+__device__ __forceinline__ int find_item(KernargNs g, int b)
+{
+    int i = 0;
+    while (i + 1 < g->count && b >= g->first[i + 1])
+        i++;
+    return __builtin_amdgcn_readfirstlane(i);
+}
+
+// An FP32 value as it stands: keeps the compiler from folding the operation
+// that made it into the conversion to FP16 (v_fma_mixlo rounds once where an
+// FP32 result is rounded twice), which it does in one place and not in the
+// next, so that the two stored copies of an element could differ.
+__device__ __forceinline__ float as_f32(float f)
+{
+    asm("" : "+v"(f));
+    return f;
+}
+
+__device__ __forceinline__ uint16_t h_bits(float f) { return __builtin_bit_cast(uint16_t, (_Float16)f); }
+__device__ __forceinline__ float h_val(uint16_t u) { return (float)__builtin_bit_cast(_Float16, u); }
+
+// ---------------------------------------------------------------------------
+// |G|_F^2 in 64 bits: kNormBlocks partial sums per matrix, each over every
+// kNormBlocks-th row.
+// ---------------------------------------------------------------------------
+__global__ __launch_bounds__(256) void ns_norm_kernel(NsGroup args)
+{
+    (void)args;
+    const KernargNs g = kernarg();
+    const int item = blockIdx.y, t = threadIdx.x;
+    const int tall = g->it[item].tall;
+    const int rows = tall ? g->it[item].N : g->it[item].M, cols = tall ? g->it[item].M : g->it[item].N;
+    const int64_t ld = g->it[item].ldg;
+    __shared__ double red[256];
+    double sum = 0.0;
+    for (int r = blockIdx.x; r < rows; r += kNormBlocks) {
+        for (int c = t; c < cols; c += 256) {
+            const float v = g->gbf16 ? Elem<uint16_t>::load((const uint16_t *)g->it[item].g + r * ld + c)
+                                     : ((const float *)g->it[item].g)[r * ld + c];
+            sum = fma((double)v, (double)v, sum);
+        }
+    }
+    red[t] = sum;
+    __syncthreads();
+    for (int w = 128; w > 0; w >>= 1) {
+        if (t < w)
+            red[t] += red[t + w];
+        __syncthreads();
+    }
+    if (t == 0)
+        g->it[item].part[blockIdx.x] = red[0];
+}
+
+// ---------------------------------------------------------------------------
+// X0: hi, lo and the transposed hi of a 64 x 64 tile, zeros in the padding.
+// ---------------------------------------------------------------------------
+__global__ __launch_bounds__(256) void ns_init_kernel(NsGroup args)
+{
+    (void)args;
+    const KernargNs g = kernarg();
+    const int i = find_item(g, blockIdx.x), t = threadIdx.x;
+    const int local = blockIdx.x - g->first[i];
+    const int M = g->it[i].M, N = g->it[i].N, Mp = g->it[i].Mp, Np = g->it[i].Np, tall = g->it[i].tall;
+    const int64_t ld = g->it[i].ldg;
+    const int m0 = local / (Np / 64) * 64, n0 = local % (Np / 64) * 64;
+    __shared__ double red[kNormBlocks];
+    __shared__ float x[64][64 + 1];   // [m][n]
+    if (t < kNormBlocks)
+        red[t] = g->it[i].part[t];
+    __syncthreads();
+    for (int w = kNormBlocks / 2; w > 0; w >>= 1) {
+        if (t < w)
+            red[t] += red[t + w];
+        __syncthreads();
+    }
+    const float scale = (float)((double)g->it[i].s / (sqrt(red[0]) + (double)g->eps));
+    for (int k = t; k < 64 * 64; k += 256) {
+        const int r = k >> 6, c = k & 63;   // c along the source's rows
+        const int m = tall ? m0 + c : m0 + r, n = tall ? n0 + r : n0 + c;
+        float v = 0.0f;
+        if (m < M && n < N) {
+            const int64_t at = tall ? (int64_t)n * ld + m : (int64_t)m * ld + n;
+            v = g->gbf16 ? Elem<uint16_t>::load((const uint16_t *)g->it[i].g + at) : ((const float *)g->it[i].g)[at];
+        }
+        x[tall ? c : r][tall ? r : c] = v * scale;
+    }
+    __syncthreads();
+    for (int k = t; k < 64 * 64; k += 256) {
+        const int r = k >> 6, c = k & 63;
+        const float v = x[r][c];
+        const uint16_t hi = h_bits(v);
+        g->it[i].xh[(int64_t)(m0 + r) * Np + n0 + c] = hi;
+        g->it[i].xl[(int64_t)(m0 + r) * Np + n0 + c] = h_bits(v - h_val(hi));
+        g->it[i].xt[0][(int64_t)(n0 + r) * Mp + m0 + c] = h_bits(x[c][r]);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Products.  A workgroup computes a TM x TN tile of P Q^T (P [..][K], Q [..][K],
+// rows contiguous along K) with WM x WN waves of IT x JT matrix-core tiles of
+// 16 x 16.  Blocks of 64 K (128 bytes a row) go from global memory straight to
+// LDS, double-buffered, with a 16-byte XOR swizzle that keeps the 16-byte
+// fragment reads free of bank conflicts.
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ uint32_t lds_addr(const void *p)
+{
+    return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void *)p;
+}
+
+// 16 bytes per lane from base + off (base wave-uniform) to the wave's LDS base
+// + 16 lane.  Inline assembly rather than the builtin: with the builtin's copy
+// in flight the compiler waits for every LDS read with lgkmcnt(0).  The copies
+// count in vmcnt, which the K loop waits on before its barrier.  M0 is set in
+// the same statement, and nothing else here reads it.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+__device__ __forceinline__ void copy16(const uint8_t *base, uint32_t off, uint8_t *lds_wave_base)
+{
+    asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %0, %1"
+                 :: "v"(off), "s"(base), "s"(lds_addr(lds_wave_base)) : "memory", "m0");
+}
+#pragma clang diagnostic pop
+
+// 16-byte segment s of row r sits at s ^ swz(r).
+__device__ __forceinline__ int swz(int row) { return (row & 7) ^ ((row >> 3) & 1); }
+
+template <int ROWS, int NW>
+__device__ __forceinline__ void stage_rows(uint8_t *t, const uint8_t *g, int64_t ld, int64_t row0, int64_t k0,
+                                           int wave, int lane)
+{
+    static_assert((ROWS / 8) % NW == 0, "whole 1 KB chunks per wave");
+#pragma unroll
+    for (int it = 0; it < ROWS / 8 / NW; it++) {
+        const int c = wave + NW * it;   // rows 8c .. 8c+7, lane's row 8c + lane / 8
+        const int seg = (lane & 7) ^ (((lane >> 3) & 7) ^ (c & 1));
+        copy16(g + (row0 + 8 * c) * ld + k0, (uint32_t)(lane >> 3) * (uint32_t)ld + (uint32_t)(seg * 16),
+               t + c * 1024);
+    }
+}
+
+// Rows row_base + lane % 16, K values 16 (lane / 16) .. +15 of a 64-wide block
+// (the same K slots in both operands, so any order of K serves).
+struct Frag {
+    v8h k[2];
+};
+__device__ __forceinline__ Frag frag(const uint8_t *t, int row_base, int lane)
+{
+    const int row = row_base + (lane & 15);
+    const int g = lane >> 4, f = swz(row);
+    Frag r;
+    r.k[0] = __builtin_bit_cast(v8h, *reinterpret_cast<const v4i *>(t + (row * 128 + (((2 * g) ^ f) << 4))));
+    r.k[1] = __builtin_bit_cast(v8h, *reinterpret_cast<const v4i *>(t + (row * 128 + (((2 * g + 1) ^ f) << 4))));
+    return r;
+}
+
+template <int WM_, int WN_, int IT_, int JT_> struct NsCfg {
+    static constexpr int WM = WM_, WN = WN_, IT = IT_, JT = JT_;
+    static constexpr int NW = WM * WN, THREADS = 64 * NW;
+    static constexpr int TM = WM * IT * 16, TN = WN * JT * 16;
+};
+typedef NsCfg<2, 4, 8, 4> NsL;   // 256 x 256, one workgroup per CU
+typedef NsCfg<2, 2, 4, 4> NsQ;   // 128 x 128, two workgroups per CU
+
+enum { NS_GRAM = 0, NS_POLY = 1, NS_UPDATE = 2 };
+
+template <class Cfg, int MODE>
+__global__ __launch_bounds__(Cfg::THREADS) void ns_product_kernel(NsGroup args)
+{
+    (void)args;
+    constexpr int NW = Cfg::NW, TM = Cfg::TM, TN = Cfg::TN, IT = Cfg::IT, JT = Cfg::JT;
+    __shared__ __attribute__((aligned(16))) uint8_t lds0[(TM + TN) * 128];
+    __shared__ __attribute__((aligned(16))) uint8_t lds1[(TM + TN) * 128];
+    const KernargNs g = kernarg();
+    const int item = find_item(g, blockIdx.x);
+    const int local = blockIdx.x - g->first[item];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wave / Cfg::WN, wn = wave % Cfg::WN;
+    const int Mp = g->it[item].Mp, Np = g->it[item].Np;
+
+    // operands and the tile's place: rows of P are tile rows, rows of Q tile columns
+    const uint8_t *P, *Q;
+    int K, tr, tc;
+    if constexpr (MODE == NS_UPDATE) {
+        // the result's transpose: rows are X's columns (X^T [Np][Mp]), columns X's rows (B [Mp][Mp])
+        P = (const uint8_t *)g->it[item].xt[g->flip];
+        Q = (const uint8_t *)g->it[item].b;
+        K = Mp;
+        tr = local / (Mp / TN);
+        tc = local % (Mp / TN);
+    } else {
+        P = Q = (const uint8_t *)(MODE == NS_GRAM ? g->it[item].xh : g->it[item].a);
+        K = MODE == NS_GRAM ? Np : Mp;
+        // tiles on and above the diagonal, column by column
+        tc = (int)((sqrtf(8.0f * (float)local + 1.0f) - 1.0f) * 0.5f);
+        while (tc * (tc + 1) / 2 > local)
+            tc--;
+        while ((tc + 1) * (tc + 2) / 2 <= local)
+            tc++;
+        tr = local - tc * (tc + 1) / 2;
+    }
+    const int64_t ld = (int64_t)K * 2;
+    const int m0 = tr * TM, n0 = tc * TN, KB = K / 64;
+
+    v4f acc[IT][JT];
+#pragma unroll
+    for (int i = 0; i < IT; i++)
+#pragma unroll
+        for (int j = 0; j < JT; j++)
+            acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+
+    auto stage = [&](int kb, uint8_t *L) {
+        stage_rows<TM, NW>(L, P, ld, m0, (int64_t)kb * 128, wave, lane);
+        stage_rows<TN, NW>(L + TM * 128, Q, ld, n0, (int64_t)kb * 128, wave, lane);
+    };
+    auto kblock = [&](int kb, const uint8_t *L, uint8_t *LN) {
+        __builtin_amdgcn_s_waitcnt(0);   // this wave's copies of block kb have landed
+        __syncthreads();                 // everyone's have; LN is no longer read
+        // the next block, or this one again after the last (never read): no branch in the loop
+        stage(kb + 1 < KB ? kb + 1 : kb, LN);
+        const uint8_t *ta = L, *tb = L + TM * 128;
+        Frag bf[JT];
+#pragma unroll
+        for (int j = 0; j < JT; j++)
+            bf[j] = frag(tb, (wn * JT + j) * 16, lane);
+        Frag next = frag(ta, wm * IT * 16, lane);
+#pragma unroll
+        for (int i = 0; i < IT; i++) {
+            const Frag af = next;
+            if (i + 1 < IT)
+                next = frag(ta, (wm * IT + i + 1) * 16, lane);
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int k = 0; k < 2; k++)
+#pragma unroll
+                for (int j = 0; j < JT; j++)
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(af.k[k], bf[j].k[k], acc[i][j], 0, 0, 0);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    };
+    stage(0, lds0);
+    int kb = 0;
+    for (; kb + 1 < KB; kb += 2) {
+        kblock(kb, lds0, lds1);
+        kblock(kb + 1, lds1, lds0);
+    }
+    if (kb < KB)
+        kblock(kb, lds0, lds1);
+    __builtin_amdgcn_s_waitcnt(0);   // the idle copy has landed before the workgroup's LDS is given away
+
+    // acc[i][j][r] is row m0 + .. + r, column n0 + .. of the tile
+    const float inv = 1.0f / kScaleA;
+#pragma unroll
+    for (int i = 0; i < IT; i++) {
+        const int m = m0 + (wm * IT + i) * 16 + 4 * (lane >> 4);
+#pragma unroll
+        for (int j = 0; j < JT; j++) {
+            const int n = n0 + (wn * JT + j) * 16 + (lane & 15);
+            const v4f v = acc[i][j];
+            if constexpr (MODE == NS_UPDATE) {
+                const int row = n, col = m;   // of X
+                const int64_t at = (int64_t)row * Np + col;
+                const v4h hi = *reinterpret_cast<const v4h *>(g->it[item].xh + at);
+                const v4h lo = *reinterpret_cast<const v4h *>(g->it[item].xl + at);
+                const float f = fmaf(g->it[item].d[row], inv, g->a);
+                float x[4];
+#pragma unroll
+                for (int r = 0; r < 4; r++)
+                    x[r] = as_f32(fmaf(f, (float)hi[r] + (float)lo[r], v[r] * inv));
+                if (g->last) {
+                    const float is = 1.0f / g->it[item].s;
+                    uint16_t *o = (uint16_t *)g->it[item].o;
+                    const int64_t ldo = g->it[item].ldo;
+#pragma unroll
+                    for (int r = 0; r < 4; r++)
+                        if (row < g->it[item].M && col + r < g->it[item].N)
+                            o[g->it[item].tall ? (int64_t)(col + r) * ldo + row : (int64_t)row * ldo + col + r] =
+                                to_bf16(x[r] * is);
+                } else {
+                    v4h nh, nl;
+#pragma unroll
+                    for (int r = 0; r < 4; r++) {
+                        nh[r] = (_Float16)x[r];
+                        nl[r] = (_Float16)as_f32(x[r] - (float)nh[r]);
+                    }
+                    *reinterpret_cast<v4h *>(g->it[item].xh + at) = nh;
+                    *reinterpret_cast<v4h *>(g->it[item].xl + at) = nl;
+                    uint16_t *xt = g->it[item].xt[g->flip ^ 1];
+#pragma unroll
+                    for (int r = 0; r < 4; r++)
+                        xt[(int64_t)(col + r) * Mp + row] = h_bits((float)nh[r]);
+                }
+            } else {
+                uint16_t *out = MODE == NS_GRAM ? g->it[item].a : g->it[item].b;
+                v4h w;
+                if constexpr (MODE == NS_GRAM) {
+                    const float is = kScaleA / (g->it[item].s * g->it[item].s);
+#pragma unroll
+                    for (int r = 0; r < 4; r++)
+                        w[r] = (_Float16)as_f32(v[r] * is);
+                } else {
+                    const v4h a4 = *reinterpret_cast<const v4h *>(g->it[item].a + (int64_t)n * Mp + m);
+#pragma unroll
+                    for (int r = 0; r < 4; r++) {
+                        const float y = as_f32(fmaf(g->b, (float)a4[r], g->c * inv * v[r]));
+                        w[r] = (_Float16)y;
+                        if (m + r == n) {
+                            g->it[item].d[n] = y;
+                            w[r] = (_Float16)0.0f;
+                        }
+                    }
+                }
+                *reinterpret_cast<v4h *>(out + (int64_t)n * Mp + m) = w;
+                if (tr != tc) {
+#pragma unroll
+                    for (int r = 0; r < 4; r++)
+                        out[(int64_t)(m + r) * Mp + n] = h_bits((float)w[r]);
+                }
+            }
+        }
+    }
+}
+
+int pad_to(int n, int t) { return (n + t - 1) / t * t; }
+
+size_t up256(size_t n) { return (n + 255) / 256 * 256; }
+
+// Lays one matrix out in the workspace from `base` on (NULL: only counts); the bytes used.
+size_t lay_out(NsItem &it, char *base)
+{
+    size_t off = 0;
+    auto take = [&](size_t bytes) {
+        char *p = base ? base + off : nullptr;
+        off += up256(bytes);
+        return p;
+    };
+    const size_t mn = (size_t)it.Mp * it.Np * 2, mm = (size_t)it.Mp * it.Mp * 2;
+    it.xh = (uint16_t *)take(mn);
+    it.xl = (uint16_t *)take(mn);
+    it.xt[0] = (uint16_t *)take(mn);
+    it.xt[1] = (uint16_t *)take(mn);
+    it.a = (uint16_t *)take(mm);
+    it.b = (uint16_t *)take(mm);
+    it.d = (float *)take((size_t)it.Mp * 4);
+    it.part = (double *)take(kNormBlocks * sizeof(double));
+    return off;
+}
+
+NsItem make_item(const NsMatrix &m)
+{
+    NsItem it;
+    it.g = m.g;
+    it.o = m.o;
+    it.ldg = m.ldg;
+    it.ldo = m.ldo;
+    it.tall = m.rows > m.cols;
+    it.M = (int)std::min(m.rows, m.cols);
+    it.N = (int)std::max(m.rows, m.cols);
+    it.Mp = pad_to(it.M, 128);
+    it.Np = pad_to(it.N, 128);
+    it.s = (float)std::exp2(std::round(0.5 * std::log2((double)it.N)));
+    return it;
+}
+
+template <class Cfg, int MODE> hipError_t launch_product(NsGroup &g, hipStream_t st)
+{
+    g.first[0] = 0;
+    for (int i = 0; i < g.count; i++) {
+        const int rows = (MODE == NS_UPDATE ? g.it[i].Np : g.it[i].Mp) / Cfg::TM, cols = g.it[i].Mp / Cfg::TN;
+        g.first[i + 1] = g.first[i] + (MODE == NS_UPDATE ? rows * cols : cols * (cols + 1) / 2);
+    }
+    hipLaunchKernelGGL((ns_product_kernel<Cfg, MODE>), dim3((unsigned)g.first[g.count]), dim3(Cfg::THREADS), 0, st, g);
+    return hipGetLastError();
+}
+
+template <class Cfg> hipError_t launch_step(NsGroup &g, hipStream_t st)
+{
+    hipError_t e = launch_product<Cfg, NS_GRAM>(g, st);
+    if (e == hipSuccess)
+        e = launch_product<Cfg, NS_POLY>(g, st);
+    if (e == hipSuccess)
+        e = launch_product<Cfg, NS_UPDATE>(g, st);
+    return e;
+}
+
+} // namespace
+
+// Matrices of one call run kNsGroupMax at a time; the groups follow each other
+// on the stream and share the workspace.
+size_t newton_workspace_bytes(const NsMatrix *ms, int count)
+{
+    size_t most = 0;
+    for (int lo = 0; lo < count; lo += kNsGroupMax) {
+        size_t sum = 0;
+        for (int i = lo; i < std::min(count, lo + kNsGroupMax); i++) {
+            NsItem it = make_item(ms[i]);
+            sum += lay_out(it, nullptr);
+        }
+        most = std::max(most, sum);
+    }
+    return most;
+}
+
+hipError_t launch_newton(const NsMatrix *ms, int count, bool gbf16, int steps, const float *coef, float eps,
+                         void *workspace, hipStream_t st)
+{
+    for (int lo = 0; lo < count; lo += kNsGroupMax) {
+        NsGroup g;
+        g.count = std::min(count - lo, kNsGroupMax);
+        g.gbf16 = gbf16;
+        g.eps = eps;
+        g.flip = 0;
+        size_t off = 0;
+        bool large = true;
+        g.first[0] = 0;
+        for (int i = 0; i < g.count; i++) {
+            g.it[i] = make_item(ms[lo + i]);
+            off += lay_out(g.it[i], (char *)workspace + off);
+            large = large && g.it[i].Mp % 256 == 0 && g.it[i].Np % 256 == 0;
+            g.first[i + 1] = g.first[i] + (g.it[i].Mp / 64) * (g.it[i].Np / 64);
+        }
+        hipLaunchKernelGGL(ns_norm_kernel, dim3(kNormBlocks, (unsigned)g.count), dim3(256), 0, st, g);
+        hipError_t e = hipGetLastError();
+        if (e != hipSuccess)
+            return e;
+        hipLaunchKernelGGL(ns_init_kernel, dim3((unsigned)g.first[g.count]), dim3(256), 0, st, g);
+        e = hipGetLastError();
+        for (int k = 0; k < steps && e == hipSuccess; k++) {
+            g.a = coef[3 * k];
+            g.b = coef[3 * k + 1];
+            g.c = coef[3 * k + 2];
+            g.last = k + 1 == steps;
+            e = large ? launch_step<NsL>(g, st) : launch_step<NsQ>(g, st);
+            g.flip ^= 1;
+        }
+        if (e != hipSuccess)
+            return e;
+    }
+    return hipSuccess;
+}
+
+} // namespace puro

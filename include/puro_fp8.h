@@ -512,6 +512,50 @@ puro_status_t puro_fp8_gemm_grouped_native(puro_layout_t layout, puro_bscale_t b
                                            const puro_gemm_desc_t *problems, int count, hipStream_t stream);
 
 /*
+ * Newton-Schulz orthogonalisation of weight gradients (or their momenta).
+ * Passage: the model card's optimiser paragraph (MuonH, a Muon-type optimiser
+ * with a hyperball projection, for the recipe's matrix parameters): such an
+ * update is the gradient's momentum with its singular values driven towards
+ * one.  This call is that product chain; momentum, projection and step are the
+ * optimiser's own.  For each matrix G [rows][cols], X = G / (|G|_F + eps),
+ * taken transposed if rows > cols, and `steps` times, with (a, b, c) =
+ * coef[3 k], coef[3 k + 1], coef[3 k + 2]:
+ *     A = X X^T,   X <- a X + (b A + c A A) X
+ * o receives X (transposed back) as BF16.  |G|_F is formed in 64 bits, the
+ * products on the FP16 matrix cores with X held to 22 bits between steps: with
+ * the usual quintic (3.4445, -4.7750, 2.0315) and five steps the result is
+ * within about 2e-3 (relative Frobenius) of the exact one before its BF16
+ * rounding, which is of that size itself.  Equal calls give equal bits.
+ *   gdt     element type of every matrix (FP32 or BF16); G must be finite
+ *   items   HOST array of `count` descriptors, read before the call returns; no
+ *           output may overlap an input or another output
+ *   count   0 .. PURO_NS_MAX_GROUP; rows and cols 0 .. PURO_NS_MAX_DIM (an
+ *           empty matrix is skipped)
+ *   steps   1 .. PURO_NS_MAX_STEPS, else PURO_ERR_VALUE
+ *   coef    HOST array of 3 steps numbers.  Starting from singular values in
+ *           [0, 1], every step has to keep |b l + c l^2| (l the squared singular
+ *           values) at most 32 and the singular values at most 2, the range of
+ *           the FP16 products; else PURO_ERR_VALUE
+ *   eps     finite and > 0, else PURO_ERR_VALUE (a zero matrix gives zeros)
+ * workspace: at least puro_fp8_newton_schulz_workspace_size(items, count) bytes
+ * (0 for invalid arguments; only rows and cols are read) of device memory,
+ * 256-byte aligned, not used by other work in flight.
+ */
+#define PURO_NS_MAX_GROUP 4096
+#define PURO_NS_MAX_DIM 16384
+#define PURO_NS_MAX_STEPS 32
+typedef struct {
+    const void *g;           /* [rows][cols], row stride ldg */
+    int64_t rows, cols, ldg;
+    void *o;                 /* BF16 [rows][cols], row stride ldo */
+    int64_t ldo;
+} puro_newton_schulz_desc_t;
+size_t puro_fp8_newton_schulz_workspace_size(const puro_newton_schulz_desc_t *items, int count);
+puro_status_t puro_fp8_newton_schulz_grouped(puro_dtype_t gdt, const puro_newton_schulz_desc_t *items, int count,
+                                             int steps, const float *coef, float eps, void *workspace,
+                                             size_t ws_bytes, hipStream_t stream);
+
+/*
  * puro_fp8_gemm without a workspace argument, for callers that cannot
  * allocate device memory (code under HIP graph capture, tight serving loops,
  * harnesses that forbid hipMalloc).  Arguments, validation, result and
