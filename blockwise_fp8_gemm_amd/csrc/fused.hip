@@ -29,7 +29,8 @@ namespace puro {
 
 namespace {
 
-constexpr int TT = 512;   // threads of a tile kernel: 16 column groups x 32 token groups
+// A tile kernel's threads hold RT tokens x 8 columns each.
+constexpr int tile_threads(int rt) { return 16 * 128 / rt; }
 
 template <int CTRL> __device__ __forceinline__ float dpp_f(float v)
 {
@@ -56,23 +57,63 @@ __device__ __forceinline__ float sum64(float v)
     return v + __shfl_xor(v, 32, 64);
 }
 
-// Code factor of a block: v * r rounds within 2 ulps of v / s.  r is 0 for a
-// zero scale (codes +-0 by sign); a subnormal scale (1 / s could overflow)
-// divides instead, which SLOW selects for a whole tile or row run.
-__device__ __forceinline__ float scale_inv(float s) { return s >= 0x1p-126f ? 1.0f / s : 0.0f; }
-__device__ __forceinline__ bool scale_slow(float s) { return s != 0.0f && s < 0x1p-126f; }
-
-template <bool SLOW> __device__ __forceinline__ float code_arg(float v, float s, float r)
+// max(|a|, |b|, m) for m >= 0, in one instruction (fmaxf would first quieten
+// values that come straight from memory).
+__device__ __forceinline__ float absmax3(float a, float b, float m)
 {
-    if (SLOW && scale_slow(s))
-        return v / s;
-    return v * r;
+    float r;
+    asm("v_max3_f32 %0, |%1|, |%2|, %3" : "=v"(r) : "v"(a), "v"(b), "v"(m));
+    return r;
 }
 
-template <bool SLOW>
-__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d, float s, float r)
+// A block's scale s and its reciprocal r + rl, rl >= 0 the part that FP32 r
+// lacks: v / s is then fma(v, r, v rl), two operations, within 0.5 + 2^-20 ulps of
+// the quotient (rl >= 0 keeps the sign of -0).  s = amax / 448 by one
+// correction step from 1/448's FP32 value, exact as IEEE division while the
+// residual does not underflow.  r = 0 for a zero scale (codes +-0 by sign).  A
+// scale below 2^-96, whose reciprocal could overflow, has that of s 2^64 and
+// its values are multiplied by 2^64 first (exact: they are at most 448 s),
+// which SLOW selects for a whole tile or run.
+struct Scale {
+    float s, r, rl;
+};
+__device__ __forceinline__ bool scale_tiny(float s) { return s < 0x1p-96f; }
+__device__ __forceinline__ bool scale_slow(float s, int pow2) { return !pow2 && s != 0.0f && scale_tiny(s); }
+
+__device__ __forceinline__ Scale make_scale(float amax, int pow2)
 {
-    return e4m3x4(code_arg<SLOW>(a, s, r), code_arg<SLOW>(b, s, r), code_arg<SLOW>(c, s, r), code_arg<SLOW>(d, s, r));
+    Scale o;
+    if (pow2) {
+        o.s = pow2_scale(amax);
+        o.r = __uint_as_float(0x7F000000u - (__float_as_uint(o.s) & 0x7F800000u));
+        o.rl = 0.0f;
+        return o;
+    }
+    const float c = 1.0f / 448.0f, q = amax * c;
+    o.s = fmaf(fmaf(-q, 448.0f, amax), c, q);
+    if (amax < 0x1p-80f)
+        o.s = amax / 448.0f;
+    const float s = scale_tiny(o.s) ? o.s * 0x1p64f : o.s, r0 = __builtin_amdgcn_rcpf(s);
+    float r = fmaf(fmaf(-s, r0, 1.0f), r0, r0), e = fmaf(-s, r, 1.0f);
+    if (e < 0.0f) {   // r above 1 / s: the float below it
+        r = __uint_as_float(__float_as_uint(r) - 1);
+        e = fmaf(-s, r, 1.0f);
+    }
+    o.r = s > 0.0f ? r : 0.0f;
+    o.rl = s > 0.0f ? e * r : 0.0f;
+    return o;
+}
+
+template <bool SLOW> __device__ __forceinline__ float code_arg(float v, const Scale &c)
+{
+    if (SLOW)
+        v = scale_tiny(c.s) ? v * 0x1p64f : v;
+    return fmaf(v, c.r, v * c.rl);
+}
+
+template <bool SLOW> __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d, const Scale &s)
+{
+    return e4m3x4(code_arg<SLOW>(a, s), code_arg<SLOW>(b, s), code_arg<SLOW>(c, s), code_arg<SLOW>(d, s));
 }
 
 // Eight BF16 values of a row from column c0 on, zeros at and past cols.
@@ -154,152 +195,235 @@ struct QuantOut {
 
 // ---------------------------------------------------------------------------
 // Quantise a 128-token x 128-column tile both ways from FP32 values.  Thread t
-// owns columns 8 (t % 16) .. +7 of the 4 tokens 4 (t / 16) .. +3; a tile's
-// values outside the tensor are zero.  Row amax: 16-lane DPP max.  Column
-// amax: over the thread's tokens, the wave's four token groups, then the
-// eight waves through LDS.  Four tokens' codes of a column are one 32-bit
-// word of the LDS tile, written out as 128-byte rows.
+// owns columns 8 (t % 16) .. +7 of the RT tokens RT (t / 16) .. + RT - 1; a
+// tile's values outside the tensor are zero.  Row amax: 16-lane DPP max; lanes
+// 0 .. RT - 1 of a 16-lane group then each form one token's scale.  Column amax:
+// over the thread's tokens, the wave's four token groups (each exchange step
+// halves the columns a lane carries on), then the waves through LDS.  The
+// column codes are turned in LDS and written out as 128-byte rows.
 // ---------------------------------------------------------------------------
-struct TileShared {
-    float red[TT / 64][128];
-    float scl[128], rcl[128];
-    uint32_t tile[128][32 + 1];   // [column][token / 4], odd stride
+template <int RT> struct TileShared {
+    static constexpr int WAVES = tile_threads(RT) / 64;
+    float red[WAVES][128];
+    float scl[128], rcl[128], rll[128];   // column scales, reciprocals and their low parts
+    uint32_t slow[WAVES];                 // whether a wave met a scale below 2^-96
+    uint8_t tile[128][128 + 4];           // [column][token] codes, odd stride in dwords
 };
 
-template <bool SLOW>
-__device__ __forceinline__ void tile_codes(const float (&v)[4][8], const float (&srow)[4], const QuantOut &ro,
-                                           int transpose_out, const QuantOut &to, int64_t tok0, int64_t col0,
-                                           int64_t tokens, int64_t cols, bool full, TileShared &sh)
+// Holds the compiler to forming a tile's values here, once: left alone it
+// carries the factors of each value along and forms it again at every use,
+// which takes more registers than the values themselves and spills.
+template <int RT> __device__ __forceinline__ void pin(float (&v)[RT][8])
 {
-    const int t = threadIdx.x, cc = t & 15, rq = t >> 4;
-    const int64_t c0 = col0 + 8 * cc;
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
-        const int64_t tk = tok0 + 4 * rq + i;
-        const float s = srow[i], r = scale_inv(s);
-        const uint32_t lo = codes4<SLOW>(v[i][0], v[i][1], v[i][2], v[i][3], s, r);
-        const uint32_t hi = codes4<SLOW>(v[i][4], v[i][5], v[i][6], v[i][7], s, r);
-        if (full)
-            store_nt(ro.q + tk * ro.ldq + c0, lo, hi);
-        else if (tk < tokens)
-            store8_codes(ro.q + tk * ro.ldq, c0, cols, lo, hi);
+    for (int i = 0; i < RT; i++)
+#pragma unroll
+        for (int j = 0; j < 8; j++)
+            asm volatile("" : "+v"(v[i][j]));
+}
+
+// This thread's place in a tile.
+template <int RT> struct Place {
+    int64_t tok0, col0, tokens, cols;
+    int cc, rq;
+    __device__ __forceinline__ int64_t tk(int i) const { return tok0 + RT * rq + i; }
+    __device__ __forceinline__ int64_t c0() const { return col0 + 8 * cc; }
+};
+template <int RT> __device__ __forceinline__ Place<RT> place(int64_t tokens, int64_t cols)
+{
+    return Place<RT>{(int64_t)blockIdx.y * 128, (int64_t)blockIdx.x * 128, tokens, cols, (int)threadIdx.x & 15,
+                 (int)threadIdx.x >> 4};
+}
+
+// Exchange between the wave's halves, then between its 16-lane rows: op over
+// the four lanes with equal lane % 16 of eight values; lane group g = lane / 16
+// ends with the results of values first(g) and first(g) + 1.
+__device__ __forceinline__ int first_of(int lane) { return ((lane >> 5) & 1) * 4 + ((lane >> 4) & 1) * 2; }
+template <class Op> __device__ __forceinline__ float2 cross4(const float (&m)[8], Op op)
+{
+    float p[4], q[2];
+#pragma unroll
+    for (int k = 0; k < 4; k++) {
+        const auto x = __builtin_amdgcn_permlane32_swap(__float_as_uint(m[k]), __float_as_uint(m[k + 4]), false, false);
+        p[k] = op(__uint_as_float(x[0]), __uint_as_float(x[1]));
     }
-    uint32_t word[8];
 #pragma unroll
-    for (int j = 0; j < 8; j++)
-        word[j] = codes4<SLOW>(v[0][j], v[1][j], v[2][j], v[3][j], sh.scl[8 * cc + j], sh.rcl[8 * cc + j]);
-    if (!transpose_out) {
+    for (int k = 0; k < 2; k++) {
+        const auto x = __builtin_amdgcn_permlane16_swap(__float_as_uint(p[k]), __float_as_uint(p[k + 2]), false, false);
+        q[k] = op(__uint_as_float(x[0]), __uint_as_float(x[1]));
+    }
+    return make_float2(q[0], q[1]);
+}
+
+template <int I> __device__ __forceinline__ Scale row_scale(const Scale &own)
+{
+    return Scale{dpp_f<0x150 + I>(own.s), dpp_f<0x150 + I>(own.r), dpp_f<0x150 + I>(own.rl)};
+}
+
+template <bool SLOW, bool FULL, bool TR, int RT>
+__device__ __forceinline__ void tile_codes(const float (&v)[RT][8], const Scale &own, const QuantOut &ro,
+                                           const QuantOut &to, const Place<RT> &p, TileShared<RT> &sh)
+{
+    Scale sr[RT];
+    sr[0] = row_scale<0>(own);
+    sr[1] = row_scale<1>(own);
+    if constexpr (RT == 4) {
+        sr[2] = row_scale<2>(own);
+        sr[3] = row_scale<3>(own);
+    }
+    uint8_t *qr = ro.q + p.tk(0) * ro.ldq + (FULL ? p.c0() : 0);
 #pragma unroll
-        for (int i = 0; i < 4; i++) {
-            const int64_t tk = tok0 + 4 * rq + i;
+    for (int i = 0; i < RT; i++) {
+        const uint32_t lo = codes4<SLOW>(v[i][0], v[i][1], v[i][2], v[i][3], sr[i]);
+        const uint32_t hi = codes4<SLOW>(v[i][4], v[i][5], v[i][6], v[i][7], sr[i]);
+        if (FULL)
+            store_nt(qr + i * ro.ldq, lo, hi);
+        else if (p.tk(i) < p.tokens)
+            store8_codes(qr + i * ro.ldq, p.c0(), p.cols, lo, hi);
+    }
+    uint32_t word[8];   // RT codes of a column, a byte each
+#pragma unroll
+    for (int j = 0; j < 8; j++) {
+        const Scale c{SLOW ? sh.scl[8 * p.cc + j] : 0.0f, sh.rcl[8 * p.cc + j], sh.rll[8 * p.cc + j]};
+        if constexpr (RT == 4)
+            word[j] = codes4<SLOW>(v[0][j], v[1][j], v[2][j], v[3][j], c);
+        else
+            word[j] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(code_arg<SLOW>(v[0][j], c), code_arg<SLOW>(v[1][j], c),
+                                                                0, false);
+    }
+    if constexpr (!TR) {
+#pragma unroll
+        for (int i = 0; i < RT; i++) {
             uint32_t b[8];
 #pragma unroll
             for (int j = 0; j < 8; j++)
                 b[j] = (word[j] >> (8 * i)) & 0xFFu;
             const uint32_t lo = b[0] | (b[1] << 8) | (b[2] << 16) | (b[3] << 24);
             const uint32_t hi = b[4] | (b[5] << 8) | (b[6] << 16) | (b[7] << 24);
-            if (tk < tokens)
-                store8_codes(to.q + tk * to.ldq, c0, cols, lo, hi);
+            if (p.tk(i) < p.tokens)
+                store8_codes(to.q + p.tk(i) * to.ldq, p.c0(), p.cols, lo, hi);
         }
         return;
     }
-#pragma unroll
-    for (int j = 0; j < 8; j++)
-        sh.tile[8 * cc + j][rq] = word[j];
-}
-
-__device__ __forceinline__ void quant_tile(const float (&v)[4][8], const QuantOut &ro, int transpose_out,
-                                           const QuantOut &to, int64_t tok0, int64_t col0, int64_t tokens,
-                                           int64_t cols, int pow2, bool full, TileShared &sh)
-{
-    const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
-    const int cc = t & 15, rq = t >> 4;
-    const int64_t bx = col0 >> 7, by = tok0 >> 7;
-    bool slow = false;
-
-    float m[8];
 #pragma unroll
     for (int j = 0; j < 8; j++) {
-        float a = fmaxf(fmaxf(fabsf(v[0][j]), fabsf(v[1][j])), fmaxf(fabsf(v[2][j]), fabsf(v[3][j])));
-        a = fmaxf(a, __shfl_xor(a, 16, 64));
-        m[j] = fmaxf(a, __shfl_xor(a, 32, 64));
+        uint8_t *dst = &sh.tile[8 * p.cc + j][RT * p.rq];
+        if constexpr (RT == 4)
+            *reinterpret_cast<uint32_t *>(dst) = word[j];
+        else
+            *reinterpret_cast<uint16_t *>(dst) = (uint16_t)word[j];
     }
-    if (lane < 16) {
+}
+
+template <bool FULL, bool TR, int RT>
+__device__ __forceinline__ void quant_tile(const float (&v)[RT][8], const QuantOut &ro, const QuantOut &to,
+                                           const Place<RT> &p, int pow2, TileShared<RT> &sh)
+{
+    constexpr int WAVES = TileShared<RT>::WAVES;
+    const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+    const int64_t bx = p.col0 >> 7, by = p.tok0 >> 7;
+
+    float m[8], a[RT];
 #pragma unroll
-        for (int j = 0; j < 8; j++)
-            sh.red[wave][8 * lane + j] = m[j];
+    for (int j = 0; j < 8; j++) {
+        m[j] = absmax3(v[0][j], v[1][j], 0.0f);
+        if constexpr (RT == 4)
+            m[j] = absmax3(v[2][j], v[3][j], m[j]);
     }
-    float srow[4];
+    *reinterpret_cast<float2 *>(&sh.red[wave][8 * p.cc + first_of(lane)]) =
+        cross4(m, [](float a, float b) { return absmax3(a, b, 0.0f); });
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
-        float a = 0.0f;
-#pragma unroll
-        for (int j = 0; j < 8; j++)
-            a = fmaxf(a, fabsf(v[i][j]));
-        srow[i] = block_scale(max16(a), pow2);
-        slow = slow || scale_slow(srow[i]);
-        const int64_t tk = tok0 + 4 * rq + i;
-        if (cc == 0 && tk < tokens)
-            ro.s[tk * ro.lds + bx] = srow[i];
-    }
+    for (int i = 0; i < RT; i++)
+        a[i] = max16(absmax3(v[i][6], v[i][7], absmax3(v[i][4], v[i][5], absmax3(v[i][2], v[i][3],
+                     absmax3(v[i][0], v[i][1], 0.0f)))));
+    float mine = p.cc & 1 ? a[1] : a[0];
+    if constexpr (RT == 4)
+        mine = p.cc & 2 ? (p.cc & 1 ? a[3] : a[2]) : mine;
+    const Scale own = make_scale(mine, pow2);
+    uint32_t slow = __any(scale_slow(own.s, pow2));
+    if (p.cc < RT && (FULL || p.tk(p.cc) < p.tokens))
+        ro.s[p.tk(p.cc) * ro.lds + bx] = own.s;
     __syncthreads();
     if (t < 128) {
-        float a = sh.red[0][t];
+        float c = sh.red[0][t];
 #pragma unroll
-        for (int k = 1; k < TT / 64; k++)
-            a = fmaxf(a, sh.red[k][t]);
-        const float s = block_scale(a, pow2);
-        sh.scl[t] = s;
-        sh.rcl[t] = scale_inv(s);
-        slow = slow || scale_slow(s);
-        const int64_t c = col0 + t;
-        if (c < cols) {
-            if (transpose_out)
-                to.s[c * to.lds + by] = s;
+        for (int k = 1; k < WAVES; k++)
+            c = absmax3(c, sh.red[k][t], 0.0f);
+        const Scale o = make_scale(c, pow2);
+        sh.scl[t] = o.s;
+        sh.rcl[t] = o.r;
+        sh.rll[t] = o.rl;
+        slow |= __any(scale_slow(o.s, pow2));
+        if (FULL || p.col0 + t < p.cols) {
+            if (TR)
+                to.s[(p.col0 + t) * to.lds + by] = o.s;
             else
-                to.s[by * to.lds + c] = s;
+                to.s[by * to.lds + p.col0 + t] = o.s;
         }
     }
-    if (__syncthreads_or(slow))
-        tile_codes<true>(v, srow, ro, transpose_out, to, tok0, col0, tokens, cols, full, sh);
+    if (lane == 0)
+        sh.slow[wave] = slow;
+    __syncthreads();
+    slow = 0;
+#pragma unroll
+    for (int k = 0; k < WAVES; k++)
+        slow |= sh.slow[k];
+    if (__builtin_amdgcn_readfirstlane(slow))
+        tile_codes<true, FULL, TR, RT>(v, own, ro, to, p, sh);
     else
-        tile_codes<false>(v, srow, ro, transpose_out, to, tok0, col0, tokens, cols, full, sh);
-    if (!transpose_out)
+        tile_codes<false, FULL, TR, RT>(v, own, ro, to, p, sh);
+    if (!TR)
         return;
     __syncthreads();
 #pragma unroll
-    for (int it = 0; it < 2; it++) {
-        const int chunk = t + TT * it;
+    for (int it = 0; it < 1024 / tile_threads(RT); it++) {
+        const int chunk = t + tile_threads(RT) * it;
         const int row = chunk >> 3, seg = chunk & 7;
-        const int64_t c = col0 + row, tk = tok0 + seg * 16;
-        const uint32_t *src = &sh.tile[row][seg * 4];
-        if (c >= cols)
-            continue;
+        const int64_t c = p.col0 + row, tk = p.tok0 + seg * 16;
+        const uint32_t *src = reinterpret_cast<const uint32_t *>(&sh.tile[row][seg * 16]);
         uint8_t *dst = to.q + c * to.ldq + tk;
-        if (tk + 16 <= tokens) {
+        if (FULL || (c < p.cols && tk + 16 <= p.tokens)) {
             store_nt(dst, src[0], src[1], src[2], src[3]);
-        } else {
+        } else if (c < p.cols) {
             for (int e = 0; e < 16; e++)
-                if (tk + e < tokens)
-                    dst[e] = (uint8_t)(src[e >> 2] >> (8 * (e & 3)));
+                if (tk + e < p.tokens)
+                    dst[e] = sh.tile[row][seg * 16 + e];
         }
     }
 }
 
-// Four rows x eight columns of a BF16 tensor for this thread (zeros outside).
-__device__ __forceinline__ void load_tile(const uint16_t *x, int64_t ldx, int64_t tok0, int64_t col0, int64_t tokens,
-                                          int64_t cols, bool full, uint4 (&a)[4])
+// RT rows x eight columns of a BF16 tensor for this thread (zeros outside).
+template <bool FULL, int RT>
+__device__ __forceinline__ void load_tile(const uint16_t *x, int64_t ldx, const Place<RT> &p, uint4 (&a)[RT])
 {
-    const int cc = threadIdx.x & 15, rq = threadIdx.x >> 4;
-    const int64_t c0 = col0 + 8 * cc;
+    const uint16_t *row = x + p.tk(0) * ldx;
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
-        const int64_t tk = tok0 + 4 * rq + i;
-        if (full)
-            a[i] = *reinterpret_cast<const uint4 *>(x + tk * ldx + c0);
+    for (int i = 0; i < RT; i++) {
+        if (FULL)
+            a[i] = *reinterpret_cast<const uint4 *>(row + i * ldx + p.c0());
         else
-            a[i] = tk < tokens ? load8_bf16(x + tk * ldx, c0, cols) : make_uint4(0, 0, 0, 0);
+            a[i] = p.tk(i) < p.tokens ? load8_bf16(row + i * ldx, p.c0(), p.cols) : make_uint4(0, 0, 0, 0);
     }
+}
+
+template <bool FULL, int RT>
+__device__ __forceinline__ void store_tile(uint16_t *x, int64_t ldx, const Place<RT> &p, const float (&v)[RT][8])
+{
+#pragma unroll
+    for (int i = 0; i < RT; i++) {
+        const uint32_t o[4] = {to_bf16x2(v[i][0], v[i][1]), to_bf16x2(v[i][2], v[i][3]), to_bf16x2(v[i][4], v[i][5]),
+                               to_bf16x2(v[i][6], v[i][7])};
+        if (FULL)
+            store_nt(x + p.tk(i) * ldx + p.c0(), o[0], o[1], o[2], o[3]);
+        else if (p.tk(i) < p.tokens)
+            store8_bf16(x + p.tk(i) * ldx, p.c0(), p.cols, o);
+    }
+}
+
+// Whole tiles (uniform over the workgroup) and edge tiles are two bodies of one kernel.
+template <int RT> __device__ __forceinline__ bool full_tile(const Place<RT> &p)
+{
+    return p.tok0 + 128 <= p.tokens && p.col0 + 128 <= p.cols;
 }
 
 // ---------------------------------------------------------------------------
@@ -383,13 +507,13 @@ __global__ __launch_bounds__(NT) void norm_row_kernel(const uint16_t *__restrict
                 n[j] = n[j] * r * wv[j];
                 amax = fmaxf(amax, fabsf(n[j]));
             }
-            const float sc = block_scale(max16(amax), pow2), ri = scale_inv(sc);
+            const Scale sc = make_scale(max16(amax), pow2);
             if (c0 >= cols)
                 return;
-            store8_codes(q + row * ldq, c0, cols, codes4<true>(n[0], n[1], n[2], n[3], sc, ri),
-                         codes4<true>(n[4], n[5], n[6], n[7], sc, ri));
+            store8_codes(q + row * ldq, c0, cols, codes4<true>(n[0], n[1], n[2], n[3], sc),
+                         codes4<true>(n[4], n[5], n[6], n[7], sc));
             if ((t & 15) == 0)
-                s[row * nb + (c0 >> 7)] = sc;
+                s[row * nb + (c0 >> 7)] = sc.s;
             if (h) {
                 const uint32_t o[4] = {to_bf16x2(n[0], n[1]), to_bf16x2(n[2], n[3]), to_bf16x2(n[4], n[5]),
                                        to_bf16x2(n[6], n[7])};
@@ -412,35 +536,42 @@ __global__ __launch_bounds__(NT) void norm_row_kernel(const uint16_t *__restrict
 
 // Tile pass: n = z r w of a tile, quantised both ways (and stored as BF16
 // when h is not NULL).
-__global__ __launch_bounds__(TT) void norm_tile_kernel(const uint16_t *__restrict__ z, int64_t ldz,
-                                                       const float *__restrict__ rstd, const void *__restrict__ w,
-                                                       int wbf16, int64_t tokens, int64_t cols,
-                                                       uint16_t *__restrict__ h, int64_t ldh, QuantOut ro,
-                                                       int transpose_out, QuantOut to, int pow2)
+constexpr int NORM_RT = 4;
+template <bool FULL, bool TR, int RT>
+__device__ __forceinline__ void norm_tile(const uint16_t *z, int64_t ldz, const float *rstd, const void *w, int wbf16,
+                                          const Place<RT> &p, uint16_t *h, int64_t ldh, const QuantOut &ro,
+                                          const QuantOut &to, int pow2, TileShared<RT> &sh)
 {
-    __shared__ TileShared sh;
-    const int64_t tok0 = (int64_t)blockIdx.y * 128, col0 = (int64_t)blockIdx.x * 128;
-    const bool full = tok0 + 128 <= tokens && col0 + 128 <= cols;
-    const int cc = threadIdx.x & 15, rq = threadIdx.x >> 4;
-    uint4 a[4];
-    load_tile(z, ldz, tok0, col0, tokens, cols, full, a);
-    float wv[8], v[4][8];
-    load8_weight(w, wbf16, col0 + 8 * cc, cols, wv);
+    uint4 a[RT];
+    load_tile<FULL>(z, ldz, p, a);
+    float wv[8], v[RT][8];
+    load8_weight(w, wbf16, p.c0(), p.cols, wv);
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
-        const int64_t tk = tok0 + 4 * rq + i;
-        const float r = tk < tokens ? rstd[tk] : 0.0f;
+    for (int i = 0; i < RT; i++) {
+        const float r = FULL || p.tk(i) < p.tokens ? rstd[p.tk(i)] : 0.0f;
         unpack8(a[i], v[i]);
 #pragma unroll
         for (int j = 0; j < 8; j++)
             v[i][j] = v[i][j] * r * wv[j];
-        if (h && tk < tokens) {
-            const uint32_t o[4] = {to_bf16x2(v[i][0], v[i][1]), to_bf16x2(v[i][2], v[i][3]),
-                                   to_bf16x2(v[i][4], v[i][5]), to_bf16x2(v[i][6], v[i][7])};
-            store8_bf16(h + tk * ldh, col0 + 8 * cc, cols, o);
-        }
     }
-    quant_tile(v, ro, transpose_out, to, tok0, col0, tokens, cols, pow2, full, sh);
+    pin(v);
+    if (h)
+        store_tile<FULL>(h, ldh, p, v);
+    quant_tile<FULL, TR, RT>(v, ro, to, p, pow2, sh);
+}
+
+template <bool TR>
+__global__ __launch_bounds__(tile_threads(NORM_RT)) __attribute__((amdgpu_waves_per_eu(5)))
+void norm_tile_kernel(const uint16_t *__restrict__ z, int64_t ldz, const float *__restrict__ rstd,
+                      const void *__restrict__ w, int wbf16, int64_t tokens, int64_t cols, uint16_t *__restrict__ h,
+                      int64_t ldh, QuantOut ro, QuantOut to, int pow2)
+{
+    __shared__ TileShared<NORM_RT> sh;
+    const auto p = place<NORM_RT>(tokens, cols);
+    if (full_tile(p))
+        norm_tile<true, TR, NORM_RT>(z, ldz, rstd, w, wbf16, p, h, ldh, ro, to, pow2, sh);
+    else
+        norm_tile<false, TR, NORM_RT>(z, ldz, rstd, w, wbf16, p, h, ldh, ro, to, pow2, sh);
 }
 
 // ---------------------------------------------------------------------------
@@ -472,86 +603,95 @@ __global__ __launch_bounds__(NT) void norm_bwd_row_kernel(const uint16_t *__rest
 
 // Tile pass: dx of a tile, stored as BF16 and quantised both ways, and the
 // tile's share of dw (its 128 tokens), to part[token tile][column].
-__global__ __launch_bounds__(TT) void norm_bwd_tile_kernel(const uint16_t *__restrict__ dy, int64_t lddy,
-                                                           const uint16_t *__restrict__ z, int64_t ldz,
-                                                           const float *__restrict__ rstd,
-                                                           const float *__restrict__ coef,
-                                                           const void *__restrict__ w, int wbf16,
-                                                           const uint16_t *__restrict__ dres, int64_t lddres,
-                                                           int64_t tokens, int64_t cols,
-                                                           uint16_t *__restrict__ dx, int64_t lddx, QuantOut ro,
-                                                           int transpose_out, QuantOut to,
-                                                           float *__restrict__ part, int pow2)
+constexpr int BWD_RT = 4;
+template <bool FULL, bool TR, int RT>
+__device__ __forceinline__ void norm_bwd_tile(const NormBwd &b, const float *coef, const Place<RT> &p, const QuantOut &ro,
+                                              const QuantOut &to, float *part, int pow2, TileShared<RT> &sh)
 {
-    __shared__ TileShared sh;
-    const int64_t tok0 = (int64_t)blockIdx.y * 128, col0 = (int64_t)blockIdx.x * 128;
-    const bool full = tok0 + 128 <= tokens && col0 + 128 <= cols;
-    const int t = threadIdx.x, cc = t & 15, rq = t >> 4, lane = t & 63, wave = t >> 6;
-    uint4 a[4], b[4], d[4];
-    load_tile(dy, lddy, tok0, col0, tokens, cols, full, a);
-    load_tile(z, ldz, tok0, col0, tokens, cols, full, b);
-    if (dres)
-        load_tile(dres, lddres, tok0, col0, tokens, cols, full, d);
-    float wv[8], v[4][8], dw[8];
-    load8_weight(w, wbf16, col0 + 8 * cc, cols, wv);
+    const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+    uint4 y[RT], z[RT], d[RT];
+    load_tile<FULL>(b.dy, b.lddy, p, y);
+    load_tile<FULL>(b.z, b.ldz, p, z);
+    if (b.dres)
+        load_tile<FULL>(b.dres, b.lddres, p, d);
+    float wv[8], v[RT][8], dw[8];
+    load8_weight(b.w, b.wbf16, p.c0(), p.cols, wv);
 #pragma unroll
     for (int j = 0; j < 8; j++)
         dw[j] = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
-        const int64_t tk = tok0 + 4 * rq + i;
-        const float r = tk < tokens ? rstd[tk] : 0.0f, ct = tk < tokens ? coef[tk] : 0.0f;
-        float y[8], x[8], e[8];
-        unpack8(a[i], y);
-        unpack8(b[i], x);
-        if (dres)
-            unpack8(d[i], e);
+    for (int i = 0; i < RT; i++) {
+        const bool in = FULL || p.tk(i) < p.tokens;
+        const float r = in ? b.rstd[p.tk(i)] : 0.0f, ct = in ? coef[p.tk(i)] : 0.0f;
+        float yv[8], x[8];
+        unpack8(y[i], yv);
+        unpack8(z[i], x);
 #pragma unroll
         for (int j = 0; j < 8; j++) {
             const float xh = x[j] * r;
-            dw[j] = fmaf(y[j], xh, dw[j]);
-            const float g = r * fmaf(-xh, ct, y[j] * wv[j]);
-            v[i][j] = dres ? g + e[j] : g;
+            dw[j] = fmaf(yv[j], xh, dw[j]);
+            v[i][j] = r * fmaf(-xh, ct, yv[j] * wv[j]);
         }
-        if (tk < tokens) {
-            const uint32_t o[4] = {to_bf16x2(v[i][0], v[i][1]), to_bf16x2(v[i][2], v[i][3]),
-                                   to_bf16x2(v[i][4], v[i][5]), to_bf16x2(v[i][6], v[i][7])};
-            store8_bf16(dx + tk * lddx, col0 + 8 * cc, cols, o);
+        if (b.dres) {
+            float e[8];
+            unpack8(d[i], e);
+#pragma unroll
+            for (int j = 0; j < 8; j++)
+                v[i][j] += e[j];
         }
     }
-#pragma unroll
-    for (int j = 0; j < 8; j++) {
-        dw[j] += __shfl_xor(dw[j], 16, 64);
-        dw[j] += __shfl_xor(dw[j], 32, 64);
-    }
-    if (lane < 16) {
-#pragma unroll
-        for (int j = 0; j < 8; j++)
-            sh.red[wave][8 * lane + j] = dw[j];
-    }
+    pin(v);
+    store_tile<FULL>(b.dx, b.lddx, p, v);
+    *reinterpret_cast<float2 *>(&sh.red[wave][8 * p.cc + first_of(lane)]) =
+        cross4(dw, [](float x, float y) { return x + y; });
     __syncthreads();
-    if (t < 128 && col0 + t < cols) {
+    if (t < 128 && (FULL || p.col0 + t < p.cols)) {
         float s = sh.red[0][t];
 #pragma unroll
-        for (int k = 1; k < TT / 64; k++)
+        for (int k = 1; k < TileShared<RT>::WAVES; k++)
             s += sh.red[k][t];
-        part[(int64_t)blockIdx.y * cols + col0 + t] = s;
+        part[(int64_t)blockIdx.y * p.cols + p.col0 + t] = s;
     }
     __syncthreads();   // red is reused by the tile's column maxima
-    quant_tile(v, ro, transpose_out, to, tok0, col0, tokens, cols, pow2, full, sh);
+    quant_tile<FULL, TR, RT>(v, ro, to, p, pow2, sh);
 }
 
-// dw = (dw +) the token tiles' shares, added in order.
-__global__ __launch_bounds__(64) void norm_dw_kernel(const float *__restrict__ part, int64_t ntb, int64_t cols,
-                                                     float *__restrict__ dw, int accumulate)
+template <bool TR>
+__global__ __launch_bounds__(tile_threads(BWD_RT)) __attribute__((amdgpu_waves_per_eu(4)))
+void norm_bwd_tile_kernel(NormBwd b, const float *__restrict__ coef, QuantOut ro, QuantOut to,
+                          float *__restrict__ part, int pow2)
 {
-    const int64_t c = (int64_t)blockIdx.x * 64 + threadIdx.x;
-    if (c >= cols)
-        return;
+    __shared__ TileShared<BWD_RT> sh;
+    const auto p = place<BWD_RT>(b.tokens, b.cols);
+    if (full_tile(p))
+        norm_bwd_tile<true, TR, BWD_RT>(b, coef, p, ro, to, part, pow2, sh);
+    else
+        norm_bwd_tile<false, TR, BWD_RT>(b, coef, p, ro, to, part, pow2, sh);
+}
+
+// dw = (dw +) the token tiles' shares: DG threads per column take every DG-th
+// tile, and their sums are added in order.
+constexpr int DC = 32, DG = 8;
+__global__ __launch_bounds__(DC *DG) void norm_dw_kernel(const float *__restrict__ part, int64_t ntb, int64_t cols,
+                                                         float *__restrict__ dw, int accumulate)
+{
+    __shared__ float red[DG][DC];
+    const int x = threadIdx.x % DC, y = threadIdx.x / DC;
+    const int64_t c = (int64_t)blockIdx.x * DC + x;
     float s = 0.0f;
-    for (int64_t k = 0; k < ntb; k++)
-        s += part[k * cols + c];
-    dw[c] = accumulate ? dw[c] + s : s;
+    if (c < cols) {
+#pragma unroll 4
+        for (int64_t k = y; k < ntb; k += DG)
+            s += part[k * cols + c];
+    }
+    red[y][x] = s;
+    __syncthreads();
+    if (y == 0 && c < cols) {
+#pragma unroll
+        for (int k = 1; k < DG; k++)
+            s += red[k][x];
+        dw[c] = accumulate ? dw[c] + s : s;
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -559,43 +699,62 @@ __global__ __launch_bounds__(64) void norm_dw_kernel(const float *__restrict__ p
 // 1 - sigmoid(g) are 1 / (1 + e) and e / (1 + e), which one by the sign of g:
 // neither overflows nor cancels.
 //   du = dh g sigmoid(g),  dg = dh u sigmoid(g) (1 + g (1 - sigmoid(g)))
+// e is the square of 2^t, t = -|g| log2(e) / 2 (v_exp_f32 gives 0 below its
+// normal range, which the square reaches only where e underflows too); what t
+// rounds off (h + l, from the two-part constant) comes back as a factor
+// 1 + l ln 2.
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ void swiglu_grad(float dh, float g, float u, float &dg, float &du)
 {
-    const float e = expf(-fabsf(g));
+    const float a = fabsf(g), h = a * -0x1.715476p-1f;
+    const float l = fmaf(a, -0x1.4ae0cp-27f, fmaf(a, -0x1.715476p-1f, -h));
+    const float x = __builtin_amdgcn_exp2f(h), q = fmaf(x, l * 0x1.62e43p-1f, x), e = q * q;
     const float i = __builtin_amdgcn_rcpf(1.0f + e), ei = e * i;
     const float sig = g < 0.0f ? ei : i, nsig = g < 0.0f ? i : ei;
     du = dh * (g * sig);
     dg = (dh * u) * (sig * fmaf(g, nsig, 1.0f));
 }
 
-__global__ __launch_bounds__(TT) void swiglu_bwd_kernel(const uint16_t *__restrict__ dh, int64_t lddh,
-                                                        const uint16_t *__restrict__ g, int64_t ldg,
-                                                        const uint16_t *__restrict__ u, int64_t ldu, int64_t tokens,
-                                                        int64_t cols, QuantOut gr, QuantOut ur, int transpose_out,
-                                                        QuantOut gt, QuantOut ut, int pow2)
+constexpr int SWIGLU_RT = 4;
+template <bool FULL, bool TR, int RT>
+__device__ __forceinline__ void swiglu_bwd_tile(const SwigluBwd &b, const Place<RT> &p, int pow2,
+                                                TileShared<RT> &sh)
 {
-    __shared__ TileShared sh;
-    const int64_t tok0 = (int64_t)blockIdx.y * 128, col0 = (int64_t)blockIdx.x * 128;
-    const bool full = tok0 + 128 <= tokens && col0 + 128 <= cols;
-    uint4 a[4], b[4], c[4];
-    load_tile(dh, lddh, tok0, col0, tokens, cols, full, a);
-    load_tile(g, ldg, tok0, col0, tokens, cols, full, b);
-    load_tile(u, ldu, tok0, col0, tokens, cols, full, c);
-    float vg[4][8], vu[4][8];
+    uint4 x[RT], g[RT], u[RT];
+    load_tile<FULL>(b.dh, b.lddh, p, x);
+    load_tile<FULL>(b.g, b.ldg, p, g);
+    load_tile<FULL>(b.u, b.ldu, p, u);
+    float vg[RT][8], vu[RT][8];
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
-        float x[8], y[8], w[8];
-        unpack8(a[i], x);
-        unpack8(b[i], y);
-        unpack8(c[i], w);
+    for (int i = 0; i < RT; i++) {
+        float xv[8], gv[8], uv[8];
+        unpack8(x[i], xv);
+        unpack8(g[i], gv);
+        unpack8(u[i], uv);
 #pragma unroll
         for (int j = 0; j < 8; j++)
-            swiglu_grad(x[j], y[j], w[j], vg[i][j], vu[i][j]);
+            swiglu_grad(xv[j], gv[j], uv[j], vg[i][j], vu[i][j]);
     }
-    quant_tile(vg, gr, transpose_out, gt, tok0, col0, tokens, cols, pow2, full, sh);
+    pin(vg);
+    pin(vu);
+    const GradOut &dg = b.dgate, &du = b.dup;
+    quant_tile<FULL, TR, RT>(vg, QuantOut{dg.q_row, dg.ldq_row, dg.s_row, dg.lds_row},
+                     QuantOut{dg.q_tok, dg.ldq_tok, dg.s_tok, dg.lds_tok}, p, pow2, sh);
     __syncthreads();   // the LDS tile of one gradient is read out before the other's is built
-    quant_tile(vu, ur, transpose_out, ut, tok0, col0, tokens, cols, pow2, full, sh);
+    quant_tile<FULL, TR, RT>(vu, QuantOut{du.q_row, du.ldq_row, du.s_row, du.lds_row},
+                     QuantOut{du.q_tok, du.ldq_tok, du.s_tok, du.lds_tok}, p, pow2, sh);
+}
+
+template <bool TR>
+__global__ __launch_bounds__(tile_threads(SWIGLU_RT)) __attribute__((amdgpu_waves_per_eu(4)))
+void swiglu_bwd_kernel(SwigluBwd b, int pow2)
+{
+    __shared__ TileShared<SWIGLU_RT> sh;
+    const auto p = place<SWIGLU_RT>(b.tokens, b.cols);
+    if (full_tile(p))
+        swiglu_bwd_tile<true, TR, SWIGLU_RT>(b, p, pow2, sh);
+    else
+        swiglu_bwd_tile<false, TR, SWIGLU_RT>(b, p, pow2, sh);
 }
 
 dim3 tile_grid(int64_t tokens, int64_t cols)
@@ -623,10 +782,11 @@ hipError_t launch_norm_dual(const NormIn &in, uint8_t *qr, int64_t ldqr, float *
     hipError_t e = hipGetLastError();
     if (e != hipSuccess)
         return e;
-    hipLaunchKernelGGL(norm_tile_kernel, tile_grid(in.tokens, in.cols), dim3(TT), 0, st, in.res ? in.z : in.x,
-                       in.res ? in.ldz : in.ldx, in.rstd, in.w, (int)in.wbf16, in.tokens, in.cols, in.h, in.ldh,
-                       QuantOut{qr, ldqr, sr, nb}, (int)transpose_out,
-                       QuantOut{qt, ldqt, stok, transpose_out ? ntb : in.cols}, (int)pow2);
+    const QuantOut ro{qr, ldqr, sr, nb}, to{qt, ldqt, stok, transpose_out ? ntb : in.cols};
+    hipLaunchKernelGGL((transpose_out ? norm_tile_kernel<true> : norm_tile_kernel<false>),
+                       tile_grid(in.tokens, in.cols), dim3(tile_threads(NORM_RT)), 0, st, in.res ? in.z : in.x,
+                       in.res ? in.ldz : in.ldx, in.rstd, in.w, (int)in.wbf16, in.tokens, in.cols, in.h, in.ldh, ro,
+                       to, (int)pow2);
     return hipGetLastError();
 }
 
@@ -649,27 +809,22 @@ hipError_t launch_norm_bwd(const NormBwd &b, uint8_t *qr, int64_t ldqr, float *s
         hipError_t e = hipGetLastError();
         if (e != hipSuccess)
             return e;
-        hipLaunchKernelGGL(norm_bwd_tile_kernel, tile_grid(b.tokens, b.cols), dim3(TT), 0, st, b.dy, b.lddy, b.z,
-                           b.ldz, b.rstd, coef, b.w, (int)b.wbf16, b.dres, b.lddres, b.tokens, b.cols, b.dx, b.lddx,
-                           QuantOut{qr, ldqr, sr, nb}, (int)transpose_out,
-                           QuantOut{qt, ldqt, stok, transpose_out ? ntb : b.cols}, part, (int)pow2);
+        const QuantOut ro{qr, ldqr, sr, nb}, to{qt, ldqt, stok, transpose_out ? ntb : b.cols};
+        hipLaunchKernelGGL((transpose_out ? norm_bwd_tile_kernel<true> : norm_bwd_tile_kernel<false>),
+                           tile_grid(b.tokens, b.cols), dim3(tile_threads(BWD_RT)), 0, st, b, coef, ro, to, part, (int)pow2);
         e = hipGetLastError();
         if (e != hipSuccess)
             return e;
     }
-    hipLaunchKernelGGL(norm_dw_kernel, dim3((unsigned)((b.cols + 63) / 64)), dim3(64), 0, st, part, ntb, b.cols,
+    hipLaunchKernelGGL(norm_dw_kernel, dim3((unsigned)((b.cols + DC - 1) / DC)), dim3(DC * DG), 0, st, part, ntb, b.cols,
                        b.dw, (int)b.accumulate);
     return hipGetLastError();
 }
 
 hipError_t launch_swiglu_bwd(const SwigluBwd &b, bool transpose_out, bool pow2, hipStream_t st)
 {
-    auto out = [](const GradOut &o, bool tok) {
-        return tok ? QuantOut{o.q_tok, o.ldq_tok, o.s_tok, o.lds_tok} : QuantOut{o.q_row, o.ldq_row, o.s_row, o.lds_row};
-    };
-    hipLaunchKernelGGL(swiglu_bwd_kernel, tile_grid(b.tokens, b.cols), dim3(TT), 0, st, b.dh, b.lddh, b.g, b.ldg, b.u,
-                       b.ldu, b.tokens, b.cols, out(b.dgate, false), out(b.dup, false), (int)transpose_out,
-                       out(b.dgate, true), out(b.dup, true), (int)pow2);
+    hipLaunchKernelGGL((transpose_out ? swiglu_bwd_kernel<true> : swiglu_bwd_kernel<false>),
+                       tile_grid(b.tokens, b.cols), dim3(tile_threads(SWIGLU_RT)), 0, st, b, (int)pow2);
     return hipGetLastError();
 }
 

@@ -35,7 +35,6 @@ namespace puro {
 namespace {
 
 typedef _Float16 v8h __attribute__((ext_vector_type(8)));
-typedef _Float16 v4h __attribute__((ext_vector_type(4)));
 typedef int v4i __attribute__((ext_vector_type(4)));
 
 constexpr float kScaleA = 1024.0f;   // A and B are held times this
@@ -236,7 +235,29 @@ template <int WM_, int WN_, int IT_, int JT_> struct NsCfg {
 typedef NsCfg<2, 4, 8, 4> NsL;   // 256 x 256, one workgroup per CU
 typedef NsCfg<2, 2, 4, 4> NsQ;   // 128 x 128, two workgroups per CU
 
+// Workgroups are dispatched round-robin over the 8 XCDs: gives each XCD a
+// contiguous share of the launch's n tiles, so that the tiles resident together
+// on one XCD read the same operand panels through its L2.
+__device__ __forceinline__ int xcd_share(int b, int n)
+{
+    const int per = n >> 3, rest = n & 7, x = b & 7;
+    return x * per + min(x, rest) + (b >> 3);
+}
+
 enum { NS_GRAM = 0, NS_POLY = 1, NS_UPDATE = 2 };
+
+// Eight 16-bit values to row[c0 ..], those before cols.
+__device__ __forceinline__ void store_run(uint16_t *row, int c0, int cols, const uint32_t w[4])
+{
+    if (c0 + 8 <= cols) {
+        store_nt(row + c0, w[0], w[1], w[2], w[3]);
+        return;
+    }
+#pragma unroll
+    for (int k = 0; k < 8; k++)
+        if (c0 + k < cols)
+            row[c0 + k] = (uint16_t)(w[k >> 1] >> (16 * (k & 1)));
+}
 
 template <class Cfg, int MODE>
 __global__ __launch_bounds__(Cfg::THREADS) void ns_product_kernel(NsGroup args)
@@ -246,8 +267,9 @@ __global__ __launch_bounds__(Cfg::THREADS) void ns_product_kernel(NsGroup args)
     __shared__ __attribute__((aligned(16))) uint8_t lds0[(TM + TN) * 128];
     __shared__ __attribute__((aligned(16))) uint8_t lds1[(TM + TN) * 128];
     const KernargNs g = kernarg();
-    const int item = find_item(g, blockIdx.x);
-    const int local = blockIdx.x - g->first[item];
+    const int b = xcd_share(blockIdx.x, gridDim.x);
+    const int item = find_item(g, b);
+    const int local = b - g->first[item];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave / Cfg::WN, wn = wave % Cfg::WN;
@@ -321,78 +343,144 @@ __global__ __launch_bounds__(Cfg::THREADS) void ns_product_kernel(NsGroup args)
     }
     if (kb < KB)
         kblock(kb, lds0, lds1);
-    __builtin_amdgcn_s_waitcnt(0);   // the idle copy has landed before the workgroup's LDS is given away
+    __builtin_amdgcn_s_waitcnt(0);   // the idle copies have landed,
+    __syncthreads();                 // everyone's, and the stages are read out
 
-    // acc[i][j][r] is row m0 + .. + r, column n0 + .. of the tile
+    // Epilogue.  acc[i][j][r] of lane l is tile row (wm IT + i) 16 + 4 (l / 16)
+    // + r, tile column (wn JT + j) 16 + l % 16.  The result is addressed
+    // [tile column][tile row] and, transposed, [tile row][tile column].  Written
+    // straight from this layout every store would touch 32 bytes of a row (2-byte
+    // stores for one of the two), which took as long as the K loop itself; instead
+    // each wave turns 16 tile columns at a time through 8 KB of LDS of its own,
+    // so that a lane holds 8 consecutive elements of RG rows of the result, and
+    // collects 32 tile columns of the transpose in another 8 KB, whose rows
+    // leave as 64 bytes each.  Both are swizzled against bank conflicts.
+    constexpr int SPAN = IT * 16;          // elements of a result row per wave
+    constexpr int LR = SPAN / 8;           // lanes per row
+    constexpr int RG = 16 * LR / 64;       // rows per lane
+    uint8_t *own = (wave < NW / 2 ? lds0 : lds1) + (wave % (NW / 2)) * 16384;
+    float *strip = reinterpret_cast<float *>(own);                 // [16][SPAN]
+    uint8_t *turn = own + 8192;                                    // [SPAN][32] FP16 / BF16
+    const int rl = lane % LR, rg = lane / LR;                      // element group and row group
+    const int e0 = m0 + wm * SPAN + 8 * rl;                        // first element of this lane
     const float inv = 1.0f / kScaleA;
+    const int last = MODE == NS_UPDATE ? g->last : 0, tall = g->it[item].tall;
+    const int64_t ld_out = MODE == NS_UPDATE ? Np : Mp;
+    const float unscale = 1.0f / g->it[item].s;
+    const bool mirror = MODE == NS_UPDATE ? !last || tall : tr != tc;
 #pragma unroll
-    for (int i = 0; i < IT; i++) {
-        const int m = m0 + (wm * IT + i) * 16 + 4 * (lane >> 4);
+    for (int j = 0; j < JT; j++) {
+        const int row0 = n0 + (wn * JT + j) * 16 + RG * rg;
+        v8h hi[RG], lo[RG];
+        if constexpr (MODE == NS_UPDATE) {
 #pragma unroll
-        for (int j = 0; j < JT; j++) {
-            const int n = n0 + (wn * JT + j) * 16 + (lane & 15);
-            const v4f v = acc[i][j];
-            if constexpr (MODE == NS_UPDATE) {
-                const int row = n, col = m;   // of X
-                const int64_t at = (int64_t)row * Np + col;
-                const v4h hi = *reinterpret_cast<const v4h *>(g->it[item].xh + at);
-                const v4h lo = *reinterpret_cast<const v4h *>(g->it[item].xl + at);
-                const float f = fmaf(g->it[item].d[row], inv, g->a);
-                float x[4];
+            for (int q = 0; q < RG; q++) {
+                hi[q] = *reinterpret_cast<const v8h *>(g->it[item].xh + (row0 + q) * ld_out + e0);
+                lo[q] = *reinterpret_cast<const v8h *>(g->it[item].xl + (row0 + q) * ld_out + e0);
+            }
+        } else if constexpr (MODE == NS_POLY) {
 #pragma unroll
-                for (int r = 0; r < 4; r++)
-                    x[r] = as_f32(fmaf(f, (float)hi[r] + (float)lo[r], v[r] * inv));
-                if (g->last) {
-                    const float is = 1.0f / g->it[item].s;
-                    uint16_t *o = (uint16_t *)g->it[item].o;
-                    const int64_t ldo = g->it[item].ldo;
+            for (int q = 0; q < RG; q++)
+                hi[q] = *reinterpret_cast<const v8h *>(g->it[item].a + (row0 + q) * ld_out + e0);
+        }
 #pragma unroll
-                    for (int r = 0; r < 4; r++)
-                        if (row < g->it[item].M && col + r < g->it[item].N)
-                            o[g->it[item].tall ? (int64_t)(col + r) * ldo + row : (int64_t)row * ldo + col + r] =
-                                to_bf16(x[r] * is);
-                } else {
-                    v4h nh, nl;
+        for (int i = 0; i < IT; i++) {
+            const int c = lane & 15, chunk = (i * 4 + (lane >> 4)) ^ c;
+            *reinterpret_cast<v4f *>(strip + (c * SPAN + (chunk & (SPAN / 4 - 1)) * 4)) = acc[i][j];
+        }
+        // the wave's own LDS accesses are in order; the fence only holds the compiler
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        uint16_t out[RG][8];
 #pragma unroll
-                    for (int r = 0; r < 4; r++) {
-                        nh[r] = (_Float16)x[r];
-                        nl[r] = (_Float16)as_f32(x[r] - (float)nh[r]);
-                    }
-                    *reinterpret_cast<v4h *>(g->it[item].xh + at) = nh;
-                    *reinterpret_cast<v4h *>(g->it[item].xl + at) = nl;
-                    uint16_t *xt = g->it[item].xt[g->flip ^ 1];
+        for (int q = 0; q < RG; q++) {
+            const int c = RG * rg + q, row = row0 + q;
+            float v[8];
 #pragma unroll
-                    for (int r = 0; r < 4; r++)
-                        xt[(int64_t)(col + r) * Mp + row] = h_bits((float)nh[r]);
+            for (int h = 0; h < 2; h++) {
+                const v4f w = *reinterpret_cast<const v4f *>(
+                    strip + (c * SPAN + (((2 * rl + h) ^ c) & (SPAN / 4 - 1)) * 4));
+#pragma unroll
+                for (int k = 0; k < 4; k++)
+                    v[4 * h + k] = w[k];
+            }
+            v8h res;
+            if constexpr (MODE == NS_GRAM) {
+                const float is = kScaleA * unscale * unscale;
+#pragma unroll
+                for (int k = 0; k < 8; k++)
+                    res[k] = (_Float16)as_f32(v[k] * is);
+            } else if constexpr (MODE == NS_POLY) {
+#pragma unroll
+                for (int k = 0; k < 8; k++) {
+                    const float y = as_f32(fmaf(g->b, (float)hi[q][k], g->c * inv * v[k]));
+                    if (e0 + k == row)
+                        g->it[item].d[row] = y;
+                    res[k] = (_Float16)(e0 + k == row ? 0.0f : y);
                 }
             } else {
-                uint16_t *out = MODE == NS_GRAM ? g->it[item].a : g->it[item].b;
-                v4h w;
-                if constexpr (MODE == NS_GRAM) {
-                    const float is = kScaleA / (g->it[item].s * g->it[item].s);
+                const float f = fmaf(g->it[item].d[row], inv, g->a);
+                v8h low;
 #pragma unroll
-                    for (int r = 0; r < 4; r++)
-                        w[r] = (_Float16)as_f32(v[r] * is);
-                } else {
-                    const v4h a4 = *reinterpret_cast<const v4h *>(g->it[item].a + (int64_t)n * Mp + m);
-#pragma unroll
-                    for (int r = 0; r < 4; r++) {
-                        const float y = as_f32(fmaf(g->b, (float)a4[r], g->c * inv * v[r]));
-                        w[r] = (_Float16)y;
-                        if (m + r == n) {
-                            g->it[item].d[n] = y;
-                            w[r] = (_Float16)0.0f;
-                        }
-                    }
+                for (int k = 0; k < 8; k++) {
+                    v[k] = as_f32(fmaf(f, (float)hi[q][k] + (float)lo[q][k], v[k] * inv));
+                    res[k] = (_Float16)v[k];
+                    low[k] = (_Float16)as_f32(v[k] - (float)res[k]);
                 }
-                *reinterpret_cast<v4h *>(out + (int64_t)n * Mp + m) = w;
-                if (tr != tc) {
+                if (!last) {
+                    *reinterpret_cast<v8h *>(g->it[item].xl + row * ld_out + e0) = low;
+                } else {
+                    uint32_t w[4];
 #pragma unroll
-                    for (int r = 0; r < 4; r++)
-                        out[(int64_t)(m + r) * Mp + n] = h_bits((float)w[r]);
+                    for (int k = 0; k < 4; k++)
+                        w[k] = to_bf16x2(v[2 * k] * unscale, v[2 * k + 1] * unscale);
+                    if (!tall && row < g->it[item].M)
+                        store_run((uint16_t *)g->it[item].o + row * g->it[item].ldo, e0, g->it[item].N, w);
+                    res = __builtin_bit_cast(v8h, make_uint4(w[0], w[1], w[2], w[3]));
                 }
             }
+            if (MODE != NS_UPDATE || !last) {
+                uint16_t *to = MODE == NS_GRAM ? g->it[item].a : MODE == NS_POLY ? g->it[item].b : g->it[item].xh;
+                *reinterpret_cast<v8h *>(to + row * ld_out + e0) = res;
+            }
+            const uint4 bits = __builtin_bit_cast(uint4, res);
+            const uint32_t w[4] = {bits.x, bits.y, bits.z, bits.w};
+#pragma unroll
+            for (int k = 0; k < 8; k++)
+                out[q][k] = (uint16_t)(w[k >> 1] >> (16 * (k & 1)));
         }
+        if (!mirror)
+            continue;
+        // element 8 rl + k of these RG rows: place k LR + rl of `turn`, 2 RG bytes
+#pragma unroll
+        for (int k = 0; k < 8; k++) {
+            const int place = k * LR + rl, byte = (j & 1) * 32 + rg * (2 * RG);
+            uint8_t *dst = turn + place * 64 + (byte ^ ((place & 1) << 5));
+            if constexpr (RG == 4)
+                *reinterpret_cast<uint2 *>(dst) = make_uint2(out[0][k] | ((uint32_t)out[1][k] << 16),
+                                                             out[2][k] | ((uint32_t)out[3][k] << 16));
+            else
+                *reinterpret_cast<uint32_t *>(dst) = out[0][k] | ((uint32_t)out[1][k] << 16);
+        }
+        if ((j & 1) == 0)
+            continue;
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+        for (int p = 0; p < SPAN / 16; p++) {
+            const int place = p * 16 + (lane >> 2), c = lane & 3;
+            const int row = m0 + wm * SPAN + 8 * (place % LR) + place / LR;   // of the transpose
+            const int col = n0 + (wn * JT + j - 1) * 16 + 8 * c;
+            const uint4 w = *reinterpret_cast<const uint4 *>(turn + place * 64 + ((16 * c) ^ ((place & 1) << 5)));
+            if (MODE == NS_UPDATE && last) {
+                const uint32_t o[4] = {w.x, w.y, w.z, w.w};
+                if (row < g->it[item].N)
+                    store_run((uint16_t *)g->it[item].o + row * g->it[item].ldo, col, g->it[item].M, o);
+            } else {
+                uint16_t *to = MODE == NS_GRAM ? g->it[item].a : MODE == NS_POLY ? g->it[item].b
+                                                                                 : g->it[item].xt[g->flip ^ 1];
+                *reinterpret_cast<uint4 *>(to + (int64_t)row * Mp + col) = w;
+            }
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     }
 }
 
