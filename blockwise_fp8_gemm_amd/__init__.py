@@ -259,9 +259,37 @@ def _stream_allocs(fn):
     @functools.wraps(fn)
     def run(*args, **kw):
         stream = args[pos] if len(args) > pos else kw.get("stream")
+        if stream is None:
+            return fn(*args, **kw)
         with _on(stream):
             return fn(*args, **kw)
     return run
+
+
+def _on_device(fn):
+    """_stream_allocs for the calls whose first argument (a tensor, or a list of them) names the GPU: the
+    call runs with that GPU current, whichever was, and refuses a stream of another one."""
+    pos = list(inspect.signature(fn).parameters).index("stream")
+
+    @functools.wraps(fn)
+    def run(first, *args, **kw):
+        stream = args[pos - 1] if len(args) >= pos else kw.get("stream")
+        t = first if isinstance(first, torch.Tensor) else first[0] if first else None
+        if stream is None:
+            if t is None or not t.is_cuda or t.get_device() == torch._C._cuda_getDevice():
+                return fn(first, *args, **kw)
+            with torch.cuda.device(t.device):
+                return fn(first, *args, **kw)
+        with _on(stream):
+            if t is not None and t.is_cuda and t.get_device() != torch.cuda.current_device():
+                raise ValueError("the stream belongs to another GPU than the tensors (%s)" % t.device)
+            return fn(first, *args, **kw)
+    return run
+
+
+def _raw_stream(stream, device):
+    """Handle of the launch stream (of `device`, which is current, when none is given)."""
+    return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else _stream(stream)
 
 
 def _need_dense(t, shape, name):
@@ -431,92 +459,130 @@ def puro_fp8_swiglu_quant_dual(gate, up, transpose_out=True, h=None, store_h=Tru
     return h, q_row, s_row, q_tok, s_tok
 
 
-def _need_in(t, shape, dtypes, name, device):
+_BF16, _F32, _U8 = torch.bfloat16, torch.float32, torch.uint8
+
+
+def _refuse(t, shape, dtypes, name, device):
     if tuple(t.shape) != tuple(shape) or t.dtype not in dtypes:
         raise ValueError("%s: expected %s %s, got %s %s" % (name, tuple(shape), "/".join(str(d) for d in dtypes),
                                                             tuple(t.shape), t.dtype))
-    if not t.is_cuda or t.device != device:
-        raise ValueError("%s: expected a tensor on the GPU that holds the other arguments (%s), got one on %s" % (
-            name, device, t.device))
+    raise ValueError("%s: expected a tensor on the GPU that holds the other arguments (%s), got one on %s" % (
+        name, device, t.device))
 
 
-def _norm_weight(weight, cols, device):
-    _need_in(weight, (cols,), (torch.float32, torch.bfloat16), "weight", device)
-    if cols > 1 and weight.stride(0) != 1:
-        raise ValueError("weight must be dense")
-    return _dtype_code(weight)
+def _mat(t, shape, dtype, name, device):
+    """(address, row stride) of a checked 2-D tensor; the address of an empty one is 0."""
+    if t.shape != shape or t.dtype is not dtype or not t.is_cuda or t.device != device:
+        _refuse(t, shape, (dtype,), name, device)
+    rows, cols = shape
+    if not rows or not cols:
+        return 0, _pad16(cols)
+    ld, unit = t.stride()
+    if unit != 1 and cols > 1:
+        raise ValueError("%s: expected unit stride along the last dimension" % name)
+    return t.data_ptr(), (ld if rows > 1 else _pad16(cols))
+
+
+def _opt_mat(t, shape, dtype, name, device):
+    return (0, 0) if t is None else _mat(t, shape, dtype, name, device)
+
+
+def _dense(t, shape, dtypes, name, device):
+    """Address of a checked dense tensor (0 for an empty one)."""
+    if t.shape != shape or t.dtype not in dtypes or not t.is_cuda or t.device != device:
+        _refuse(t, shape, dtypes, name, device)
+    if not t.is_contiguous():
+        raise ValueError("%s must be dense (contiguous)" % name)
+    return t.data_ptr() if t.numel() else 0
+
+
+def _new(rows, cols, dtype, device):
+    """Uninitialised [rows][cols] whose row stride is a multiple of 16 elements."""
+    return torch.empty_strided((rows, cols), (_pad16(cols), 1), dtype=dtype, device=device)
+
+
+def _codes(tokens, cols, device, q, s, tok=False, transpose_out=True):
+    """Checked or allocated codes and scales of one copy, with their addresses: (q, s, q address, its row
+    stride, s address)."""
+    if not tok:
+        qs, ss = (tokens, cols), (tokens, _nblk(cols))
+    elif transpose_out:
+        qs, ss = (cols, tokens), (cols, _nblk(tokens))
+    else:
+        qs, ss = (tokens, cols), (_nblk(tokens), cols)
+    if q is None:
+        q = _new(qs[0], qs[1], _U8, device)
+    if s is None:
+        s = torch.empty(ss, dtype=_F32, device=device)
+    name = ("q_tok", "s_tok") if tok else ("q", "s")
+    qp, ld = _mat(q, qs, _U8, name[0], device)
+    return q, s, qp, ld, _dense(s, ss, (_F32,), name[1], device)
 
 
 def _norm_forward(x, weight, residual, z, rstd, h, store_h):
-    """Checked and allocated arguments shared by the norm's two forms."""
-    tokens, cols = x.shape
-    dev = x.device
-    _need_in(x, (tokens, cols), (torch.bfloat16,), "x", dev)
-    wdt = _norm_weight(weight, cols, dev)
+    """Checked and allocated arguments shared by the norm's two forms: (C arguments up to h's stride, less
+    eps and the extents, as three groups; z, rstd, h)."""
+    shape, dev = x.shape, x.device
+    if len(shape) != 2:
+        raise ValueError("x: expected a 2-D tensor, got shape %s" % (tuple(shape),))
+    tokens, cols = shape
+    xp, ldx = _mat(x, shape, _BF16, "x", dev)
+    wp = _dense(weight, (cols,), (_F32, _BF16), "weight", dev)
     if residual is not None:
-        _need_in(residual, (tokens, cols), (torch.bfloat16,), "residual", dev)
         if z is None:
-            z = empty_2d(tokens, cols, torch.bfloat16, dev)
-        _need_in(z, (tokens, cols), (torch.bfloat16,), "z", dev)
+            z = _new(tokens, cols, _BF16, dev)
     elif z is not None:
         raise ValueError("z is written with a residual only (without one it is x)")
     if rstd is None:
-        rstd = torch.empty((tokens,), dtype=torch.float32, device=dev)
-    _need_in(rstd, (tokens,), (torch.float32,), "rstd", dev)
-    if tokens > 1 and rstd.stride(0) != 1:
-        raise ValueError("rstd must be dense")
+        rstd = torch.empty((tokens,), dtype=_F32, device=dev)
     if store_h and h is None:
-        h = empty_2d(tokens, cols, torch.bfloat16, dev)
-    if h is not None:
-        _need_in(h, (tokens, cols), (torch.bfloat16,), "h", dev)
-    return tokens, cols, wdt, z, rstd, h
+        h = _new(tokens, cols, _BF16, dev)
+    ins = (xp, ldx, *_opt_mat(residual, shape, _BF16, "residual", dev), wp,
+           PURO_BF16 if weight.dtype is _BF16 else PURO_F32)
+    outs = (*_opt_mat(z, shape, _BF16, "z", dev), _dense(rstd, (tokens,), (_F32,), "rstd", dev),
+            *_opt_mat(h, shape, _BF16, "h", dev))
+    return ins, outs, (x if residual is None else z), rstd, h
 
 
-def _opt(t):
-    """(pointer, row stride) of an optional tensor."""
-    return (_ptr(t), _ld(t)) if t is not None else (ctypes.c_void_p(0), 0)
-
-
-@_stream_allocs
+@_on_device
 def puro_fp8_rmsnorm_quant_act(x, weight, residual=None, eps=1e-6, z=None, rstd=None, h=None, store_h=False, q=None,
                                s=None, stream=None, pow2=False):
     """z = bf16(x + residual) (x without one), n = z / sqrt(mean z^2 + eps) * weight, and n's 1x128 blocks
     as puro_fp8_quant_act lays them out (n is quantised in FP32, not rounded to bfloat16 first).
     x, residual: bfloat16 [tokens][cols]; weight: float32 / bfloat16 [cols].  h (given, or allocated with
     store_h): bf16(n).  Returns (z, rstd, h or None, q, s)."""
-    tokens, cols, wdt, z, rstd, h = _norm_forward(x, weight, residual, z, rstd, h, store_h)
-    if q is None:
-        q = empty_2d(tokens, cols, torch.uint8, x.device)
-    if s is None:
-        s = torch.empty((tokens, _nblk(cols)), dtype=torch.float32, device=x.device)
-    _need(q, (tokens, cols), torch.uint8, "q")
-    _need_dense(s, (tokens, _nblk(cols)), "s")
-    fn = lib().puro_fp8_rmsnorm_quant_act_pow2 if pow2 else lib().puro_fp8_rmsnorm_quant_act
-    _check(fn(_ptr(x), _ld(x), *_opt(residual), _ptr(weight), wdt, eps, tokens, cols, *_opt(z), _ptr(rstd), *_opt(h),
-              _ptr(q), _ld(q), _ptr(s), _stream(stream)), "puro_fp8_rmsnorm_quant_act")
-    return (x if residual is None else z), rstd, h, q, s
+    ins, outs, z, rstd, h = _norm_forward(x, weight, residual, z, rstd, h, store_h)
+    tokens, cols = x.shape
+    q, s, qp, ldq, sp = _codes(tokens, cols, x.device, q, s)
+    L = lib()
+    fn = L.puro_fp8_rmsnorm_quant_act_pow2 if pow2 else L.puro_fp8_rmsnorm_quant_act
+    _check(fn(*ins, eps, tokens, cols, *outs, qp, ldq, sp, _raw_stream(stream, x.device)),
+           "puro_fp8_rmsnorm_quant_act")
+    return z, rstd, h, q, s
 
 
-@_stream_allocs
+@_on_device
 def puro_fp8_rmsnorm_quant_dual(x, weight, residual=None, eps=1e-6, transpose_out=True, z=None, rstd=None, h=None,
                                 store_h=False, q_row=None, s_row=None, q_tok=None, s_tok=None, stream=None,
                                 pow2=False):
     """puro_fp8_rmsnorm_quant_act with both copies of n, as puro_fp8_quant_dual lays them out.
     Returns (z, rstd, h or None, q_row, s_row, q_tok, s_tok); z and rstd are what the gradient takes."""
-    tokens, cols, wdt, z, rstd, h = _norm_forward(x, weight, residual, z, rstd, h, store_h)
-    q_row, s_row, q_tok, s_tok = _dual_outs(tokens, cols, transpose_out, x.device, q_row, s_row, q_tok, s_tok)
-    fn = lib().puro_fp8_rmsnorm_quant_dual_pow2 if pow2 else lib().puro_fp8_rmsnorm_quant_dual
-    _check(fn(_ptr(x), _ld(x), *_opt(residual), _ptr(weight), wdt, eps, tokens, cols, *_opt(z), _ptr(rstd), *_opt(h),
-              _ptr(q_row), _ld(q_row), _ptr(s_row), 1 if transpose_out else 0, _ptr(q_tok), _ld(q_tok), _ptr(s_tok),
-              _stream(stream)), "puro_fp8_rmsnorm_quant_dual")
-    return (x if residual is None else z), rstd, h, q_row, s_row, q_tok, s_tok
+    ins, outs, z, rstd, h = _norm_forward(x, weight, residual, z, rstd, h, store_h)
+    tokens, cols = x.shape
+    q_row, s_row, *row = _codes(tokens, cols, x.device, q_row, s_row)
+    q_tok, s_tok, *tok = _codes(tokens, cols, x.device, q_tok, s_tok, True, transpose_out)
+    L = lib()
+    fn = L.puro_fp8_rmsnorm_quant_dual_pow2 if pow2 else L.puro_fp8_rmsnorm_quant_dual
+    _check(fn(*ins, eps, tokens, cols, *outs, *row, 1 if transpose_out else 0, *tok, _raw_stream(stream, x.device)),
+           "puro_fp8_rmsnorm_quant_dual")
+    return z, rstd, h, q_row, s_row, q_tok, s_tok
 
 
 def puro_fp8_rmsnorm_bwd_workspace_size(tokens, cols):
     return int(lib().puro_fp8_rmsnorm_bwd_workspace_size(tokens, cols))
 
 
-@_stream_allocs
+@_on_device
 def puro_fp8_rmsnorm_bwd_quant_dual(dy, z, rstd, weight, dres=None, transpose_out=True, dx=None, dw=None,
                                     accumulate=False, q_row=None, s_row=None, q_tok=None, s_tok=None, workspace=None,
                                     stream=None, pow2=False):
@@ -524,45 +590,37 @@ def puro_fp8_rmsnorm_bwd_quant_dual(dy, z, rstd, weight, dres=None, transpose_ou
     gradient along the residual stream), with dx's dual quantisation, and dw = sum over tokens of dy xh
     (added to the given dw with accumulate).  dy, z, dres: bfloat16 [tokens][cols]; z, rstd: the forward's.
     Returns (dx bfloat16, dw float32, q_row, s_row, q_tok, s_tok)."""
-    tokens, cols = dy.shape
-    dev = dy.device
-    _need_in(dy, (tokens, cols), (torch.bfloat16,), "dy", dev)
-    _need_in(z, (tokens, cols), (torch.bfloat16,), "z", dev)
-    _need_in(rstd, (tokens,), (torch.float32,), "rstd", dev)
-    if tokens > 1 and rstd.stride(0) != 1:
-        raise ValueError("rstd must be dense")
-    wdt = _norm_weight(weight, cols, dev)
-    if dres is not None:
-        _need_in(dres, (tokens, cols), (torch.bfloat16,), "dres", dev)
+    shape, dev = dy.shape, dy.device
+    if len(shape) != 2:
+        raise ValueError("dy: expected a 2-D tensor, got shape %s" % (tuple(shape),))
+    tokens, cols = shape
+    dyp, lddy = _mat(dy, shape, _BF16, "dy", dev)
+    zp, ldz = _mat(z, shape, _BF16, "z", dev)
+    rp = _dense(rstd, (tokens,), (_F32,), "rstd", dev)
+    wp = _dense(weight, (cols,), (_F32, _BF16), "weight", dev)
+    resp, ldres = _opt_mat(dres, shape, _BF16, "dres", dev)
     if dx is None:
-        dx = empty_2d(tokens, cols, torch.bfloat16, dev)
-    _need_in(dx, (tokens, cols), (torch.bfloat16,), "dx", dev)
+        dx = _new(tokens, cols, _BF16, dev)
+    dxp, lddx = _mat(dx, shape, _BF16, "dx", dev)
     if dw is None:
         if accumulate:
             raise ValueError("accumulate needs dw")
-        dw = torch.empty((cols,), dtype=torch.float32, device=dev)
-    _need_in(dw, (cols,), (torch.float32,), "dw", dev)
-    if cols > 1 and dw.stride(0) != 1:
-        raise ValueError("dw must be dense")
-    q_row, s_row, q_tok, s_tok = _dual_outs(tokens, cols, transpose_out, dev, q_row, s_row, q_tok, s_tok)
+        dw = torch.empty((cols,), dtype=_F32, device=dev)
+    dwp = _dense(dw, (cols,), (_F32,), "dw", dev)
+    q_row, s_row, *row = _codes(tokens, cols, dev, q_row, s_row)
+    q_tok, s_tok, *tok = _codes(tokens, cols, dev, q_tok, s_tok, True, transpose_out)
+    L = lib()
     if workspace is None:
-        workspace = torch.empty(puro_fp8_rmsnorm_bwd_workspace_size(tokens, cols), dtype=torch.uint8, device=dev)
-    fn = lib().puro_fp8_rmsnorm_bwd_quant_dual_pow2 if pow2 else lib().puro_fp8_rmsnorm_bwd_quant_dual
-    _check(fn(_ptr(dy), _ld(dy), _ptr(z), _ld(z), _ptr(rstd), _ptr(weight), wdt, *_opt(dres), tokens, cols, _ptr(dx),
-              _ld(dx), _ptr(dw), 1 if accumulate else 0, _ptr(q_row), _ld(q_row), _ptr(s_row),
-              1 if transpose_out else 0, _ptr(q_tok), _ld(q_tok), _ptr(s_tok), _ptr(workspace), workspace.numel(),
-              _stream(stream)), "puro_fp8_rmsnorm_bwd_quant_dual")
+        workspace = torch.empty((L.puro_fp8_rmsnorm_bwd_workspace_size(tokens, cols),), dtype=_U8, device=dev)
+    fn = L.puro_fp8_rmsnorm_bwd_quant_dual_pow2 if pow2 else L.puro_fp8_rmsnorm_bwd_quant_dual
+    _check(fn(dyp, lddy, zp, ldz, rp, wp, PURO_BF16 if weight.dtype is _BF16 else PURO_F32, resp, ldres, tokens, cols,
+              dxp, lddx, dwp, 1 if accumulate else 0, *row, 1 if transpose_out else 0, *tok, workspace.data_ptr(),
+              workspace.numel() * workspace.element_size(), _raw_stream(stream, dev)),
+           "puro_fp8_rmsnorm_bwd_quant_dual")
     return dx, dw, q_row, s_row, q_tok, s_tok
 
 
-def _sld(t):
-    """Row stride of a scale array that may be a column slice of a wider one."""
-    if t.numel() and t.shape[1] > 1 and t.stride(1) != 1:
-        raise ValueError("expected unit stride along the last dimension of a scale array")
-    return t.stride(0) if t.numel() and t.shape[0] > 1 else t.shape[1]
-
-
-@_stream_allocs
+@_on_device
 def puro_fp8_swiglu_bwd_quant_dual(dh, gate, up, transpose_out=True, joined=False, q_row=None, s_row=None, q_tok=None,
                                    s_tok=None, stream=None, pow2=False):
     """Gradient of h = silu(gate) * up: dup = dh silu(gate), dgate = dh up silu'(gate), each quantised both
@@ -571,31 +629,40 @@ def puro_fp8_swiglu_bwd_quant_dual(dh, gate, up, transpose_out=True, joined=Fals
     joined=False: returns two (q_row, s_row, q_tok, s_tok), dgate's and dup's, laid out as
     puro_fp8_quant_dual's.  joined=True (cols a multiple of 128): one such tuple for the [tokens][2 cols]
     tensor that holds dgate's columns, then dup's; q_row, s_row, q_tok and s_tok may then be given."""
-    tokens, cols = dh.shape
-    dev = dh.device
-    for t, name in ((dh, "dh"), (gate, "gate"), (up, "up")):
-        _need_in(t, (tokens, cols), (torch.bfloat16,), name, dev)
+    shape, dev = dh.shape, dh.device
+    if len(shape) != 2:
+        raise ValueError("dh: expected a 2-D tensor, got shape %s" % (tuple(shape),))
+    tokens, cols = shape
+    ins = (*_mat(dh, shape, _BF16, "dh", dev), *_mat(gate, shape, _BF16, "gate", dev),
+           *_mat(up, shape, _BF16, "up", dev))
     if joined:
         if cols % 128:
             raise ValueError("joined gradients need a multiple of 128 columns, got %d" % cols)
-        res = _dual_outs(tokens, 2 * cols, transpose_out, dev, q_row, s_row, q_tok, s_tok)
-        qr, sr, qt, st = res
-        nb = cols // 128
-        if transpose_out:
-            halves = [(qr[:, :cols], sr[:, :nb], qt[:cols], st[:cols]), (qr[:, cols:], sr[:, nb:], qt[cols:], st[cols:])]
+        q_row, s_row, qr, ldqr, sr = _codes(tokens, 2 * cols, dev, q_row, s_row)
+        q_tok, s_tok, qt, ldqt, st = _codes(tokens, 2 * cols, dev, q_tok, s_tok, True, transpose_out)
+        nb, nt = cols // 128, _nblk(tokens)
+        gate_out = QuantDualOut(qr, ldqr, sr, 2 * nb, qt, ldqt, st, nt if transpose_out else 2 * cols)
+        if qr:   # dup's half: behind dgate's columns, or its rows of the transposed copy
+            tq, ts = (cols * ldqt, cols * nt) if transpose_out else (cols, cols)
+            up_out = QuantDualOut(qr + cols, ldqr, sr + 4 * nb, 2 * nb, qt + tq, ldqt, st + 4 * ts, gate_out.lds_tok)
         else:
-            halves = [(qr[:, :cols], sr[:, :nb], qt[:, :cols], st[:, :cols]),
-                      (qr[:, cols:], sr[:, nb:], qt[:, cols:], st[:, cols:])]
+            up_out = gate_out
+        res = q_row, s_row, q_tok, s_tok
     else:
-        if any(t is not None for t in (q_row, s_row, q_tok, s_tok)):
+        if q_row is not None or s_row is not None or q_tok is not None or s_tok is not None:
             raise ValueError("outputs can be given for joined gradients only")
-        halves = [_dual_outs(tokens, cols, transpose_out, dev, None, None, None, None) for _ in range(2)]
-        res = tuple(halves)
-    outs = [QuantDualOut(_ptr(qr), _ld(qr), _ptr(sr), _sld(sr), _ptr(qt), _ld(qt), _ptr(st), _sld(st))
-            for qr, sr, qt, st in halves]
-    fn = lib().puro_fp8_swiglu_bwd_quant_dual_pow2 if pow2 else lib().puro_fp8_swiglu_bwd_quant_dual
-    _check(fn(_ptr(dh), _ld(dh), _ptr(gate), _ld(gate), _ptr(up), _ld(up), tokens, cols, 1 if transpose_out else 0,
-              outs[0], outs[1], _stream(stream)), "puro_fp8_swiglu_bwd_quant_dual")
+        res, outs = [], []
+        lds_row, lds_tok = _nblk(cols), _nblk(tokens) if transpose_out else cols
+        for _ in range(2):
+            qr, sr, qrp, ldqr, srp = _codes(tokens, cols, dev, None, None)
+            qt, st, qtp, ldqt, stp = _codes(tokens, cols, dev, None, None, True, transpose_out)
+            res.append((qr, sr, qt, st))
+            outs.append(QuantDualOut(qrp, ldqr, srp, lds_row, qtp, ldqt, stp, lds_tok))
+        res, (gate_out, up_out) = tuple(res), outs
+    L = lib()
+    fn = L.puro_fp8_swiglu_bwd_quant_dual_pow2 if pow2 else L.puro_fp8_swiglu_bwd_quant_dual
+    _check(fn(*ins, tokens, cols, 1 if transpose_out else 0, gate_out, up_out, _raw_stream(stream, dev)),
+           "puro_fp8_swiglu_bwd_quant_dual")
     return res
 
 
@@ -755,7 +822,7 @@ def puro_fp8_newton_schulz_workspace_size(shapes):
     return int(lib().puro_fp8_newton_schulz_workspace_size(descs, len(shapes)))
 
 
-@_stream_allocs
+@_on_device
 def puro_fp8_newton_schulz_grouped(grads, steps=5, coefficients=(3.4445, -4.7750, 2.0315), eps=1e-7, outs=None,
                                    workspace=None, stream=None):
     """Orthogonalised directions of several gradients (or momenta), one call: each matrix is divided by its
@@ -776,18 +843,20 @@ def puro_fp8_newton_schulz_grouped(grads, steps=5, coefficients=(3.4445, -4.7750
     descs = (NewtonSchulzDesc * len(grads))()
     res = []
     for i, (g, o) in enumerate(zip(grads, outs)):
-        _need_in(g, tuple(g.shape), (dtype,), "grads[%d]" % i, dev)
-        rows, cols = g.shape
+        shape = g.shape
+        if len(shape) != 2:
+            raise ValueError("grads[%d]: expected a 2-D tensor, got shape %s" % (i, tuple(shape)))
         if o is None:
-            o = empty_2d(rows, cols, torch.bfloat16, dev)
-        _need_in(o, (rows, cols), (torch.bfloat16,), "outs[%d]" % i, dev)
-        descs[i] = NewtonSchulzDesc(_ptr(g), rows, cols, _ld(g), _ptr(o), _ld(o))
+            o = _new(shape[0], shape[1], _BF16, dev)
+        gp, ldg = _mat(g, shape, dtype, "grads[%d]" % i, dev)
+        op, ldo = _mat(o, shape, _BF16, "outs[%d]" % i, dev)
+        descs[i] = NewtonSchulzDesc(gp, shape[0], shape[1], ldg, op, ldo)
         res.append(o)
     if workspace is None:
         need = int(lib().puro_fp8_newton_schulz_workspace_size(descs, len(grads)))
         workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     coef = (ctypes.c_float * (3 * steps))(*[v for t in triples for v in t])
-    _check(lib().puro_fp8_newton_schulz_grouped(code, descs, len(grads), steps, coef, eps, _ptr(workspace),
-                                                workspace.numel() * workspace.element_size(), _stream(stream)),
-           "puro_fp8_newton_schulz_grouped")
+    _check(lib().puro_fp8_newton_schulz_grouped(code, descs, len(grads), steps, coef, eps, workspace.data_ptr(),
+                                                workspace.numel() * workspace.element_size(),
+                                                _raw_stream(stream, dev)), "puro_fp8_newton_schulz_grouped")
     return res
