@@ -22,8 +22,9 @@
 // 0.5e-2 to 1.6e-2.
 //
 // A and B are symmetric: only the tiles on and above the diagonal are formed,
-// and each is stored twice.  B X reads X^T, which every step writes beside X,
-// so that all three products have both operands contiguous along K.
+// and each is stored twice.  In B X, X is contiguous along N and not along K: its
+// fragments come through the LDS's transposing reads, which saves keeping
+// (and writing, every step) a transposed copy of X.
 #include "common.h"
 #include "kernels.h"
 
@@ -36,9 +37,10 @@ namespace {
 
 typedef _Float16 v8h __attribute__((ext_vector_type(8)));
 typedef int v4i __attribute__((ext_vector_type(4)));
+typedef short v4s __attribute__((ext_vector_type(4)));
 
 constexpr float kScaleA = 1024.0f;   // A and B are held times this
-constexpr int kNormBlocks = 128;     // partial sums of |G|^2 per matrix
+constexpr int kNormBlocks = 256;     // partial sums of |G|^2 per matrix
 
 struct NsItem {
     const void *g;
@@ -48,8 +50,7 @@ struct NsItem {
     int Mp, Np;    // padded to whole tiles; the padding holds zeros
     int tall;
     float s;       // X is held times s
-    uint16_t *xh, *xl;      // [Mp][Np]
-    uint16_t *xt[2];        // [Np][Mp], hi, read and written in turn
+    uint16_t *xh[2], *xl;   // [Mp][Np]; hi is read from one and written to the other
     uint16_t *a, *b;        // [Mp][Mp]
     float *d;               // [Mp] diagonal of B
     double *part;           // [kNormBlocks]
@@ -60,7 +61,7 @@ struct NsGroup {
     int first[kNsGroupMax + 1];   // workgroups of item i: [first[i], first[i+1])
     int count;
     int gbf16;
-    int flip;                     // which xt is read
+    int flip;                     // which xh is read
     int last;                     // the step whose result is the output
     float a, b, c, eps;
 };
@@ -90,13 +91,38 @@ __device__ __forceinline__ float as_f32(float f)
     return f;
 }
 
-__device__ __forceinline__ uint16_t h_bits(float f) { return __builtin_bit_cast(uint16_t, (_Float16)f); }
-__device__ __forceinline__ float h_val(uint16_t u) { return (float)__builtin_bit_cast(_Float16, u); }
+// ---------------------------------------------------------------------------
+// |G|_F^2 in 64 bits: kNormBlocks partial sums per matrix.  A wave takes a row
+// at a time, 16 bytes a lane.
+// ---------------------------------------------------------------------------
+template <typename T> __device__ __forceinline__ double row_squares(const T *row, int cols, int lane)
+{
+    constexpr int V = 16 / sizeof(T);
+    double s0 = 0.0, s1 = 0.0;
+#pragma unroll 4
+    for (int c = lane * V; c < cols; c += 64 * V) {
+        float v[8];
+        if (c + V <= cols) {
+            if constexpr (V == 8) {
+                Elem<T>::load8(row + c, v);
+            } else {
+                const float4 f = *reinterpret_cast<const float4 *>(row + c);
+                v[0] = f.x; v[1] = f.y; v[2] = f.z; v[3] = f.w;
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < V; k++)
+                v[k] = c + k < cols ? Elem<T>::load(row + c + k) : 0.0f;
+        }
+#pragma unroll
+        for (int k = 0; k < V; k += 2) {
+            s0 = fma((double)v[k], (double)v[k], s0);
+            s1 = fma((double)v[k + 1], (double)v[k + 1], s1);
+        }
+    }
+    return s0 + s1;
+}
 
-// ---------------------------------------------------------------------------
-// |G|_F^2 in 64 bits: kNormBlocks partial sums per matrix, each over every
-// kNormBlocks-th row.
-// ---------------------------------------------------------------------------
 __global__ __launch_bounds__(256) void ns_norm_kernel(NsGroup args)
 {
     (void)args;
@@ -105,15 +131,12 @@ __global__ __launch_bounds__(256) void ns_norm_kernel(NsGroup args)
     const int tall = g->it[item].tall;
     const int rows = tall ? g->it[item].N : g->it[item].M, cols = tall ? g->it[item].M : g->it[item].N;
     const int64_t ld = g->it[item].ldg;
+    const void *src = g->it[item].g;
     __shared__ double red[256];
     double sum = 0.0;
-    for (int r = blockIdx.x; r < rows; r += kNormBlocks) {
-        for (int c = t; c < cols; c += 256) {
-            const float v = g->gbf16 ? Elem<uint16_t>::load((const uint16_t *)g->it[item].g + r * ld + c)
-                                     : ((const float *)g->it[item].g)[r * ld + c];
-            sum = fma((double)v, (double)v, sum);
-        }
-    }
+    for (int r = blockIdx.x * 4 + (t >> 6); r < rows; r += kNormBlocks * 4)
+        sum += g->gbf16 ? row_squares((const uint16_t *)src + r * ld, cols, t & 63)
+                        : row_squares((const float *)src + r * ld, cols, t & 63);
     red[t] = sum;
     __syncthreads();
     for (int w = 128; w > 0; w >>= 1) {
@@ -126,7 +149,7 @@ __global__ __launch_bounds__(256) void ns_norm_kernel(NsGroup args)
 }
 
 // ---------------------------------------------------------------------------
-// X0: hi, lo and the transposed hi of a 64 x 64 tile, zeros in the padding.
+// X0: hi and lo of a 64 x 64 tile, zeros in the padding.
 // ---------------------------------------------------------------------------
 __global__ __launch_bounds__(256) void ns_init_kernel(NsGroup args)
 {
@@ -134,38 +157,72 @@ __global__ __launch_bounds__(256) void ns_init_kernel(NsGroup args)
     const KernargNs g = kernarg();
     const int i = find_item(g, blockIdx.x), t = threadIdx.x;
     const int local = blockIdx.x - g->first[i];
-    const int M = g->it[i].M, N = g->it[i].N, Mp = g->it[i].Mp, Np = g->it[i].Np, tall = g->it[i].tall;
+    const int M = g->it[i].M, N = g->it[i].N, Np = g->it[i].Np, tall = g->it[i].tall;
+    const int rows = tall ? N : M, cols = tall ? M : N;
     const int64_t ld = g->it[i].ldg;
     const int m0 = local / (Np / 64) * 64, n0 = local % (Np / 64) * 64;
-    __shared__ double red[kNormBlocks];
-    __shared__ float x[64][64 + 1];   // [m][n]
-    if (t < kNormBlocks)
-        red[t] = g->it[i].part[t];
+    const int r0 = tall ? n0 : m0, c0 = tall ? m0 : n0;
+    __shared__ double red[4];
+    __shared__ float x[64][64 + 1];   // as the source lies
+    double sum = g->it[i].part[t];
+    static_assert(kNormBlocks == 256, "a partial sum per thread");
+#pragma unroll
+    for (int k = 1; k < 64; k <<= 1)
+        sum += __shfl_xor(sum, k, 64);
+    if ((t & 63) == 0)
+        red[t >> 6] = sum;
     __syncthreads();
-    for (int w = kNormBlocks / 2; w > 0; w >>= 1) {
-        if (t < w)
-            red[t] += red[t + w];
-        __syncthreads();
-    }
-    const float scale = (float)((double)g->it[i].s / (sqrt(red[0]) + (double)g->eps));
-    for (int k = t; k < 64 * 64; k += 256) {
-        const int r = k >> 6, c = k & 63;   // c along the source's rows
-        const int m = tall ? m0 + c : m0 + r, n = tall ? n0 + r : n0 + c;
-        float v = 0.0f;
-        if (m < M && n < N) {
-            const int64_t at = tall ? (int64_t)n * ld + m : (int64_t)m * ld + n;
-            v = g->gbf16 ? Elem<uint16_t>::load((const uint16_t *)g->it[i].g + at) : ((const float *)g->it[i].g)[at];
+    const float scale = (float)((double)g->it[i].s / (sqrt(red[0] + red[1] + red[2] + red[3]) + (double)g->eps));
+    // thread t takes 16 elements of row t / 4, eight at a time; a tall source goes through LDS
+    const int q = t >> 2, r = r0 + q;
+    auto store = [&](int h, const float (&v)[8]) {
+        const int64_t at = (int64_t)(m0 + q) * Np + n0 + 16 * (t & 3) + 8 * h;
+        v8h hi, lo;
+#pragma unroll
+        for (int k = 0; k < 8; k++) {
+            const float y = as_f32(v[k] * scale);
+            hi[k] = (_Float16)y;
+            lo[k] = (_Float16)as_f32(y - (float)hi[k]);
         }
-        x[tall ? c : r][tall ? r : c] = v * scale;
+        *reinterpret_cast<v8h *>(g->it[i].xh[0] + at) = hi;
+        *reinterpret_cast<v8h *>(g->it[i].xl + at) = lo;
+    };
+#pragma unroll
+    for (int h = 0; h < 2; h++) {
+        const int c = c0 + 16 * (t & 3) + 8 * h;
+        float v[8];
+        if (r < rows && c + 8 <= cols) {
+            if (g->gbf16)
+                Elem<uint16_t>::load8((const uint16_t *)g->it[i].g + r * ld + c, v);
+            else
+                Elem<float>::load8((const float *)g->it[i].g + r * ld + c, v);
+        } else {
+#pragma unroll
+            for (int k = 0; k < 8; k++) {
+                v[k] = 0.0f;
+                if (r < rows && c + k < cols)
+                    v[k] = g->gbf16 ? Elem<uint16_t>::load((const uint16_t *)g->it[i].g + r * ld + c + k)
+                                    : ((const float *)g->it[i].g)[r * ld + c + k];
+            }
+        }
+        if (!tall) {
+            store(h, v);
+        } else {
+#pragma unroll
+            for (int k = 0; k < 8; k++)
+                x[q][16 * (t & 3) + 8 * h + k] = v[k];
+        }
     }
+    if (!tall)
+        return;
     __syncthreads();
-    for (int k = t; k < 64 * 64; k += 256) {
-        const int r = k >> 6, c = k & 63;
-        const float v = x[r][c];
-        const uint16_t hi = h_bits(v);
-        g->it[i].xh[(int64_t)(m0 + r) * Np + n0 + c] = hi;
-        g->it[i].xl[(int64_t)(m0 + r) * Np + n0 + c] = h_bits(v - h_val(hi));
-        g->it[i].xt[0][(int64_t)(n0 + r) * Mp + m0 + c] = h_bits(x[c][r]);
+#pragma unroll
+    for (int h = 0; h < 2; h++) {
+        float v[8];
+#pragma unroll
+        for (int k = 0; k < 8; k++)
+            v[k] = x[16 * (t & 3) + 8 * h + k][q];
+        store(h, v);
     }
 }
 
@@ -227,13 +284,60 @@ __device__ __forceinline__ Frag frag(const uint8_t *t, int row_base, int lane)
     return r;
 }
 
-template <int WM_, int WN_, int IT_, int JT_> struct NsCfg {
-    static constexpr int WM = WM_, WN = WN_, IT = IT_, JT = JT_;
+// The same for an operand that is contiguous along its rows' dimension: 64 rows
+// of K, W elements each.  A transposing read takes 4 K rows x 16 elements per 16
+// lanes; the swizzle puts the 16 pieces of 32 bytes that a wave reads at once
+// (4 rows of 4 lane groups) on different banks.
+__device__ __forceinline__ int swz_k(int k) { return ((k & 3) << 1) | (((k >> 4) & 1) << 3) | (((k >> 5) & 1) << 4); }
+
+template <int W> __device__ __forceinline__ int swz_kw(int k) { return swz_k(k) & (W / 8 - 1); }
+
+template <int W, int NW>
+__device__ __forceinline__ void stage_k(uint8_t *t, const uint8_t *g, int64_t ld, int64_t k0, int64_t col0, int wave,
+                                        int lane)
+{
+    constexpr int SEGS = W / 8, RPC = 64 / SEGS;   // 16-byte segments per row, rows per 1 KB chunk
+    static_assert((64 / RPC) % NW == 0, "whole 1 KB chunks per wave");
+#pragma unroll
+    for (int it = 0; it < 64 / RPC / NW; it++) {
+        const int c = wave + NW * it, row = RPC * c + lane / SEGS;
+        const int seg = (lane % SEGS) ^ swz_kw<W>(row);
+        copy16(g + (k0 + RPC * c) * ld + col0 * 2, (uint32_t)(lane / SEGS) * (uint32_t)ld + (uint32_t)(seg * 16),
+               t + c * 1024);
+    }
+}
+
+template <int W> __device__ __forceinline__ Frag frag_k(const uint8_t *t, int col_base, int lane)
+{
+    typedef __attribute__((address_space(3))) v4s lds_v4s;
+    const int i = lane & 15, g = lane >> 4;
+    Frag r;
+#pragma unroll
+    for (int kk = 0; kk < 2; kk++) {
+        v4s q[2];
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+            const int k = 16 * g + 8 * kk + 4 * h + (i >> 2), col = col_base * 2 + 8 * (i & 3);
+            q[h] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                (lds_v4s *)(t + (k * (2 * W) + (((col >> 4) ^ swz_kw<W>(k)) << 4) + (col & 8))));
+        }
+        r.k[kk] = __builtin_bit_cast(v8h, __builtin_shufflevector(q[0], q[1], 0, 1, 2, 3, 4, 5, 6, 7));
+    }
+    return r;
+}
+
+// WM x WN waves of IT x JT tiles of 16 x 16; S stages of 64 K in LDS.
+template <int WM_, int WN_, int IT_, int JT_, int S_> struct NsCfg {
+    static constexpr int WM = WM_, WN = WN_, IT = IT_, JT = JT_, S = S_;
     static constexpr int NW = WM * WN, THREADS = 64 * NW;
     static constexpr int TM = WM * IT * 16, TN = WN * JT * 16;
+    static constexpr int STAGE = (TM + TN) * 128, LOADS = (TM + TN) / 8 / NW;
+    static_assert(S * STAGE >= NW * 16384, "16 KB per wave for the epilogue");
 };
-typedef NsCfg<2, 4, 8, 4> NsL;   // 256 x 256, one workgroup per CU
-typedef NsCfg<2, 2, 4, 4> NsQ;   // 128 x 128, two workgroups per CU
+typedef NsCfg<2, 4, 8, 4, 2> NsL;   // 256 x 256
+typedef NsCfg<2, 2, 4, 4, 4> NsQ;   // 128 x 128
+
+enum { NS_GRAM = 0, NS_POLY = 1, NS_UPDATE = 2 };
 
 // Workgroups are dispatched round-robin over the 8 XCDs: gives each XCD a
 // contiguous share of the launch's n tiles, so that the tiles resident together
@@ -243,8 +347,6 @@ __device__ __forceinline__ int xcd_share(int b, int n)
     const int per = n >> 3, rest = n & 7, x = b & 7;
     return x * per + min(x, rest) + (b >> 3);
 }
-
-enum { NS_GRAM = 0, NS_POLY = 1, NS_UPDATE = 2 };
 
 // Eight 16-bit values to row[c0 ..], those before cols.
 __device__ __forceinline__ void store_run(uint16_t *row, int c0, int cols, const uint32_t w[4])
@@ -259,13 +361,14 @@ __device__ __forceinline__ void store_run(uint16_t *row, int c0, int cols, const
             row[c0 + k] = (uint16_t)(w[k >> 1] >> (16 * (k & 1)));
 }
 
+template <int N> __device__ __forceinline__ void wait_copies() { asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory"); }
+
 template <class Cfg, int MODE>
 __global__ __launch_bounds__(Cfg::THREADS) void ns_product_kernel(NsGroup args)
 {
     (void)args;
-    constexpr int NW = Cfg::NW, TM = Cfg::TM, TN = Cfg::TN, IT = Cfg::IT, JT = Cfg::JT;
-    __shared__ __attribute__((aligned(16))) uint8_t lds0[(TM + TN) * 128];
-    __shared__ __attribute__((aligned(16))) uint8_t lds1[(TM + TN) * 128];
+    constexpr int NW = Cfg::NW, TM = Cfg::TM, TN = Cfg::TN, IT = Cfg::IT, JT = Cfg::JT, S = Cfg::S;
+    __shared__ __attribute__((aligned(16))) uint8_t lds[S * Cfg::STAGE];
     const KernargNs g = kernarg();
     const int b = xcd_share(blockIdx.x, gridDim.x);
     const int item = find_item(g, b);
@@ -275,18 +378,18 @@ __global__ __launch_bounds__(Cfg::THREADS) void ns_product_kernel(NsGroup args)
     const int wm = wave / Cfg::WN, wn = wave % Cfg::WN;
     const int Mp = g->it[item].Mp, Np = g->it[item].Np;
 
-    // operands and the tile's place: rows of P are tile rows, rows of Q tile columns
+    // operands and the tile's place: P along the tile's rows, Q along its columns
     const uint8_t *P, *Q;
     int K, tr, tc;
     if constexpr (MODE == NS_UPDATE) {
-        // the result's transpose: rows are X's columns (X^T [Np][Mp]), columns X's rows (B [Mp][Mp])
-        P = (const uint8_t *)g->it[item].xt[g->flip];
+        // the result's transpose: rows are X's columns (X [Mp][Np]), columns X's rows (B [Mp][Mp])
+        P = (const uint8_t *)g->it[item].xh[g->flip];
         Q = (const uint8_t *)g->it[item].b;
         K = Mp;
         tr = local / (Mp / TN);
         tc = local % (Mp / TN);
     } else {
-        P = Q = (const uint8_t *)(MODE == NS_GRAM ? g->it[item].xh : g->it[item].a);
+        P = Q = (const uint8_t *)(MODE == NS_GRAM ? g->it[item].xh[g->flip] : g->it[item].a);
         K = MODE == NS_GRAM ? Np : Mp;
         // tiles on and above the diagonal, column by column
         tc = (int)((sqrtf(8.0f * (float)local + 1.0f) - 1.0f) * 0.5f);
@@ -296,7 +399,7 @@ __global__ __launch_bounds__(Cfg::THREADS) void ns_product_kernel(NsGroup args)
             tc++;
         tr = local - tc * (tc + 1) / 2;
     }
-    const int64_t ld = (int64_t)K * 2;
+    const int64_t ldp = (int64_t)(MODE == NS_UPDATE ? Np : K) * 2, ldq = (int64_t)K * 2;
     const int m0 = tr * TM, n0 = tc * TN, KB = K / 64;
 
     v4f acc[IT][JT];
@@ -306,43 +409,75 @@ __global__ __launch_bounds__(Cfg::THREADS) void ns_product_kernel(NsGroup args)
         for (int j = 0; j < JT; j++)
             acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
 
-    auto stage = [&](int kb, uint8_t *L) {
-        stage_rows<TM, NW>(L, P, ld, m0, (int64_t)kb * 128, wave, lane);
-        stage_rows<TN, NW>(L + TM * 128, Q, ld, n0, (int64_t)kb * 128, wave, lane);
+    // Block kb into its stage; past the end the last block again (never read),
+    // so that the number of copies in flight is the same at every block.
+    auto stage = [&](int kb) {
+        uint8_t *L = lds + kb % S * Cfg::STAGE;
+        const int k = min(kb, KB - 1);
+        if constexpr (MODE == NS_UPDATE)
+            stage_k<TM, NW>(L, P, ldp, (int64_t)k * 64, m0, wave, lane);
+        else
+            stage_rows<TM, NW>(L, P, ldp, m0, (int64_t)k * 128, wave, lane);
+        stage_rows<TN, NW>(L + TM * 128, Q, ldq, n0, (int64_t)k * 128, wave, lane);
     };
-    auto kblock = [&](int kb, const uint8_t *L, uint8_t *LN) {
-        __builtin_amdgcn_s_waitcnt(0);   // this wave's copies of block kb have landed
-        __syncthreads();                 // everyone's have; LN is no longer read
-        // the next block, or this one again after the last (never read): no branch in the loop
-        stage(kb + 1 < KB ? kb + 1 : kb, LN);
-        const uint8_t *ta = L, *tb = L + TM * 128;
-        Frag bf[JT];
+    auto read_p = [&](int kb, int i) {
+        const uint8_t *L = lds + kb % S * Cfg::STAGE;
+        if constexpr (MODE == NS_UPDATE)
+            return frag_k<TM>(L, (wm * IT + i) * 16, lane);
+        else
+            return frag(L, (wm * IT + i) * 16, lane);
+    };
+    auto read_q = [&](int kb, int j) {
+        return frag(lds + kb % S * Cfg::STAGE + TM * 128, (wn * JT + j) * 16, lane);
+    };
+
+    // The K loop.  All of a block's fragments are in registers two row blocks
+    // before its end; there the waves meet, block kb + S is copied over the
+    // stage just read, and the next block's first fragments are read under the
+    // last two row blocks' products.
+    Frag q[2][JT], p[2];
 #pragma unroll
-        for (int j = 0; j < JT; j++)
-            bf[j] = frag(tb, (wn * JT + j) * 16, lane);
-        Frag next = frag(ta, wm * IT * 16, lane);
+    for (int k = 0; k < S; k++)
+        stage(k);
+    wait_copies<(S - 1) * Cfg::LOADS>();
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < JT; j++)
+        q[0][j] = read_q(0, j);
+    p[0] = read_p(0, 0);
+    p[1] = read_p(0, 1);
+    auto block = [&](int kb, Frag (&cur)[JT], Frag (&nxt)[JT]) {
+        Frag np[2];
 #pragma unroll
         for (int i = 0; i < IT; i++) {
-            const Frag af = next;
-            if (i + 1 < IT)
-                next = frag(ta, (wm * IT + i + 1) * 16, lane);
+            const Frag a = p[i & 1];
+            if (i == IT - 2) {
+                wait_copies<(S - 2) * Cfg::LOADS>();
+                __syncthreads();
+                stage(kb + S);
+#pragma unroll
+                for (int j = 0; j < JT; j++)
+                    nxt[j] = read_q(kb + 1, j);
+                np[0] = read_p(kb + 1, 0);
+                np[1] = read_p(kb + 1, 1);
+            }
+            if (i + 2 < IT)
+                p[i & 1] = read_p(kb, i + 2);
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int k = 0; k < 2; k++)
 #pragma unroll
                 for (int j = 0; j < JT; j++)
-                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(af.k[k], bf[j].k[k], acc[i][j], 0, 0, 0);
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a.k[k], cur[j].k[k], acc[i][j], 0, 0, 0);
             __builtin_amdgcn_sched_barrier(0);
         }
+        p[0] = np[0];
+        p[1] = np[1];
     };
-    stage(0, lds0);
-    int kb = 0;
-    for (; kb + 1 < KB; kb += 2) {
-        kblock(kb, lds0, lds1);
-        kblock(kb + 1, lds1, lds0);
+    for (int kb = 0; kb < KB; kb += 2) {   // KB is even: K is a multiple of 128
+        block(kb, q[0], q[1]);
+        block(kb + 1, q[1], q[0]);
     }
-    if (kb < KB)
-        kblock(kb, lds0, lds1);
     __builtin_amdgcn_s_waitcnt(0);   // the idle copies have landed,
     __syncthreads();                 // everyone's, and the stages are read out
 
@@ -358,7 +493,7 @@ __global__ __launch_bounds__(Cfg::THREADS) void ns_product_kernel(NsGroup args)
     constexpr int SPAN = IT * 16;          // elements of a result row per wave
     constexpr int LR = SPAN / 8;           // lanes per row
     constexpr int RG = 16 * LR / 64;       // rows per lane
-    uint8_t *own = (wave < NW / 2 ? lds0 : lds1) + (wave % (NW / 2)) * 16384;
+    uint8_t *own = lds + wave * 16384;
     float *strip = reinterpret_cast<float *>(own);                 // [16][SPAN]
     uint8_t *turn = own + 8192;                                    // [SPAN][32] FP16 / BF16
     const int rl = lane % LR, rg = lane / LR;                      // element group and row group
@@ -367,7 +502,7 @@ __global__ __launch_bounds__(Cfg::THREADS) void ns_product_kernel(NsGroup args)
     const int last = MODE == NS_UPDATE ? g->last : 0, tall = g->it[item].tall;
     const int64_t ld_out = MODE == NS_UPDATE ? Np : Mp;
     const float unscale = 1.0f / g->it[item].s;
-    const bool mirror = MODE == NS_UPDATE ? !last || tall : tr != tc;
+    const bool mirror = MODE == NS_UPDATE ? last && tall : tr != tc;
 #pragma unroll
     for (int j = 0; j < JT; j++) {
         const int row0 = n0 + (wn * JT + j) * 16 + RG * rg;
@@ -375,7 +510,7 @@ __global__ __launch_bounds__(Cfg::THREADS) void ns_product_kernel(NsGroup args)
         if constexpr (MODE == NS_UPDATE) {
 #pragma unroll
             for (int q = 0; q < RG; q++) {
-                hi[q] = *reinterpret_cast<const v8h *>(g->it[item].xh + (row0 + q) * ld_out + e0);
+                hi[q] = *reinterpret_cast<const v8h *>(g->it[item].xh[g->flip] + (row0 + q) * ld_out + e0);
                 lo[q] = *reinterpret_cast<const v8h *>(g->it[item].xl + (row0 + q) * ld_out + e0);
             }
         } else if constexpr (MODE == NS_POLY) {
@@ -439,7 +574,8 @@ __global__ __launch_bounds__(Cfg::THREADS) void ns_product_kernel(NsGroup args)
                 }
             }
             if (MODE != NS_UPDATE || !last) {
-                uint16_t *to = MODE == NS_GRAM ? g->it[item].a : MODE == NS_POLY ? g->it[item].b : g->it[item].xh;
+                uint16_t *to = MODE == NS_GRAM ? g->it[item].a : MODE == NS_POLY ? g->it[item].b
+                                                                                 : g->it[item].xh[g->flip ^ 1];
                 *reinterpret_cast<v8h *>(to + row * ld_out + e0) = res;
             }
             const uint4 bits = __builtin_bit_cast(uint4, res);
@@ -470,14 +606,12 @@ __global__ __launch_bounds__(Cfg::THREADS) void ns_product_kernel(NsGroup args)
             const int row = m0 + wm * SPAN + 8 * (place % LR) + place / LR;   // of the transpose
             const int col = n0 + (wn * JT + j - 1) * 16 + 8 * c;
             const uint4 w = *reinterpret_cast<const uint4 *>(turn + place * 64 + ((16 * c) ^ ((place & 1) << 5)));
-            if (MODE == NS_UPDATE && last) {
+            if constexpr (MODE == NS_UPDATE) {
                 const uint32_t o[4] = {w.x, w.y, w.z, w.w};
                 if (row < g->it[item].N)
                     store_run((uint16_t *)g->it[item].o + row * g->it[item].ldo, col, g->it[item].M, o);
             } else {
-                uint16_t *to = MODE == NS_GRAM ? g->it[item].a : MODE == NS_POLY ? g->it[item].b
-                                                                                 : g->it[item].xt[g->flip ^ 1];
-                *reinterpret_cast<uint4 *>(to + (int64_t)row * Mp + col) = w;
+                *reinterpret_cast<uint4 *>((MODE == NS_GRAM ? g->it[item].a : g->it[item].b) + (int64_t)row * Mp + col) = w;
             }
         }
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
@@ -498,10 +632,9 @@ size_t lay_out(NsItem &it, char *base)
         return p;
     };
     const size_t mn = (size_t)it.Mp * it.Np * 2, mm = (size_t)it.Mp * it.Mp * 2;
-    it.xh = (uint16_t *)take(mn);
+    it.xh[0] = (uint16_t *)take(mn);
+    it.xh[1] = (uint16_t *)take(mn);
     it.xl = (uint16_t *)take(mn);
-    it.xt[0] = (uint16_t *)take(mn);
-    it.xt[1] = (uint16_t *)take(mn);
     it.a = (uint16_t *)take(mm);
     it.b = (uint16_t *)take(mm);
     it.d = (float *)take((size_t)it.Mp * 4);
