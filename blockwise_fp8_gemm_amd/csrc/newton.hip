@@ -332,20 +332,33 @@ template <int WM_, int WN_, int IT_, int JT_, int S_> struct NsCfg {
     static constexpr int NW = WM * WN, THREADS = 64 * NW;
     static constexpr int TM = WM * IT * 16, TN = WN * JT * 16;
     static constexpr int STAGE = (TM + TN) * 128, LOADS = (TM + TN) / 8 / NW;
-    static_assert(S * STAGE >= NW * 16384, "16 KB per wave for the epilogue");
+    static constexpr int SPAN = IT * 16;           // elements of a result row per wave
+    static constexpr int TURN = SPAN * 64;         // bytes of each of a wave's two epilogue buffers
+    static_assert(S * STAGE >= NW * 2 * TURN, "the epilogue's buffers take the stages' place");
 };
+// Eight waves each (two per SIMD; with four a product took a fifth to a third
+// longer at every tile size).  The large tile reads least from LDS per product;
+// the smaller ones fill the GPU where there are few tiles or some are deep, and
+// have LDS left for a third and fourth stage.
 typedef NsCfg<2, 4, 8, 4, 2> NsL;   // 256 x 256
-typedef NsCfg<2, 2, 4, 4, 4> NsQ;   // 128 x 128
+typedef NsCfg<4, 2, 4, 4, 3> NsM;   // 256 x 128
+typedef NsCfg<2, 4, 4, 2, 4> NsQ;   // 128 x 128
 
 enum { NS_GRAM = 0, NS_POLY = 1, NS_UPDATE = 2 };
 
-// Workgroups are dispatched round-robin over the 8 XCDs: gives each XCD a
-// contiguous share of the launch's n tiles, so that the tiles resident together
-// on one XCD read the same operand panels through its L2.
-__device__ __forceinline__ int xcd_share(int b, int n)
+// Workgroups are dispatched round-robin over the 8 XCDs.  Of the workgroups
+// [first, end) of one matrix, those on XCD x take a contiguous run of its tiles,
+// so that the tiles resident together on one XCD read the same operand panels
+// through its L2, and every XCD has its share of every matrix.
+__device__ __forceinline__ int xcd_local(int b, int first, int end)
 {
-    const int per = n >> 3, rest = n & 7, x = b & 7;
-    return x * per + min(x, rest) + (b >> 3);
+    // workgroups of [0, n) on XCD y
+    auto on = [](int n, int y) { return (n - y + 7) >> 3; };
+    const int x = b & 7;
+    int start = 0;
+    for (int y = 0; y < x; y++)
+        start += on(end, y) - on(first, y);
+    return start + on(b, x) - on(first, x);
 }
 
 // Eight 16-bit values to row[c0 ..], those before cols.
@@ -370,9 +383,8 @@ __global__ __launch_bounds__(Cfg::THREADS) void ns_product_kernel(NsGroup args)
     constexpr int NW = Cfg::NW, TM = Cfg::TM, TN = Cfg::TN, IT = Cfg::IT, JT = Cfg::JT, S = Cfg::S;
     __shared__ __attribute__((aligned(16))) uint8_t lds[S * Cfg::STAGE];
     const KernargNs g = kernarg();
-    const int b = xcd_share(blockIdx.x, gridDim.x);
-    const int item = find_item(g, b);
-    const int local = b - g->first[item];
+    const int item = find_item(g, blockIdx.x);
+    const int local = xcd_local(blockIdx.x, g->first[item], g->first[item + 1]);
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave / Cfg::WN, wn = wave % Cfg::WN;
@@ -391,13 +403,12 @@ __global__ __launch_bounds__(Cfg::THREADS) void ns_product_kernel(NsGroup args)
     } else {
         P = Q = (const uint8_t *)(MODE == NS_GRAM ? g->it[item].xh[g->flip] : g->it[item].a);
         K = MODE == NS_GRAM ? Np : Mp;
-        // tiles on and above the diagonal, column by column
-        tc = (int)((sqrtf(8.0f * (float)local + 1.0f) - 1.0f) * 0.5f);
-        while (tc * (tc + 1) / 2 > local)
-            tc--;
-        while ((tc + 1) * (tc + 2) / 2 <= local)
-            tc++;
-        tr = local - tc * (tc + 1) / 2;
+        // tiles that reach the diagonal or lie above it, row by row of tiles
+        tr = 0;
+        tc = local;
+        for (int left = Mp / TN; tc >= left; left -= TM / TN, tr++)
+            tc -= left;
+        tc += tr * (TM / TN);
     }
     const int64_t ldp = (int64_t)(MODE == NS_UPDATE ? Np : K) * 2, ldq = (int64_t)K * 2;
     const int m0 = tr * TM, n0 = tc * TN, KB = K / 64;
@@ -486,23 +497,23 @@ __global__ __launch_bounds__(Cfg::THREADS) void ns_product_kernel(NsGroup args)
     // [tile column][tile row] and, transposed, [tile row][tile column].  Written
     // straight from this layout every store would touch 32 bytes of a row (2-byte
     // stores for one of the two), which took as long as the K loop itself; instead
-    // each wave turns 16 tile columns at a time through 8 KB of LDS of its own,
+    // each wave turns 16 tile columns at a time through LDS of its own,
     // so that a lane holds 8 consecutive elements of RG rows of the result, and
-    // collects 32 tile columns of the transpose in another 8 KB, whose rows
-    // leave as 64 bytes each.  Both are swizzled against bank conflicts.
-    constexpr int SPAN = IT * 16;          // elements of a result row per wave
+    // collects 32 tile columns of the transpose in another part, whose rows leave
+    // as 64 bytes each.  Both are swizzled against bank conflicts.
+    constexpr int SPAN = Cfg::SPAN;        // elements of a result row per wave
     constexpr int LR = SPAN / 8;           // lanes per row
     constexpr int RG = 16 * LR / 64;       // rows per lane
-    uint8_t *own = lds + wave * 16384;
+    uint8_t *own = lds + wave * 2 * Cfg::TURN;
     float *strip = reinterpret_cast<float *>(own);                 // [16][SPAN]
-    uint8_t *turn = own + 8192;                                    // [SPAN][32] FP16 / BF16
+    uint8_t *turn = own + Cfg::TURN;                                    // [SPAN][32] FP16 / BF16
     const int rl = lane % LR, rg = lane / LR;                      // element group and row group
     const int e0 = m0 + wm * SPAN + 8 * rl;                        // first element of this lane
     const float inv = 1.0f / kScaleA;
     const int last = MODE == NS_UPDATE ? g->last : 0, tall = g->it[item].tall;
     const int64_t ld_out = MODE == NS_UPDATE ? Np : Mp;
     const float unscale = 1.0f / g->it[item].s;
-    const bool mirror = MODE == NS_UPDATE ? last && tall : tr != tc;
+    const bool mirror = MODE == NS_UPDATE ? last && tall : tc >= (tr + 1) * (TM / TN);
 #pragma unroll
     for (int j = 0; j < JT; j++) {
         const int row0 = n0 + (wn * JT + j) * 16 + RG * rg;
@@ -658,24 +669,68 @@ NsItem make_item(const NsMatrix &m)
     return it;
 }
 
-template <class Cfg, int MODE> hipError_t launch_product(NsGroup &g, hipStream_t st)
+template <class Cfg, int MODE> bool fits(const NsItem &it)
+{
+    return it.Mp % Cfg::TN == 0 && (MODE == NS_UPDATE ? it.Np : it.Mp) % Cfg::TM == 0;
+}
+
+template <class Cfg, int MODE> int tiles_of(const NsItem &it)
+{
+    const int rows = (MODE == NS_UPDATE ? it.Np : it.Mp) / Cfg::TM, cols = it.Mp / Cfg::TN;
+    // on and above the diagonal: less the tiles wholly below it
+    return rows * cols - (MODE == NS_UPDATE ? 0 : Cfg::TM / Cfg::TN * (rows * (rows - 1) / 2));
+}
+
+template <int MODE> int depth_of(const NsItem &it) { return (MODE == NS_GRAM ? it.Np : it.Mp) / 64; }
+
+// Estimated time of a product on Cfg's tiles, us: the K blocks of the busiest
+// of the 256 CUs (the items are sorted, deepest first) times what a block takes
+// with at most a tile on every CU (`one`) or more (`many`).
+template <class Cfg, int MODE> double estimate(const NsGroup &g, double one, double many)
+{
+    double n = 0, work = 0, most = 0;
+    for (int i = 0; i < g.count; i++) {
+        if (!fits<Cfg, MODE>(g.it[i]))
+            return 1e30;
+        const double t = tiles_of<Cfg, MODE>(g.it[i]), k = depth_of<MODE>(g.it[i]);
+        n += t;
+        work += t * k;
+        most = std::max(most, std::ceil(n / 256) * k);
+    }
+    return std::max(most, work / 256) * (n <= 256 ? one : many);
+}
+
+template <class Cfg, int MODE> hipError_t launch_tiles(NsGroup &g, hipStream_t st)
 {
     g.first[0] = 0;
-    for (int i = 0; i < g.count; i++) {
-        const int rows = (MODE == NS_UPDATE ? g.it[i].Np : g.it[i].Mp) / Cfg::TM, cols = g.it[i].Mp / Cfg::TN;
-        g.first[i + 1] = g.first[i] + (MODE == NS_UPDATE ? rows * cols : cols * (cols + 1) / 2);
-    }
+    for (int i = 0; i < g.count; i++)
+        g.first[i + 1] = g.first[i] + tiles_of<Cfg, MODE>(g.it[i]);
     hipLaunchKernelGGL((ns_product_kernel<Cfg, MODE>), dim3((unsigned)g.first[g.count]), dim3(Cfg::THREADS), 0, st, g);
     return hipGetLastError();
 }
 
-template <class Cfg> hipError_t launch_step(NsGroup &g, hipStream_t st)
+// One product of every matrix, the deepest first: their tiles take longest.
+// The block times are measured: 2048 x 2048 (one matrix: X X^T 48, 31 and 21
+// us on 256 x 256, 256 x 128 and 128 x 128 tiles) and a layer's seven gradients
+// (X X^T 139 to 151, 124 and 133 us, B X 215, 269 and 312 us).
+template <int MODE> hipError_t launch_product(NsGroup &g, hipStream_t st)
 {
-    hipError_t e = launch_product<Cfg, NS_GRAM>(g, st);
+    std::stable_sort(g.it, g.it + g.count,
+                     [](const NsItem &x, const NsItem &y) { return depth_of<MODE>(x) > depth_of<MODE>(y); });
+    const double l = estimate<NsL, MODE>(g, 1.47, 1.47), m = estimate<NsM, MODE>(g, 0.8, 1.05),
+                 q = estimate<NsQ, MODE>(g, 0.5, 0.63);
+    if (l <= m && l <= q)
+        return launch_tiles<NsL, MODE>(g, st);
+    return m <= q ? launch_tiles<NsM, MODE>(g, st) : launch_tiles<NsQ, MODE>(g, st);
+}
+
+hipError_t launch_step(NsGroup &g, hipStream_t st)
+{
+    hipError_t e = launch_product<NS_GRAM>(g, st);
     if (e == hipSuccess)
-        e = launch_product<Cfg, NS_POLY>(g, st);
+        e = launch_product<NS_POLY>(g, st);
     if (e == hipSuccess)
-        e = launch_product<Cfg, NS_UPDATE>(g, st);
+        e = launch_product<NS_UPDATE>(g, st);
     return e;
 }
 
@@ -707,12 +762,10 @@ hipError_t launch_newton(const NsMatrix *ms, int count, bool gbf16, int steps, c
         g.eps = eps;
         g.flip = 0;
         size_t off = 0;
-        bool large = true;
         g.first[0] = 0;
         for (int i = 0; i < g.count; i++) {
             g.it[i] = make_item(ms[lo + i]);
             off += lay_out(g.it[i], (char *)workspace + off);
-            large = large && g.it[i].Mp % 256 == 0 && g.it[i].Np % 256 == 0;
             g.first[i + 1] = g.first[i] + (g.it[i].Mp / 64) * (g.it[i].Np / 64);
         }
         hipLaunchKernelGGL(ns_norm_kernel, dim3(kNormBlocks, (unsigned)g.count), dim3(256), 0, st, g);
@@ -726,7 +779,7 @@ hipError_t launch_newton(const NsMatrix *ms, int count, bool gbf16, int steps, c
             g.b = coef[3 * k + 1];
             g.c = coef[3 * k + 2];
             g.last = k + 1 == steps;
-            e = large ? launch_step<NsL>(g, st) : launch_step<NsQ>(g, st);
+            e = launch_step(g, st);
             g.flip ^= 1;
         }
         if (e != hipSuccess)

@@ -125,6 +125,19 @@ def test_grouped_equals_single_and_repeats(dev):
         assert torch.equal(a, pf.puro_fp8_newton_schulz_grouped([g])[0])
 
 
+@pytest.mark.parametrize("count", [1, 2, 4, 8])
+def test_every_tile_size_gives_the_same_bits(dev, count):
+    """More equal matrices in a call move its products to larger tiles: the same results, bit for bit."""
+    shape = (2048, 512)
+    g = gradient(*shape, 901, torch.float32, dev)
+    one, = pf.puro_fp8_newton_schulz_grouped([g], steps=2)
+    outs = pf.puro_fp8_newton_schulz_grouped([g] * count + [gradient(1024, 1024, 902, torch.float32, dev)], steps=2)
+    torch.cuda.synchronize()
+    check(one, g, steps=2)
+    for o in outs[:count]:
+        assert torch.equal(o, one)
+
+
 def test_whole_tiles_of_256(dev):
     """Sizes that the 256 x 256 tiles take, in a group and alone."""
     grads = [gradient(r, c, 200 + i, torch.float32, dev) for i, (r, c) in enumerate([(1024, 512), (512, 512),
