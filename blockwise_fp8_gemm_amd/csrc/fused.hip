@@ -116,41 +116,78 @@ template <bool SLOW> __device__ __forceinline__ uint32_t codes4(float a, float b
     return e4m3x4(code_arg<SLOW>(a, s), code_arg<SLOW>(b, s), code_arg<SLOW>(c, s), code_arg<SLOW>(d, s));
 }
 
-// Eight BF16 values of a row from column c0 on, zeros at and past cols.
+// The first n of 16 bytes (0 < n < 16) to a 16-byte aligned address, in at most
+// four stores.
+__device__ __forceinline__ void store_some(uint8_t *p, const uint32_t w[4], int n)
+{
+    uint32_t a = w[0], b = w[1];
+    if (n & 8) {
+        *reinterpret_cast<uint2 *>(p) = make_uint2(a, b);
+        a = w[2];
+        b = w[3];
+        p += 8;
+    }
+    if (n & 4) {
+        *reinterpret_cast<uint32_t *>(p) = a;
+        a = b;
+        p += 4;
+    }
+    if (n & 2) {
+        *reinterpret_cast<uint16_t *>(p) = (uint16_t)a;
+        a >>= 16;
+        p += 2;
+    }
+    if (n & 1)
+        *p = (uint8_t)a;
+}
+
+// Eight BF16 values of a row from column c0 on (a multiple of 8), zeros at and past cols.
 __device__ __forceinline__ uint4 load8_bf16(const uint16_t *row, int64_t c0, int64_t cols)
 {
     if (c0 + 8 <= cols)
         return *reinterpret_cast<const uint4 *>(row + c0);
-    uint32_t w[4] = {0, 0, 0, 0};
-#pragma unroll
-    for (int j = 0; j < 8; j++)
-        if (c0 + j < cols)
-            w[j >> 1] |= (uint32_t)row[c0 + j] << (16 * (j & 1));
-    return make_uint4(w[0], w[1], w[2], w[3]);
+    uint4 r = make_uint4(0, 0, 0, 0);
+    if (c0 >= cols)
+        return r;
+    const int n = (int)(cols - c0);
+    const uint16_t *p = row + c0;
+    uint32_t two = 0, one = 0;
+    if (n & 4) {
+        const uint2 v = *reinterpret_cast<const uint2 *>(p);
+        r.x = v.x;
+        r.y = v.y;
+    }
+    if (n & 2)
+        two = *reinterpret_cast<const uint32_t *>(p + (n & 4));
+    if (n & 1)
+        one = p[n & 6];
+    const uint32_t lo = n & 2 ? two : one, hi = n & 2 ? one : 0;
+    if (n & 4) {
+        r.z = lo;
+        r.w = hi;
+    } else {
+        r.x = lo;
+        r.y = hi;
+    }
+    return r;
 }
 
 __device__ __forceinline__ void store8_bf16(uint16_t *row, int64_t c0, int64_t cols, const uint32_t w[4])
 {
-    if (c0 + 8 <= cols) {
+    if (c0 + 8 <= cols)
         store_nt(row + c0, w[0], w[1], w[2], w[3]);
-        return;
-    }
-#pragma unroll
-    for (int j = 0; j < 8; j++)
-        if (c0 + j < cols)
-            row[c0 + j] = (uint16_t)(w[j >> 1] >> (16 * (j & 1)));
+    else if (c0 < cols)
+        store_some(reinterpret_cast<uint8_t *>(row + c0), w, 2 * (int)(cols - c0));
 }
 
 __device__ __forceinline__ void store8_codes(uint8_t *row, int64_t c0, int64_t cols, uint32_t lo, uint32_t hi)
 {
     if (c0 + 8 <= cols) {
         store_nt(row + c0, lo, hi);
-        return;
+    } else if (c0 < cols) {
+        const uint32_t w[4] = {lo, hi, 0, 0};
+        store_some(row + c0, w, (int)(cols - c0));
     }
-#pragma unroll
-    for (int j = 0; j < 8; j++)
-        if (c0 + j < cols)
-            row[c0 + j] = (uint8_t)((j < 4 ? lo : hi) >> (8 * (j & 3)));
 }
 
 __device__ __forceinline__ void unpack8(const uint4 &a, float v[8])
@@ -384,10 +421,9 @@ __device__ __forceinline__ void quant_tile(const float (&v)[RT][8], const QuantO
         uint8_t *dst = to.q + c * to.ldq + tk;
         if (FULL || (c < p.cols && tk + 16 <= p.tokens)) {
             store_nt(dst, src[0], src[1], src[2], src[3]);
-        } else if (c < p.cols) {
-            for (int e = 0; e < 16; e++)
-                if (tk + e < p.tokens)
-                    dst[e] = sh.tile[row][seg * 16 + e];
+        } else if (c < p.cols && tk < p.tokens) {
+            const uint32_t w[4] = {src[0], src[1], src[2], src[3]};
+            store_some(dst, w, (int)(p.tokens - tk));
         }
     }
 }
