@@ -636,50 +636,104 @@ void norm_tile_kernel(const uint16_t *__restrict__ z, int64_t ldz, const float *
 }
 
 // ---------------------------------------------------------------------------
-// Norm gradient, row pass: c_t = mean over the row of w dy z r.
+// Norm gradient.  Row pass, over every gridDim-th row like the norm's: c_t =
+// mean over the row of w dy z r, and this workgroup's share of dw, its rows'
+// dy z r, to part[workgroup][column] (rows of ldp, a multiple of 16).
 // ---------------------------------------------------------------------------
-__global__ __launch_bounds__(NT) void norm_bwd_row_kernel(const uint16_t *__restrict__ dy, int64_t lddy,
-                                                          const uint16_t *__restrict__ z, int64_t ldz,
-                                                          const float *__restrict__ rstd,
-                                                          const void *__restrict__ w, int wbf16, int64_t cols,
-                                                          float *__restrict__ coef)
+template <int RUN>
+__global__ __launch_bounds__(NT) void norm_bwd_row_kernel(NormBwd b, float *__restrict__ coef,
+                                                          float *__restrict__ part, int64_t ldp)
 {
-    __shared__ float red[NT / 64];
-    const int64_t row = blockIdx.x;
-    const uint16_t *dr = dy + row * lddy, *zr = z + row * ldz;
-    float sum = 0.0f;
-    for (int64_t c0 = 8 * (int64_t)threadIdx.x; c0 < cols; c0 += 8 * NT) {
-        float d[8], v[8], wv[8];
-        unpack8(load8_bf16(dr, c0, cols), d);
-        unpack8(load8_bf16(zr, c0, cols), v);
-        load8_weight(w, wbf16, c0, cols, wv);
+    constexpr bool WIDE = RUN == 4;   // rows that do not fit the registers reach the widest form only
+    __shared__ float red[2][NT / 64];
+    const int t = threadIdx.x;
+    const int64_t cols = b.cols;
+    float *mine = part + blockIdx.x * ldp;
+
+    float w[RUN][8], dw[RUN][8];
+    uint4 y[RUN], x[RUN];
+    float rstd = 0.0f;
+    auto fetch = [&](int64_t row) {
+        rstd = b.rstd[row];
+#pragma unroll
+        for (int k = 0; k < RUN; k++) {
+            const int64_t c0 = 8 * (int64_t)(t + NT * k);
+            y[k] = load8_bf16(b.dy + row * b.lddy, c0, cols);
+            x[k] = load8_bf16(b.z + row * b.ldz, c0, cols);
+        }
+    };
+    // sum of w dy z, and dw += dy z r
+    auto inner = [&](const uint4 &dy, const uint4 &z, const float (&wv)[8], float r, float (&acc)[8]) {
+        float yv[8], xv[8], p = 0.0f;
+        unpack8(dy, yv);
+        unpack8(z, xv);
+#pragma unroll
+        for (int j = 0; j < 8; j++) {
+            p = fmaf(yv[j] * wv[j], xv[j], p);
+            acc[j] = fmaf(yv[j], xv[j] * r, acc[j]);
+        }
+        return p;
+    };
+    auto put = [&](int64_t c0, const float (&v)[8]) {
+        *reinterpret_cast<float4 *>(mine + c0) = make_float4(v[0], v[1], v[2], v[3]);
+        *reinterpret_cast<float4 *>(mine + c0 + 4) = make_float4(v[4], v[5], v[6], v[7]);
+    };
+
+    fetch(blockIdx.x);
+#pragma unroll
+    for (int k = 0; k < RUN; k++) {
+        load8_weight(b.w, b.wbf16, 8 * (int64_t)(t + NT * k), cols, w[k]);
 #pragma unroll
         for (int j = 0; j < 8; j++)
-            sum = fmaf(d[j] * wv[j], v[j], sum);
+            dw[k][j] = 0.0f;
     }
-    const float total = block_sum(sum, red);
-    if (threadIdx.x == 0)
-        coef[row] = total * rstd[row] / (float)cols;
+    int turn = 0;
+    for (int64_t row = blockIdx.x; row < b.tokens; row += gridDim.x, turn ^= 1) {
+        const float r = rstd;
+        float sum = 0.0f;
+#pragma unroll
+        for (int k = 0; k < RUN; k++)
+            sum += inner(y[k], x[k], w[k], r, dw[k]);
+        if (row + gridDim.x < b.tokens)
+            fetch(row + gridDim.x);
+        for (int64_t c0 = 8 * (int64_t)(t + NT * RUN); WIDE && c0 < cols; c0 += 8 * NT) {
+            // columns past the registers: this workgroup's share of dw is kept in part itself
+            float wv[8], acc[8];
+            load8_weight(b.w, b.wbf16, c0, cols, wv);
+            if (row == blockIdx.x) {
+#pragma unroll
+                for (int j = 0; j < 8; j++)
+                    acc[j] = 0.0f;
+            } else {
+                Elem<float>::load8(mine + c0, acc);
+            }
+            sum += inner(load8_bf16(b.dy + row * b.lddy, c0, cols), load8_bf16(b.z + row * b.ldz, c0, cols), wv, r, acc);
+            put(c0, acc);
+        }
+        const float total = block_sum(sum, red[turn]);
+        if (t == 0)
+            coef[row] = total * r / (float)cols;
+    }
+#pragma unroll
+    for (int k = 0; k < RUN; k++) {
+        const int64_t c0 = 8 * (int64_t)(t + NT * k);
+        if (c0 < cols)
+            put(c0, dw[k]);
+    }
 }
 
-// Tile pass: dx of a tile, stored as BF16 and quantised both ways, and the
-// tile's share of dw (its 128 tokens), to part[token tile][column].
-constexpr int BWD_RT = 4;
+// Tile pass: dx of a tile, stored as BF16 and quantised both ways.
 template <bool FULL, bool TR, int RT>
-__device__ __forceinline__ void norm_bwd_tile(const NormBwd &b, const float *coef, const Place<RT> &p, const QuantOut &ro,
-                                              const QuantOut &to, float *part, int pow2, TileShared<RT> &sh)
+__device__ __forceinline__ void norm_bwd_tile(const NormBwd &b, const float *coef, const Place<RT> &p,
+                                              const QuantOut &ro, const QuantOut &to, int pow2, TileShared<RT> &sh)
 {
-    const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
     uint4 y[RT], z[RT], d[RT];
     load_tile<FULL>(b.dy, b.lddy, p, y);
     load_tile<FULL>(b.z, b.ldz, p, z);
     if (b.dres)
         load_tile<FULL>(b.dres, b.lddres, p, d);
-    float wv[8], v[RT][8], dw[8];
+    float wv[8], v[RT][8];
     load8_weight(b.w, b.wbf16, p.c0(), p.cols, wv);
-#pragma unroll
-    for (int j = 0; j < 8; j++)
-        dw[j] = 0.0f;
 #pragma unroll
     for (int i = 0; i < RT; i++) {
         const bool in = FULL || p.tk(i) < p.tokens;
@@ -688,11 +742,8 @@ __device__ __forceinline__ void norm_bwd_tile(const NormBwd &b, const float *coe
         unpack8(y[i], yv);
         unpack8(z[i], x);
 #pragma unroll
-        for (int j = 0; j < 8; j++) {
-            const float xh = x[j] * r;
-            dw[j] = fmaf(yv[j], xh, dw[j]);
-            v[i][j] = r * fmaf(-xh, ct, yv[j] * wv[j]);
-        }
+        for (int j = 0; j < 8; j++)
+            v[i][j] = r * fmaf(-(x[j] * r), ct, yv[j] * wv[j]);
         if (b.dres) {
             float e[8];
             unpack8(d[i], e);
@@ -703,56 +754,52 @@ __device__ __forceinline__ void norm_bwd_tile(const NormBwd &b, const float *coe
     }
     pin(v);
     store_tile<FULL>(b.dx, b.lddx, p, v);
-    *reinterpret_cast<float2 *>(&sh.red[wave][8 * p.cc + first_of(lane)]) =
-        cross4(dw, [](float x, float y) { return x + y; });
-    __syncthreads();
-    if (t < 128 && (FULL || p.col0 + t < p.cols)) {
-        float s = sh.red[0][t];
-#pragma unroll
-        for (int k = 1; k < TileShared<RT>::WAVES; k++)
-            s += sh.red[k][t];
-        part[(int64_t)blockIdx.y * p.cols + p.col0 + t] = s;
-    }
-    __syncthreads();   // red is reused by the tile's column maxima
     quant_tile<FULL, TR, true, RT>(v, ro, to, p, pow2, sh);
 }
 
-template <bool TR>
-__global__ __launch_bounds__(tile_threads(BWD_RT)) __attribute__((amdgpu_waves_per_eu(4)))
-void norm_bwd_tile_kernel(NormBwd b, const float *__restrict__ coef, QuantOut ro, QuantOut to,
-                          float *__restrict__ part, int pow2)
+// dw = (dw +) the workgroups' shares, for 32 columns: 16 threads per column take
+// every 16th share, and their sums are added in a fixed order.
+constexpr int DW_COLS = 32, DW_ROWS = tile_threads(NORM_RT) / DW_COLS;
+__device__ __forceinline__ void sum_dw(const float *part, int parts, int64_t ldp, int64_t cols, int64_t col0,
+                                       float *dw, bool accumulate, float (*red)[DW_COLS])
 {
-    __shared__ TileShared<BWD_RT> sh;
-    const auto p = place<BWD_RT>(b.tokens, b.cols);
-    if (full_tile(p))
-        norm_bwd_tile<true, TR, BWD_RT>(b, coef, p, ro, to, part, pow2, sh);
-    else
-        norm_bwd_tile<false, TR, BWD_RT>(b, coef, p, ro, to, part, pow2, sh);
-}
-
-// dw = (dw +) the token tiles' shares: DG threads per column take every DG-th
-// tile, and their sums are added in order.
-constexpr int DC = 32, DG = 8;
-__global__ __launch_bounds__(DC *DG) void norm_dw_kernel(const float *__restrict__ part, int64_t ntb, int64_t cols,
-                                                         float *__restrict__ dw, int accumulate)
-{
-    __shared__ float red[DG][DC];
-    const int x = threadIdx.x % DC, y = threadIdx.x / DC;
-    const int64_t c = (int64_t)blockIdx.x * DC + x;
+    const int x = threadIdx.x % DW_COLS, y = threadIdx.x / DW_COLS;
+    const int64_t c = col0 + x;
     float s = 0.0f;
     if (c < cols) {
-#pragma unroll 4
-        for (int64_t k = y; k < ntb; k += DG)
-            s += part[k * cols + c];
+#pragma unroll 8
+        for (int k = y; k < parts; k += DW_ROWS)
+            s += part[k * ldp + c];
     }
     red[y][x] = s;
-    __syncthreads();
-    if (y == 0 && c < cols) {
-#pragma unroll
-        for (int k = 1; k < DG; k++)
-            s += red[k][x];
-        dw[c] = accumulate ? dw[c] + s : s;
+    for (int n = DW_ROWS / 2; n > 0; n >>= 1) {
+        __syncthreads();
+        if (y < n)
+            red[y][x] += red[y + n][x];
     }
+    if (y == 0 && c < cols)
+        dw[c] = accumulate ? dw[c] + red[0][x] : red[0][x];
+}
+
+// The first DW_BLOCKS rows of workgroups add up dw, the others take a tile each.
+constexpr int DW_BLOCKS = 128 / DW_COLS;
+template <bool TR>
+__global__ __launch_bounds__(tile_threads(NORM_RT)) __attribute__((amdgpu_waves_per_eu(4)))
+void norm_bwd_tile_kernel(NormBwd b, const float *__restrict__ coef, const float *__restrict__ part, int parts,
+                          int64_t ldp, QuantOut ro, QuantOut to, int pow2)
+{
+    __shared__ TileShared<NORM_RT> sh;
+    if (blockIdx.y < DW_BLOCKS) {
+        sum_dw(part, parts, ldp, b.cols, (int64_t)blockIdx.x * 128 + blockIdx.y * DW_COLS, b.dw, b.accumulate,
+               reinterpret_cast<float(*)[DW_COLS]>(&sh.red[0][0]));
+        return;
+    }
+    auto p = place<NORM_RT>(b.tokens, b.cols);
+    p.tok0 -= 128 * DW_BLOCKS;
+    if (full_tile(p))
+        norm_bwd_tile<true, TR, NORM_RT>(b, coef, p, ro, to, pow2, sh);
+    else
+        norm_bwd_tile<false, TR, NORM_RT>(b, coef, p, ro, to, pow2, sh);
 }
 
 // ---------------------------------------------------------------------------
@@ -860,32 +907,36 @@ hipError_t launch_norm_dual(const NormIn &in, uint8_t *qr, int64_t ldqr, float *
 
 static size_t coef_bytes(int64_t tokens) { return ((size_t)tokens * 4 + 255) / 256 * 256; }
 
+// Workgroups of the gradient's row pass: two rows each or more, at most 1024, so
+// that their shares of dw stay small beside the rows they read.
+static int64_t bwd_groups(int64_t tokens) { return tokens < 2048 ? (tokens + 1) / 2 : 1024; }
+static int64_t bwd_part_ld(int64_t cols) { return (cols + 15) / 16 * 16; }
+
 size_t norm_bwd_workspace_bytes(int64_t tokens, int64_t cols)
 {
-    return coef_bytes(tokens) + (size_t)((tokens + 127) / 128) * (size_t)cols * 4;
+    return coef_bytes(tokens) + (size_t)bwd_groups(tokens) * (size_t)bwd_part_ld(cols) * 4;
 }
 
 hipError_t launch_norm_bwd(const NormBwd &b, uint8_t *qr, int64_t ldqr, float *sr, bool transpose_out, uint8_t *qt,
                            int64_t ldqt, float *stok, bool pow2, void *workspace, hipStream_t st)
 {
-    const int64_t nb = (b.cols + 127) / 128, ntb = (b.tokens + 127) / 128;
+    const int64_t nb = (b.cols + 127) / 128, ntb = (b.tokens + 127) / 128, groups = bwd_groups(b.tokens);
+    const int64_t ldp = bwd_part_ld(b.cols);
     float *coef = (float *)workspace;
     float *part = (float *)((char *)workspace + coef_bytes(b.tokens));
     if (b.tokens > 0) {
-        hipLaunchKernelGGL(norm_bwd_row_kernel, dim3((unsigned)b.tokens), dim3(NT), 0, st, b.dy, b.lddy, b.z, b.ldz,
-                           b.rstd, b.w, (int)b.wbf16, b.cols, coef);
-        hipError_t e = hipGetLastError();
-        if (e != hipSuccess)
-            return e;
-        const QuantOut ro{qr, ldqr, sr, nb}, to{qt, ldqt, stok, transpose_out ? ntb : b.cols};
-        hipLaunchKernelGGL((transpose_out ? norm_bwd_tile_kernel<true> : norm_bwd_tile_kernel<false>),
-                           tile_grid(b.tokens, b.cols), dim3(tile_threads(BWD_RT)), 0, st, b, coef, ro, to, part, (int)pow2);
-        e = hipGetLastError();
+        auto *kernel = b.cols <= 8 * NT    ? norm_bwd_row_kernel<1>
+                       : b.cols <= 16 * NT ? norm_bwd_row_kernel<2>
+                                           : norm_bwd_row_kernel<4>;
+        hipLaunchKernelGGL(kernel, dim3((unsigned)groups), dim3(NT), 0, st, b, coef, part, ldp);
+        const hipError_t e = hipGetLastError();
         if (e != hipSuccess)
             return e;
     }
-    hipLaunchKernelGGL(norm_dw_kernel, dim3((unsigned)((b.cols + DC - 1) / DC)), dim3(DC * DG), 0, st, part, ntb, b.cols,
-                       b.dw, (int)b.accumulate);
+    const QuantOut ro{qr, ldqr, sr, nb}, to{qt, ldqt, stok, transpose_out ? ntb : b.cols};
+    hipLaunchKernelGGL((transpose_out ? norm_bwd_tile_kernel<true> : norm_bwd_tile_kernel<false>),
+                       dim3((unsigned)nb, (unsigned)(ntb + DW_BLOCKS)), dim3(tile_threads(NORM_RT)), 0, st, b, coef,
+                       part, (int)groups, ldp, ro, to, (int)pow2);
     return hipGetLastError();
 }
 
