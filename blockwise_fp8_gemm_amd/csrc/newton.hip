@@ -29,6 +29,7 @@
 #include "kernels.h"
 
 #include <algorithm>
+#include <climits>
 #include <cmath>
 
 namespace puro {
@@ -42,7 +43,8 @@ typedef short v4s __attribute__((ext_vector_type(4)));
 constexpr float kScaleA = 1024.0f;   // A and B are held times this
 constexpr int kNormBlocks = 256;     // partial sums of |G|^2 per matrix
 
-struct NsItem {
+// One 128-byte line: a kernel fetches its matrix's in one go.
+struct alignas(128) NsItem {
     const void *g;
     void *o;
     int64_t ldg, ldo;
@@ -56,14 +58,16 @@ struct NsItem {
     double *part;           // [kNormBlocks]
 };
 
+static_assert(sizeof(NsItem) == 128, "one line");
+
 struct NsGroup {
-    NsItem it[kNsGroupMax];
-    int first[kNsGroupMax + 1];   // workgroups of item i: [first[i], first[i+1])
+    int first[kNsGroupMax + 1];   // workgroups of item i: [first[i], first[i+1]); past the last item, INT_MAX
     int count;
     int gbf16;
     int flip;                     // which xh is read
     int last;                     // the step whose result is the output
     float a, b, c, eps;
+    NsItem it[kNsGroupMax];
 };
 
 typedef __attribute__((address_space(4))) const NsGroup *KernargNs;
@@ -73,11 +77,21 @@ __device__ __forceinline__ KernargNs kernarg()
     return (KernargNs)__builtin_amdgcn_kernarg_segment_ptr();
 }
 
-__device__ __forceinline__ int find_item(KernargNs g, int b)
+// The item that holds workgroup b.  All of `first` is read at once and compared
+// without a loop: the arguments come from memory, and loads that wait for each
+// other are a good part of a small launch's time.
+__device__ __forceinline__ int find_item(KernargNs g, int b, int &begin, int &end)
 {
     int i = 0;
-    while (i + 1 < g->count && b >= g->first[i + 1])
-        i++;
+    begin = 0;
+    end = g->first[1];
+#pragma unroll
+    for (int k = 1; k < kNsGroupMax; k++) {
+        const bool past = b >= g->first[k];
+        i += past;
+        begin = past ? g->first[k] : begin;
+        end = past ? g->first[k + 1] : end;
+    }
     return __builtin_amdgcn_readfirstlane(i);
 }
 
@@ -155,8 +169,9 @@ __global__ __launch_bounds__(256) void ns_init_kernel(NsGroup args)
 {
     (void)args;
     const KernargNs g = kernarg();
-    const int i = find_item(g, blockIdx.x), t = threadIdx.x;
-    const int local = blockIdx.x - g->first[i];
+    int begin, end;
+    const int i = find_item(g, blockIdx.x, begin, end), t = threadIdx.x;
+    const int local = blockIdx.x - begin;
     const int M = g->it[i].M, N = g->it[i].N, Np = g->it[i].Np, tall = g->it[i].tall;
     const int rows = tall ? N : M, cols = tall ? M : N;
     const int64_t ld = g->it[i].ldg;
@@ -383,8 +398,9 @@ __global__ __launch_bounds__(Cfg::THREADS) void ns_product_kernel(NsGroup args)
     constexpr int NW = Cfg::NW, TM = Cfg::TM, TN = Cfg::TN, IT = Cfg::IT, JT = Cfg::JT, S = Cfg::S;
     __shared__ __attribute__((aligned(16))) uint8_t lds[S * Cfg::STAGE];
     const KernargNs g = kernarg();
-    const int item = find_item(g, blockIdx.x);
-    const int local = xcd_local(blockIdx.x, g->first[item], g->first[item + 1]);
+    int begin, end;
+    const int item = find_item(g, blockIdx.x, begin, end);
+    const int local = xcd_local(blockIdx.x, begin, end);
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave / Cfg::WN, wn = wave % Cfg::WN;
@@ -700,12 +716,21 @@ template <class Cfg, int MODE> double estimate(const NsGroup &g, double one, dou
     return std::max(most, work / 256) * (n <= 256 ? one : many);
 }
 
+// first[] from the items' workgroup counts; the launch's number of workgroups.
+template <class Count> unsigned deal(NsGroup &g, Count count)
+{
+    int n = 0;
+    for (int i = 0; i <= kNsGroupMax; i++) {
+        g.first[i] = i <= g.count ? n : INT_MAX;
+        n += i < g.count ? count(g.it[i]) : 0;
+    }
+    return (unsigned)n;
+}
+
 template <class Cfg, int MODE> hipError_t launch_tiles(NsGroup &g, hipStream_t st)
 {
-    g.first[0] = 0;
-    for (int i = 0; i < g.count; i++)
-        g.first[i + 1] = g.first[i] + tiles_of<Cfg, MODE>(g.it[i]);
-    hipLaunchKernelGGL((ns_product_kernel<Cfg, MODE>), dim3((unsigned)g.first[g.count]), dim3(Cfg::THREADS), 0, st, g);
+    const unsigned n = deal(g, tiles_of<Cfg, MODE>);
+    hipLaunchKernelGGL((ns_product_kernel<Cfg, MODE>), dim3(n), dim3(Cfg::THREADS), 0, st, g);
     return hipGetLastError();
 }
 
@@ -762,17 +787,16 @@ hipError_t launch_newton(const NsMatrix *ms, int count, bool gbf16, int steps, c
         g.eps = eps;
         g.flip = 0;
         size_t off = 0;
-        g.first[0] = 0;
         for (int i = 0; i < g.count; i++) {
             g.it[i] = make_item(ms[lo + i]);
             off += lay_out(g.it[i], (char *)workspace + off);
-            g.first[i + 1] = g.first[i] + (g.it[i].Mp / 64) * (g.it[i].Np / 64);
         }
         hipLaunchKernelGGL(ns_norm_kernel, dim3(kNormBlocks, (unsigned)g.count), dim3(256), 0, st, g);
         hipError_t e = hipGetLastError();
         if (e != hipSuccess)
             return e;
-        hipLaunchKernelGGL(ns_init_kernel, dim3((unsigned)g.first[g.count]), dim3(256), 0, st, g);
+        const unsigned n = deal(g, [](const NsItem &it) { return (it.Mp / 64) * (it.Np / 64); });
+        hipLaunchKernelGGL(ns_init_kernel, dim3(n), dim3(256), 0, st, g);
         e = hipGetLastError();
         for (int k = 0; k < steps && e == hipSuccess; k++) {
             g.a = coef[3 * k];
