@@ -351,13 +351,14 @@ template <int WM_, int WN_, int IT_, int JT_, int S_> struct NsCfg {
     static constexpr int TURN = SPAN * 64;         // bytes of each of a wave's two epilogue buffers
     static_assert(S * STAGE >= NW * 2 * TURN, "the epilogue's buffers take the stages' place");
 };
-// Eight waves each (two per SIMD; with four a product took a fifth to a third
-// longer at every tile size).  The large tile reads least from LDS per product;
-// the smaller ones fill the GPU where there are few tiles or some are deep, and
-// have LDS left for a third and fourth stage.
+// The large tile reads least from LDS per product; the smaller ones fill the GPU
+// where there are few tiles or some are deep, and have LDS left for a third and
+// fourth stage.  Eight waves (two per SIMD) on the three large ones: with four a
+// product took a fifth to a third longer.
 typedef NsCfg<2, 4, 8, 4, 2> NsL;   // 256 x 256
 typedef NsCfg<4, 2, 4, 4, 3> NsM;   // 256 x 128
 typedef NsCfg<2, 4, 4, 2, 4> NsQ;   // 128 x 128
+typedef NsCfg<2, 2, 2, 2, 4> NsE;   // 64 x 64
 
 enum { NS_GRAM = 0, NS_POLY = 1, NS_UPDATE = 2 };
 
@@ -621,8 +622,10 @@ __global__ __launch_bounds__(Cfg::THREADS) void ns_product_kernel(NsGroup args)
             if constexpr (RG == 4)
                 *reinterpret_cast<uint2 *>(dst) = make_uint2(out[0][k] | ((uint32_t)out[1][k] << 16),
                                                              out[2][k] | ((uint32_t)out[3][k] << 16));
-            else
+            else if constexpr (RG == 2)
                 *reinterpret_cast<uint32_t *>(dst) = out[0][k] | ((uint32_t)out[1][k] << 16);
+            else
+                *reinterpret_cast<uint16_t *>(dst) = out[0][k];
         }
         if ((j & 1) == 0)
             continue;
@@ -699,10 +702,10 @@ template <class Cfg, int MODE> int tiles_of(const NsItem &it)
 
 template <int MODE> int depth_of(const NsItem &it) { return (MODE == NS_GRAM ? it.Np : it.Mp) / 64; }
 
-// Estimated time of a product on Cfg's tiles, us: the K blocks of the busiest
-// of the 256 CUs (the items are sorted, deepest first) times what a block takes
-// with at most a tile on every CU (`one`) or more (`many`).
-template <class Cfg, int MODE> double estimate(const NsGroup &g, double one, double many)
+// Estimated time of a product on Cfg's tiles, us: a fixed part, and the K blocks
+// of the busiest of the 256 CUs (the items are sorted, deepest first) times what
+// a block takes with at most a tile on every CU (`one`) or more (`many`).
+template <class Cfg, int MODE> double estimate(const NsGroup &g, double fixed, double one, double many)
 {
     double n = 0, work = 0, most = 0;
     for (int i = 0; i < g.count; i++) {
@@ -713,7 +716,7 @@ template <class Cfg, int MODE> double estimate(const NsGroup &g, double one, dou
         work += t * k;
         most = std::max(most, std::ceil(n / 256) * k);
     }
-    return std::max(most, work / 256) * (n <= 256 ? one : many);
+    return fixed + std::max(most, work / 256) * (n <= 256 ? one : many);
 }
 
 // first[] from the items' workgroup counts; the launch's number of workgroups.
@@ -735,18 +738,22 @@ template <class Cfg, int MODE> hipError_t launch_tiles(NsGroup &g, hipStream_t s
 }
 
 // One product of every matrix, the deepest first: their tiles take longest.
-// The block times are measured: 2048 x 2048 (one matrix: X X^T 48, 31 and 21
-// us on 256 x 256, 256 x 128 and 128 x 128 tiles) and a layer's seven gradients
-// (X X^T 139 to 151, 124 and 133 us, B X 215, 269 and 312 us).
+// The block times are measured, with 256 x 256, 256 x 128, 128 x 128 and 64 x 64
+// tiles: X X^T of one 2048 x 2048 matrix 48, 31, 21 and 25 us, of one 1024 x 4096
+// 30 and 17 (the last two), of one 256 x 1024 11 and 7; a layer's seven gradients
+// X X^T 139 to 151, 124 and 133 us, B X 215, 269 and 312.
 template <int MODE> hipError_t launch_product(NsGroup &g, hipStream_t st)
 {
     std::stable_sort(g.it, g.it + g.count,
                      [](const NsItem &x, const NsItem &y) { return depth_of<MODE>(x) > depth_of<MODE>(y); });
-    const double l = estimate<NsL, MODE>(g, 1.47, 1.47), m = estimate<NsM, MODE>(g, 0.8, 1.05),
-                 q = estimate<NsQ, MODE>(g, 0.5, 0.63);
-    if (l <= m && l <= q)
+    const double l = estimate<NsL, MODE>(g, 7.0, 1.47, 1.47), m = estimate<NsM, MODE>(g, 6.0, 0.8, 1.05),
+                 q = estimate<NsQ, MODE>(g, 4.5, 0.48, 0.63), e = estimate<NsE, MODE>(g, 3.8, 0.2, 0.3);
+    const double best = std::min(std::min(l, m), std::min(q, e));
+    if (best == l)
         return launch_tiles<NsL, MODE>(g, st);
-    return m <= q ? launch_tiles<NsM, MODE>(g, st) : launch_tiles<NsQ, MODE>(g, st);
+    if (best == m)
+        return launch_tiles<NsM, MODE>(g, st);
+    return best == q ? launch_tiles<NsQ, MODE>(g, st) : launch_tiles<NsE, MODE>(g, st);
 }
 
 hipError_t launch_step(NsGroup &g, hipStream_t st)
