@@ -179,65 +179,61 @@ __global__ __launch_bounds__(256) void ns_init_kernel(NsGroup args)
     const int r0 = tall ? n0 : m0, c0 = tall ? m0 : n0;
     __shared__ double red[4];
     __shared__ float x[64][64 + 1];   // as the source lies
+    // thread t takes 16 elements of row t / 4, eight at a time; a tall source goes through LDS
+    const int q = t >> 2, r = r0 + q;
     double sum = g->it[i].part[t];
     static_assert(kNormBlocks == 256, "a partial sum per thread");
+    float v[2][8];
+#pragma unroll
+    for (int h = 0; h < 2; h++) {
+        const int c = c0 + 16 * (t & 3) + 8 * h;
+        if (r < rows && c + 8 <= cols) {
+            if (g->gbf16)
+                Elem<uint16_t>::load8((const uint16_t *)g->it[i].g + r * ld + c, v[h]);
+            else
+                Elem<float>::load8((const float *)g->it[i].g + r * ld + c, v[h]);
+        } else {
+#pragma unroll
+            for (int k = 0; k < 8; k++) {
+                v[h][k] = 0.0f;
+                if (r < rows && c + k < cols)
+                    v[h][k] = g->gbf16 ? Elem<uint16_t>::load((const uint16_t *)g->it[i].g + r * ld + c + k)
+                                       : ((const float *)g->it[i].g)[r * ld + c + k];
+            }
+        }
+    }
+    // the norm, while the elements are on their way
 #pragma unroll
     for (int k = 1; k < 64; k <<= 1)
         sum += __shfl_xor(sum, k, 64);
     if ((t & 63) == 0)
         red[t >> 6] = sum;
+    if (tall) {
+#pragma unroll
+        for (int h = 0; h < 2; h++)
+#pragma unroll
+            for (int k = 0; k < 8; k++)
+                x[q][16 * (t & 3) + 8 * h + k] = v[h][k];
+    }
     __syncthreads();
     const float scale = (float)((double)g->it[i].s / (sqrt(red[0] + red[1] + red[2] + red[3]) + (double)g->eps));
-    // thread t takes 16 elements of row t / 4, eight at a time; a tall source goes through LDS
-    const int q = t >> 2, r = r0 + q;
-    auto store = [&](int h, const float (&v)[8]) {
+#pragma unroll
+    for (int h = 0; h < 2; h++) {
+        if (tall) {
+#pragma unroll
+            for (int k = 0; k < 8; k++)
+                v[h][k] = x[16 * (t & 3) + 8 * h + k][q];
+        }
         const int64_t at = (int64_t)(m0 + q) * Np + n0 + 16 * (t & 3) + 8 * h;
         v8h hi, lo;
 #pragma unroll
         for (int k = 0; k < 8; k++) {
-            const float y = as_f32(v[k] * scale);
+            const float y = as_f32(v[h][k] * scale);
             hi[k] = (_Float16)y;
             lo[k] = (_Float16)as_f32(y - (float)hi[k]);
         }
         *reinterpret_cast<v8h *>(g->it[i].xh[0] + at) = hi;
         *reinterpret_cast<v8h *>(g->it[i].xl + at) = lo;
-    };
-#pragma unroll
-    for (int h = 0; h < 2; h++) {
-        const int c = c0 + 16 * (t & 3) + 8 * h;
-        float v[8];
-        if (r < rows && c + 8 <= cols) {
-            if (g->gbf16)
-                Elem<uint16_t>::load8((const uint16_t *)g->it[i].g + r * ld + c, v);
-            else
-                Elem<float>::load8((const float *)g->it[i].g + r * ld + c, v);
-        } else {
-#pragma unroll
-            for (int k = 0; k < 8; k++) {
-                v[k] = 0.0f;
-                if (r < rows && c + k < cols)
-                    v[k] = g->gbf16 ? Elem<uint16_t>::load((const uint16_t *)g->it[i].g + r * ld + c + k)
-                                    : ((const float *)g->it[i].g)[r * ld + c + k];
-            }
-        }
-        if (!tall) {
-            store(h, v);
-        } else {
-#pragma unroll
-            for (int k = 0; k < 8; k++)
-                x[q][16 * (t & 3) + 8 * h + k] = v[k];
-        }
-    }
-    if (!tall)
-        return;
-    __syncthreads();
-#pragma unroll
-    for (int h = 0; h < 2; h++) {
-        float v[8];
-#pragma unroll
-        for (int k = 0; k < 8; k++)
-            v[k] = x[16 * (t & 3) + 8 * h + k][q];
-        store(h, v);
     }
 }
 
