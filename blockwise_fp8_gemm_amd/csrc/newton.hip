@@ -345,6 +345,10 @@ template <int WM_, int WN_, int IT_, int JT_, int S_> struct NsCfg {
     static constexpr int STAGE = (TM + TN) * 128, LOADS = (TM + TN) / 8 / NW;
     static constexpr int SPAN = IT * 16;           // elements of a result row per wave
     static constexpr int TURN = SPAN * 64;         // bytes of each of a wave's two epilogue buffers
+    // the low halves go past the caches where the many tiles of the large form leave them no
+    // use there (B X of a layer's seven gradients 221 -> 216 us); one 2048 x 2048 matrix on
+    // 128 x 128 tiles keeps them (26.9, and 27.6 past the caches)
+    static constexpr bool STREAM = TM * TN == 256 * 256;
     static_assert(S * STAGE >= NW * 2 * TURN, "the epilogue's buffers take the stages' place");
 };
 // The large tile reads least from LDS per product; the smaller ones fill the GPU
@@ -535,7 +539,8 @@ __global__ __launch_bounds__(Cfg::THREADS) void ns_product_kernel(NsGroup args)
 #pragma unroll
             for (int q = 0; q < RG; q++) {
                 hi[q] = *reinterpret_cast<const v8h *>(g->it[item].xh[g->flip] + (row0 + q) * ld_out + e0);
-                lo[q] = *reinterpret_cast<const v8h *>(g->it[item].xl + (row0 + q) * ld_out + e0);
+                const v8h *xl = reinterpret_cast<const v8h *>(g->it[item].xl + (row0 + q) * ld_out + e0);
+                lo[q] = Cfg::STREAM ? __builtin_nontemporal_load(xl) : *xl;
             }
         } else if constexpr (MODE == NS_POLY) {
 #pragma unroll
@@ -586,7 +591,11 @@ __global__ __launch_bounds__(Cfg::THREADS) void ns_product_kernel(NsGroup args)
                     low[k] = (_Float16)as_f32(v[k] - (float)res[k]);
                 }
                 if (!last) {
-                    *reinterpret_cast<v8h *>(g->it[item].xl + row * ld_out + e0) = low;
+                    v8h *xl = reinterpret_cast<v8h *>(g->it[item].xl + row * ld_out + e0);
+                    if constexpr (Cfg::STREAM)
+                        __builtin_nontemporal_store(low, xl);
+                    else
+                        *xl = low;
                 } else {
                     uint32_t w[4];
 #pragma unroll
