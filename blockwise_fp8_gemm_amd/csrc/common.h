@@ -110,25 +110,6 @@ __device__ __forceinline__ uint16_t to_bf16(float f)
     return (uint16_t)(to_bf16x2(f, 0.0f) & 0xFFFFu);
 }
 
-// Streaming stores for the quantisers' codes (and the fused form's
-// activation): the writing kernel never reads them back, and the
-// non-temporal hint keeps them from displacing in the caches the inputs that
-// are still being read.  Measured on gfx950 with identical outputs: the dual
-// quantiser at 8192 x 2048 in 14.2 us instead of 17.1, at 8192 x 12288 in
-// 70.6 us instead of 89.0.  (Non-temporal loads of the inputs made it slower.)
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-__device__ __forceinline__ void store_nt(void *p, uint32_t a, uint32_t b)
-{
-    const u32x2 v = {a, b};
-    __builtin_nontemporal_store(v, reinterpret_cast<u32x2 *>(p));
-}
-__device__ __forceinline__ void store_nt(void *p, uint32_t a, uint32_t b, uint32_t c, uint32_t d)
-{
-    const u32x4 v = {a, b, c, d};
-    __builtin_nontemporal_store(v, reinterpret_cast<u32x4 *>(p));
-}
-
 // Element loads widened to FP32.
 template <typename T> struct Elem;
 template <> struct Elem<float> {

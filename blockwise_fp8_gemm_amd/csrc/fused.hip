@@ -24,6 +24,7 @@
 // each kind per token and per column.
 #include "common.h"
 #include "kernels.h"
+#include "stores.h"
 
 namespace puro {
 

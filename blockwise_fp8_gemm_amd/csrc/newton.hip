@@ -27,6 +27,7 @@
 // (and writing, every step) a transposed copy of X.
 #include "common.h"
 #include "kernels.h"
+#include "stores.h"
 
 #include <algorithm>
 #include <climits>

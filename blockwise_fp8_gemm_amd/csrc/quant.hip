@@ -16,6 +16,7 @@
 // registers across the amax reduction, and written once as a byte.
 #include "common.h"
 #include "kernels.h"
+#include "stores.h"
 
 namespace puro {
 
