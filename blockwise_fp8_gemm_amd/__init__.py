@@ -269,21 +269,24 @@ def _stream_allocs(fn):
 def _on_device(fn):
     """_stream_allocs for the calls whose first argument (a tensor, or a list of them) names the GPU: the
     call runs with that GPU current, whichever was, and refuses a stream of another one."""
-    pos = list(inspect.signature(fn).parameters).index("stream")
+    names = list(inspect.signature(fn).parameters)
+    pos = names.index("stream")
 
     @functools.wraps(fn)
-    def run(first, *args, **kw):
-        stream = args[pos - 1] if len(args) >= pos else kw.get("stream")
-        t = first if isinstance(first, torch.Tensor) else first[0] if first else None
+    def run(*args, **kw):
+        stream = args[pos] if len(args) > pos else kw.get("stream")
+        t = args[0] if args else kw.get(names[0])
+        if not isinstance(t, torch.Tensor):
+            t = t[0] if t else None
         if stream is None:
             if t is None or not t.is_cuda or t.get_device() == torch._C._cuda_getDevice():
-                return fn(first, *args, **kw)
+                return fn(*args, **kw)
             with torch.cuda.device(t.device):
-                return fn(first, *args, **kw)
+                return fn(*args, **kw)
         with _on(stream):
             if t is not None and t.is_cuda and t.get_device() != torch.cuda.current_device():
                 raise ValueError("the stream belongs to another GPU than the tensors (%s)" % t.device)
-            return fn(first, *args, **kw)
+            return fn(*args, **kw)
     return run
 
 
@@ -496,6 +499,15 @@ def _dense(t, shape, dtypes, name, device):
     return t.data_ptr() if t.numel() else 0
 
 
+def _workspace(workspace, need, device):
+    """(tensor, address, bytes) of the caller's checked workspace, or of a new one of need() bytes."""
+    if workspace is None:
+        workspace = torch.empty((need(),), dtype=_U8, device=device)
+    elif not workspace.is_cuda or workspace.device != device or not workspace.is_contiguous():
+        raise ValueError("workspace: expected a contiguous tensor on %s, got one on %s" % (device, workspace.device))
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
 def _new(rows, cols, dtype, device):
     """Uninitialised [rows][cols] whose row stride is a multiple of 16 elements."""
     return torch.empty_strided((rows, cols), (_pad16(cols), 1), dtype=dtype, device=device)
@@ -550,7 +562,8 @@ def puro_fp8_rmsnorm_quant_act(x, weight, residual=None, eps=1e-6, z=None, rstd=
     """z = bf16(x + residual) (x without one), n = z / sqrt(mean z^2 + eps) * weight, and n's 1x128 blocks
     as puro_fp8_quant_act lays them out (n is quantised in FP32, not rounded to bfloat16 first).
     x, residual: bfloat16 [tokens][cols]; weight: float32 / bfloat16 [cols].  h (given, or allocated with
-    store_h): bf16(n).  Returns (z, rstd, h or None, q, s)."""
+    store_h): bf16(n).  z may be x or residual itself (the sum in place).
+    Returns (z, rstd, h or None, q, s)."""
     ins, outs, z, rstd, h = _norm_forward(x, weight, residual, z, rstd, h, store_h)
     tokens, cols = x.shape
     q, s, qp, ldq, sp = _codes(tokens, cols, x.device, q, s)
@@ -610,12 +623,11 @@ def puro_fp8_rmsnorm_bwd_quant_dual(dy, z, rstd, weight, dres=None, transpose_ou
     q_row, s_row, *row = _codes(tokens, cols, dev, q_row, s_row)
     q_tok, s_tok, *tok = _codes(tokens, cols, dev, q_tok, s_tok, True, transpose_out)
     L = lib()
-    if workspace is None:
-        workspace = torch.empty((L.puro_fp8_rmsnorm_bwd_workspace_size(tokens, cols),), dtype=_U8, device=dev)
+    workspace, wsp, ws_bytes = _workspace(workspace, lambda: L.puro_fp8_rmsnorm_bwd_workspace_size(tokens, cols), dev)
     fn = L.puro_fp8_rmsnorm_bwd_quant_dual_pow2 if pow2 else L.puro_fp8_rmsnorm_bwd_quant_dual
     _check(fn(dyp, lddy, zp, ldz, rp, wp, PURO_BF16 if weight.dtype is _BF16 else PURO_F32, resp, ldres, tokens, cols,
-              dxp, lddx, dwp, 1 if accumulate else 0, *row, 1 if transpose_out else 0, *tok, workspace.data_ptr(),
-              workspace.numel() * workspace.element_size(), _raw_stream(stream, dev)),
+              dxp, lddx, dwp, 1 if accumulate else 0, *row, 1 if transpose_out else 0, *tok, wsp,
+              ws_bytes, _raw_stream(stream, dev)),
            "puro_fp8_rmsnorm_bwd_quant_dual")
     return dx, dw, q_row, s_row, q_tok, s_tok
 
@@ -852,11 +864,10 @@ def puro_fp8_newton_schulz_grouped(grads, steps=5, coefficients=(3.4445, -4.7750
         op, ldo = _mat(o, shape, _BF16, "outs[%d]" % i, dev)
         descs[i] = NewtonSchulzDesc(gp, shape[0], shape[1], ldg, op, ldo)
         res.append(o)
-    if workspace is None:
-        need = int(lib().puro_fp8_newton_schulz_workspace_size(descs, len(grads)))
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    L = lib()
+    workspace, wsp, ws_bytes = _workspace(workspace, lambda: L.puro_fp8_newton_schulz_workspace_size(descs, len(grads)),
+                                          dev)
     coef = (ctypes.c_float * (3 * steps))(*[v for t in triples for v in t])
-    _check(lib().puro_fp8_newton_schulz_grouped(code, descs, len(grads), steps, coef, eps, workspace.data_ptr(),
-                                                workspace.numel() * workspace.element_size(),
-                                                _raw_stream(stream, dev)), "puro_fp8_newton_schulz_grouped")
+    _check(L.puro_fp8_newton_schulz_grouped(code, descs, len(grads), steps, coef, eps, wsp, ws_bytes,
+                                            _raw_stream(stream, dev)), "puro_fp8_newton_schulz_grouped")
     return res

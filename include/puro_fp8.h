@@ -216,7 +216,8 @@ puro_status_t puro_fp8_swiglu_quant_dual(const void *gate, int64_t ldg, const vo
  *   weight  [cols], FP32 or BF16 (wdt), dense, 16-byte aligned
  *   eps     finite and > 0, else PURO_ERR_VALUE
  * The squares of a row must sum to a finite FP32 value.  The outputs must not
- * overlap each other or the inputs.
+ * overlap each other or the inputs, but z may be x or residual itself, with its
+ * row stride (the sum in place).  tokens = 0 or cols = 0 writes nothing.
  *
  * puro_fp8_rmsnorm_quant_act writes the 1x128 row blocks only (q, s as
  * puro_fp8_quant_act): the form for serving, down to single tokens; rstd may
@@ -536,7 +537,9 @@ puro_status_t puro_fp8_gemm_grouped_native(puro_layout_t layout, puro_bscale_t b
  *           [0, 1], every step has to keep |b l + c l^2| (l the squared singular
  *           values) at most 32 and the singular values at most 2, the range of
  *           the FP16 products; else PURO_ERR_VALUE
- *   eps     finite and > 0, else PURO_ERR_VALUE (a zero matrix gives zeros)
+ *   eps     finite and > 0, else PURO_ERR_VALUE (a zero matrix gives zeros, and
+ *           one whose norm is far below eps loses low bits and then elements:
+ *           X is held to 2^-24 / sqrt(max(rows, cols)) at best)
  * workspace: at least puro_fp8_newton_schulz_workspace_size(items, count) bytes
  * (0 for invalid arguments; only rows and cols are read) of device memory,
  * 256-byte aligned, not used by other work in flight.
