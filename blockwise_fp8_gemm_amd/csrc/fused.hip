@@ -18,10 +18,11 @@
 // E4M3(v / s).  Rounding to BF16 first would only add an error, and would
 // let a last-bit difference of a sum move a scale by 2^-8.
 //
-// All of them are HBM-bound.  The token blocks of one column span 128 tokens
-// and the norm's statistics a whole row, so the norm and its gradient take
-// two passes: per-row statistics, then 128 x 128 tiles that hold one block of
-// each kind per token and per column.
+// All of them are HBM-bound (a copy moves 5.1 TB/s).  The token blocks of one
+// column span 128 tokens and the norm's statistics a whole row, so the norm and
+// its gradient take two passes: whole rows, then 128 x 128 tiles that hold one
+// block of each kind per token and per column.  What the second pass reads again
+// comes partly from the caches.  Small calls are launches: 2.6 us for a row of 2048.
 #include "common.h"
 #include "kernels.h"
 #include "stores.h"
@@ -30,8 +31,11 @@ namespace puro {
 
 namespace {
 
-// A tile kernel's threads hold RT tokens x 8 columns each.
-constexpr int tile_threads(int rt) { return 16 * 128 / rt; }
+// A tile kernel's threads hold RT tokens x 8 columns each.  With two tokens and
+// 1024 threads large tensors took longer (8192 x 2048 norm 12.1 against 9.2 us,
+// its gradient 36.5 and 33.6; activation gradient of 8192 x 6144 147 and 112) and
+// small ones little less (gradient of 700 x 1100: 9.2 against 10.7).
+constexpr int RT = 4, TILE_THREADS = 16 * 128 / RT;
 
 template <int CTRL> __device__ __forceinline__ float dpp_f(float v)
 {
@@ -240,8 +244,8 @@ struct QuantOut {
 // halves the columns a lane carries on), then the waves through LDS.  The
 // column codes are turned in LDS and written out as 128-byte rows.
 // ---------------------------------------------------------------------------
-template <int RT> struct TileShared {
-    static constexpr int WAVES = tile_threads(RT) / 64;
+struct TileShared {
+    static constexpr int WAVES = TILE_THREADS / 64;
     float red[WAVES][128];
     float scl[128], rcl[128], rll[128];   // column scales, reciprocals and their low parts
     uint32_t slow[WAVES];                 // whether a wave met a scale below 2^-96
@@ -251,7 +255,7 @@ template <int RT> struct TileShared {
 // Holds the compiler to forming a tile's values here, once: left alone it
 // carries the factors of each value along and forms it again at every use,
 // which takes more registers than the values themselves and spills.
-template <int RT> __device__ __forceinline__ void pin(float (&v)[RT][8])
+__device__ __forceinline__ void pin(float (&v)[RT][8])
 {
 #pragma unroll
     for (int i = 0; i < RT; i++)
@@ -261,7 +265,7 @@ template <int RT> __device__ __forceinline__ void pin(float (&v)[RT][8])
 }
 
 // This thread's place in a tile.
-template <int RT> struct Place {
+struct Place {
     int64_t tok0, col0, tokens, cols;
     int cc, rq;
     __device__ __forceinline__ int64_t tk(int i) const { return tok0 + RT * rq + i; }
@@ -269,10 +273,9 @@ template <int RT> struct Place {
 };
 // Tiles are taken row by row (measured against eight neighbours per XCD, which
 // saves partial sectors of the row scales: 5 to 8% slower).
-template <int RT>
-__device__ __forceinline__ Place<RT> place(unsigned row, unsigned col, int64_t tokens, int64_t cols)
+__device__ __forceinline__ Place place(unsigned row, unsigned col, int64_t tokens, int64_t cols)
 {
-    return Place<RT>{(int64_t)row * 128, (int64_t)col * 128, tokens, cols, (int)threadIdx.x & 15,
+    return Place{(int64_t)row * 128, (int64_t)col * 128, tokens, cols, (int)threadIdx.x & 15,
                      (int)threadIdx.x >> 4};
 }
 
@@ -301,18 +304,12 @@ template <int I> __device__ __forceinline__ Scale row_scale(const Scale &own)
     return Scale{dpp_f<0x150 + I>(own.s), dpp_f<0x150 + I>(own.r), dpp_f<0x150 + I>(own.rl)};
 }
 
-template <bool SLOW, bool FULL, bool TR, bool ROWS, int RT>
+template <bool SLOW, bool FULL, bool TR, bool ROWS>
 __device__ __forceinline__ void tile_codes(const float (&v)[RT][8], const Scale &own, const QuantOut &ro,
-                                           const QuantOut &to, const Place<RT> &p, TileShared<RT> &sh)
+                                           const QuantOut &to, const Place &p, TileShared &sh)
 {
     if constexpr (ROWS) {
-        Scale sr[RT];
-        sr[0] = row_scale<0>(own);
-        sr[1] = row_scale<1>(own);
-        if constexpr (RT == 4) {
-            sr[2] = row_scale<2>(own);
-            sr[3] = row_scale<3>(own);
-        }
+        const Scale sr[RT] = {row_scale<0>(own), row_scale<1>(own), row_scale<2>(own), row_scale<3>(own)};
         uint8_t *qr = ro.q + p.tk(0) * ro.ldq + (FULL ? p.c0() : 0);
 #pragma unroll
         for (int i = 0; i < RT; i++) {
@@ -328,11 +325,7 @@ __device__ __forceinline__ void tile_codes(const float (&v)[RT][8], const Scale 
 #pragma unroll
     for (int j = 0; j < 8; j++) {
         const Scale c{SLOW ? sh.scl[8 * p.cc + j] : 0.0f, sh.rcl[8 * p.cc + j], sh.rll[8 * p.cc + j]};
-        if constexpr (RT == 4)
-            word[j] = codes4<SLOW>(v[0][j], v[1][j], v[2][j], v[3][j], c);
-        else
-            word[j] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(code_arg<SLOW>(v[0][j], c), code_arg<SLOW>(v[1][j], c),
-                                                                0, false);
+        word[j] = codes4<SLOW>(v[0][j], v[1][j], v[2][j], v[3][j], c);
     }
     if constexpr (!TR) {
 #pragma unroll
@@ -349,30 +342,22 @@ __device__ __forceinline__ void tile_codes(const float (&v)[RT][8], const Scale 
         return;
     }
 #pragma unroll
-    for (int j = 0; j < 8; j++) {
-        uint8_t *dst = &sh.tile[8 * p.cc + j][RT * p.rq];
-        if constexpr (RT == 4)
-            *reinterpret_cast<uint32_t *>(dst) = word[j];
-        else
-            *reinterpret_cast<uint16_t *>(dst) = (uint16_t)word[j];
-    }
+    for (int j = 0; j < 8; j++)
+        *reinterpret_cast<uint32_t *>(&sh.tile[8 * p.cc + j][RT * p.rq]) = word[j];
 }
 
-template <bool FULL, bool TR, bool ROWS, int RT>
+template <bool FULL, bool TR, bool ROWS>
 __device__ __forceinline__ void quant_tile(const float (&v)[RT][8], const QuantOut &ro, const QuantOut &to,
-                                           const Place<RT> &p, int pow2, TileShared<RT> &sh)
+                                           const Place &p, int pow2, TileShared &sh)
 {
-    constexpr int WAVES = TileShared<RT>::WAVES;
+    constexpr int WAVES = TileShared::WAVES;
     const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
     const int64_t bx = p.col0 >> 7, by = p.tok0 >> 7;
 
     float m[8];
 #pragma unroll
-    for (int j = 0; j < 8; j++) {
-        m[j] = absmax3(v[0][j], v[1][j], 0.0f);
-        if constexpr (RT == 4)
-            m[j] = absmax3(v[2][j], v[3][j], m[j]);
-    }
+    for (int j = 0; j < 8; j++)
+        m[j] = absmax3(v[2][j], v[3][j], absmax3(v[0][j], v[1][j], 0.0f));
     *reinterpret_cast<float2 *>(&sh.red[wave][8 * p.cc + first_of(lane)]) =
         cross4(m, [](float a, float b) { return absmax3(a, b, 0.0f); });
     Scale own{0.0f, 0.0f, 0.0f};
@@ -383,10 +368,7 @@ __device__ __forceinline__ void quant_tile(const float (&v)[RT][8], const QuantO
         for (int i = 0; i < RT; i++)
             a[i] = max16(absmax3(v[i][6], v[i][7], absmax3(v[i][4], v[i][5], absmax3(v[i][2], v[i][3],
                          absmax3(v[i][0], v[i][1], 0.0f)))));
-        float mine = p.cc & 1 ? a[1] : a[0];
-        if constexpr (RT == 4)
-            mine = p.cc & 2 ? (p.cc & 1 ? a[3] : a[2]) : mine;
-        own = make_scale(mine, pow2);
+        own = make_scale(p.cc & 2 ? (p.cc & 1 ? a[3] : a[2]) : (p.cc & 1 ? a[1] : a[0]), pow2);
         slow = __any(scale_slow(own.s, pow2));
         if (p.cc < RT && (FULL || p.tk(p.cc) < p.tokens))
             ro.s[p.tk(p.cc) * ro.lds + bx] = own.s;
@@ -417,15 +399,15 @@ __device__ __forceinline__ void quant_tile(const float (&v)[RT][8], const QuantO
     for (int k = 0; k < WAVES; k++)
         slow |= sh.slow[k];
     if (__builtin_amdgcn_readfirstlane(slow))
-        tile_codes<true, FULL, TR, ROWS, RT>(v, own, ro, to, p, sh);
+        tile_codes<true, FULL, TR, ROWS>(v, own, ro, to, p, sh);
     else
-        tile_codes<false, FULL, TR, ROWS, RT>(v, own, ro, to, p, sh);
+        tile_codes<false, FULL, TR, ROWS>(v, own, ro, to, p, sh);
     if (!TR)
         return;
     __syncthreads();
 #pragma unroll
-    for (int it = 0; it < 1024 / tile_threads(RT); it++) {
-        const int chunk = t + tile_threads(RT) * it;
+    for (int it = 0; it < 1024 / TILE_THREADS; it++) {
+        const int chunk = t + TILE_THREADS * it;
         const int row = chunk >> 3, seg = chunk & 7;
         const int64_t c = p.col0 + row, tk = p.tok0 + seg * 16;
         const uint32_t *src = reinterpret_cast<const uint32_t *>(&sh.tile[row][seg * 16]);
@@ -440,8 +422,8 @@ __device__ __forceinline__ void quant_tile(const float (&v)[RT][8], const QuantO
 }
 
 // RT rows x eight columns of a BF16 tensor for this thread (zeros outside).
-template <bool FULL, int RT>
-__device__ __forceinline__ void load_tile(const uint16_t *x, int64_t ldx, const Place<RT> &p, uint4 (&a)[RT])
+template <bool FULL>
+__device__ __forceinline__ void load_tile(const uint16_t *x, int64_t ldx, const Place &p, uint4 (&a)[RT])
 {
     const uint16_t *row = x + p.tk(0) * ldx;
 #pragma unroll
@@ -453,8 +435,8 @@ __device__ __forceinline__ void load_tile(const uint16_t *x, int64_t ldx, const 
     }
 }
 
-template <bool FULL, int RT>
-__device__ __forceinline__ void store_tile(uint16_t *x, int64_t ldx, const Place<RT> &p, const float (&v)[RT][8])
+template <bool FULL>
+__device__ __forceinline__ void store_tile(uint16_t *x, int64_t ldx, const Place &p, const float (&v)[RT][8])
 {
 #pragma unroll
     for (int i = 0; i < RT; i++) {
@@ -468,7 +450,7 @@ __device__ __forceinline__ void store_tile(uint16_t *x, int64_t ldx, const Place
 }
 
 // Whole tiles (uniform over the workgroup) and edge tiles are two bodies of one kernel.
-template <int RT> __device__ __forceinline__ bool full_tile(const Place<RT> &p)
+__device__ __forceinline__ bool full_tile(const Place &p)
 {
     return p.tok0 + 128 <= p.tokens && p.col0 + 128 <= p.cols;
 }
@@ -479,7 +461,8 @@ template <int RT> __device__ __forceinline__ bool full_tile(const Place<RT> &p)
 // weights in registers, and has the next row's loads in flight while it works
 // on this one; rows wider than 8 NT RUN read the rest of z a second time.  The
 // row's codes and scales are written here (all there is in the serving form): a
-// 128-column block is 16 consecutive lanes, so its amax is a DPP max.
+// 128-column block is 16 consecutive lanes, so its amax is a DPP max.  8192 x 2048
+// with a residual: 20.7 us for 118 MB, 5.7 TB/s; 1037 x 2048: 5.5 us.
 // ---------------------------------------------------------------------------
 constexpr int NT = 256;
 
@@ -604,11 +587,12 @@ __global__ __launch_bounds__(NT) void norm_row_kernel(NormIn in, uint8_t *__rest
     }
 }
 
-// Tile pass: n = z r w of a tile, quantised along the tokens.
-constexpr int NORM_RT = 4;
-template <bool FULL, bool TR, int RT>
+// Tile pass: n = z r w of a tile, formed again and quantised along the tokens
+// (8192 x 2048: 9.2 us, 51 MB).  The row pass has a row in registers and writes
+// its codes: with those written here too both passes took 36.9 us instead of 31.7.
+template <bool FULL, bool TR>
 __device__ __forceinline__ void norm_tile(const uint16_t *z, int64_t ldz, const float *rstd, const void *w, int wbf16,
-                                          const Place<RT> &p, const QuantOut &to, int pow2, TileShared<RT> &sh)
+                                          const Place &p, const QuantOut &to, int pow2, TileShared &sh)
 {
     uint4 a[RT];
     load_tile<FULL>(z, ldz, p, a);
@@ -623,26 +607,28 @@ __device__ __forceinline__ void norm_tile(const uint16_t *z, int64_t ldz, const 
             v[i][j] = v[i][j] * r * wv[j];
     }
     pin(v);
-    quant_tile<FULL, TR, false, RT>(v, QuantOut{}, to, p, pow2, sh);
+    quant_tile<FULL, TR, false>(v, QuantOut{}, to, p, pow2, sh);
 }
 
 template <bool TR>
-__global__ __launch_bounds__(tile_threads(NORM_RT)) __attribute__((amdgpu_waves_per_eu(5)))
+__global__ __launch_bounds__(TILE_THREADS) __attribute__((amdgpu_waves_per_eu(5)))
 void norm_tile_kernel(const uint16_t *__restrict__ z, int64_t ldz, const float *__restrict__ rstd,
                       const void *__restrict__ w, int wbf16, int64_t tokens, int64_t cols, QuantOut to, int pow2)
 {
-    __shared__ TileShared<NORM_RT> sh;
-    const auto p = place<NORM_RT>(blockIdx.y, blockIdx.x, tokens, cols);
+    __shared__ TileShared sh;
+    const auto p = place(blockIdx.y, blockIdx.x, tokens, cols);
     if (full_tile(p))
-        norm_tile<true, TR, NORM_RT>(z, ldz, rstd, w, wbf16, p, to, pow2, sh);
+        norm_tile<true, TR>(z, ldz, rstd, w, wbf16, p, to, pow2, sh);
     else
-        norm_tile<false, TR, NORM_RT>(z, ldz, rstd, w, wbf16, p, to, pow2, sh);
+        norm_tile<false, TR>(z, ldz, rstd, w, wbf16, p, to, pow2, sh);
 }
 
 // ---------------------------------------------------------------------------
 // Norm gradient.  Row pass, over every gridDim-th row like the norm's: c_t =
 // mean over the row of w dy z r, and this workgroup's share of dw, its rows'
-// dy z r, to part[workgroup][column] (rows of ldp, a multiple of 16).
+// dy z r, to part[workgroup][column] (rows of ldp, a multiple of 16).  8192 x
+// 2048: 14.4 us for 76 MB.  Writing dx and its row codes here as well, with a tile
+// pass for the token copy only, took 54 us for both passes against 48.
 // ---------------------------------------------------------------------------
 template <int RUN>
 __global__ __launch_bounds__(NT) void norm_bwd_row_kernel(NormBwd b, float *__restrict__ coef,
@@ -726,10 +712,11 @@ __global__ __launch_bounds__(NT) void norm_bwd_row_kernel(NormBwd b, float *__re
     }
 }
 
-// Tile pass: dx of a tile, stored as BF16 and quantised both ways.
-template <bool FULL, bool TR, int RT>
-__device__ __forceinline__ void norm_bwd_tile(const NormBwd &b, const float *coef, const Place<RT> &p,
-                                              const QuantOut &ro, const QuantOut &to, int pow2, TileShared<RT> &sh)
+// Tile pass: dx of a tile, stored as BF16 and quantised both ways (8192 x 2048:
+// 33.6 us for 182 MB, 5.4 TB/s).
+template <bool FULL, bool TR>
+__device__ __forceinline__ void norm_bwd_tile(const NormBwd &b, const float *coef, const Place &p,
+                                              const QuantOut &ro, const QuantOut &to, int pow2, TileShared &sh)
 {
     uint4 y[RT], z[RT], d[RT];
     load_tile<FULL>(b.dy, b.lddy, p, y);
@@ -758,12 +745,12 @@ __device__ __forceinline__ void norm_bwd_tile(const NormBwd &b, const float *coe
     }
     pin(v);
     store_tile<FULL>(b.dx, b.lddx, p, v);
-    quant_tile<FULL, TR, true, RT>(v, ro, to, p, pow2, sh);
+    quant_tile<FULL, TR, true>(v, ro, to, p, pow2, sh);
 }
 
 // dw = (dw +) the workgroups' shares, for 32 columns: 16 threads per column take
 // every 16th share, and their sums are added in a fixed order.
-constexpr int DW_COLS = 32, DW_ROWS = tile_threads(NORM_RT) / DW_COLS;
+constexpr int DW_COLS = 32, DW_ROWS = TILE_THREADS / DW_COLS;
 __device__ __forceinline__ void sum_dw(const float *part, int parts, int64_t ldp, int64_t cols, int64_t col0,
                                        float *dw, bool accumulate, float (*red)[DW_COLS])
 {
@@ -789,11 +776,11 @@ __device__ __forceinline__ void sum_dw(const float *part, int parts, int64_t ldp
 // 2^16 rows of tiles that 2^23 tokens have are all that a grid's second one holds.)
 __host__ __device__ inline unsigned dw_groups(int64_t cols) { return (unsigned)((cols + DW_COLS - 1) / DW_COLS); }
 template <bool TR>
-__global__ __launch_bounds__(tile_threads(NORM_RT)) __attribute__((amdgpu_waves_per_eu(4)))
+__global__ __launch_bounds__(TILE_THREADS) __attribute__((amdgpu_waves_per_eu(4)))
 void norm_bwd_tile_kernel(NormBwd b, const float *__restrict__ coef, const float *__restrict__ part, int parts,
                           int64_t ldp, QuantOut ro, QuantOut to, int pow2)
 {
-    __shared__ TileShared<NORM_RT> sh;
+    __shared__ TileShared sh;
     const unsigned sums = dw_groups(b.cols);
     if (blockIdx.x < sums) {
         sum_dw(part, parts, ldp, b.cols, (int64_t)blockIdx.x * DW_COLS, b.dw, b.accumulate,
@@ -802,11 +789,11 @@ void norm_bwd_tile_kernel(NormBwd b, const float *__restrict__ coef, const float
     }
     const unsigned tile = blockIdx.x - sums, nb = (unsigned)((b.cols + 127) >> 7);
     const unsigned row = __builtin_amdgcn_readfirstlane(tile / nb);   // formed in a vector register
-    const auto p = place<NORM_RT>(row, tile - row * nb, b.tokens, b.cols);
+    const auto p = place(row, tile - row * nb, b.tokens, b.cols);
     if (full_tile(p))
-        norm_bwd_tile<true, TR, NORM_RT>(b, coef, p, ro, to, pow2, sh);
+        norm_bwd_tile<true, TR>(b, coef, p, ro, to, pow2, sh);
     else
-        norm_bwd_tile<false, TR, NORM_RT>(b, coef, p, ro, to, pow2, sh);
+        norm_bwd_tile<false, TR>(b, coef, p, ro, to, pow2, sh);
 }
 
 // ---------------------------------------------------------------------------
@@ -817,7 +804,10 @@ void norm_bwd_tile_kernel(NormBwd b, const float *__restrict__ coef, const float
 // e is the square of 2^t, t = -|g| log2(e) / 2 (v_exp_f32 gives 0 below its
 // normal range, which the square reaches only where e underflows too); what t
 // rounds off (h + l, from the two-part constant) comes back as a factor
-// 1 + l ln 2.
+// 1 + l ln 2.  One pass over tiles; 8192 x 6144: 110 us for 540 MB, of which 510
+// are the operands and results (row scales leave as partial sectors), 4.9 TB/s.
+// The 51 vector instructions an element takes with both its quantisations fill
+// 0.6 of that time; a single tile alone on a CU takes 12 us.
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ void swiglu_grad(float dh, float g, float u, float &dg, float &du)
 {
@@ -830,10 +820,9 @@ __device__ __forceinline__ void swiglu_grad(float dh, float g, float u, float &d
     dg = (dh * u) * (sig * fmaf(g, nsig, 1.0f));
 }
 
-constexpr int SWIGLU_RT = 4;
-template <bool FULL, bool TR, int RT>
-__device__ __forceinline__ void swiglu_bwd_tile(const SwigluBwd &b, const Place<RT> &p, int pow2,
-                                                TileShared<RT> &sh)
+template <bool FULL, bool TR>
+__device__ __forceinline__ void swiglu_bwd_tile(const SwigluBwd &b, const Place &p, int pow2,
+                                                TileShared &sh)
 {
     uint4 x[RT], g[RT], u[RT];
     load_tile<FULL>(b.dh, b.lddh, p, x);
@@ -853,23 +842,23 @@ __device__ __forceinline__ void swiglu_bwd_tile(const SwigluBwd &b, const Place<
     pin(vg);
     pin(vu);
     const GradOut &dg = b.dgate, &du = b.dup;
-    quant_tile<FULL, TR, true, RT>(vg, QuantOut{dg.q_row, dg.ldq_row, dg.s_row, dg.lds_row},
+    quant_tile<FULL, TR, true>(vg, QuantOut{dg.q_row, dg.ldq_row, dg.s_row, dg.lds_row},
                      QuantOut{dg.q_tok, dg.ldq_tok, dg.s_tok, dg.lds_tok}, p, pow2, sh);
     __syncthreads();   // the LDS tile of one gradient is read out before the other's is built
-    quant_tile<FULL, TR, true, RT>(vu, QuantOut{du.q_row, du.ldq_row, du.s_row, du.lds_row},
+    quant_tile<FULL, TR, true>(vu, QuantOut{du.q_row, du.ldq_row, du.s_row, du.lds_row},
                      QuantOut{du.q_tok, du.ldq_tok, du.s_tok, du.lds_tok}, p, pow2, sh);
 }
 
 template <bool TR>
-__global__ __launch_bounds__(tile_threads(SWIGLU_RT)) __attribute__((amdgpu_waves_per_eu(4)))
+__global__ __launch_bounds__(TILE_THREADS) __attribute__((amdgpu_waves_per_eu(4)))
 void swiglu_bwd_kernel(SwigluBwd b, int pow2)
 {
-    __shared__ TileShared<SWIGLU_RT> sh;
-    const auto p = place<SWIGLU_RT>(blockIdx.y, blockIdx.x, b.tokens, b.cols);
+    __shared__ TileShared sh;
+    const auto p = place(blockIdx.y, blockIdx.x, b.tokens, b.cols);
     if (full_tile(p))
-        swiglu_bwd_tile<true, TR, SWIGLU_RT>(b, p, pow2, sh);
+        swiglu_bwd_tile<true, TR>(b, p, pow2, sh);
     else
-        swiglu_bwd_tile<false, TR, SWIGLU_RT>(b, p, pow2, sh);
+        swiglu_bwd_tile<false, TR>(b, p, pow2, sh);
 }
 
 dim3 tile_grid(int64_t tokens, int64_t cols)
@@ -884,8 +873,9 @@ dim3 tile_grid(int64_t tokens, int64_t cols)
 static hipError_t launch_norm_rows(const NormIn &in, uint8_t *q, int64_t ldq, float *s, bool pow2, bool keep_z,
                                    hipStream_t st)
 {
-    // registers for rows of 2048, 4096 and 8192 columns; two rows or more per workgroup where
-    // there are many (8192 x 2048: 22.9 us, against 25.2 with a workgroup per row)
+    // registers for rows of 2048, 4096 and 8192 columns; two rows or more per workgroup where there
+    // are many: up to 4096 workgroups of the narrow form (8192 x 2048: 21.2 us, 23.8 with 2048, 23.3
+    // with 8192), up to 2048 of the others (8192 x 6144: 72.8 us, 84.8 with 1024, 77.6 with 8192)
     auto *kernel = in.cols <= 8 * NT ? norm_row_kernel<1> : in.cols <= 16 * NT ? norm_row_kernel<2> : norm_row_kernel<4>;
     const int64_t most = in.cols <= 8 * NT ? 4096 : 2048;
     hipLaunchKernelGGL(kernel, dim3((unsigned)(in.tokens < most ? in.tokens : most)), dim3(NT), 0, st, in, q, ldq, s,
@@ -907,7 +897,7 @@ hipError_t launch_norm_dual(const NormIn &in, uint8_t *qr, int64_t ldqr, float *
         return e;
     const QuantOut to{qt, ldqt, stok, transpose_out ? ntb : in.cols};
     hipLaunchKernelGGL((transpose_out ? norm_tile_kernel<true> : norm_tile_kernel<false>),
-                       tile_grid(in.tokens, in.cols), dim3(tile_threads(NORM_RT)), 0, st,
+                       tile_grid(in.tokens, in.cols), dim3(TILE_THREADS), 0, st,
                        in.res ? in.z : in.x, in.res ? in.ldz : in.ldx, in.rstd, in.w, (int)in.wbf16, in.tokens, in.cols,
                        to, (int)pow2);
     return hipGetLastError();
@@ -915,20 +905,30 @@ hipError_t launch_norm_dual(const NormIn &in, uint8_t *qr, int64_t ldqr, float *
 
 static size_t coef_bytes(int64_t tokens) { return ((size_t)tokens * 4 + 255) / 256 * 256; }
 
-// Workgroups of the gradient's row pass: two rows each or more, at most 1024, so
-// that their shares of dw stay small beside the rows they read.
-static int64_t bwd_groups(int64_t tokens) { return tokens < 2048 ? (tokens + 1) / 2 : 1024; }
+// Workgroups of the gradient's row pass: two rows each or more, so that their
+// shares of dw stay small beside the rows they read, up to 512, two on every CU
+// (2048 x 2048, both passes: 16.4 us, 18.1 with 1024; 8192 x 6144: 142 us,
+// 147 with 1024 and 150 with 384).  Rows of up to 2048 columns leave registers for
+// more workgroups on a CU: up to 1024 where each then has four rows (8192 x 2048:
+// 47.3 us, and 49.5 with 512).
+static int64_t bwd_groups(int64_t tokens, int64_t cols)
+{
+    int64_t most = 512;
+    if (cols <= 8 * NT && tokens > 4 * most)
+        most = tokens < 4 * 1024 ? (tokens + 3) / 4 : 1024;
+    return (tokens + 1) / 2 < most ? (tokens + 1) / 2 : most;
+}
 static int64_t bwd_part_ld(int64_t cols) { return (cols + 15) / 16 * 16; }
 
 size_t norm_bwd_workspace_bytes(int64_t tokens, int64_t cols)
 {
-    return coef_bytes(tokens) + (size_t)bwd_groups(tokens) * (size_t)bwd_part_ld(cols) * 4;
+    return coef_bytes(tokens) + (size_t)bwd_groups(tokens, cols) * (size_t)bwd_part_ld(cols) * 4;
 }
 
 hipError_t launch_norm_bwd(const NormBwd &b, uint8_t *qr, int64_t ldqr, float *sr, bool transpose_out, uint8_t *qt,
                            int64_t ldqt, float *stok, bool pow2, void *workspace, hipStream_t st)
 {
-    const int64_t nb = (b.cols + 127) / 128, ntb = (b.tokens + 127) / 128, groups = bwd_groups(b.tokens);
+    const int64_t nb = (b.cols + 127) / 128, ntb = (b.tokens + 127) / 128, groups = bwd_groups(b.tokens, b.cols);
     const int64_t ldp = bwd_part_ld(b.cols);
     float *coef = (float *)workspace;
     float *part = (float *)((char *)workspace + coef_bytes(b.tokens));
@@ -943,7 +943,7 @@ hipError_t launch_norm_bwd(const NormBwd &b, uint8_t *qr, int64_t ldqr, float *s
     }
     const QuantOut ro{qr, ldqr, sr, nb}, to{qt, ldqt, stok, transpose_out ? ntb : b.cols};
     hipLaunchKernelGGL((transpose_out ? norm_bwd_tile_kernel<true> : norm_bwd_tile_kernel<false>),
-                       dim3(dw_groups(b.cols) + (unsigned)(nb * ntb)), dim3(tile_threads(NORM_RT)), 0,
+                       dim3(dw_groups(b.cols) + (unsigned)(nb * ntb)), dim3(TILE_THREADS), 0,
                        st, b, coef, part, (int)groups, ldp, ro, to, (int)pow2);
     return hipGetLastError();
 }
@@ -951,7 +951,7 @@ hipError_t launch_norm_bwd(const NormBwd &b, uint8_t *qr, int64_t ldqr, float *s
 hipError_t launch_swiglu_bwd(const SwigluBwd &b, bool transpose_out, bool pow2, hipStream_t st)
 {
     hipLaunchKernelGGL((transpose_out ? swiglu_bwd_kernel<true> : swiglu_bwd_kernel<false>),
-                       tile_grid(b.tokens, b.cols), dim3(tile_threads(SWIGLU_RT)), 0, st, b, (int)pow2);
+                       tile_grid(b.tokens, b.cols), dim3(TILE_THREADS), 0, st, b, (int)pow2);
     return hipGetLastError();
 }
 
