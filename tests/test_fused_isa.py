@@ -40,7 +40,8 @@ def test_m0_only_feeds_the_copies(asm):
         if not re.search(r"\bm0\b", line):
             continue
         assert re.match(r"\s*s_mov_b32 m0, s\d+\s*$", line), ("M0 used outside the LDS copies", i, line)
-        assert "global_load_lds_dwordx4" in code[i + 1], ("M0 write not followed by its copy", i, code[i + 1])
+        assert re.match(r"\s*s_nop 0\s*$", code[i + 1]), ("no wait state between M0 and its copy", i, code[i + 1])
+        assert "global_load_lds_dwordx4" in code[i + 2], ("M0 write not followed by its copy", i, code[i + 2])
         writes += 1
     assert writes > 0
     banned = re.compile(r"movrel|set_gpr_idx|s_sendmsg|ds_gws|ds_append|ds_consume|v_interp|lds_direct|ds_ordered")
