@@ -347,8 +347,11 @@ template <int WM_, int WN_, int IT_, int JT_, int S_> struct NsCfg {
 };
 // The large tile reads least from LDS per product; the smaller ones fill the GPU
 // where there are few tiles or some are deep, and have LDS left for a third and
-// fourth stage.  Eight waves (two per SIMD) on the three large ones: with four a
-// product took a fifth to a third longer.
+// fourth stage.  Eight waves (two per SIMD) on the three large ones: with four the
+// two smaller of them took a fifth to a third longer; four waves of 128 x 128 on the
+// largest run their K loop at the matrix cores' rate (0.94 us a block instead of
+// 1.00), but alone on their SIMDs lose more in the epilogue (A A of a layer's
+// gradients 59 us instead of 54).
 typedef NsCfg<2, 4, 8, 4, 2> NsL;   // 256 x 256
 typedef NsCfg<4, 2, 4, 4, 3> NsM;   // 256 x 128
 typedef NsCfg<2, 4, 4, 2, 4> NsQ;   // 128 x 128
@@ -767,10 +770,12 @@ template <class Cfg, int MODE> hipError_t launch_tiles(NsGroup &g, hipStream_t s
 }
 
 // One product of every matrix, the deepest first: their tiles take longest.
-// The block times are measured, with 256 x 256, 256 x 128, 128 x 128 and 64 x 64
-// tiles: X X^T of one 2048 x 2048 matrix 48, 31, 21 and 25 us, of one 1024 x 4096
-// 30 and 17 (the last two), of one 256 x 1024 11 and 7; a layer's seven gradients
-// X X^T 139 to 151, 124 and 133 us, B X 215, 269 and 312.
+// The block times are measured on a busy GPU; what they choose is the fastest of
+// the four in all of these (us, with 256 x 256, 256 x 128, 128 x 128 and 64 x 64
+// tiles): X X^T of one 1024 x 1024 matrix 28, 17, 11 and 8, one 1024 x 4096 74, 43,
+// 25 and 16, one 2048 x 2048 44, 26, 19 and 24, two of them 45, 29, 37 and 40, a
+// layer's seven gradients 147, 117, 129 and 210; B X of one 2048 x 2048 51, 33, 26
+// and 35, two of them 55, 42, 47 and 62, a layer's 205, 252, 283 and 381.
 template <int MODE> hipError_t launch_product(NsGroup &g, hipStream_t st)
 {
     std::stable_sort(g.it, g.it + g.count,
