@@ -54,7 +54,7 @@ struct alignas(128) NsItem {
     int Mp, Np;    // padded to whole tiles; the padding holds zeros
     int tall;
     float s;       // X is held times s
-    uint16_t *xh[2], *xl;   // [Mp][Np]; hi is read from one and written to the other
+    uint16_t *xh[2], *xl;   // [Mp][Np]; hi is read from the first and written to the second
     uint16_t *a, *b;        // [Mp][Mp]
     float *d;               // [Mp] diagonal of B
     double *part;           // [kNormBlocks]
@@ -66,7 +66,6 @@ struct NsGroup {
     int first[kNsGroupMax + 1];   // workgroups of item i: [first[i], first[i+1]); past the last item, INT_MAX
     int count;
     int gbf16;
-    int flip;                     // which xh is read
     int last;                     // the step whose result is the output
     float a, b, c, eps;
     NsItem it[kNsGroupMax];
@@ -106,6 +105,20 @@ __device__ __forceinline__ float as_f32(float f)
     asm("" : "+v"(f));
     return f;
 }
+
+// Values of the arguments, fetched together and kept: left alone the compiler
+// loads each where it is used, and waits for it there (three small matrices 92
+// against 88 us, B X of a layer's gradients 213 against 211).
+template <typename T> __device__ __forceinline__ void keep(T *&p)
+{
+    uint64_t v = (uint64_t)p;
+    asm volatile("" : "+s"(v));
+    p = (T *)(__attribute__((address_space(1))) T *)v;
+}
+__device__ __forceinline__ void keep(int &v) { asm volatile("" : "+s"(v)); }
+__device__ __forceinline__ void keep(int64_t &v) { asm volatile("" : "+s"(v)); }
+__device__ __forceinline__ void keep(float &v) { asm volatile("" : "+s"(v)); }
+template <typename... T> __device__ __forceinline__ void keep_all(T &...v) { (keep(v), ...); }
 
 // ---------------------------------------------------------------------------
 // |G|_F^2 in 64 bits: kNormBlocks partial sums per matrix.  A wave takes a row
@@ -365,13 +378,11 @@ enum { NS_GRAM = 0, NS_POLY = 1, NS_UPDATE = 2 };
 // through its L2, and every XCD has its share of every matrix.
 __device__ __forceinline__ int xcd_local(int b, int first, int end)
 {
-    // workgroups of [0, n) on XCD y
-    auto on = [](int n, int y) { return (n - y + 7) >> 3; };
     const int x = b & 7;
-    int start = 0;
-    for (int y = 0; y < x; y++)
-        start += on(end, y) - on(first, y);
-    return start + on(b, x) - on(first, x);
+    // workgroups of [0, n) on the XCDs before x, and on x itself
+    auto before = [x](int n) { return (n >> 3) * x + min(n & 7, x); };
+    auto on = [x](int n) { return (n - x + 7) >> 3; };
+    return before(end) - before(first) + on(b) - on(first);
 }
 
 // Eight 16-bit values to row[c0 ..], those before cols.
@@ -411,15 +422,27 @@ __global__ __launch_bounds__(Cfg::THREADS) void ns_product_kernel(NsGroup args)
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave / Cfg::WN, wn = wave % Cfg::WN;
-    const int Mp = g->it[item].Mp, Np = g->it[item].Np;
+    int Mp = g->it[item].Mp, Np = g->it[item].Np, M = g->it[item].M, N = g->it[item].N, tall = g->it[item].tall;
+    int last = g->last;
+    int64_t ldo = g->it[item].ldo;
+    float s = g->it[item].s, ga = g->a, gb = g->b, gc = g->c;
+    uint16_t *xin = g->it[item].xh[0], *xout = g->it[item].xh[1], *xlow = g->it[item].xl, *ma = g->it[item].a,
+             *mb = g->it[item].b, *result = (uint16_t *)g->it[item].o;
+    float *diag = g->it[item].d;
+    if constexpr (MODE == NS_GRAM)
+        keep_all(Mp, Np, s, xin, ma);
+    else if constexpr (MODE == NS_POLY)
+        keep_all(Mp, gb, gc, ma, mb, diag);
+    else
+        keep_all(Mp, Np, M, N, tall, last, ldo, s, ga, xin, xout, xlow, mb, result, diag);
 
     // operands and the tile's place: P along the tile's rows, Q along its columns
     const uint8_t *P, *Q;
     int K, tr, tc;
     if constexpr (MODE == NS_UPDATE) {
         // the result's transpose: rows are X's columns (X [Mp][Np]), columns X's rows (B [Mp][Mp])
-        P = (const uint8_t *)g->it[item].xh[g->flip];
-        Q = (const uint8_t *)g->it[item].b;
+        P = (const uint8_t *)xin;
+        Q = (const uint8_t *)mb;
         K = Mp;
         // strips of four tile columns, so that an XCD's run of tiles is nearly square and reads few
         // panels of both (a layer's gradients: 656 MB fetched instead of 801, 210 us instead of 212)
@@ -427,7 +450,7 @@ __global__ __launch_bounds__(Cfg::THREADS) void ns_product_kernel(NsGroup args)
         tr = (local - 4 * R * strip) / w;
         tc = 4 * strip + (local - 4 * R * strip) % w;
     } else {
-        P = Q = (const uint8_t *)(MODE == NS_GRAM ? g->it[item].xh[g->flip] : g->it[item].a);
+        P = Q = (const uint8_t *)(MODE == NS_GRAM ? xin : ma);
         K = MODE == NS_GRAM ? Np : Mp;
         // tiles that reach the diagonal or lie above it, row by row of tiles
         tr = 0;
@@ -554,9 +577,8 @@ __global__ __launch_bounds__(Cfg::THREADS) void ns_product_kernel(NsGroup args)
     const int rl = lane % LR, rg = lane / LR;                      // element group and row group
     const int e0 = m0 + wm * SPAN + 8 * rl;                        // first element of this lane
     const float inv = 1.0f / kScaleA;
-    const int last = MODE == NS_UPDATE ? g->last : 0, tall = g->it[item].tall;
     const int64_t ld_out = MODE == NS_UPDATE ? Np : Mp;
-    const float unscale = 1.0f / g->it[item].s;
+    const float unscale = 1.0f / s;
     const bool mirror = MODE == NS_UPDATE ? last && tall : tc >= (tr + 1) * (TM / TN);
 #pragma unroll
     for (int j = 0; j < JT; j++) {
@@ -565,14 +587,14 @@ __global__ __launch_bounds__(Cfg::THREADS) void ns_product_kernel(NsGroup args)
         if constexpr (MODE == NS_UPDATE) {
 #pragma unroll
             for (int q = 0; q < RG; q++) {
-                hi[q] = *reinterpret_cast<const v8h *>(g->it[item].xh[g->flip] + (row0 + q) * ld_out + e0);
-                const v8h *xl = reinterpret_cast<const v8h *>(g->it[item].xl + (row0 + q) * ld_out + e0);
+                hi[q] = *reinterpret_cast<const v8h *>(xin + (row0 + q) * ld_out + e0);
+                const v8h *xl = reinterpret_cast<const v8h *>(xlow + (row0 + q) * ld_out + e0);
                 lo[q] = Cfg::STREAM ? __builtin_nontemporal_load(xl) : *xl;
             }
         } else if constexpr (MODE == NS_POLY) {
 #pragma unroll
             for (int q = 0; q < RG; q++)
-                hi[q] = *reinterpret_cast<const v8h *>(g->it[item].a + (row0 + q) * ld_out + e0);
+                hi[q] = *reinterpret_cast<const v8h *>(ma + (row0 + q) * ld_out + e0);
         }
 #pragma unroll
         for (int i = 0; i < IT; i++) {
@@ -603,13 +625,13 @@ __global__ __launch_bounds__(Cfg::THREADS) void ns_product_kernel(NsGroup args)
             } else if constexpr (MODE == NS_POLY) {
 #pragma unroll
                 for (int k = 0; k < 8; k++) {
-                    const float y = as_f32(fmaf(g->b, (float)hi[q][k], g->c * inv * v[k]));
+                    const float y = as_f32(fmaf(gb, (float)hi[q][k], gc * inv * v[k]));
                     if (e0 + k == row)
-                        g->it[item].d[row] = y;
+                        diag[row] = y;
                     res[k] = (_Float16)(e0 + k == row ? 0.0f : y);
                 }
             } else {
-                const float f = fmaf(g->it[item].d[row], inv, g->a);
+                const float f = fmaf(diag[row], inv, ga);
                 v8h low;
 #pragma unroll
                 for (int k = 0; k < 8; k++) {
@@ -618,7 +640,7 @@ __global__ __launch_bounds__(Cfg::THREADS) void ns_product_kernel(NsGroup args)
                     low[k] = (_Float16)as_f32(v[k] - (float)res[k]);
                 }
                 if (!last) {
-                    v8h *xl = reinterpret_cast<v8h *>(g->it[item].xl + row * ld_out + e0);
+                    v8h *xl = reinterpret_cast<v8h *>(xlow + row * ld_out + e0);
                     if constexpr (Cfg::STREAM)
                         __builtin_nontemporal_store(low, xl);
                     else
@@ -628,14 +650,13 @@ __global__ __launch_bounds__(Cfg::THREADS) void ns_product_kernel(NsGroup args)
 #pragma unroll
                     for (int k = 0; k < 4; k++)
                         w[k] = to_bf16x2(v[2 * k] * unscale, v[2 * k + 1] * unscale);
-                    if (!tall && row < g->it[item].M)
-                        store_run((uint16_t *)g->it[item].o + row * g->it[item].ldo, e0, g->it[item].N, w);
+                    if (!tall && row < M)
+                        store_run(result + row * ldo, e0, N, w);
                     res = __builtin_bit_cast(v8h, make_uint4(w[0], w[1], w[2], w[3]));
                 }
             }
             if (MODE != NS_UPDATE || !last) {
-                uint16_t *to = MODE == NS_GRAM ? g->it[item].a : MODE == NS_POLY ? g->it[item].b
-                                                                                 : g->it[item].xh[g->flip ^ 1];
+                uint16_t *to = MODE == NS_GRAM ? ma : MODE == NS_POLY ? mb : xout;
                 *reinterpret_cast<v8h *>(to + row * ld_out + e0) = res;
             }
             const uint4 bits = __builtin_bit_cast(uint4, res);
@@ -670,10 +691,10 @@ __global__ __launch_bounds__(Cfg::THREADS) void ns_product_kernel(NsGroup args)
             const uint4 w = *reinterpret_cast<const uint4 *>(turn + place * 64 + ((16 * c) ^ ((place & 1) << 5)));
             if constexpr (MODE == NS_UPDATE) {
                 const uint32_t o[4] = {w.x, w.y, w.z, w.w};
-                if (row < g->it[item].N)
-                    store_run((uint16_t *)g->it[item].o + row * g->it[item].ldo, col, g->it[item].M, o);
+                if (row < N)
+                    store_run(result + row * ldo, col, M, o);
             } else {
-                *reinterpret_cast<uint4 *>((MODE == NS_GRAM ? g->it[item].a : g->it[item].b) + (int64_t)row * Mp + col) = w;
+                *reinterpret_cast<uint4 *>((MODE == NS_GRAM ? ma : mb) + (int64_t)row * Mp + col) = w;
             }
         }
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
@@ -826,7 +847,6 @@ hipError_t launch_newton(const NsMatrix *ms, int count, bool gbf16, int steps, c
         g.count = std::min(count - lo, kNsGroupMax);
         g.gbf16 = gbf16;
         g.eps = eps;
-        g.flip = 0;
         size_t off = 0;
         for (int i = 0; i < g.count; i++) {
             g.it[i] = make_item(ms[lo + i]);
@@ -845,7 +865,8 @@ hipError_t launch_newton(const NsMatrix *ms, int count, bool gbf16, int steps, c
             g.c = coef[3 * k + 2];
             g.last = k + 1 == steps;
             e = launch_step(g, st);
-            g.flip ^= 1;
+            for (int i = 0; i < g.count; i++)
+                std::swap(g.it[i].xh[0], g.it[i].xh[1]);
         }
         if (e != hipSuccess)
             return e;
