@@ -509,8 +509,10 @@ def _workspace(workspace, need, device):
 
 
 def _new(rows, cols, dtype, device):
-    """Uninitialised [rows][cols] whose row stride is a multiple of 16 elements."""
-    return torch.empty_strided((rows, cols), (_pad16(cols), 1), dtype=dtype, device=device)
+    """Uninitialised [rows][cols] whose row stride is a multiple of 16 elements, its address and that stride."""
+    ld = _pad16(cols)
+    t = torch.empty_strided((rows, cols), (ld, 1), dtype=dtype, device=device)
+    return t, t.data_ptr(), ld
 
 
 def _codes(tokens, cols, device, q, s, tok=False, transpose_out=True):
@@ -523,12 +525,13 @@ def _codes(tokens, cols, device, q, s, tok=False, transpose_out=True):
     else:
         qs, ss = (tokens, cols), (_nblk(tokens), cols)
     if q is None:
-        q = _new(qs[0], qs[1], _U8, device)
+        q, qp, ld = _new(qs[0], qs[1], _U8, device)
+    else:
+        qp, ld = _mat(q, qs, _U8, "q_tok" if tok else "q", device)
     if s is None:
         s = torch.empty(ss, dtype=_F32, device=device)
-    name = ("q_tok", "s_tok") if tok else ("q", "s")
-    qp, ld = _mat(q, qs, _U8, name[0], device)
-    return q, s, qp, ld, _dense(s, ss, (_F32,), name[1], device)
+        return q, s, qp, ld, s.data_ptr()
+    return q, s, qp, ld, _dense(s, ss, (_F32,), "s_tok" if tok else "s", device)
 
 
 def _norm_forward(x, weight, residual, z, rstd, h, store_h):
@@ -540,19 +543,26 @@ def _norm_forward(x, weight, residual, z, rstd, h, store_h):
     tokens, cols = shape
     xp, ldx = _mat(x, shape, _BF16, "x", dev)
     wp = _dense(weight, (cols,), (_F32, _BF16), "weight", dev)
-    if residual is not None:
-        if z is None:
-            z = _new(tokens, cols, _BF16, dev)
-    elif z is not None:
-        raise ValueError("z is written with a residual only (without one it is x)")
+    resp, ldres = _opt_mat(residual, shape, _BF16, "residual", dev)
+    if residual is None:
+        if z is not None:
+            raise ValueError("z is written with a residual only (without one it is x)")
+        zp, ldz = 0, 0
+    elif z is None:
+        z, zp, ldz = _new(tokens, cols, _BF16, dev)
+    else:
+        zp, ldz = _mat(z, shape, _BF16, "z", dev)
     if rstd is None:
         rstd = torch.empty((tokens,), dtype=_F32, device=dev)
+        rp = rstd.data_ptr()
+    else:
+        rp = _dense(rstd, (tokens,), (_F32,), "rstd", dev)
     if store_h and h is None:
-        h = _new(tokens, cols, _BF16, dev)
-    ins = (xp, ldx, *_opt_mat(residual, shape, _BF16, "residual", dev), wp,
-           PURO_BF16 if weight.dtype is _BF16 else PURO_F32)
-    outs = (*_opt_mat(z, shape, _BF16, "z", dev), _dense(rstd, (tokens,), (_F32,), "rstd", dev),
-            *_opt_mat(h, shape, _BF16, "h", dev))
+        h, hp, ldh = _new(tokens, cols, _BF16, dev)
+    else:
+        hp, ldh = _opt_mat(h, shape, _BF16, "h", dev)
+    ins = (xp, ldx, resp, ldres, wp, PURO_BF16 if weight.dtype is _BF16 else PURO_F32)
+    outs = (zp, ldz, rp, hp, ldh)
     return ins, outs, (x if residual is None else z), rstd, h
 
 
@@ -613,13 +623,16 @@ def puro_fp8_rmsnorm_bwd_quant_dual(dy, z, rstd, weight, dres=None, transpose_ou
     wp = _dense(weight, (cols,), (_F32, _BF16), "weight", dev)
     resp, ldres = _opt_mat(dres, shape, _BF16, "dres", dev)
     if dx is None:
-        dx = _new(tokens, cols, _BF16, dev)
-    dxp, lddx = _mat(dx, shape, _BF16, "dx", dev)
+        dx, dxp, lddx = _new(tokens, cols, _BF16, dev)
+    else:
+        dxp, lddx = _mat(dx, shape, _BF16, "dx", dev)
     if dw is None:
         if accumulate:
             raise ValueError("accumulate needs dw")
         dw = torch.empty((cols,), dtype=_F32, device=dev)
-    dwp = _dense(dw, (cols,), (_F32,), "dw", dev)
+        dwp = dw.data_ptr()
+    else:
+        dwp = _dense(dw, (cols,), (_F32,), "dw", dev)
     q_row, s_row, *row = _codes(tokens, cols, dev, q_row, s_row)
     q_tok, s_tok, *tok = _codes(tokens, cols, dev, q_tok, s_tok, True, transpose_out)
     L = lib()
@@ -858,10 +871,11 @@ def puro_fp8_newton_schulz_grouped(grads, steps=5, coefficients=(3.4445, -4.7750
         shape = g.shape
         if len(shape) != 2:
             raise ValueError("grads[%d]: expected a 2-D tensor, got shape %s" % (i, tuple(shape)))
-        if o is None:
-            o = _new(shape[0], shape[1], _BF16, dev)
         gp, ldg = _mat(g, shape, dtype, "grads[%d]" % i, dev)
-        op, ldo = _mat(o, shape, _BF16, "outs[%d]" % i, dev)
+        if o is None:
+            o, op, ldo = _new(shape[0], shape[1], _BF16, dev)
+        else:
+            op, ldo = _mat(o, shape, _BF16, "outs[%d]" % i, dev)
         descs[i] = NewtonSchulzDesc(gp, shape[0], shape[1], ldg, op, ldo)
         res.append(o)
     L = lib()
