@@ -13,12 +13,22 @@ typedef float v4f __attribute__((ext_vector_type(4)));
 // Four floats -> four E4M3 codes packed little-endian into one dword.
 // v_cvt_pk_fp8_f32 rounds to nearest even into the OCP E4M3 format; it was
 // checked on gfx950 against an integer-only round-to-nearest-even,
-// saturating encoder for every FP32 value with |y| <= 449, which covers every
-// quotient x/s the quantisers form (|x/s| <= 448 * (1 + 2^-23)).
+// saturating encoder for every FP32 value with |y| <= 449; it does not saturate
+// itself (from 464 on it gives NaN).  A normal scale s = amax / 448 bounds the
+// quotients |x / s| by 448 (1 + 2^-23), and so do power-of-two scales; a BF16
+// block's scale is at least 146 units of 2^-149, so they reach 448.9.  Blocks of
+// FP32 values have scales down to one unit, and quotients up to 671: those go
+// through saturate() first.
 __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d)
 {
     uint32_t lo = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
     return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, (int)lo, true);
+}
+
+// y limited to +-448; NaN stays NaN.
+__device__ __forceinline__ float saturate(float y)
+{
+    return fabsf(y) > 448.0f ? __builtin_copysignf(448.0f, y) : y;
 }
 
 // Code of +-0 by the sign of x: 0x80 for negative values and -0.

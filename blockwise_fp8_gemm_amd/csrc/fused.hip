@@ -77,8 +77,10 @@ __device__ __forceinline__ float absmax3(float a, float b, float m)
 // correction step from 1/448's FP32 value, exact as IEEE division while the
 // residual does not underflow.  r = 0 for a zero scale (codes +-0 by sign).  A
 // scale below 2^-96, whose reciprocal could overflow, has that of s 2^64 and
-// its values are multiplied by 2^64 first (exact: they are at most 448 s),
-// which SLOW selects for a whole tile or run.
+// its values are multiplied by 2^64 first (exact: they are at most 671 s, see
+// below), which SLOW selects for a whole tile or run.  There a subnormal scale of
+// few bits can lie a third below amax / 448 (amax = 671 x 2^-149 has the scale
+// 2^-149), so the quotient is limited to +-448 before the cast.
 struct Scale {
     float s, r, rl;
 };
@@ -113,7 +115,8 @@ template <bool SLOW> __device__ __forceinline__ float code_arg(float v, const Sc
 {
     if (SLOW)
         v = scale_tiny(c.s) ? v * 0x1p64f : v;
-    return fmaf(v, c.r, v * c.rl);
+    const float y = fmaf(v, c.r, v * c.rl);
+    return SLOW ? saturate(y) : y;
 }
 
 template <bool SLOW> __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d, const Scale &s)
