@@ -17,8 +17,8 @@ typedef float v4f __attribute__((ext_vector_type(4)));
 // itself (from 464 on it gives NaN).  A normal scale s = amax / 448 bounds the
 // quotients |x / s| by 448 (1 + 2^-23), and so do power-of-two scales; a BF16
 // block's scale is at least 146 units of 2^-149, so they reach 448.9.  Blocks of
-// FP32 values have scales down to one unit, and quotients up to 671: those go
-// through saturate() first.
+// FP32 values have scales down to one unit, and quotients up to 671: below their
+// forms for ordinary scales the kernels limit the quotient with saturate().
 __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d)
 {
     uint32_t lo = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
@@ -63,7 +63,7 @@ __device__ __forceinline__ Divider make_divider(float s)
 __device__ __forceinline__ float quotient(const Divider &d, float x)
 {
     if (!d.fast)
-        return x / d.s;
+        return saturate(x / d.s);
     const float y0 = x * d.r;
     const float e = fmaf(-y0, d.s, x);
     return __builtin_copysignf(fmaf(e, d.r, y0), x);
