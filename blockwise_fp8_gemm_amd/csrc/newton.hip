@@ -231,7 +231,12 @@ __global__ __launch_bounds__(256) void ns_init_kernel(NsGroup args)
                 x[q][16 * (t & 3) + 8 * h + k] = v[h][k];
     }
     __syncthreads();
-    const float scale = (float)((double)g->it[i].s / (sqrt(red[0] + red[1] + red[2] + red[3]) + (double)g->eps));
+    // s / (|G| + eps) lies between 2^-142 and 2^156, past what one FP32 number holds at both ends:
+    // two factors, a power of two (exact: it brings no element past s, and what it takes below FP32's
+    // normal range is far below the last bit of lo) and a number of that size's square root
+    int e;
+    const double m = frexp((double)g->it[i].s / (sqrt(red[0] + red[1] + red[2] + red[3]) + (double)g->eps), &e);
+    const float shift = ldexpf(1.0f, e / 2), scale = ldexpf((float)m, e - e / 2);
 #pragma unroll
     for (int h = 0; h < 2; h++) {
         if (tall) {
@@ -243,7 +248,7 @@ __global__ __launch_bounds__(256) void ns_init_kernel(NsGroup args)
         v8h hi, lo;
 #pragma unroll
         for (int k = 0; k < 8; k++) {
-            const float y = as_f32(v[h][k] * scale);
+            const float y = as_f32(v[h][k] * shift * scale);
             hi[k] = (_Float16)y;
             lo[k] = (_Float16)as_f32(y - (float)hi[k]);
         }
