@@ -870,18 +870,16 @@ static bool newton_in_range(int steps, const float *coef)
         auto f = [&](double s) { return std::fabs(s * (a + s * s * (b + c * s * s))); };
         auto p = [&](double l) { return std::fabs(l * (b + c * l)); };
         double most = f(top), widest = p(top * top);
-        if (c != 0.0) {
-            const double turn = -b / (2.0 * c);
-            if (turn > 0.0 && turn < top * top)
-                widest = std::fmax(widest, p(turn));
-            const double disc = 9.0 * b * b - 20.0 * a * c;   // a + 3 b l + 5 c l^2 = 0
-            for (int sign = -1; sign <= 1 && disc >= 0.0; sign += 2) {
-                const double l = (-3.0 * b + sign * std::sqrt(disc)) / (10.0 * c);
+        const double turn = -b / (2.0 * c);   // of b l + c l^2 (infinite or NaN for c = 0: none)
+        if (turn > 0.0 && turn < top * top)
+            widest = std::fmax(widest, p(turn));
+        // of f: a + 3 b l + 5 c l^2 = 0.  q adds what has equal signs, so that neither root cancels for small c
+        const double disc = 9.0 * b * b - 20.0 * a * c;
+        if (disc >= 0.0) {
+            const double q = -0.5 * (3.0 * b + std::copysign(std::sqrt(disc), b));
+            for (const double l : {q / (5.0 * c), a / q})
                 if (l > 0.0 && l < top * top)
                     most = std::fmax(most, f(std::sqrt(l)));
-            }
-        } else if (b != 0.0 && -a / (3.0 * b) > 0.0 && -a / (3.0 * b) < top * top) {
-            most = std::fmax(most, f(std::sqrt(-a / (3.0 * b))));
         }
         if (!(widest <= 32.0) || !(most <= 2.0))
             return false;
