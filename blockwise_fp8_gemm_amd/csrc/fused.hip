@@ -655,15 +655,17 @@ __global__ __launch_bounds__(NT) void norm_bwd_row_kernel(NormBwd b, float *__re
             x[k] = load8_bf16(b.z + row * b.ldz, c0, cols);
         }
     };
-    // sum of w dy z, and dw += dy z r
+    // sum of w dy (z r), and dw += dy (z r): the factor r first, which brings z to order one, so that
+    // neither leaves FP32's range where the result does not
     auto inner = [&](const uint4 &dy, const uint4 &z, const float (&wv)[8], float r, float (&acc)[8]) {
         float yv[8], xv[8], p = 0.0f;
         unpack8(dy, yv);
         unpack8(z, xv);
 #pragma unroll
         for (int j = 0; j < 8; j++) {
-            p = fmaf(yv[j] * wv[j], xv[j], p);
-            acc[j] = fmaf(yv[j], xv[j] * r, acc[j]);
+            const float xh = xv[j] * r;
+            p = fmaf(yv[j] * wv[j], xh, p);
+            acc[j] = fmaf(yv[j], xh, acc[j]);
         }
         return p;
     };
@@ -705,7 +707,7 @@ __global__ __launch_bounds__(NT) void norm_bwd_row_kernel(NormBwd b, float *__re
         }
         const float total = block_sum(sum, red[turn]);
         if (t == 0)
-            coef[row] = total * r / (float)cols;
+            coef[row] = total / (float)cols;
     }
 #pragma unroll
     for (int k = 0; k < RUN; k++) {

@@ -242,8 +242,10 @@ puro_status_t puro_fp8_rmsnorm_quant_dual(const void *x, int64_t ldx, const void
  *     dx[t][c] = dres + r ( g - xh mean over c of (g xh) )      (dres NULL: 0)
  *     dw[c]    = (accumulate ? dw[c] : 0) + sum over t of dy xh
  * dres is the gradient that reaches z past the norm, along the residual
- * stream.  dx is stored as BF16 (the gradient of x and of the residual) and its
- * FP32 value, unrounded, is quantised both ways as above.  dw is FP32 [cols];
+ * stream.  The products are formed in that order, xh first: w dy, the sums over
+ * g xh and dy xh, and dx must be finite in FP32.  dx is stored as BF16 (the
+ * gradient of x and of the residual) and its FP32 value, unrounded, is quantised
+ * both ways as above.  dw is FP32 [cols];
  * tokens are added in a fixed order (equal calls give equal bits).
  * tokens = 0 leaves dw zero, or as it was with accumulate.  accumulate other
  * than 0 or 1 is PURO_ERR_ENUM.
