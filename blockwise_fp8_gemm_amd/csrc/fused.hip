@@ -329,6 +329,8 @@ __device__ __forceinline__ void tile_codes(const float (&v)[RT][8], const Scale 
     for (int j = 0; j < 8; j++) {
         const Scale c{SLOW ? sh.scl[8 * p.cc + j] : 0.0f, sh.rcl[8 * p.cc + j], sh.rll[8 * p.cc + j]};
         word[j] = codes4<SLOW>(v[0][j], v[1][j], v[2][j], v[3][j], c);
+        if (SLOW)
+            __builtin_amdgcn_sched_barrier(0);   // a column at a time: the wide form's temporaries do not fit several
     }
     if constexpr (!TR) {
 #pragma unroll
@@ -806,20 +808,29 @@ void norm_bwd_tile_kernel(NormBwd b, const float *__restrict__ coef, const float
 // 1 - sigmoid(g) are 1 / (1 + e) and e / (1 + e), which one by the sign of g:
 // neither overflows nor cancels.
 //   du = dh g sigmoid(g),  dg = dh u sigmoid(g) (1 + g (1 - sigmoid(g)))
-// e is the square of 2^t, t = -|g| log2(e) / 2 (v_exp_f32 gives 0 below its
-// normal range, which the square reaches only where e underflows too); what t
-// rounds off (h + l, from the two-part constant) comes back as a factor
-// 1 + l ln 2.  One pass over tiles; 8192 x 6144: 110 us for 540 MB, of which 510
-// are the operands and results (row scales leave as partial sectors), 4.9 TB/s.
-// The 51 vector instructions an element takes with both its quantisations fill
-// 0.6 of that time; a single tile alone on a CU takes 12 us.
+// e = 2^t, t = -|g| log2(e): what t rounds off (h + l, from the two-part
+// constant) comes back as a factor 1 + l ln 2, and 1 / (1 + e) is v_rcp_f32's
+// value with a correction step, so that the two cost one rounding each beside
+// v_exp_f32's one step.  (e as the square of 2^(t / 2) and the bare reciprocal
+// were 1.3 to 1.7 times as far from the exact values for negative gates, and
+// 0.5 us of 110 faster.)  v_exp_f32 gives 0 below its normal range: where one of a
+// wave's gates is that far out (FAR), those take 2^(t + 64) 2^-64, which keeps e down
+// to its subnormals; the others' values are the same bits in both forms.  One
+// pass over tiles; 8192 x 6144: 110 us for 540 MB, of which 510 are the operands
+// and results (row scales leave as partial sectors), 4.9 TB/s.  Some 53 vector
+// instructions an element takes with both its quantisations fill 0.6 of that time; a
+// single tile alone on a CU takes 12 us.
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ void swiglu_grad(float dh, float g, float u, float &dg, float &du)
+constexpr float kNearGate = 87.0f;   // e^-87 = 2^-125.5
+template <bool FAR> __device__ __forceinline__ void swiglu_grad(float dh, float g, float u, float &dg, float &du)
 {
-    const float a = fabsf(g), h = a * -0x1.715476p-1f;
-    const float l = fmaf(a, -0x1.4ae0cp-27f, fmaf(a, -0x1.715476p-1f, -h));
-    const float x = __builtin_amdgcn_exp2f(h), q = fmaf(x, l * 0x1.62e43p-1f, x), e = q * q;
-    const float i = __builtin_amdgcn_rcpf(1.0f + e), ei = e * i;
+    // past 256 e is 0, and h must stay finite
+    const float a = FAR ? fminf(fabsf(g), 256.0f) : fabsf(g), h = a * -0x1.715476p0f;
+    const float l = fmaf(a, -0x1.4ae0cp-26f, fmaf(a, -0x1.715476p0f, -h));
+    const bool far = FAR && h < -126.0f;
+    const float x = __builtin_amdgcn_exp2f(far ? h + 64.0f : h), q = fmaf(x, l * 0x1.62e43p-1f, x);
+    const float e = far ? q * 0x1p-64f : q;
+    const float d = 1.0f + e, i0 = __builtin_amdgcn_rcpf(d), i = fmaf(fmaf(-d, i0, 1.0f), i0, i0), ei = e * i;
     const float sig = g < 0.0f ? ei : i, nsig = g < 0.0f ? i : ei;
     du = dh * (g * sig);
     dg = (dh * u) * (sig * fmaf(g, nsig, 1.0f));
@@ -840,9 +851,20 @@ __device__ __forceinline__ void swiglu_bwd_tile(const SwigluBwd &b, const Place 
         unpack8(x[i], xv);
         unpack8(g[i], gv);
         unpack8(u[i], uv);
+        float m = 0.0f;
 #pragma unroll
-        for (int j = 0; j < 8; j++)
-            swiglu_grad(xv[j], gv[j], uv[j], vg[i][j], vu[i][j]);
+        for (int j = 0; j < 8; j += 2)
+            m = absmax3(gv[j], gv[j + 1], m);
+        if (__any(!(m < kNearGate))) {
+#pragma unroll
+            for (int j = 0; j < 8; j++)
+                swiglu_grad<true>(xv[j], gv[j], uv[j], vg[i][j], vu[i][j]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; j++)
+                swiglu_grad<false>(xv[j], gv[j], uv[j], vg[i][j], vu[i][j]);
+        }
+        __builtin_amdgcn_sched_barrier(0);   // a token's temporaries are dead before the next one's
     }
     pin(vg);
     pin(vu);
