@@ -290,8 +290,10 @@ typedef struct {
  * the two results may be the column halves of one [tokens][2 cols] tensor
  * (q_row, s_row; and the row halves of q_tok, s_tok with transpose_out = 1): the
  * operands of one data-gradient GEMM over the concatenated gate/up outputs.
- * dgate and dup point to HOST structures, read before the call returns.  |dh up
- * gate| must be finite in FP32.
+ * dgate and dup point to HOST structures, read before the call returns.  |dh up|
+ * and the results must be finite in FP32 (dgate is formed as dh up times the
+ * rest, which lies in (-0.1, 1.1)).  sg is an FP32 number: below 2^-126 (gate <
+ * -87.3) it is known to 2^-149.
  */
 puro_status_t puro_fp8_swiglu_bwd_quant_dual(const void *dh, int64_t lddh, const void *gate, int64_t ldg,
                                              const void *up, int64_t ldu, int64_t tokens, int64_t cols,

@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import blockwise_fp8_gemm_amd as pf
-from fused_ref import f64
+from fused_ref import check_dual, f64, swiglu_bwd
 
 pytestmark = pytest.mark.gpu
 
@@ -46,3 +46,20 @@ def test_no_further_than_elementary_fp32(dev, lo, hi):
         rel = [float((((v - want.abs()) / want.abs())[some]).square().mean().sqrt()) * 2 ** 24
                for v in (448 * f64(s), 448 * (plain.abs() / 448).double())]
         assert rel[0] <= 1.5 * rel[1], rel
+
+
+def test_largest_products(dev):
+    """|dh up| up to FP32's largest is what the header asks for: gates small and large beside it."""
+    tokens, cols = 40, 256
+    gen = torch.Generator().manual_seed(2)
+    dh = (torch.rand((tokens, cols), generator=gen) + 1) * 2.0 ** 64
+    up = (torch.rand((tokens, cols), generator=gen) + 1) * 2.0 ** 60
+    gate = torch.randn((tokens, cols), generator=gen) * torch.tensor([0.01, 1.0, 30.0, 1e9]).repeat(10)[:, None]
+    dh, up, gate = (t.to(torch.bfloat16) for t in (dh, up, gate))
+    got = pf.puro_fp8_swiglu_bwd_quant_dual(dh.to(dev), gate.to(dev), up.to(dev))
+    torch.cuda.synchronize()
+    dg, du, tg, tu = swiglu_bwd(f64(dh), f64(gate), f64(up))
+    # the products with gate pass FP32's range, the results do not
+    assert float((dh.double() * up.double() * gate.double()).abs().max()) > 3.5e38 > 2 * float(dg.abs().max())
+    check_dual(dg, tg, *got[0], "dgate")
+    check_dual(du, tu, *got[1], "dup")
