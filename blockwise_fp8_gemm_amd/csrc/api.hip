@@ -238,7 +238,8 @@ static puro_status_t check_norm(const puro::NormIn &in, int wdt, bool need_rstd)
         return PURO_ERR_NULL;
     if ((in.w && !aligned(in.w, 16)) || (in.rstd && !aligned(in.rstd, 4)))
         return PURO_ERR_ALIGN;
-    if (!(in.eps > 0.0f) || in.eps > 3.0e38f)
+    // below 2^-126 the squares beside it would be subnormal, and r off by percents
+    if (!(in.eps >= 0x1p-126f) || !std::isfinite(in.eps))
         return PURO_ERR_VALUE;
     return PURO_OK;
 }

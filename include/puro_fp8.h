@@ -214,8 +214,8 @@ puro_status_t puro_fp8_swiglu_quant_dual(const void *gate, int64_t ldg, const vo
  * quantisers above).  Quantising n before any rounding to BF16 is what sets
  * them apart from quantising h.
  *   weight  [cols], FP32 or BF16 (wdt), dense, 16-byte aligned
- *   eps     finite and > 0, else PURO_ERR_VALUE
- * The squares of a row must sum to a finite FP32 value.  The outputs must not
+ *   eps     finite and at least 2^-126 (a normal FP32 number), else PURO_ERR_VALUE
+ * The sum of a row's squares, and its mean + eps, must be finite in FP32.  The outputs must not
  * overlap each other or the inputs, but z may be x or residual itself, with its
  * row stride (the sum in place).  tokens = 0 or cols = 0 writes nothing.
  *
