@@ -645,6 +645,14 @@ def puro_fp8_rmsnorm_bwd_quant_dual(dy, z, rstd, weight, dres=None, transpose_ou
     return dx, dw, q_row, s_row, q_tok, s_tok
 
 
+def _pair(t, name):
+    if t is None:
+        return None, None
+    if not isinstance(t, (tuple, list)) or len(t) != 2:
+        raise ValueError("%s: separate gradients take a pair (dgate's, dup's)" % name)
+    return t
+
+
 @_on_device
 def puro_fp8_swiglu_bwd_quant_dual(dh, gate, up, transpose_out=True, joined=False, q_row=None, s_row=None, q_tok=None,
                                    s_tok=None, stream=None, pow2=False):
@@ -653,7 +661,8 @@ def puro_fp8_swiglu_bwd_quant_dual(dh, gate, up, transpose_out=True, joined=Fals
 
     joined=False: returns two (q_row, s_row, q_tok, s_tok), dgate's and dup's, laid out as
     puro_fp8_quant_dual's.  joined=True (cols a multiple of 128): one such tuple for the [tokens][2 cols]
-    tensor that holds dgate's columns, then dup's; q_row, s_row, q_tok and s_tok may then be given."""
+    tensor that holds dgate's columns, then dup's.  q_row, s_row, q_tok and s_tok may be given: tensors for
+    joined gradients, else pairs (dgate's, dup's), either of which may be None."""
     shape, dev = dh.shape, dh.device
     if len(shape) != 2:
         raise ValueError("dh: expected a 2-D tensor, got shape %s" % (tuple(shape),))
@@ -674,13 +683,14 @@ def puro_fp8_swiglu_bwd_quant_dual(dh, gate, up, transpose_out=True, joined=Fals
             up_out = gate_out
         res = q_row, s_row, q_tok, s_tok
     else:
+        given = ((None, None),) * 4
         if q_row is not None or s_row is not None or q_tok is not None or s_tok is not None:
-            raise ValueError("outputs can be given for joined gradients only")
+            given = [_pair(t, name) for t, name in zip((q_row, s_row, q_tok, s_tok), ("q_row", "s_row", "q_tok", "s_tok"))]
         res, outs = [], []
         lds_row, lds_tok = _nblk(cols), _nblk(tokens) if transpose_out else cols
-        for _ in range(2):
-            qr, sr, qrp, ldqr, srp = _codes(tokens, cols, dev, None, None)
-            qt, st, qtp, ldqt, stp = _codes(tokens, cols, dev, None, None, True, transpose_out)
+        for a, b, c, d in zip(*given):   # dgate's, then dup's
+            qr, sr, qrp, ldqr, srp = _codes(tokens, cols, dev, a, b)
+            qt, st, qtp, ldqt, stp = _codes(tokens, cols, dev, c, d, True, transpose_out)
             res.append((qr, sr, qt, st))
             outs.append(QuantDualOut(qrp, ldqr, srp, lds_row, qtp, ldqt, stp, lds_tok))
         res, (gate_out, up_out) = tuple(res), outs
