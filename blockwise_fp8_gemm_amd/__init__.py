@@ -870,8 +870,9 @@ def puro_fp8_newton_schulz_grouped(grads, steps=5, coefficients=(3.4445, -4.7750
         raise ValueError("outs must have one entry per gradient")
     if not grads:
         return []
-    triples = list(coefficients) if hasattr(coefficients[0], "__len__") else [coefficients] * steps
-    if len(triples) != steps or any(len(t) != 3 for t in triples):
+    coefficients = list(coefficients)
+    triples = coefficients if any(hasattr(t, "__len__") for t in coefficients) else [coefficients] * steps
+    if len(triples) != steps or any(not hasattr(t, "__len__") or len(t) != 3 for t in triples):
         raise ValueError("coefficients: one (a, b, c), or one per step")
     dev, dtype = grads[0].device, grads[0].dtype
     code = _dtype_code(grads[0])

@@ -4,6 +4,7 @@ import ctypes
 
 import numpy as np
 import pytest
+import torch
 
 import blockwise_fp8_gemm_amd as pf
 
@@ -52,3 +53,10 @@ def test_against_a_search():
         assert accepted(t) == want, (t, most, widest)
         yes, no = yes + want, no + (not want)
     assert yes > 200 and no > 200
+
+
+def test_coefficients_of_no_step_or_of_two_kinds():
+    g = torch.zeros((16, 16))
+    for steps, coef in ((5, ()), (2, ((1, 0, 0), 1.0)), (2, (1.0, (1, 0, 0))), (1, (1, 0)), (3, (1, 0, 0, 0))):
+        with pytest.raises(ValueError, match="coefficients"):
+            pf.puro_fp8_newton_schulz_grouped([g], steps=steps, coefficients=coef)
