@@ -812,12 +812,12 @@ void norm_bwd_tile_kernel(NormBwd b, const float *__restrict__ coef, const float
 // constant) comes back as a factor 1 + l ln 2, and 1 / (1 + e) is v_rcp_f32's
 // value with a correction step, so that the two cost one rounding each beside
 // v_exp_f32's one step.  (e as the square of 2^(t / 2) and the bare reciprocal
-// were 1.3 to 1.7 times as far from the exact values for negative gates, and
-// 0.5 us of 110 faster.)  v_exp_f32 gives 0 below its normal range: where one of a
+// were 1.5 to 1.9 times as far from the exact values for negative gates, and
+// 1% faster.)  v_exp_f32 gives 0 below its normal range: where one of a
 // wave's gates is that far out (FAR), those take 2^(t + 64) 2^-64, which keeps e down
 // to its subnormals; the others' values are the same bits in both forms.  One
 // pass over tiles; 8192 x 6144: 110 us for 540 MB, of which 510 are the operands
-// and results (row scales leave as partial sectors), 4.9 TB/s.  Some 53 vector
+// and results (row scales leave as partial sectors), 4.9 TB/s.  The 54 vector
 // instructions an element takes with both its quantisations fill 0.6 of that time; a
 // single tile alone on a CU takes 12 us.
 // ---------------------------------------------------------------------------

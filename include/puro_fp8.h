@@ -527,7 +527,8 @@ puro_status_t puro_fp8_gemm_grouped_native(puro_layout_t layout, puro_bscale_t b
  * coef[3 k], coef[3 k + 1], coef[3 k + 2]:
  *     A = X X^T,   X <- a X + (b A + c A A) X
  * o receives X (transposed back) as BF16.  |G|_F is formed in 64 bits, the
- * products on the FP16 matrix cores with X held to 22 bits between steps: with
+ * products on the FP16 matrix cores (there is no form with FP32 products), X held
+ * between steps as the sum of two FP16 numbers: with
  * the usual quintic (3.4445, -4.7750, 2.0315) and five steps the result is
  * within about 2e-3 (relative Frobenius) of the exact one before its BF16
  * rounding, which is of that size itself.  Equal calls give equal bits.
