@@ -21,6 +21,10 @@ Names mirror the C entry points:
     puro_fp8_gemm(..., mx=True)           -> puro_fp8_gemm_mx (power-of-two scales, scaled matrix cores)
     puro_fp8_gemm(..., native=True)       -> puro_fp8_gemm_native (partials on the FP8 matrix cores)
     puro_fp8_gemm_grouped(..., mx=True / native=True) -> the grouped forms of those two
+    puro_fp8_qk_norm_rope(q, k, head_dim, positions, inv_freq, ...)  -> normed and rotated query and key heads
+    puro_fp8_qk_norm_rope_bwd_quant_dual(dq, dk, dv, q, k, ...)      -> the joint q/k/v gradient's dual quantisation
+    puro_fp8_attention(q, k, v, head_dim, q_offsets, k_offsets, max_q, max_k)  -> o, lse of packed sequences
+    puro_fp8_attention_bwd(do, q, k, v, o, lse, ...)                 -> dq, dk, dv
     puro_fp8_newton_schulz_grouped([grads])  -> their Newton-Schulz orthogonalised directions
     puro_status_string(status)
 Tensors are 2-D, row-major (stride(1) == 1), with a row stride that is a
@@ -86,6 +90,23 @@ class NewtonSchulzDesc(ctypes.Structure):
                 ("o", ctypes.c_void_p), ("ldo", ctypes.c_int64)]
 
 
+class QkNormRope(ctypes.Structure):
+    """puro_qk_norm_rope_t: heads, rotation and norm of puro_fp8_qk_norm_rope."""
+    _fields_ = [("heads_q", ctypes.c_int), ("heads_kv", ctypes.c_int), ("head_dim", ctypes.c_int),
+                ("rotary_dim", ctypes.c_int), ("interleaved", ctypes.c_int), ("tokens", ctypes.c_int64),
+                ("positions", ctypes.c_void_p), ("inv_freq", ctypes.c_void_p), ("rope_scale", ctypes.c_float),
+                ("wq", ctypes.c_void_p), ("wk", ctypes.c_void_p), ("wdt", ctypes.c_int), ("eps", ctypes.c_float)]
+
+
+class Attention(ctypes.Structure):
+    """puro_attention_t: heads and sequences of puro_fp8_attention."""
+    _fields_ = [("heads_q", ctypes.c_int), ("heads_kv", ctypes.c_int), ("head_dim", ctypes.c_int),
+                ("sequences", ctypes.c_int), ("causal", ctypes.c_int), ("tokens_q", ctypes.c_int64),
+                ("tokens_k", ctypes.c_int64), ("max_q", ctypes.c_int64), ("max_k", ctypes.c_int64),
+                ("q_offsets", ctypes.c_void_p), ("q_lengths", ctypes.c_void_p), ("k_offsets", ctypes.c_void_p),
+                ("k_lengths", ctypes.c_void_p), ("scale", ctypes.c_float)]
+
+
 def gemm_desc(M, N, segments, C, ldc, accumulate=False):
     """GemmDesc from (K, A, lda, sA, B, ldb, sB) tuples of pointers and strides."""
     if not 1 <= len(segments) <= MAX_SEGMENTS:
@@ -145,6 +166,19 @@ def lib():
         L.puro_fp8_newton_schulz_grouped.restype = i32
         L.puro_fp8_newton_schulz_grouped.argtypes = [i32, ctypes.POINTER(NewtonSchulzDesc), i32, i32,
                                                      ctypes.POINTER(f32), f32, vp, ctypes.c_size_t, vp]
+        rope, attn, size = ctypes.POINTER(QkNormRope), ctypes.POINTER(Attention), ctypes.c_size_t
+        mat = [vp, i64]
+        L.puro_fp8_qk_norm_rope.restype, L.puro_fp8_qk_norm_rope.argtypes = i32, [rope] + mat * 4 + [vp, vp]
+        for suffix in ("", "_pow2"):
+            f = getattr(L, "puro_fp8_qk_norm_rope_bwd_quant_dual" + suffix)
+            f.restype, f.argtypes = i32, [rope] + mat * 5 + [vp] + mat + [vp, vp, i32, vp, i64, vp, i32, vp, i64, vp,
+                                                                          vp, size, vp]
+        L.puro_fp8_attention.restype, L.puro_fp8_attention.argtypes = i32, [attn] + mat * 4 + [vp, vp, size, vp]
+        L.puro_fp8_attention_bwd.restype = i32
+        L.puro_fp8_attention_bwd.argtypes = [attn] + mat * 5 + [vp] + mat * 3 + [vp, size, vp]
+        for name, arg in (("qk_norm_rope_bwd", rope), ("attention", attn), ("attention_bwd", attn)):
+            f = getattr(L, "puro_fp8_%s_workspace_size" % name)
+            f.restype, f.argtypes = size, [arg]
         L.puro_fp8_gemm_workspace_size.restype = ctypes.c_size_t
         L.puro_fp8_gemm_workspace_size.argtypes = [i32, i64, i64, i64, i32]
         for name in ("puro_fp8_gemm", "puro_fp8_gemm_mx", "puro_fp8_gemm_native"):
@@ -699,6 +733,203 @@ def puro_fp8_swiglu_bwd_quant_dual(dh, gate, up, transpose_out=True, joined=Fals
     _check(fn(*ins, tokens, cols, 1 if transpose_out else 0, gate_out, up_out, _raw_stream(stream, dev)),
            "puro_fp8_swiglu_bwd_quant_dual")
     return res
+
+
+def _rope(q, k, head_dim, positions, inv_freq, q_weight, k_weight, eps, rope_scale, interleaved):
+    """Checked QkNormRope for query heads q and key heads k (shapes and devices of tensors), with its device."""
+    dev = q.device
+    for t, name in ((q, "q"), (k, "k")):
+        if len(t.shape) != 2:
+            raise ValueError("%s: expected a 2-D tensor, got shape %s" % (name, tuple(t.shape)))
+    if head_dim not in (64, 128):
+        raise ValueError("head_dim is 64 or 128, got %r" % (head_dim,))
+    tokens, rotary = q.shape[0], 0 if inv_freq is None else 2 * inv_freq.numel()
+    for t, name in ((q, "q"), (k, "k")):
+        if t.shape[1] % head_dim or not t.shape[1]:
+            raise ValueError("%s: %d columns are no whole heads of %d" % (name, t.shape[1], head_dim))
+    pos = freq = wqp = wkp = 0
+    wdt = PURO_F32
+    if rotary:
+        if positions is None:
+            raise ValueError("positions are needed with inv_freq")
+        pos = _dense(positions, (tokens,), (torch.int32,), "positions", dev)
+        freq = _dense(inv_freq, (rotary // 2,), (_F32,), "inv_freq", dev)
+    if (q_weight is None) != (k_weight is None):
+        raise ValueError("q_weight and k_weight: both or neither")
+    if q_weight is not None:
+        wqp = _dense(q_weight, (head_dim,), (_F32, _BF16), "q_weight", dev)
+        wkp = _dense(k_weight, (head_dim,), (q_weight.dtype,), "k_weight", dev)
+        wdt = PURO_BF16 if q_weight.dtype is _BF16 else PURO_F32
+    return QkNormRope(q.shape[1] // head_dim, k.shape[1] // head_dim, head_dim, rotary, 1 if interleaved else 0,
+                      tokens, pos, freq, rope_scale, wqp, wkp, wdt, eps)
+
+
+@_on_device
+def puro_fp8_qk_norm_rope(q, k, head_dim, positions=None, inv_freq=None, q_weight=None, k_weight=None, eps=1e-6,
+                          rope_scale=1.0, interleaved=False, q_out=None, k_out=None, rstd=None, store_rstd=True,
+                          stream=None):
+    """Every query and key head normed (x / sqrt(mean x^2 + eps) * weight; not without weights) and its first
+    2 len(inv_freq) elements rotated by positions * inv_freq: pairs (j, j + len(inv_freq)), or (2 j, 2 j + 1)
+    with interleaved, times rope_scale.  q: bfloat16 [tokens][heads_q * head_dim], k the same with heads_kv;
+    positions: int32 [tokens]; inv_freq: float32; weights: float32 / bfloat16 [head_dim].  q_out and k_out may
+    be q and k themselves.  Returns (q_out, k_out, rstd [tokens][heads_q + heads_kv]; None without weights or
+    store_rstd)."""
+    r, dev = _rope(q, k, head_dim, positions, inv_freq, q_weight, k_weight, eps, rope_scale, interleaved), q.device
+    shapes = (r.tokens, q.shape[1]), (r.tokens, k.shape[1])
+    ins = (*_mat(q, shapes[0], _BF16, "q", dev), *_mat(k, shapes[1], _BF16, "k", dev))
+    outs, args = [], []
+    for t, shape, name in ((q_out, shapes[0], "q_out"), (k_out, shapes[1], "k_out")):
+        if t is None:
+            t, p, ld = _new(*shape, _BF16, dev)
+        else:
+            p, ld = _mat(t, shape, _BF16, name, dev)
+        outs.append(t)
+        args += [p, ld]
+    rp, heads = 0, (r.tokens, r.heads_q + r.heads_kv)
+    if q_weight is None or not (store_rstd or rstd is not None):
+        rstd = None
+    elif rstd is None:
+        rstd = torch.empty(heads, dtype=_F32, device=dev)
+        rp = rstd.data_ptr()
+    else:
+        rp = _dense(rstd, heads, (_F32,), "rstd", dev)
+    _check(lib().puro_fp8_qk_norm_rope(r, *ins, *args, rp, _raw_stream(stream, dev)), "puro_fp8_qk_norm_rope")
+    return outs[0], outs[1], rstd
+
+
+@_on_device
+def puro_fp8_qk_norm_rope_bwd_quant_dual(dq, dk, dv, q, k, head_dim, positions=None, inv_freq=None, rstd=None,
+                                         q_weight=None, k_weight=None, rope_scale=1.0, interleaved=False,
+                                         transpose_out=True, dx=None, store_dx=False, dwq=None, dwk=None,
+                                         accumulate=False, q_row=None, s_row=None, q_tok=None, s_tok=None,
+                                         workspace=None, stream=None, pow2=False):
+    """Gradient of puro_fp8_qk_norm_rope with dv beside it, as the joint q/k/v product's output gradient
+    [tokens][(heads_q + 2 heads_kv) * head_dim], quantised both ways in FP32 (not rounded to bfloat16 first).
+    dq, dk: gradients of q_out and k_out; dv: that of the values; q, k, rstd: the forward's inputs and rstd
+    (not read without weights; q and k may be None then).  dx (given, or allocated with store_dx): the joint
+    gradient in bfloat16.  dwq, dwk: float32 [head_dim], added to with accumulate.
+    Returns (dx or None, dwq, dwk, q_row, s_row, q_tok, s_tok); dwq and dwk are None without weights."""
+    r = _rope(dq, dk, head_dim, positions, inv_freq, q_weight, k_weight, 1.0, rope_scale, interleaved)
+    dev, tokens, norm = dq.device, r.tokens, q_weight is not None
+    sq, sk = (tokens, dq.shape[1]), (tokens, dk.shape[1])
+    ins = [*_mat(dq, sq, _BF16, "dq", dev), *_mat(dk, sk, _BF16, "dk", dev), *_mat(dv, sk, _BF16, "dv", dev)]
+    rp = dwqp = dwkp = 0
+    if norm:
+        if q is None or k is None or rstd is None:
+            raise ValueError("q, k and rstd are needed with weights")
+        ins += [*_mat(q, sq, _BF16, "q", dev), *_mat(k, sk, _BF16, "k", dev)]
+        rp = _dense(rstd, (tokens, r.heads_q + r.heads_kv), (_F32,), "rstd", dev)
+        if accumulate and (dwq is None or dwk is None):
+            raise ValueError("accumulate needs dwq and dwk")
+        dwq, dwk = (torch.empty((head_dim,), dtype=_F32, device=dev) if t is None else t for t in (dwq, dwk))
+        dwqp, dwkp = _dense(dwq, (head_dim,), (_F32,), "dwq", dev), _dense(dwk, (head_dim,), (_F32,), "dwk", dev)
+    else:
+        ins += [0, 0, 0, 0]
+        dwq = dwk = None
+    cols = sq[1] + 2 * sk[1]
+    if store_dx and dx is None:
+        dx, dxp, lddx = _new(tokens, cols, _BF16, dev)
+    else:
+        dxp, lddx = _opt_mat(dx, (tokens, cols), _BF16, "dx", dev)
+    q_row, s_row, *row = _codes(tokens, cols, dev, q_row, s_row)
+    q_tok, s_tok, *tok = _codes(tokens, cols, dev, q_tok, s_tok, True, transpose_out)
+    L = lib()
+    workspace, wsp, ws_bytes = _workspace(workspace, lambda: L.puro_fp8_qk_norm_rope_bwd_workspace_size(r), dev)
+    fn = L.puro_fp8_qk_norm_rope_bwd_quant_dual_pow2 if pow2 else L.puro_fp8_qk_norm_rope_bwd_quant_dual
+    _check(fn(r, *ins, rp, dxp, lddx, dwqp, dwkp, 1 if accumulate else 0, *row, 1 if transpose_out else 0, *tok, wsp,
+              ws_bytes, _raw_stream(stream, dev)), "puro_fp8_qk_norm_rope_bwd_quant_dual")
+    return dx, dwq, dwk, q_row, s_row, q_tok, s_tok
+
+
+def _sequences(off, lengths, name, dev):
+    """(addresses of a checked offset and length array, the number of sequences)."""
+    if off.dim() != 1 or off.numel() < 1:
+        raise ValueError("%s_offsets: expected one int32 per sequence and one more, got shape %s" % (name, tuple(off.shape)))
+    p = _dense(off, off.shape, (torch.int32,), name + "_offsets", dev)
+    if lengths is None:
+        return p, 0, off.numel() - 1
+    n = lengths.numel()
+    if off.numel() not in (n, n + 1):
+        raise ValueError("%s_offsets: %d entries for %d lengths" % (name, off.numel(), n))
+    return p, _dense(lengths, (n,), (torch.int32,), name + "_lengths", dev), n
+
+
+def _attention(q, k, v, head_dim, q_offsets, k_offsets, max_q, max_k, q_lengths, k_lengths, causal, scale):
+    """Checked Attention and the addresses and strides of q, k and v."""
+    dev = q.device
+    for t, name in ((q, "q"), (k, "k")):
+        if len(t.shape) != 2:
+            raise ValueError("%s: expected a 2-D tensor, got shape %s" % (name, tuple(t.shape)))
+        if head_dim not in (64, 128) or t.shape[1] % head_dim or not t.shape[1]:
+            raise ValueError("%s: %d columns are no whole heads of %r (64 or 128)" % (name, t.shape[1], head_dim))
+    ins = (*_mat(q, q.shape, _BF16, "q", dev), *_mat(k, k.shape, _BF16, "k", dev), *_mat(v, k.shape, _BF16, "v", dev))
+    qo, ql, n = _sequences(q_offsets, q_lengths, "q", dev)
+    ko, kl, m = _sequences(k_offsets, k_lengths, "k", dev)
+    if n != m:
+        raise ValueError("%d sequences of queries and %d of keys" % (n, m))
+    a = Attention(q.shape[1] // head_dim, k.shape[1] // head_dim, head_dim, n, 1 if causal else 0, q.shape[0],
+                  k.shape[0], max_q, max_k, qo, ql, ko, kl, head_dim ** -0.5 if scale is None else scale)
+    return a, ins
+
+
+@_on_device
+def puro_fp8_attention(q, k, v, head_dim, q_offsets, k_offsets, max_q, max_k, q_lengths=None, k_lengths=None,
+                       causal=True, scale=None, o=None, lse=None, workspace=None, stream=None):
+    """Attention of packed sequences: sequence s's queries are rows q_offsets[s] .. q_offsets[s + 1] of q, its
+    keys and values rows k_offsets[s] .. of k and v (with q_lengths / k_lengths only the first so many of them,
+    as in padded caches).  A query sees every key, or with causal those up to its place from the end.
+    q: bfloat16 [tokens_q][heads_q * head_dim], k and v: [tokens_k][heads_kv * head_dim]; offsets and lengths:
+    int32 on the GPU; max_q, max_k: the longest sequence's rows (upper bounds); scale: head_dim^-0.5 by default.
+    Returns (o as q, lse float32 [heads_q][tokens_q], the rows' log-sums); rows outside every sequence are
+    left as they were."""
+    a, ins = _attention(q, k, v, head_dim, q_offsets, k_offsets, max_q, max_k, q_lengths, k_lengths, causal, scale)
+    dev = q.device
+    if o is None:
+        o, op, ldo = _new(*q.shape, _BF16, dev)
+    else:
+        op, ldo = _mat(o, q.shape, _BF16, "o", dev)
+    if lse is None:
+        lse = torch.empty((a.heads_q, a.tokens_q), dtype=_F32, device=dev)
+        lp = lse.data_ptr()
+    else:
+        lp = _dense(lse, (a.heads_q, a.tokens_q), (_F32,), "lse", dev)
+    L = lib()
+    wsp = ws_bytes = 0
+    need = L.puro_fp8_attention_workspace_size(a)
+    if need or workspace is not None:
+        workspace, wsp, ws_bytes = _workspace(workspace, lambda: need, dev)
+    _check(L.puro_fp8_attention(a, *ins, op, ldo, lp, wsp, ws_bytes, _raw_stream(stream, dev)), "puro_fp8_attention")
+    return o, lse
+
+
+def puro_fp8_attention_workspace_size(heads_q, heads_kv, head_dim, sequences, tokens_q, tokens_k, max_q, max_k):
+    return int(lib().puro_fp8_attention_workspace_size(
+        Attention(heads_q, heads_kv, head_dim, sequences, 0, tokens_q, tokens_k, max_q, max_k, None, None, None, None, 1.0)))
+
+
+@_on_device
+def puro_fp8_attention_bwd(do, q, k, v, o, lse, head_dim, q_offsets, k_offsets, max_q, max_k, q_lengths=None,
+                           k_lengths=None, causal=True, scale=None, dq=None, dk=None, dv=None, workspace=None,
+                           stream=None):
+    """Gradients (dq, dk, dv) of puro_fp8_attention for do, the gradient of o, and the forward's arguments and
+    results; dk and dv are summed over the query heads that share them.  dq, dk and dv may be given (columns of
+    one joint gradient, for example); rows outside every sequence are left as they were."""
+    a, ins = _attention(q, k, v, head_dim, q_offsets, k_offsets, max_q, max_k, q_lengths, k_lengths, causal, scale)
+    dev = q.device
+    ins = (*_mat(do, q.shape, _BF16, "do", dev), *ins, *_mat(o, q.shape, _BF16, "o", dev),
+           _dense(lse, (a.heads_q, a.tokens_q), (_F32,), "lse", dev))
+    res, outs = [], []
+    for t, shape, name in ((dq, q.shape, "dq"), (dk, k.shape, "dk"), (dv, k.shape, "dv")):
+        if t is None:
+            t, p, ld = _new(*shape, _BF16, dev)
+        else:
+            p, ld = _mat(t, shape, _BF16, name, dev)
+        res.append(t)
+        outs += [p, ld]
+    L = lib()
+    workspace, wsp, ws_bytes = _workspace(workspace, lambda: L.puro_fp8_attention_bwd_workspace_size(a), dev)
+    _check(L.puro_fp8_attention_bwd(a, *ins, *outs, wsp, ws_bytes, _raw_stream(stream, dev)), "puro_fp8_attention_bwd")
+    return tuple(res)
 
 
 def gemm_dims(layout, A, B):

@@ -6,7 +6,7 @@ import sys
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libpuro_fp8.so")
-SOURCES = ["api.hip", "quant.hip", "fused.hip", "newton.hip", "gemm.hip"]
+SOURCES = ["api.hip", "quant.hip", "fused.hip", "newton.hip", "qknorm.hip", "attention.hip", "gemm.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 FLAGS = [

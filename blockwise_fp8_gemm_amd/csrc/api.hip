@@ -952,6 +952,294 @@ puro_status_t puro_fp8_newton_schulz_grouped(puro_dtype_t gdt, const puro_newton
     }
 }
 
+// Head counts and dimension, shared by the calls on attention's operands.
+static bool bad_heads(int heads_q, int heads_kv, int head_dim)
+{
+    return heads_q < 1 || heads_q > PURO_MAX_HEADS || heads_kv < 1 || heads_kv > PURO_MAX_HEADS ||
+           (head_dim != 64 && head_dim != 128);
+}
+
+static bool bad_rope_shape(const puro_qk_norm_rope_t &r)
+{
+    return bad_heads(r.heads_q, r.heads_kv, r.head_dim) || r.rotary_dim < 0 || r.rotary_dim > r.head_dim ||
+           r.rotary_dim % 16 || bad_extent(r.tokens);
+}
+
+// Everything of the shape but q and k themselves.
+static puro_status_t check_rope(const puro_qk_norm_rope_t &r)
+{
+    if (r.interleaved != 0 && r.interleaved != 1)
+        return PURO_ERR_ENUM;
+    if (r.wq && r.wdt != PURO_F32 && r.wdt != PURO_BF16)
+        return PURO_ERR_ENUM;
+    if (bad_rope_shape(r))
+        return PURO_ERR_SHAPE;
+    if (!r.wq != !r.wk || (r.tokens > 0 && r.rotary_dim > 0 && (!r.positions || !r.inv_freq)))
+        return PURO_ERR_NULL;
+    if ((r.wq && !(aligned(r.wq, 16) && aligned(r.wk, 16))) || !aligned(r.positions, 4) || !aligned(r.inv_freq, 4))
+        return PURO_ERR_ALIGN;
+    if ((r.wq && (!(r.eps >= 0x1p-126f) || !std::isfinite(r.eps))) || !std::isfinite(r.rope_scale))
+        return PURO_ERR_VALUE;
+    return PURO_OK;
+}
+
+static puro::RopeShape rope_shape(const puro_qk_norm_rope_t &r, const void *q, int64_t ldq, const void *k, int64_t ldk)
+{
+    return puro::RopeShape{static_cast<const uint16_t *>(q), ldq, static_cast<const uint16_t *>(k), ldk, r.heads_q,
+                           r.heads_kv, r.head_dim, r.tokens, r.wq, r.wk, r.wdt == PURO_BF16, r.eps, r.positions,
+                           r.inv_freq, r.rotary_dim, r.rope_scale, r.interleaved == 1};
+}
+
+puro_status_t puro_fp8_qk_norm_rope(const puro_qk_norm_rope_t *shape, const void *q, int64_t ldq, const void *k,
+                                    int64_t ldk, void *qo, int64_t ldqo, void *ko, int64_t ldko, float *rstd,
+                                    hipStream_t stream)
+{
+    try {
+        if (!shape)
+            return PURO_ERR_NULL;
+        const puro_qk_norm_rope_t &r = *shape;
+        puro_status_t st = check_rope(r);
+        const int64_t cq = (int64_t)r.heads_q * r.head_dim, ck = (int64_t)r.heads_kv * r.head_dim;
+        const bool empty = r.tokens == 0;
+        if (st == PURO_OK)
+            st = check_bf16(q, ldq, cq, empty);
+        if (st == PURO_OK)
+            st = check_bf16(k, ldk, ck, empty);
+        if (st == PURO_OK)
+            st = check_bf16(qo, ldqo, cq, empty);
+        if (st == PURO_OK)
+            st = check_bf16(ko, ldko, ck, empty);
+        if (st != PURO_OK)
+            return st;
+        if (rstd && !aligned(rstd, 4))
+            return PURO_ERR_ALIGN;
+        if (empty)
+            return PURO_OK;
+        const puro::RopeFwd a{rope_shape(r, q, ldq, k, ldk), static_cast<uint16_t *>(qo), ldqo,
+                              static_cast<uint16_t *>(ko), ldko, rstd, 0};
+        return from_hip(puro::launch_rope(a, stream));
+    } catch (...) {
+        return PURO_ERR_INTERNAL;
+    }
+}
+
+size_t puro_fp8_qk_norm_rope_bwd_workspace_size(const puro_qk_norm_rope_t *shape)
+{
+    if (!shape || bad_rope_shape(*shape))
+        return 0;
+    return puro::rope_bwd_workspace_bytes(rope_shape(*shape, nullptr, 0, nullptr, 0), shape->wq != nullptr);
+}
+
+static puro_status_t rope_bwd_impl(const puro_qk_norm_rope_t *shape, const void *dq, int64_t lddq, const void *dk,
+                                   int64_t lddk, const void *dv, int64_t lddv, const void *q, int64_t ldq,
+                                   const void *k, int64_t ldk, const float *rstd, void *dx, int64_t lddx, float *dwq,
+                                   float *dwk, int accumulate, uint8_t *q_row, int64_t ldq_row, float *s_row,
+                                   int transpose_out, uint8_t *q_tok, int64_t ldq_tok, float *s_tok, void *workspace,
+                                   size_t ws_bytes, bool pow2, hipStream_t stream)
+{
+    try {
+        if (!shape)
+            return PURO_ERR_NULL;
+        const puro_qk_norm_rope_t &r = *shape;
+        if ((transpose_out != 0 && transpose_out != 1) || (accumulate != 0 && accumulate != 1))
+            return PURO_ERR_ENUM;
+        puro_status_t st = check_rope(r);
+        if (st != PURO_OK)
+            return st;
+        const int64_t cq = (int64_t)r.heads_q * r.head_dim, ck = (int64_t)r.heads_kv * r.head_dim, cols = cq + 2 * ck;
+        const bool empty = r.tokens == 0, norm = r.wq != nullptr;
+        // the quantised tensor is formed here: dv stands for its input in the shared checks
+        st = check_quant(dv, PURO_BF16, r.tokens, cols, cols, q_row, ldq_row, cols, s_row);
+        if (st == PURO_OK)
+            st = check_quant(dv, PURO_BF16, r.tokens, cols, cols, q_tok, ldq_tok, transpose_out ? r.tokens : cols, s_tok);
+        if (st == PURO_OK)
+            st = check_bf16(dv, lddv, ck, empty);
+        if (st == PURO_OK)
+            st = check_bf16(dq, lddq, cq, empty);
+        if (st == PURO_OK)
+            st = check_bf16(dk, lddk, ck, empty);
+        if (st == PURO_OK && norm)
+            st = check_bf16(q, ldq, cq, empty);
+        if (st == PURO_OK && norm)
+            st = check_bf16(k, ldk, ck, empty);
+        if (st == PURO_OK && dx)
+            st = check_bf16(dx, lddx, cols, empty);
+        if (st != PURO_OK)
+            return st;
+        if (norm && (!dwq || !dwk || (!empty && !rstd)))
+            return PURO_ERR_NULL;
+        if (norm && (!aligned(rstd, 4) || !aligned(dwq, 4) || !aligned(dwk, 4)))
+            return PURO_ERR_ALIGN;
+        const puro::RopeShape rs = rope_shape(r, q, ldq, k, ldk);
+        const size_t need = puro::rope_bwd_workspace_bytes(rs, norm);
+        if (need > 0 && (!workspace || ws_bytes < need || !aligned(workspace, 256)))
+            return PURO_ERR_WORKSPACE;
+        if (empty && !norm)
+            return PURO_OK;
+        const puro::RopeBwd b{rs, static_cast<const uint16_t *>(dq), lddq, static_cast<const uint16_t *>(dk), lddk,
+                              static_cast<const uint16_t *>(dv), lddv, rstd, static_cast<uint16_t *>(dx), lddx, dwq,
+                              dwk, accumulate == 1, nullptr, nullptr};
+        return from_hip(puro::launch_rope_bwd(b, q_row, ldq_row, s_row, transpose_out == 1, q_tok, ldq_tok, s_tok, pow2,
+                                              workspace, stream));
+    } catch (...) {
+        return PURO_ERR_INTERNAL;
+    }
+}
+
+puro_status_t puro_fp8_qk_norm_rope_bwd_quant_dual(const puro_qk_norm_rope_t *shape, const void *dq, int64_t lddq,
+                                                   const void *dk, int64_t lddk, const void *dv, int64_t lddv,
+                                                   const void *q, int64_t ldq, const void *k, int64_t ldk,
+                                                   const float *rstd, void *dx, int64_t lddx, float *dwq, float *dwk,
+                                                   int accumulate, uint8_t *q_row, int64_t ldq_row, float *s_row,
+                                                   int transpose_out, uint8_t *q_tok, int64_t ldq_tok, float *s_tok,
+                                                   void *workspace, size_t ws_bytes, hipStream_t stream)
+{
+    return rope_bwd_impl(shape, dq, lddq, dk, lddk, dv, lddv, q, ldq, k, ldk, rstd, dx, lddx, dwq, dwk, accumulate,
+                         q_row, ldq_row, s_row, transpose_out, q_tok, ldq_tok, s_tok, workspace, ws_bytes, false, stream);
+}
+
+puro_status_t puro_fp8_qk_norm_rope_bwd_quant_dual_pow2(const puro_qk_norm_rope_t *shape, const void *dq,
+                                                        int64_t lddq, const void *dk, int64_t lddk, const void *dv,
+                                                        int64_t lddv, const void *q, int64_t ldq, const void *k,
+                                                        int64_t ldk, const float *rstd, void *dx, int64_t lddx,
+                                                        float *dwq, float *dwk, int accumulate, uint8_t *q_row,
+                                                        int64_t ldq_row, float *s_row, int transpose_out,
+                                                        uint8_t *q_tok, int64_t ldq_tok, float *s_tok, void *workspace,
+                                                        size_t ws_bytes, hipStream_t stream)
+{
+    return rope_bwd_impl(shape, dq, lddq, dk, lddk, dv, lddv, q, ldq, k, ldk, rstd, dx, lddx, dwq, dwk, accumulate,
+                         q_row, ldq_row, s_row, transpose_out, q_tok, ldq_tok, s_tok, workspace, ws_bytes, true, stream);
+}
+
+static bool bad_attention_shape(const puro_attention_t &a)
+{
+    return bad_heads(a.heads_q, a.heads_kv, a.head_dim) || a.heads_q % a.heads_kv || a.sequences < 0 ||
+           bad_extent(a.tokens_q) || bad_extent(a.tokens_k) || bad_extent(a.max_q) || bad_extent(a.max_k);
+}
+
+static puro::AttnShape attention_shape(const puro_attention_t &a)
+{
+    // no sequence has more rows than its tensor
+    const int64_t mq = a.max_q < a.tokens_q ? a.max_q : a.tokens_q, mk = a.max_k < a.tokens_k ? a.max_k : a.tokens_k;
+    return puro::AttnShape{a.heads_q, a.heads_kv, a.head_dim, a.sequences, a.q_offsets, a.q_lengths, a.k_offsets,
+                           a.k_lengths, a.tokens_q, a.tokens_k, (int)mq, (int)mk, a.causal == 1};
+}
+
+static puro_status_t check_attention(const puro_attention_t &a, bool backward)
+{
+    if (a.causal != 0 && a.causal != 1)
+        return PURO_ERR_ENUM;
+    if (bad_attention_shape(a) || !puro::attn_fits(attention_shape(a), backward))
+        return PURO_ERR_SHAPE;
+    if (a.sequences > 0 && (!a.q_offsets || !a.k_offsets))
+        return PURO_ERR_NULL;
+    if (!aligned(a.q_offsets, 4) || !aligned(a.q_lengths, 4) || !aligned(a.k_offsets, 4) || !aligned(a.k_lengths, 4))
+        return PURO_ERR_ALIGN;
+    if (!(a.scale > 0.0f) || !std::isfinite(a.scale))
+        return PURO_ERR_VALUE;
+    return PURO_OK;
+}
+
+// q, k and v of both directions.
+static puro_status_t check_qkv(const puro_attention_t &a, const void *q, int64_t ldq, const void *k, int64_t ldk,
+                               const void *v, int64_t ldv)
+{
+    const int64_t cq = (int64_t)a.heads_q * a.head_dim, ck = (int64_t)a.heads_kv * a.head_dim;
+    puro_status_t st = check_bf16(q, ldq, cq, a.tokens_q == 0);
+    if (st == PURO_OK)
+        st = check_bf16(k, ldk, ck, a.tokens_k == 0);
+    if (st == PURO_OK)
+        st = check_bf16(v, ldv, ck, a.tokens_k == 0);
+    return st;
+}
+
+size_t puro_fp8_attention_workspace_size(const puro_attention_t *shape)
+{
+    if (!shape || bad_attention_shape(*shape) || !puro::attn_fits(attention_shape(*shape), false))
+        return 0;
+    return puro::attn_workspace_bytes(attention_shape(*shape));
+}
+
+size_t puro_fp8_attention_bwd_workspace_size(const puro_attention_t *shape)
+{
+    if (!shape || bad_attention_shape(*shape) || !puro::attn_fits(attention_shape(*shape), true))
+        return 0;
+    return puro::attn_bwd_workspace_bytes(attention_shape(*shape));
+}
+
+puro_status_t puro_fp8_attention(const puro_attention_t *shape, const void *q, int64_t ldq, const void *k, int64_t ldk,
+                                 const void *v, int64_t ldv, void *o, int64_t ldo, float *lse, void *workspace,
+                                 size_t ws_bytes, hipStream_t stream)
+{
+    try {
+        if (!shape)
+            return PURO_ERR_NULL;
+        puro_status_t st = check_attention(*shape, false);
+        if (st == PURO_OK)
+            st = check_qkv(*shape, q, ldq, k, ldk, v, ldv);
+        if (st == PURO_OK)
+            st = check_bf16(o, ldo, (int64_t)shape->heads_q * shape->head_dim, shape->tokens_q == 0);
+        if (st != PURO_OK)
+            return st;
+        if (!aligned(lse, 4))
+            return PURO_ERR_ALIGN;
+        const puro::AttnShape s = attention_shape(*shape);
+        const size_t need = puro::attn_workspace_bytes(s);
+        if (need > 0 && (!workspace || ws_bytes < need || !aligned(workspace, 256)))
+            return PURO_ERR_WORKSPACE;
+        if (s.seqs == 0 || s.max_q == 0)
+            return PURO_OK;
+        const puro::AttnFwd a{s, static_cast<const uint16_t *>(q), ldq, static_cast<const uint16_t *>(k), ldk,
+                              static_cast<const uint16_t *>(v), ldv, shape->scale, static_cast<uint16_t *>(o), ldo,
+                              lse, 0.0f, 0, 0, nullptr, nullptr};
+        return from_hip(puro::launch_attn(a, workspace, stream));
+    } catch (...) {
+        return PURO_ERR_INTERNAL;
+    }
+}
+
+puro_status_t puro_fp8_attention_bwd(const puro_attention_t *shape, const void *dout, int64_t lddout, const void *q,
+                                     int64_t ldq, const void *k, int64_t ldk, const void *v, int64_t ldv,
+                                     const void *o, int64_t ldo, const float *lse, void *dq, int64_t lddq, void *dk,
+                                     int64_t lddk, void *dv, int64_t lddv, void *workspace, size_t ws_bytes,
+                                     hipStream_t stream)
+{
+    try {
+        if (!shape)
+            return PURO_ERR_NULL;
+        puro_status_t st = check_attention(*shape, true);
+        if (st == PURO_OK)
+            st = check_qkv(*shape, q, ldq, k, ldk, v, ldv);
+        if (st == PURO_OK)
+            st = check_qkv(*shape, dq, lddq, dk, lddk, dv, lddv);
+        const int64_t cq = (int64_t)shape->heads_q * shape->head_dim;
+        if (st == PURO_OK)
+            st = check_bf16(dout, lddout, cq, shape->tokens_q == 0);
+        if (st == PURO_OK)
+            st = check_bf16(o, ldo, cq, shape->tokens_q == 0);
+        if (st != PURO_OK)
+            return st;
+        if (shape->tokens_q > 0 && !lse)
+            return PURO_ERR_NULL;
+        if (!aligned(lse, 4))
+            return PURO_ERR_ALIGN;
+        const puro::AttnShape s = attention_shape(*shape);
+        const size_t need = puro::attn_bwd_workspace_bytes(s);
+        if (need > 0 && (!workspace || ws_bytes < need || !aligned(workspace, 256)))
+            return PURO_ERR_WORKSPACE;
+        if (s.seqs == 0)
+            return PURO_OK;
+        const puro::AttnBwd b{s, static_cast<const uint16_t *>(dout), lddout, static_cast<const uint16_t *>(q), ldq,
+                              static_cast<const uint16_t *>(k), ldk, static_cast<const uint16_t *>(v), ldv,
+                              static_cast<const uint16_t *>(o), ldo, lse, shape->scale, static_cast<uint16_t *>(dq),
+                              lddq, static_cast<uint16_t *>(dk), lddk, static_cast<uint16_t *>(dv), lddv, 0.0f, 0,
+                              nullptr, nullptr};
+        return from_hip(puro::launch_attn_bwd(b, workspace, stream));
+    } catch (...) {
+        return PURO_ERR_INTERNAL;
+    }
+}
+
 const char *puro_status_string(puro_status_t status)
 {
     switch (status) {

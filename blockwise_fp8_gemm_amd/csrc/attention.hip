@@ -1,0 +1,777 @@
+// Attention of packed sequences with grouped heads, and its gradient (gfx950).
+//
+//   S = c q k^T,  L = log sum exp S,  P = exp(S - L),  o = P v
+//   dP = do v^T,  dS = P (dP - D),  D = sum over the head of do o
+//   dv = P^T do,  dq = c dS k,  dk = c dS^T q
+//
+// Query i of n sees keys 0 .. m - 1, or 0 .. i + m - n with a causal mask.
+// Products run on the BF16 matrix cores (32x32x16) with FP32 accumulation.
+// Every operand tile is a [rows][D] run of BF16 rows in LDS, copied there
+// straight from memory, and read in two ways: rows (a lane takes 8 consecutive
+// elements of one row) and columns (transposing reads).  Scores are formed
+// transposed where the softmax runs along the keys (a lane then owns one query,
+// so that maximum, sum and rescaling are per lane), and an accumulator's 16
+// values of a lane are, in order, what the next product wants as its operand:
+// the order of a product's contraction is free, so that the transposing reads
+// take their rows in the accumulator's order instead of moving P between lanes.
+//
+// P and dS enter their products as BF16 numbers (each rounded once, 2^-9 of
+// itself; the results are BF16 too, and the roundings of a row's many terms
+// average out); scores, statistics and every sum are FP32.
+#include "common.h"
+#include "kernels.h"
+
+#include <type_traits>
+
+namespace puro {
+
+namespace {
+
+typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
+typedef short v4s __attribute__((ext_vector_type(4)));
+typedef float v16f __attribute__((ext_vector_type(16)));
+typedef uint32_t v4u __attribute__((ext_vector_type(4)));
+
+constexpr float kNoMax = -0x1p100f;   // running maximum (log2 units) before the first visible key
+constexpr float kLog2e = 0x1.715476p0f, kLn2 = 0x1.62e430p-1f;
+
+__device__ __forceinline__ uint32_t lds_addr(const void *p)
+{
+    return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void *)p;
+}
+
+// 16 (4) bytes per lane from base + off (base wave-uniform) to the wave's LDS
+// base + 16 (4) lane.  M0 is set in the same statement and nothing else here
+// reads it; the copies count in vmcnt, which wait_copies() waits on.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+__device__ __forceinline__ void copy16(const void *base, uint32_t off, uint8_t *lds_wave_base)
+{
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
+                 :: "v"(off), "s"(base), "s"(lds_addr(lds_wave_base)) : "memory", "m0");
+}
+__device__ __forceinline__ void copy4(const void *base, uint32_t off, void *lds_wave_base)
+{
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dword %0, %1"
+                 :: "v"(off), "s"(base), "s"(lds_addr(lds_wave_base)) : "memory", "m0");
+}
+#pragma clang diagnostic pop
+template <int N> __device__ __forceinline__ void wait_copies() { asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory"); }
+
+// ---------------------------------------------------------------------------
+// Tiles of BF16 rows in LDS.  16-byte segment s of row r sits at s ^ swz(r): any
+// 16 consecutive rows hold one segment column on 16 different banks' places
+// (row reads), and the four rows x 64 bytes of a transposing read lie on
+// different banks too.
+// ---------------------------------------------------------------------------
+template <int D> struct Tile {
+    static constexpr int ROW = 2 * D, SEGS = D / 8, SLICES = D / 16, BLOCKS = D / 32;
+    static constexpr int ROWS_PER_KB = 1024 / ROW;
+
+    __device__ __forceinline__ static int swz(int row)
+    {
+        return D == 128 ? ((row & 3) << 2) | ((row >> 2) & 3) : (((row >> 1) & 1) << 2) | ((row >> 2) & 3);
+    }
+
+    // This wave's share of a tile of ROWS rows from g on (row stride ld bytes); rows past `last` are
+    // copies of it, so that nothing behind a sequence is read.
+    template <int ROWS, int NW>
+    __device__ __forceinline__ static void stage(uint8_t *t, const uint16_t *g, uint32_t ld, int last, int wave, int lane)
+    {
+        constexpr int CHUNKS = ROWS / ROWS_PER_KB;
+        static_assert(CHUNKS % NW == 0, "whole 1 KB pieces per wave");
+#pragma unroll
+        for (int it = 0; it < CHUNKS / NW; it++) {
+            const int c = wave + NW * it, row = c * ROWS_PER_KB + lane / SEGS;
+            const int seg = (lane % SEGS) ^ swz(row);
+            copy16(g, (uint32_t)min(row, last) * ld + (uint32_t)(seg * 16), t + c * 1024);
+        }
+    }
+
+    // Rows row0 + lane % 32 (row0 a multiple of 32), elements 16 s + 8 (lane / 32) .. +7.
+    __device__ __forceinline__ static v8bf rows(const uint8_t *t, int row0, int s, int lane)
+    {
+        const int r = lane & 31;
+        return __builtin_bit_cast(v8bf, *reinterpret_cast<const v4u *>(
+                                            t + (row0 + r) * ROW + (((2 * s + (lane >> 5)) ^ swz(r)) << 4)));
+    }
+
+    // Column 32 b + lane % 32 of the 16 rows from row0 on (a multiple of 16): rows 4 h .. 4 h + 3 and
+    // 8 + 4 h .. 8 + 4 h + 3, h = lane / 32, which is the order of an accumulator's 8 values.
+    __device__ __forceinline__ static v8bf cols(const uint8_t *t, int row0, int b, int lane)
+    {
+        typedef __attribute__((address_space(3))) v4s lds_v4s;
+        const int i = lane & 15, seg = 4 * b + 2 * ((lane >> 4) & 1) + ((i & 3) >> 1);
+        v4s q[2];
+#pragma unroll
+        for (int j = 0; j < 2; j++) {
+            const int r = 8 * j + 4 * (lane >> 5) + (i >> 2);
+            q[j] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                (lds_v4s *)(t + (row0 + r) * ROW + ((seg ^ swz(r)) << 4) + 8 * (i & 1)));
+        }
+        return __builtin_bit_cast(v8bf, __builtin_shufflevector(q[0], q[1], 0, 1, 2, 3, 4, 5, 6, 7));
+    }
+
+    // Row `row`'s elements for rows()'s place in a product, straight from memory.
+    __device__ __forceinline__ static void load(const uint16_t *row, int lane, v8bf (&f)[SLICES])
+    {
+#pragma unroll
+        for (int s = 0; s < SLICES; s++)
+            f[s] = __builtin_bit_cast(v8bf, *reinterpret_cast<const v4u *>(row + 16 * s + 8 * (lane >> 5)));
+    }
+};
+
+__device__ __forceinline__ v16f mfma(v8bf a, v8bf b, v16f c) { return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0); }
+
+__device__ __forceinline__ v16f splat(float x) { return v16f{x, x, x, x, x, x, x, x, x, x, x, x, x, x, x, x}; }
+
+// Row of an accumulator's value i in this lane.
+__device__ __forceinline__ int acc_row(int i, int lane) { return 8 * (i >> 2) + 4 * (lane >> 5) + (i & 3); }
+
+// Values 8 s .. 8 s + 7 of an accumulator as an operand.
+__device__ __forceinline__ v8bf operand(const v16f &v, int s)
+{
+    const v4u w = {to_bf16x2(v[8 * s], v[8 * s + 1]), to_bf16x2(v[8 * s + 2], v[8 * s + 3]),
+                   to_bf16x2(v[8 * s + 4], v[8 * s + 5]), to_bf16x2(v[8 * s + 6], v[8 * s + 7])};
+    return __builtin_bit_cast(v8bf, w);
+}
+
+// x of the lane's other half (lane ^ 32).
+__device__ __forceinline__ float other_half(float x)
+{
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return __uint_as_float((threadIdx.x & 32) ? r[0] : r[1]);
+}
+
+// A sequence's rows, held inside the tensor and the announced maximum whatever the arrays say.
+struct Rows {
+    int start, len;
+};
+__device__ __forceinline__ Rows rows_of(const int32_t *off, const int32_t *len, int s, int64_t tokens, int most)
+{
+    const int64_t total = tokens, a = off[s];
+    const int64_t start = a < 0 ? 0 : a > total ? total : a;
+    int64_t n = len ? (int64_t)len[s] : (int64_t)off[s + 1] - a;
+    n = n < total - start ? n : total - start;
+    n = n < most ? n : most;
+    return Rows{(int)start, (int)(n < 0 ? 0 : n)};
+}
+__device__ __forceinline__ Rows q_rows(const AttnShape &a, int s) { return rows_of(a.q_off, a.q_len, s, a.tokens_q, a.max_q); }
+__device__ __forceinline__ Rows k_rows(const AttnShape &a, int s) { return rows_of(a.k_off, a.k_len, s, a.tokens_k, a.max_k); }
+
+// A lane's 4 D / 32 runs of four values of one row (acc_row's order), times f, as BF16.
+template <int D> __device__ __forceinline__ void store_row(uint16_t *row, const v16f (&acc)[D / 32], float f, int lane)
+{
+#pragma unroll
+    for (int b = 0; b < D / 32; b++)
+#pragma unroll
+        for (int g = 0; g < 4; g++)
+            *reinterpret_cast<uint2 *>(row + 32 * b + 8 * g + 4 * (lane >> 5)) =
+                make_uint2(to_bf16x2(acc[b][4 * g] * f, acc[b][4 * g + 1] * f),
+                           to_bf16x2(acc[b][4 * g + 2] * f, acc[b][4 * g + 3] * f));
+}
+
+// ---------------------------------------------------------------------------
+// Forward.  Running state of 32 queries of a wave (one per lane and half):
+// maximum m in log2 units, this half's share of the sum, the transposed output.
+// The maximum only moves, and sum and output are only rescaled, when a score
+// passes it by more than 8 (2^8): P stays below 2^8 and keeps its relative
+// precision, and most tiles need no rescaling.
+// ---------------------------------------------------------------------------
+template <int D> struct Softmax {
+    float m = kNoMax, l = 0.0f;
+    v16f o[D / 32];
+
+    __device__ __forceinline__ Softmax()
+    {
+#pragma unroll
+        for (int b = 0; b < D / 32; b++)
+            o[b] = splat(0.0f);
+    }
+
+    // N blocks of 32 keys: scores (transposed) of rows kt, then P v of rows vt.  first .. : the blocks' first
+    // key; lim: the lane's last visible key; masked: whether some key of the blocks may be hidden.
+    template <int N>
+    __device__ __forceinline__ void step(const uint8_t *kt, const uint8_t *vt, const v8bf (&q)[D / 16], float c2,
+                                         int first, int lim, bool masked, int lane)
+    {
+        v16f s[N];
+#pragma unroll
+        for (int n = 0; n < N; n++) {
+            s[n] = splat(0.0f);
+#pragma unroll
+            for (int k = 0; k < D / 16; k++)
+                s[n] = mfma(Tile<D>::rows(kt, 32 * n, k, lane), q[k], s[n]);
+        }
+        if (masked) {
+#pragma unroll
+            for (int n = 0; n < N; n++)
+#pragma unroll
+                for (int i = 0; i < 16; i++)
+                    s[n][i] = first + 32 * n + acc_row(i, lane) > lim ? -INFINITY : s[n][i];
+        }
+        float top = s[0][0];
+#pragma unroll
+        for (int n = 0; n < N; n++)
+#pragma unroll
+            for (int i = 0; i < 16; i++)
+                top = fmaxf(top, s[n][i]);
+        top = fmaxf(top, other_half(top)) * c2;
+        if (__any(top > m + 8.0f)) {
+            const float now = fmaxf(m, top), f = __builtin_amdgcn_exp2f(m - now);
+            m = now;
+            l *= f;
+#pragma unroll
+            for (int b = 0; b < D / 32; b++)
+                o[b] *= f;
+        }
+#pragma unroll
+        for (int n = 0; n < N; n++)
+#pragma unroll
+            for (int i = 0; i < 16; i++) {
+                s[n][i] = __builtin_amdgcn_exp2f(fmaf(s[n][i], c2, -m));
+                l += s[n][i];
+            }
+#pragma unroll
+        for (int n = 0; n < N; n++)
+#pragma unroll
+            for (int k = 0; k < 2; k++) {
+                const v8bf p = operand(s[n], k);
+#pragma unroll
+                for (int b = 0; b < D / 32; b++)
+                    o[b] = mfma(Tile<D>::cols(vt, 32 * n + 16 * k, b, lane), p, o[b]);
+            }
+    }
+};
+
+// Share `split` of n tiles.
+__device__ __forceinline__ int share(int n, int split, int splits) { return (int)((int64_t)n * split / splits); }
+
+// Where row t's partial results of a split go: [split][head][row].
+__device__ __forceinline__ int64_t part_row(const AttnFwd &a, int split, int head, int t)
+{
+    return ((int64_t)split * a.s.hq + head) * a.s.tokens_q + t;
+}
+
+// The results of one query row, whole or a split's share.
+template <int D>
+__device__ __forceinline__ void put_row(const AttnFwd &a, Softmax<D> &x, int split, int head, int t, int lane)
+{
+    const float l = x.l + other_half(x.l);
+    if (a.splits == 1) {
+        store_row<D>(a.o + (int64_t)t * a.ldo + head * D, x.o, l > 0.0f ? 1.0f / l : 0.0f, lane);
+        if (a.lse && lane < 32)
+            a.lse[(int64_t)head * a.s.tokens_q + t] = l > 0.0f ? (x.m + __log2f(l)) * kLn2 : -INFINITY;
+        return;
+    }
+    const int64_t p = part_row(a, split, head, t);
+    float *o = a.part + p * D;
+#pragma unroll
+    for (int b = 0; b < D / 32; b++)
+#pragma unroll
+        for (int g = 0; g < 4; g++)
+            *reinterpret_cast<float4 *>(o + 32 * b + 8 * g + 4 * (lane >> 5)) =
+                make_float4(x.o[b][4 * g], x.o[b][4 * g + 1], x.o[b][4 * g + 2], x.o[b][4 * g + 3]);
+    if (lane < 32)
+        a.stat[p] = make_float2(x.m, l);
+}
+
+// Many rows: NW waves of 32 queries of one head, 64 keys at a time through LDS.
+constexpr int KT = 64;
+template <int D, int NW>
+__global__ __launch_bounds__(64 * NW) void attn_fwd_kernel(AttnFwd a)
+{
+    constexpr int R = 32 * NW, TILE = KT * 2 * D;
+    __shared__ __attribute__((aligned(16))) uint8_t lds[2][2][TILE];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    // blocks of later rows, which see more keys, first; a sequence's key head on one XCD where their
+    // number is a multiple of 8 (workgroups go round the XCDs)
+    const int units = a.s.seqs * a.s.hk, group = a.s.hq / a.s.hk;
+    const int x = (int)blockIdx.x / (units * group), y = (int)blockIdx.x % (units * group);
+    const int unit = y % units, seq = unit / a.s.hk, kh = unit % a.s.hk, head = kh * group + y / units;
+    const int split = x % a.splits, block = a.blocks - 1 - x / a.splits;
+    const Rows q = q_rows(a.s, seq), k = k_rows(a.s, seq);
+    const int q0 = block * R;
+    if (q0 >= q.len)
+        return;
+    const int shift = k.len - q.len;
+    const int seen = a.s.causal ? max(0, min(k.len, min(q0 + R, q.len) + shift)) : k.len;
+    const int tiles = (seen + KT - 1) / KT, t0 = share(tiles, split, a.splits), t1 = share(tiles, split + 1, a.splits);
+
+    const uint16_t *kp = a.k + (int64_t)k.start * a.ldk + kh * D, *vp = a.v + (int64_t)k.start * a.ldv + kh * D;
+    auto stage = [&](int t) {
+        uint8_t *dst = lds[t & 1][0];
+        const int last = k.len - 1 - t * KT;
+        Tile<D>::template stage<KT, NW>(dst, kp + (int64_t)t * KT * a.ldk, (uint32_t)a.ldk * 2, last, wave, lane);
+        Tile<D>::template stage<KT, NW>(dst + TILE, vp + (int64_t)t * KT * a.ldv, (uint32_t)a.ldv * 2, last, wave, lane);
+    };
+    if (t0 < t1)
+        stage(t0);
+    const int w0 = q0 + 32 * wave, i = w0 + (lane & 31), row = q.start + min(i, q.len - 1);
+    v8bf qf[D / 16];
+    Tile<D>::load(a.q + (int64_t)row * a.ldq + head * D, lane, qf);
+    const int lim = a.s.causal ? min(k.len - 1, i + shift) : k.len - 1;
+    const int low = a.s.causal ? min(k.len - 1, w0 + shift) : k.len - 1;           // the wave's first row's
+    const int high = a.s.causal ? min(k.len - 1, w0 + 31 + shift) : k.len - 1;     // and its last one's
+
+    Softmax<D> st;
+    for (int t = t0; t < t1; t++) {
+        wait_copies<0>();
+        __syncthreads();
+        if (t + 1 < t1)
+            stage(t + 1);
+        if (t * KT <= high)
+            st.template step<KT / 32>(lds[t & 1][0], lds[t & 1][1], qf, a.c2, t * KT, lim, t * KT + KT - 1 > low, lane);
+    }
+    if (i < q.len)
+        put_row<D>(a, st, split, head, q.start + i, lane);
+}
+
+// Few rows (at most 32 of a key head's queries over all its query heads): a wave
+// holds them all and the workgroup's four waves take keys of their own, 32 at a
+// time through LDS of their own; their results are added up at the end.
+template <int D>
+__global__ __launch_bounds__(256) void attn_rows_kernel(AttnFwd a)
+{
+    constexpr int NW = 4, KW = 32, TILE = KW * 2 * D, S = 2, WAVE = S * 2 * TILE;
+    static_assert(WAVE >= 32 * (D + 4) * 4, "a wave's results take its tiles' place");
+    __shared__ __attribute__((aligned(16))) uint8_t lds[NW][WAVE];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int units = a.s.seqs * a.s.hk, group = a.s.hq / a.s.hk;
+    const int unit = (int)blockIdx.x % units, split = (int)blockIdx.x / units, seq = unit / a.s.hk, kh = unit % a.s.hk;
+    const Rows q = q_rows(a.s, seq), k = k_rows(a.s, seq);
+    const int cols = q.len * group;
+    if (cols == 0)
+        return;
+    const int shift = k.len - q.len, seen = k.len;
+    const int tiles = (seen + KW - 1) / KW, parts = a.splits * NW, part = split * NW + wave;
+    const int t0 = share(tiles, part, parts), t1 = share(tiles, part + 1, parts);
+
+    const uint16_t *kp = a.k + (int64_t)k.start * a.ldk + kh * D, *vp = a.v + (int64_t)k.start * a.ldv + kh * D;
+    auto stage = [&](int t) {
+        uint8_t *dst = lds[wave] + (t & 1) * 2 * TILE;
+        const int last = k.len - 1 - t * KW;
+        Tile<D>::template stage<KW, 1>(dst, kp + (int64_t)t * KW * a.ldk, (uint32_t)a.ldk * 2, last, 0, lane);
+        Tile<D>::template stage<KW, 1>(dst + TILE, vp + (int64_t)t * KW * a.ldv, (uint32_t)a.ldv * 2, last, 0, lane);
+    };
+    constexpr int COPIES = 2 * TILE / 1024;
+    const int c = min(lane & 31, cols - 1), i = c / group, head = kh * group + c % group;
+    v8bf qf[D / 16];
+    Tile<D>::load(a.q + (int64_t)(q.start + i) * a.ldq + head * D, lane, qf);
+    const int lim = a.s.causal ? min(k.len - 1, i + shift) : k.len - 1;
+    const int low = a.s.causal ? min(k.len - 1, shift) : k.len - 1;
+
+    Softmax<D> st;
+    if (t0 < t1)
+        stage(t0);
+    for (int t = t0; t < t1; t++) {
+        // the tile after this one, or this one again in its place's other half, so that the count in flight is the same
+        if (t + 1 < t1) {
+            stage(t + 1);
+            wait_copies<COPIES>();
+        } else {
+            wait_copies<0>();
+        }
+        st.template step<1>(lds[wave] + (t & 1) * 2 * TILE, lds[wave] + (t & 1) * 2 * TILE + TILE, qf, a.c2, t * KW, lim,
+                            t * KW + KW - 1 > low, lane);
+        __builtin_amdgcn_s_waitcnt(0xc07f);   // lgkmcnt(0): the tile is read before copies go over it
+    }
+    // the waves' results: [column][D + 4] floats, output then maximum and sum
+    constexpr int LD = D + 4;
+    float *mine = reinterpret_cast<float *>(lds[wave]) + (lane & 31) * LD;
+    const float l = st.l + other_half(st.l);
+#pragma unroll
+    for (int b = 0; b < D / 32; b++)
+#pragma unroll
+        for (int g = 0; g < 4; g++)
+            *reinterpret_cast<float4 *>(mine + 32 * b + 8 * g + 4 * (lane >> 5)) =
+                make_float4(st.o[b][4 * g], st.o[b][4 * g + 1], st.o[b][4 * g + 2], st.o[b][4 * g + 3]);
+    if (lane < 32)
+        *reinterpret_cast<float2 *>(mine + D) = make_float2(st.m, l);
+    __syncthreads();
+    constexpr int RUN = 8, PER = 256 / (D / RUN);   // columns at a time, 8 elements a thread
+    for (int cc = threadIdx.x / (D / RUN); cc < cols; cc += PER) {
+        const int d = (threadIdx.x % (D / RUN)) * RUN;
+        float m = kNoMax, sum = 0.0f, v[RUN];
+#pragma unroll
+        for (int w = 0; w < NW; w++)
+            m = fmaxf(m, reinterpret_cast<const float *>(lds[w])[cc * LD + D]);
+#pragma unroll
+        for (int e = 0; e < RUN; e++)
+            v[e] = 0.0f;
+#pragma unroll
+        for (int w = 0; w < NW; w++) {
+            const float *p = reinterpret_cast<const float *>(lds[w]) + cc * LD;
+            const float f = __builtin_amdgcn_exp2f(p[D] - m);
+            sum = fmaf(f, p[D + 1], sum);
+#pragma unroll
+            for (int e = 0; e < RUN; e++)
+                v[e] = fmaf(f, p[d + e], v[e]);
+        }
+        const int t = q.start + cc / group, hd = kh * group + cc % group;
+        if (a.splits == 1) {
+            const float f = sum > 0.0f ? 1.0f / sum : 0.0f;
+            *reinterpret_cast<uint4 *>(a.o + (int64_t)t * a.ldo + hd * D + d) =
+                make_uint4(to_bf16x2(v[0] * f, v[1] * f), to_bf16x2(v[2] * f, v[3] * f), to_bf16x2(v[4] * f, v[5] * f),
+                           to_bf16x2(v[6] * f, v[7] * f));
+            if (a.lse && d == 0)
+                a.lse[(int64_t)hd * a.s.tokens_q + t] = sum > 0.0f ? (m + __log2f(sum)) * kLn2 : -INFINITY;
+        } else {
+            const int64_t p = part_row(a, split, hd, t);
+            *reinterpret_cast<float4 *>(a.part + p * D + d) = make_float4(v[0], v[1], v[2], v[3]);
+            *reinterpret_cast<float4 *>(a.part + p * D + d + 4) = make_float4(v[4], v[5], v[6], v[7]);
+            if (d == 0)
+                a.stat[p] = make_float2(m, sum);
+        }
+    }
+}
+
+// The splits' shares of a row and head: o = sum 2^(m_s - m) o_s / sum 2^(m_s - m) l_s.
+template <int D>
+__global__ __launch_bounds__(256) void attn_join_kernel(AttnFwd a)
+{
+    constexpr int PER = 256 / (D / 4);   // rows and heads of a workgroup
+    const int64_t n = (int64_t)blockIdx.x * PER + threadIdx.x / (D / 4), rows = (int64_t)a.s.max_q * a.s.hq;
+    const int seq = (int)(n / rows), head = (int)(n % a.s.hq), i = (int)(n % rows / a.s.hq), d = (threadIdx.x % (D / 4)) * 4;
+    if (seq >= a.s.seqs)
+        return;
+    const Rows q = q_rows(a.s, seq);
+    if (i >= q.len)
+        return;
+    const int t = q.start + i;
+    float m = kNoMax, sum = 0.0f;
+    for (int s = 0; s < a.splits; s++)
+        m = fmaxf(m, a.stat[part_row(a, s, head, t)].x);
+    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int s = 0; s < a.splits; s++) {
+        const int64_t p = part_row(a, s, head, t);
+        const float2 st = a.stat[p];
+        const float f = __builtin_amdgcn_exp2f(st.x - m);
+        const float4 o = *reinterpret_cast<const float4 *>(a.part + p * D + d);
+        sum = fmaf(f, st.y, sum);
+        v = make_float4(fmaf(f, o.x, v.x), fmaf(f, o.y, v.y), fmaf(f, o.z, v.z), fmaf(f, o.w, v.w));
+    }
+    const float f = sum > 0.0f ? 1.0f / sum : 0.0f;
+    *reinterpret_cast<uint2 *>(a.o + (int64_t)t * a.ldo + head * D + d) =
+        make_uint2(to_bf16x2(v.x * f, v.y * f), to_bf16x2(v.z * f, v.w * f));
+    if (a.lse && d == 0)
+        a.lse[(int64_t)head * a.s.tokens_q + t] = sum > 0.0f ? (m + __log2f(sum)) * kLn2 : -INFINITY;
+}
+
+// ---------------------------------------------------------------------------
+// Gradient.  A first pass forms -L / c and -D of every row and head, with which
+// the two products S and dP start their accumulators: P is then 2^(c log2(e) S')
+// and dS is P dP'.  Two kernels follow: keys' gradients (a workgroup owns keys and
+// goes through the queries of the key head's group) and queries' gradients (it
+// owns queries and goes through the keys).  S, P and dP are formed in both, seven
+// products instead of five, so that no sum is added up in memory: results do not
+// depend on the order workgroups run in.
+// ---------------------------------------------------------------------------
+template <int D>
+__global__ __launch_bounds__(256) void attn_bwd_rows_kernel(AttnBwd a)
+{
+    constexpr int PER = 256 / (D / 8);
+    const int64_t n = (int64_t)blockIdx.x * PER + threadIdx.x / (D / 8);
+    const int64_t t = n / a.s.hq;
+    const int head = (int)(n % a.s.hq), d = (threadIdx.x % (D / 8)) * 8;
+    float sum = 0.0f;
+    if (t < a.s.tokens_q) {
+        float x[8], y[8];
+        Elem<uint16_t>::load8(a.o + t * a.ldo + head * D + d, x);
+        Elem<uint16_t>::load8(a.dout + t * a.lddo + head * D + d, y);
+#pragma unroll
+        for (int e = 0; e < 8; e++)
+            sum = fmaf(x[e], y[e], sum);
+    }
+#pragma unroll
+    for (int w = 1; w < D / 8; w <<= 1)
+        sum += __shfl_xor(sum, w, 64);
+    if (t < a.s.tokens_q && d == 0) {
+        const int64_t r = (int64_t)head * a.s.tokens_q + t;
+        const float lse = a.lse[r];
+        a.nl[r] = fabsf(lse) < INFINITY ? -lse / a.scale : 0.0f;   // rows that see nothing are masked everywhere
+        a.nd[r] = -sum;
+    }
+}
+
+// Keys' and values' gradients: NW waves of 32 keys, 64 queries of one head at a time.
+template <int D, int NW>
+__global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2, 2))) void attn_bwd_k_kernel(AttnBwd a)
+{
+    constexpr int R = 32 * NW, QT = 64, TILE = QT * 2 * D;
+    __shared__ __attribute__((aligned(16))) uint8_t lds[2][2 * TILE + 2 * QT * 4];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int units = a.s.seqs * a.s.hk, group = a.s.hq / a.s.hk;
+    const int block = (int)blockIdx.x / units, unit = (int)blockIdx.x % units;   // earlier keys, seen by more, first
+    const int seq = unit / a.s.hk, kh = unit % a.s.hk;
+    const Rows q = q_rows(a.s, seq), k = k_rows(a.s, seq);
+    const int k0 = block * R;
+    if (k0 >= k.len)
+        return;
+    const int shift = k.len - q.len, tiles = (q.len + QT - 1) / QT;
+    const int t0 = a.s.causal ? min(tiles, max(0, k0 - shift) / QT) : 0, per = tiles - t0, steps = per * group;
+
+    auto stage = [&](int n) {
+        const int h = kh * group + n / per, t = t0 + n % per, last = q.len - 1 - t * QT;
+        const int64_t row = (int64_t)q.start + t * QT;
+        uint8_t *dst = lds[n & 1];
+        Tile<D>::template stage<QT, NW>(dst, a.q + row * a.ldq + h * D, (uint32_t)a.ldq * 2, last, wave, lane);
+        Tile<D>::template stage<QT, NW>(dst + TILE, a.dout + row * a.lddo + h * D, (uint32_t)a.lddo * 2, last, wave, lane);
+        if (wave == 0) {
+            const uint32_t off = (uint32_t)min(lane, last) * 4;
+            copy4(a.nl + (int64_t)h * a.s.tokens_q + row, off, dst + 2 * TILE);
+            copy4(a.nd + (int64_t)h * a.s.tokens_q + row, off, dst + 2 * TILE + QT * 4);
+        }
+    };
+    if (steps > 0)
+        stage(0);
+    const int w0 = k0 + 32 * wave, j = w0 + (lane & 31), row = k.start + min(j, k.len - 1);
+    v8bf kf[D / 16], vf[D / 16];
+    Tile<D>::load(a.k + (int64_t)row * a.ldk + kh * D, lane, kf);
+    Tile<D>::load(a.v + (int64_t)row * a.ldv + kh * D, lane, vf);
+    const int from = a.s.causal ? j - shift : 0;              // the lane's first query
+    const int wfirst = a.s.causal ? w0 - shift : 0, wlast = a.s.causal ? w0 + 31 - shift : 0;
+
+    v16f dk[D / 32], dv[D / 32];
+#pragma unroll
+    for (int b = 0; b < D / 32; b++)
+        dk[b] = dv[b] = splat(0.0f);
+    for (int n = 0; n < steps; n++) {
+        wait_copies<0>();
+        __syncthreads();
+        if (n + 1 < steps)
+            stage(n + 1);
+        const uint8_t *qt = lds[n & 1], *dt = qt + TILE;
+        const float *nl = reinterpret_cast<const float *>(qt + 2 * TILE), *nd = nl + QT;
+        const int i0 = (t0 + n % per) * QT;
+#pragma unroll
+        for (int u = 0; u < QT / 32; u++) {
+            const int i1 = i0 + 32 * u;
+            if (i1 + 31 < wfirst || i1 >= q.len)
+                continue;
+            v16f s, dp;
+#pragma unroll
+            for (int g = 0; g < 4; g++) {
+                const float4 x = *reinterpret_cast<const float4 *>(nl + 32 * u + 8 * g + 4 * (lane >> 5));
+                const float4 y = *reinterpret_cast<const float4 *>(nd + 32 * u + 8 * g + 4 * (lane >> 5));
+                s[4 * g] = x.x; s[4 * g + 1] = x.y; s[4 * g + 2] = x.z; s[4 * g + 3] = x.w;
+                dp[4 * g] = y.x; dp[4 * g + 1] = y.y; dp[4 * g + 2] = y.z; dp[4 * g + 3] = y.w;
+            }
+#pragma unroll
+            for (int x = 0; x < D / 16; x++)
+                s = mfma(Tile<D>::rows(qt, 32 * u, x, lane), kf[x], s);
+#pragma unroll
+            for (int x = 0; x < D / 16; x++)
+                dp = mfma(Tile<D>::rows(dt, 32 * u, x, lane), vf[x], dp);
+            if (i1 < wlast || i1 + 32 > q.len) {
+#pragma unroll
+                for (int e = 0; e < 16; e++) {
+                    const int i = i1 + acc_row(e, lane);
+                    s[e] = i < from || i >= q.len ? -INFINITY : s[e];
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < 16; e++) {
+                s[e] = __builtin_amdgcn_exp2f(s[e] * a.c2);
+                dp[e] *= s[e];
+            }
+#pragma unroll
+            for (int x = 0; x < 2; x++) {
+                const v8bf p = operand(s, x), ds = operand(dp, x);
+#pragma unroll
+                for (int b = 0; b < D / 32; b++) {
+                    dv[b] = mfma(Tile<D>::cols(dt, 32 * u + 16 * x, b, lane), p, dv[b]);
+                    dk[b] = mfma(Tile<D>::cols(qt, 32 * u + 16 * x, b, lane), ds, dk[b]);
+                }
+            }
+        }
+    }
+    if (j < k.len) {
+        store_row<D>(a.dk + (int64_t)row * a.lddk + kh * D, dk, a.scale, lane);
+        store_row<D>(a.dv + (int64_t)row * a.lddv + kh * D, dv, 1.0f, lane);
+    }
+}
+
+// Queries' gradients: NW waves of 32 queries of one head, 64 keys at a time.
+template <int D, int NW>
+__global__ __launch_bounds__(64 * NW) void attn_bwd_q_kernel(AttnBwd a)
+{
+    constexpr int R = 32 * NW, TILE = KT * 2 * D;
+    __shared__ __attribute__((aligned(16))) uint8_t lds[2][2][TILE];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int units = a.s.seqs * a.s.hk, group = a.s.hq / a.s.hk;
+    const int x = (int)blockIdx.x / (units * group), y = (int)blockIdx.x % (units * group);
+    const int unit = y % units, seq = unit / a.s.hk, kh = unit % a.s.hk, head = kh * group + y / units;
+    const Rows q = q_rows(a.s, seq), k = k_rows(a.s, seq);
+    const int q0 = (a.q_blocks - 1 - x) * R;
+    if (q0 >= q.len)
+        return;
+    const int shift = k.len - q.len;
+    const int seen = a.s.causal ? max(0, min(k.len, min(q0 + R, q.len) + shift)) : k.len;
+    const int tiles = (seen + KT - 1) / KT;
+
+    const uint16_t *kp = a.k + (int64_t)k.start * a.ldk + kh * D, *vp = a.v + (int64_t)k.start * a.ldv + kh * D;
+    auto stage = [&](int t) {
+        const int last = k.len - 1 - t * KT;
+        Tile<D>::template stage<KT, NW>(lds[t & 1][0], kp + (int64_t)t * KT * a.ldk, (uint32_t)a.ldk * 2, last, wave, lane);
+        Tile<D>::template stage<KT, NW>(lds[t & 1][1], vp + (int64_t)t * KT * a.ldv, (uint32_t)a.ldv * 2, last, wave, lane);
+    };
+    if (tiles > 0)
+        stage(0);
+    const int w0 = q0 + 32 * wave, i = w0 + (lane & 31), row = q.start + min(i, q.len - 1);
+    v8bf qf[D / 16], df[D / 16];
+    Tile<D>::load(a.q + (int64_t)row * a.ldq + head * D, lane, qf);
+    Tile<D>::load(a.dout + (int64_t)row * a.lddo + head * D, lane, df);
+    const float nl = a.nl[(int64_t)head * a.s.tokens_q + row] * a.c2, nd = a.nd[(int64_t)head * a.s.tokens_q + row];
+    const int lim = a.s.causal ? min(k.len - 1, i + shift) : k.len - 1;
+    const int low = a.s.causal ? min(k.len - 1, w0 + shift) : k.len - 1;
+    const int high = a.s.causal ? min(k.len - 1, w0 + 31 + shift) : k.len - 1;
+
+    v16f dq[D / 32];
+#pragma unroll
+    for (int b = 0; b < D / 32; b++)
+        dq[b] = splat(0.0f);
+    for (int t = 0; t < tiles; t++) {
+        wait_copies<0>();
+        __syncthreads();
+        if (t + 1 < tiles)
+            stage(t + 1);
+        const uint8_t *kt = lds[t & 1][0], *vt = lds[t & 1][1];
+#pragma unroll
+        for (int u = 0; u < KT / 32; u++) {
+            const int j0 = t * KT + 32 * u;
+            if (j0 > high)
+                continue;
+            v16f s = splat(0.0f), dp = splat(nd);
+#pragma unroll
+            for (int e = 0; e < D / 16; e++)
+                s = mfma(Tile<D>::rows(kt, 32 * u, e, lane), qf[e], s);
+#pragma unroll
+            for (int e = 0; e < D / 16; e++)
+                dp = mfma(Tile<D>::rows(vt, 32 * u, e, lane), df[e], dp);
+            if (j0 + 31 > low) {
+#pragma unroll
+                for (int e = 0; e < 16; e++)
+                    s[e] = j0 + acc_row(e, lane) > lim ? -INFINITY : s[e];
+            }
+#pragma unroll
+            for (int e = 0; e < 16; e++)
+                dp[e] *= __builtin_amdgcn_exp2f(fmaf(s[e], a.c2, nl));
+#pragma unroll
+            for (int e = 0; e < 2; e++) {
+                const v8bf ds = operand(dp, e);
+#pragma unroll
+                for (int b = 0; b < D / 32; b++)
+                    dq[b] = mfma(Tile<D>::cols(kt, 32 * u + 16 * e, b, lane), ds, dq[b]);
+            }
+        }
+    }
+    if (i < q.len)
+        store_row<D>(a.dq + (int64_t)row * a.lddq + head * D, dq, a.scale, lane);
+}
+
+constexpr int FWD_WAVES = 8, BWD_K_WAVES = 4, BWD_Q_WAVES = 8;
+
+int64_t blocks_of(int64_t n, int64_t per) { return (n + per - 1) / per; }
+
+// Whether a key head's queries of every sequence fit one wave.
+bool few_rows(const AttnShape &s) { return (int64_t)s.max_q * (s.hq / s.hk) <= 32; }
+
+// Shares of the key axis: where workgroups are fewer than two rounds of the 256 CUs, up to one share for each
+// 256 keys.
+int splits_of(const AttnShape &s)
+{
+    if (s.seqs == 0 || s.max_q == 0)
+        return 1;
+    const int64_t units = (int64_t)s.seqs * s.hk;
+    const int64_t groups = few_rows(s) ? units : units * (s.hq / s.hk) * blocks_of(s.max_q, 32 * FWD_WAVES);
+    int64_t want = groups ? 512 / groups : 1;
+    const int64_t most = s.max_k / (few_rows(s) ? 512 : 1024);
+    want = want < most ? want : most;
+    return (int)(want < 1 ? 1 : want > 64 ? 64 : want);
+}
+
+size_t pad256(size_t n) { return (n + 255) / 256 * 256; }
+
+size_t part_bytes(const AttnShape &s, int splits) { return pad256((size_t)splits * s.hq * s.tokens_q * s.dim * 4); }
+
+template <int D> hipError_t fwd(AttnFwd a, hipStream_t st)
+{
+    const int64_t units = (int64_t)a.s.seqs * a.s.hk;
+    if (few_rows(a.s)) {
+        hipLaunchKernelGGL((attn_rows_kernel<D>), dim3((unsigned)(units * a.splits)), dim3(256), 0, st, a);
+    } else {
+        a.blocks = (int)blocks_of(a.s.max_q, 32 * FWD_WAVES);
+        hipLaunchKernelGGL((attn_fwd_kernel<D, FWD_WAVES>), dim3((unsigned)(units * (a.s.hq / a.s.hk) * a.splits * a.blocks)),
+                           dim3(64 * FWD_WAVES), 0, st, a);
+    }
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess || a.splits == 1)
+        return e;
+    const int64_t rows = (int64_t)a.s.seqs * a.s.max_q * a.s.hq;
+    hipLaunchKernelGGL((attn_join_kernel<D>), dim3((unsigned)blocks_of(rows, 256 / (D / 4))), dim3(256), 0, st, a);
+    return hipGetLastError();
+}
+
+template <int D> hipError_t bwd(const AttnBwd &b, hipStream_t st)
+{
+    const int64_t units = (int64_t)b.s.seqs * b.s.hk;
+    hipError_t e = hipSuccess;
+    if (b.s.tokens_q > 0) {
+        hipLaunchKernelGGL((attn_bwd_rows_kernel<D>), dim3((unsigned)blocks_of(b.s.tokens_q * b.s.hq, 256 / (D / 8))),
+                           dim3(256), 0, st, b);
+        e = hipGetLastError();
+    }
+    if (e == hipSuccess && b.s.max_k > 0 && b.s.tokens_k > 0) {
+        hipLaunchKernelGGL((attn_bwd_k_kernel<D, BWD_K_WAVES>),
+                           dim3((unsigned)(units * blocks_of(b.s.max_k, 32 * BWD_K_WAVES))), dim3(64 * BWD_K_WAVES), 0, st, b);
+        e = hipGetLastError();
+    }
+    if (e == hipSuccess && b.s.max_q > 0 && b.s.tokens_q > 0) {
+        hipLaunchKernelGGL((attn_bwd_q_kernel<D, BWD_Q_WAVES>), dim3((unsigned)(units * (b.s.hq / b.s.hk) * b.q_blocks)),
+                           dim3(64 * BWD_Q_WAVES), 0, st, b);
+        e = hipGetLastError();
+    }
+    return e;
+}
+
+} // namespace
+
+bool attn_fits(const AttnShape &s, bool backward)
+{
+    const double units = (double)s.seqs * s.hk, heads = (double)s.seqs * s.hq, most = 4294967295.0;
+    if (backward)
+        return (double)s.tokens_q * s.hq * (s.dim / 8) + 256 <= most &&
+               units * (double)blocks_of(s.max_k, 32 * BWD_K_WAVES) * 64 * BWD_K_WAVES <= most &&
+               heads * (double)blocks_of(s.max_q, 32 * BWD_Q_WAVES) * 64 * BWD_Q_WAVES <= most;
+    const double groups = few_rows(s) ? units * 256 : heads * (double)blocks_of(s.max_q, 32 * FWD_WAVES) * 64 * FWD_WAVES;
+    return groups * splits_of(s) <= most && heads * s.max_q * (s.dim / 4) + 256 <= most;
+}
+
+size_t attn_workspace_bytes(const AttnShape &s)
+{
+    const int splits = splits_of(s);
+    return splits == 1 ? 0 : part_bytes(s, splits) + pad256((size_t)splits * s.hq * s.tokens_q * sizeof(float2));
+}
+
+hipError_t launch_attn(AttnFwd a, void *workspace, hipStream_t st)
+{
+    a.c2 = a.scale * kLog2e;
+    a.splits = splits_of(a.s);
+    a.part = (float *)workspace;
+    a.stat = a.splits == 1 ? nullptr : (float2 *)((char *)workspace + part_bytes(a.s, a.splits));
+    return a.s.dim == 64 ? fwd<64>(a, st) : fwd<128>(a, st);
+}
+
+size_t attn_bwd_workspace_bytes(const AttnShape &s) { return 2 * pad256((size_t)s.hq * s.tokens_q * 4); }
+
+hipError_t launch_attn_bwd(AttnBwd b, void *workspace, hipStream_t st)
+{
+    b.c2 = b.scale * kLog2e;
+    b.q_blocks = (int)blocks_of(b.s.max_q, 32 * BWD_Q_WAVES);
+    b.nl = (float *)workspace;
+    b.nd = (float *)((char *)workspace + attn_bwd_workspace_bytes(b.s) / 2);
+    return b.s.dim == 64 ? bwd<64>(b, st) : bwd<128>(b, st);
+}
+
+} // namespace puro

@@ -124,6 +124,114 @@ size_t newton_workspace_bytes(const NsMatrix *ms, int count);
 hipError_t launch_newton(const NsMatrix *ms, int count, bool gbf16, int steps, const float *coef, float eps,
                          void *workspace, hipStream_t st);
 
+// Norm of query and key heads (none when wq is NULL) and rotation of the first `rotary` elements of each.
+struct RopeShape {
+    const uint16_t *q;
+    int64_t ldq;
+    const uint16_t *k;
+    int64_t ldk;
+    int hq, hk, dim;   // 64 or 128 elements a head
+    int64_t tokens;
+    const void *wq, *wk;
+    bool wbf16;
+    float eps;
+    const int32_t *pos;    // [tokens]
+    const float *freq;     // [rotary / 2]
+    int rotary;            // a multiple of 16
+    float mscale;
+    bool interleaved;      // pairs (2 j, 2 j + 1) instead of (j, j + rotary / 2)
+};
+// parts (waves a token's heads are spread over), turn and part are the launchers'.
+struct RopeFwd {
+    RopeShape r;
+    uint16_t *qo;
+    int64_t ldqo;
+    uint16_t *ko;
+    int64_t ldko;
+    float *rstd;           // [tokens][hq + hk], or NULL
+    int parts;
+};
+hipError_t launch_rope(RopeFwd a, hipStream_t st);
+struct RopeBwd {
+    RopeShape r;
+    const uint16_t *dq;
+    int64_t lddq;
+    const uint16_t *dk;
+    int64_t lddk;
+    const uint16_t *dv;
+    int64_t lddv;
+    const float *rstd;
+    uint16_t *dx;          // joint gradient in BF16, or NULL
+    int64_t lddx;
+    float *dwq, *dwk;
+    bool accumulate;
+    const float2 *turn;    // [tokens][rotary / 2]
+    float *part;           // [token tile][(hq + hk) dim]
+};
+size_t rope_bwd_workspace_bytes(const RopeShape &r, bool norm);
+hipError_t launch_rope_bwd(RopeBwd b, uint8_t *qr, int64_t ldqr, float *sr, bool transpose_out, uint8_t *qt, int64_t ldqt,
+                           float *stok, bool pow2, void *workspace, hipStream_t st);
+
+// Attention of packed sequences: sequence s's query rows are q_off[s] .. and its key rows k_off[s] .., len[s] of
+// them (up to the next offset where len is NULL; all arrays in device memory).
+struct AttnShape {
+    int hq, hk, dim;   // query heads, key heads (hq a multiple), 64 or 128 elements each
+    int seqs;
+    const int32_t *q_off, *q_len, *k_off, *k_len;
+    int64_t tokens_q, tokens_k;
+    int max_q, max_k;  // no sequence's rows count past these
+    bool causal;
+};
+// c2, splits, blocks and the pointers into the workspace are the launchers'.
+struct AttnFwd {
+    AttnShape s;
+    const uint16_t *q;
+    int64_t ldq;
+    const uint16_t *k;
+    int64_t ldk;
+    const uint16_t *v;
+    int64_t ldv;
+    float scale;
+    uint16_t *o;
+    int64_t ldo;
+    float *lse;        // [hq][tokens_q], or NULL
+    float c2;
+    int splits, blocks;
+    float *part;       // [split][hq][tokens_q][dim]
+    float2 *stat;      // [split][hq][tokens_q]: maximum (log2 units), sum
+};
+// Whether every launch's work items fit the 32 bits that a grid has.
+bool attn_fits(const AttnShape &s, bool backward);
+size_t attn_workspace_bytes(const AttnShape &s);
+hipError_t launch_attn(AttnFwd a, void *workspace, hipStream_t st);
+
+struct AttnBwd {
+    AttnShape s;
+    const uint16_t *dout;
+    int64_t lddo;
+    const uint16_t *q;
+    int64_t ldq;
+    const uint16_t *k;
+    int64_t ldk;
+    const uint16_t *v;
+    int64_t ldv;
+    const uint16_t *o;
+    int64_t ldo;
+    const float *lse;
+    float scale;
+    uint16_t *dq;
+    int64_t lddq;
+    uint16_t *dk;
+    int64_t lddk;
+    uint16_t *dv;
+    int64_t lddv;
+    float c2;
+    int q_blocks;
+    float *nl, *nd;    // [hq][tokens_q]: -lse / scale, -sum of do o
+};
+size_t attn_bwd_workspace_bytes(const AttnShape &s);
+hipError_t launch_attn_bwd(AttnBwd b, void *workspace, hipStream_t st);
+
 constexpr int kGemmMaxSeg = 4;
 
 // One K segment of a product: A, B and their block scales over K indices 0 .. K-1.

@@ -1,0 +1,360 @@
+// Norm of every query and key head and the rotation by its position, in one
+// pass, and its gradient (gfx950): what stands between the joint q/k/v product
+// and attention.
+//
+//   n = x r w, r = 1 / sqrt(mean x^2 + eps) over one head (n = x without weights)
+//   y = n with its pairs (a, b) turned by theta = position * frequency:
+//       m (a cos - b sin), m (b cos + a sin); elements past the rotated ones stay
+//   gradient: g = dy turned back, xh = x r,
+//       dx = r (w g - xh mean(w g xh)), dw = sum over tokens and heads of g xh
+//
+// Angles are formed in 64 bits, in turns, and reduced to half a turn either way
+// before cosine and sine in FP32: a position of 2^20 has as exact a rotation as
+// position 1.  Everything else is FP32.  Both directions are HBM-bound.
+#include "kernels.h"
+#include "tile.h"
+
+namespace puro {
+
+namespace {
+
+// Sum over each group of N lanes (8 or 16): every lane ends with the same bits.
+template <int N> __device__ __forceinline__ float sum_lanes(float v)
+{
+    v += dpp_f<0xB1>(v);    // lane ^ 1
+    v += dpp_f<0x4E>(v);    // lane ^ 2
+    v += dpp_f<0x141>(v);   // 7 - lane
+    if (N == 16)
+        v += dpp_f<0x140>(v);   // 15 - lane
+    return v;
+}
+
+// (cos, sin) of position * frequency, times m.  The frequency in turns and the
+// product are off by 2^-53 of themselves each: for |position * frequency| < 2^31,
+// below 2^-20 radians, and for less than 2^20, below 2^-31.
+__device__ __forceinline__ float2 rotation(int32_t position, float frequency, float m)
+{
+    const double turns = (double)position * ((double)frequency * 0.15915494309189533577);
+    float s, c;
+    sincospif(2.0f * (float)(turns - rint(turns)), &s, &c);
+    return make_float2(c * m, s * m);
+}
+
+__device__ __forceinline__ void unpack4(const uint2 &a, float v[4])
+{
+    v[0] = bf16_lo(a.x); v[1] = bf16_hi(a.x); v[2] = bf16_lo(a.y); v[3] = bf16_hi(a.y);
+}
+
+__device__ __forceinline__ void load4_weight(const void *w, int wbf16, int at, float v[4])
+{
+    if (wbf16) {
+        unpack4(*reinterpret_cast<const uint2 *>((const uint16_t *)w + at), v);
+    } else {
+        const float4 f = *reinterpret_cast<const float4 *>((const float *)w + at);
+        v[0] = f.x; v[1] = f.y; v[2] = f.z; v[3] = f.w;
+    }
+}
+
+// Forward.  D / 8 lanes hold a head, eight elements each: in the half layout a
+// rotated lane has four consecutive a and their four b (two 8-byte accesses), so
+// that no pair crosses lanes.  A wave turns 512 / D heads of one token at a
+// time; it forms the token's angles once, four a lane, and goes through its share
+// of the heads with the next ones' loads in flight.
+template <int D, bool INTER>
+__global__ __launch_bounds__(256) void rope_kernel(RopeFwd a)
+{
+    constexpr int L = D / 8, HEADS = 64 / L;
+    const int lane = threadIdx.x & 63, l = lane % L;
+    const int64_t wave = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6), t = wave / a.parts;
+    const int part = (int)(wave % a.parts);
+    if (t >= a.r.tokens)
+        return;
+    const int H = a.r.hq + a.r.hk, turned = a.r.rotary / 8;
+    const bool rot = l < turned, half = rot && !INTER;
+    const int at0 = half ? 4 * l : 8 * l, at1 = half ? a.r.rotary / 2 + 4 * l : 8 * l + 4;
+
+    auto src = [&](int h) {
+        return h < a.r.hq ? a.r.q + t * a.r.ldq + h * D : a.r.k + t * a.r.ldk + (h - a.r.hq) * D;
+    };
+    uint2 x0 = make_uint2(0, 0), x1 = x0;
+    int h = part * HEADS + lane / L;
+    if (h < H) {
+        x0 = *reinterpret_cast<const uint2 *>(src(h) + at0);
+        x1 = *reinterpret_cast<const uint2 *>(src(h) + at1);
+    }
+    float wq[8], wk[8];
+    if (a.r.wq) {
+        load4_weight(a.r.wq, a.r.wbf16, at0, wq);
+        load4_weight(a.r.wq, a.r.wbf16, at1, wq + 4);
+        load4_weight(a.r.wk, a.r.wbf16, at0, wk);
+        load4_weight(a.r.wk, a.r.wbf16, at1, wk + 4);
+    }
+    float2 turn[4];
+    if (rot) {
+        const int32_t p = a.r.pos[t];
+#pragma unroll
+        for (int e = 0; e < 4; e++)
+            turn[e] = rotation(p, a.r.freq[4 * l + e], a.r.mscale);
+    }
+    for (; h < H; h += a.parts * HEADS) {
+        float v[8];
+        unpack4(x0, v);
+        unpack4(x1, v + 4);
+        const int next = h + a.parts * HEADS;
+        if (next < H) {
+            x0 = *reinterpret_cast<const uint2 *>(src(next) + at0);
+            x1 = *reinterpret_cast<const uint2 *>(src(next) + at1);
+        }
+        if (a.r.wq) {
+            float s = 0.0f;
+#pragma unroll
+            for (int e = 0; e < 8; e++)
+                s = fmaf(v[e], v[e], s);
+            const float r = 1.0f / sqrtf(sum_lanes<L>(s) * (1.0f / D) + a.r.eps);
+            if (l == 0 && a.rstd)
+                a.rstd[t * H + h] = r;
+#pragma unroll
+            for (int e = 0; e < 8; e++)
+                v[e] = v[e] * r * (h < a.r.hq ? wq[e] : wk[e]);
+        }
+        if (rot) {
+#pragma unroll
+            for (int e = 0; e < 4; e++) {
+                float &p = v[INTER ? 2 * e : e], &q = v[INTER ? 2 * e + 1 : e + 4];
+                const float u = p, w = q;
+                p = fmaf(u, turn[e].x, -(w * turn[e].y));
+                q = fmaf(w, turn[e].x, u * turn[e].y);
+            }
+        }
+        uint16_t *dst = h < a.r.hq ? a.qo + t * a.ldqo + h * D : a.ko + t * a.ldko + (h - a.r.hq) * D;
+        *reinterpret_cast<uint2 *>(dst + at0) = make_uint2(to_bf16x2(v[0], v[1]), to_bf16x2(v[2], v[3]));
+        *reinterpret_cast<uint2 *>(dst + at1) = make_uint2(to_bf16x2(v[4], v[5]), to_bf16x2(v[6], v[7]));
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Gradient.  Rotations of every token once ([token][rotary / 2], read by all the
+// token's heads out of the caches), then 128 x 128 tiles of the joint gradient
+// [tokens][(hq + 2 hk) D], which hold whole heads: turned back, taken through the
+// norm and quantised both ways; the values' columns are quantised as they are.
+// A tile's sums over its tokens of g xh go to part [token tile][column] and are
+// added up in a fixed order by the last kernel.
+// ---------------------------------------------------------------------------
+__global__ __launch_bounds__(256) void rope_turn_kernel(RopeShape r, float2 *__restrict__ turn)
+{
+    const int half = r.rotary / 2;
+    const int64_t n = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (n < r.tokens * half)
+        turn[n] = rotation(r.pos[n / half], r.freq[n % half], r.mscale);
+}
+
+template <int D, bool FULL, bool TR, bool INTER>
+__device__ __forceinline__ void rope_bwd_tile(const RopeBwd &b, const Place &p, const QuantOut &ro, const QuantOut &to,
+                                              int pow2, TileShared &sh, float (*red)[128])
+{
+    constexpr int L = D / 8;
+    const int H = b.r.hq + b.r.hk, R = b.r.rotary;
+    const int64_t c0 = p.c0();
+    const int h = (int)(c0 / D), d0 = (int)(c0 % D);
+    const bool in = FULL || c0 < p.cols, norm = in && h < H && b.r.wq, rot = in && h < H && d0 < R;
+    const uint16_t *dy, *x = nullptr;
+    int64_t lddy, ldx = 0;
+    if (h < b.r.hq) {
+        dy = b.dq + h * D + d0;
+        lddy = b.lddq;
+        x = b.r.q + h * D + d0;
+        ldx = b.r.ldq;
+    } else if (h < H) {
+        dy = b.dk + (h - b.r.hq) * D + d0;
+        lddy = b.lddk;
+        x = b.r.k + (h - b.r.hq) * D + d0;
+        ldx = b.r.ldk;
+    } else {
+        dy = b.dv + (h - H) * D + d0;
+        lddy = b.lddv;
+    }
+    // in the half layout the other member of a pair is R / 2 elements away
+    const bool low = d0 < R / 2;
+    const int other = INTER ? 0 : low ? R / 2 : -(R / 2), f0 = INTER ? d0 / 2 : low ? d0 : d0 - R / 2;
+    float w[8], dw[8], v[RT][8];
+#pragma unroll
+    for (int j = 0; j < 8; j++)
+        dw[j] = w[j] = 0.0f;
+    if (norm)
+        load8_weight(h < b.r.hq ? b.r.wq : b.r.wk, b.r.wbf16, d0, D, w);
+#pragma unroll
+    for (int i = 0; i < RT; i++) {
+        const int64_t t = p.tk(i);
+#pragma unroll
+        for (int j = 0; j < 8; j++)
+            v[i][j] = 0.0f;
+        if (!in || (!FULL && t >= p.tokens))
+            continue;
+        float g[8];
+        unpack8(*reinterpret_cast<const uint4 *>(dy + t * lddy), g);
+        if (rot) {
+            const float4 *turn = reinterpret_cast<const float4 *>(b.turn + t * (R / 2) + f0);
+            if (INTER) {
+#pragma unroll
+                for (int j = 0; j < 2; j++) {
+                    const float4 c = turn[j];
+                    const float a0 = g[4 * j], b0 = g[4 * j + 1], a1 = g[4 * j + 2], b1 = g[4 * j + 3];
+                    g[4 * j] = fmaf(a0, c.x, b0 * c.y);
+                    g[4 * j + 1] = fmaf(b0, c.x, -(a0 * c.y));
+                    g[4 * j + 2] = fmaf(a1, c.z, b1 * c.w);
+                    g[4 * j + 3] = fmaf(b1, c.z, -(a1 * c.w));
+                }
+            } else {
+                float o[8];
+                unpack8(*reinterpret_cast<const uint4 *>(dy + t * lddy + other), o);
+#pragma unroll
+                for (int j = 0; j < 4; j++) {
+                    const float4 c = turn[j];
+                    g[2 * j] = fmaf(g[2 * j], c.x, low ? o[2 * j] * c.y : -(o[2 * j] * c.y));
+                    g[2 * j + 1] = fmaf(g[2 * j + 1], c.z, low ? o[2 * j + 1] * c.w : -(o[2 * j + 1] * c.w));
+                }
+            }
+        }
+        if (norm) {
+            const float r = b.rstd[t * H + h];
+            float xh[8], s = 0.0f;
+            unpack8(*reinterpret_cast<const uint4 *>(x + t * ldx), xh);
+#pragma unroll
+            for (int j = 0; j < 8; j++) {
+                xh[j] *= r;
+                dw[j] = fmaf(g[j], xh[j], dw[j]);
+                g[j] *= w[j];
+                s = fmaf(g[j], xh[j], s);
+            }
+            s = sum_lanes<L>(s) * (1.0f / D);
+#pragma unroll
+            for (int j = 0; j < 8; j++)
+                g[j] = r * fmaf(-xh[j], s, g[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; j++)
+            v[i][j] = g[j];
+    }
+    pin(v);
+    if (b.r.wq) {
+        const int t = threadIdx.x, lane = t & 63;
+        *reinterpret_cast<float2 *>(&red[t >> 6][8 * p.cc + first_of(lane)]) =
+            cross4(dw, [](float a, float c) { return a + c; });
+        __syncthreads();
+        if (t < 128 && p.col0 + t < (int64_t)H * D) {
+            float s = red[0][t];
+#pragma unroll
+            for (int k = 1; k < TileShared::WAVES; k++)
+                s += red[k][t];
+            b.part[(p.tok0 >> 7) * ((int64_t)H * D) + p.col0 + t] = s;
+        }
+    }
+    if (b.dx)
+        store_tile<FULL>(b.dx, b.lddx, p, v);
+    quant_tile<FULL, TR, true>(v, ro, to, p, pow2, sh);
+}
+
+template <int D, bool TR, bool INTER>
+__global__ __launch_bounds__(TILE_THREADS) __attribute__((amdgpu_waves_per_eu(4)))
+void rope_bwd_kernel(RopeBwd b, QuantOut ro, QuantOut to, int pow2)
+{
+    __shared__ TileShared sh;
+    __shared__ float red[TileShared::WAVES][128];
+    const auto p = place(blockIdx.y, blockIdx.x, b.r.tokens, (int64_t)(b.r.hq + 2 * b.r.hk) * D);
+    if (full_tile(p))
+        rope_bwd_tile<D, true, TR, INTER>(b, p, ro, to, pow2, sh, red);
+    else
+        rope_bwd_tile<D, false, TR, INTER>(b, p, ro, to, pow2, sh, red);
+}
+
+// dw of 32 elements of the queries' (then the keys') weight: 16 threads each add every 16th of the (token tile,
+// head) shares, and their sums are added in a fixed order.
+__global__ __launch_bounds__(512) void rope_dw_kernel(RopeBwd b, int ntb)
+{
+    __shared__ float red[16][32];
+    const int x = threadIdx.x % 32, y = threadIdx.x / 32, D = b.r.dim, per = D / 32;
+    const bool keys = (int)blockIdx.x >= per;
+    const int d = ((int)blockIdx.x - (keys ? per : 0)) * 32 + x, heads = keys ? b.r.hk : b.r.hq, H = b.r.hq + b.r.hk;
+    const float *part = b.part + (keys ? b.r.hq * D : 0) + d;
+    float s = 0.0f;
+    const int64_t n = (int64_t)ntb * heads;
+#pragma unroll 8
+    for (int64_t i = y; i < n; i += 16)
+        s += part[(i / heads) * ((int64_t)H * D) + (i % heads) * D];
+    red[y][x] = s;
+    for (int m = 8; m > 0; m >>= 1) {
+        __syncthreads();
+        if (y < m)
+            red[y][x] += red[y + m][x];
+    }
+    float *dw = keys ? b.dwk : b.dwq;
+    if (y == 0)
+        dw[d] = b.accumulate ? dw[d] + red[0][x] : red[0][x];
+}
+
+size_t pad256(size_t n) { return (n + 255) / 256 * 256; }
+int64_t turn_count(const RopeShape &r) { return r.tokens * (r.rotary / 2); }
+
+template <int D, bool TR, bool INTER> void bwd_tiles(const RopeBwd &b, const QuantOut &ro, const QuantOut &to, int pow2, hipStream_t st)
+{
+    const int64_t cols = (int64_t)(b.r.hq + 2 * b.r.hk) * D;
+    hipLaunchKernelGGL((rope_bwd_kernel<D, TR, INTER>), dim3((unsigned)((cols + 127) / 128), (unsigned)((b.r.tokens + 127) / 128)),
+                       dim3(TILE_THREADS), 0, st, b, ro, to, pow2);
+}
+
+template <int D, bool TR> void bwd_tiles(const RopeBwd &b, const QuantOut &ro, const QuantOut &to, int pow2, hipStream_t st)
+{
+    b.r.interleaved ? bwd_tiles<D, TR, true>(b, ro, to, pow2, st) : bwd_tiles<D, TR, false>(b, ro, to, pow2, st);
+}
+
+} // namespace
+
+hipError_t launch_rope(RopeFwd a, hipStream_t st)
+{
+    // a token's heads over several waves where tokens are few
+    const int passes = (a.r.hq + a.r.hk + 512 / a.r.dim - 1) / (512 / a.r.dim);
+    const int64_t want = a.r.tokens ? 4096 / a.r.tokens : 1;
+    a.parts = (int)(want < 1 ? 1 : want < passes ? want : passes);
+    const unsigned grid = (unsigned)((a.r.tokens * a.parts + 3) / 4);
+    auto *kernel = a.r.dim == 64 ? (a.r.interleaved ? rope_kernel<64, true> : rope_kernel<64, false>)
+                                 : (a.r.interleaved ? rope_kernel<128, true> : rope_kernel<128, false>);
+    hipLaunchKernelGGL(kernel, dim3(grid), dim3(256), 0, st, a);
+    return hipGetLastError();
+}
+
+size_t rope_bwd_workspace_bytes(const RopeShape &r, bool norm)
+{
+    const int64_t ntb = (r.tokens + 127) / 128;
+    return pad256((size_t)turn_count(r) * sizeof(float2)) +
+           (norm ? pad256((size_t)ntb * (size_t)(r.hq + r.hk) * (size_t)r.dim * 4) : 0);
+}
+
+hipError_t launch_rope_bwd(RopeBwd b, uint8_t *qr, int64_t ldqr, float *sr, bool transpose_out, uint8_t *qt, int64_t ldqt,
+                           float *stok, bool pow2, void *workspace, hipStream_t st)
+{
+    const int64_t turns = turn_count(b.r), ntb = (b.r.tokens + 127) / 128;
+    const int64_t cols = (int64_t)(b.r.hq + 2 * b.r.hk) * b.r.dim;
+    float2 *turn = (float2 *)workspace;
+    b.turn = turn;
+    b.part = (float *)((char *)workspace + pad256((size_t)turns * sizeof(float2)));
+    hipError_t e = hipSuccess;
+    if (turns > 0) {
+        hipLaunchKernelGGL(rope_turn_kernel, dim3((unsigned)((turns + 255) / 256)), dim3(256), 0, st, b.r, turn);
+        e = hipGetLastError();
+    }
+    if (e == hipSuccess && b.r.tokens > 0) {
+        const QuantOut ro{qr, ldqr, sr, (cols + 127) / 128}, to{qt, ldqt, stok, transpose_out ? ntb : cols};
+        if (b.r.dim == 64)
+            transpose_out ? bwd_tiles<64, true>(b, ro, to, pow2, st) : bwd_tiles<64, false>(b, ro, to, pow2, st);
+        else
+            transpose_out ? bwd_tiles<128, true>(b, ro, to, pow2, st) : bwd_tiles<128, false>(b, ro, to, pow2, st);
+        e = hipGetLastError();
+    }
+    if (e == hipSuccess && b.r.wq) {
+        hipLaunchKernelGGL(rope_dw_kernel, dim3((unsigned)(2 * b.r.dim / 32)), dim3(512), 0, st, b, (int)ntb);
+        e = hipGetLastError();
+    }
+    return e;
+}
+
+} // namespace puro

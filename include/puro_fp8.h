@@ -564,6 +564,161 @@ puro_status_t puro_fp8_newton_schulz_grouped(puro_dtype_t gdt, const puro_newton
                                              size_t ws_bytes, hipStream_t stream);
 
 /*
+ * Norm of every query and key head and its rotation by the token's position:
+ * what stands between the joint q/k/v product and attention.
+ * Passage: the model card's configuration table (Qwen3-1.7B: 16 query and 8
+ * key/value heads, head dimension 128, a root-mean-square norm of each query
+ * and key head, rotary positions) and its setup paragraph (norms and attention
+ * in BF16 or FP32).  For one head x of head_dim elements of a token at position p:
+ *     n = x r w,  r = 1 / sqrt( mean x^2 + eps )    (n = x when wq and wk are NULL)
+ *     theta_j = p inv_freq[j],  j < rotary_dim / 2
+ *     (a, b) = (n[j], n[j + rotary_dim / 2]), or (n[2 j], n[2 j + 1]) when interleaved,
+ *     becomes rope_scale (a cos theta_j - b sin theta_j, b cos theta_j + a sin theta_j)
+ * and the head's elements from rotary_dim on stay n.  Any scaling of positions
+ * for long contexts is one of inv_freq and rope_scale.  Angles are formed in 64
+ * bits (below 2^-20 radians off for |p inv_freq| < 2^31, below 2^-31 for less than
+ * 2^20), everything else is FP32 and rounded to BF16 once.
+ *   heads_q, heads_kv   1 .. PURO_MAX_HEADS each (any two numbers)
+ *   head_dim     64 or 128
+ *   rotary_dim   0 .. head_dim, a multiple of 16 (0: positions and inv_freq may be NULL)
+ *   positions    [tokens] int32 and inv_freq [rotary_dim / 2] FP32, dense, device memory
+ *   wq, wk       [head_dim] FP32 or BF16 (wdt), dense, 16-byte aligned, device memory; both or neither
+ *   eps          as the norm's above (not looked at without weights)
+ *   rope_scale   finite
+ * shape is a HOST structure, read before the call returns.  q BF16 [tokens]
+ * [heads_q head_dim] and k BF16 [tokens][heads_kv head_dim], strides ldq and ldk,
+ * are usually columns of one product.  qo and ko may be q and k themselves, with
+ * their strides (the rotation in place); apart from that no output overlaps
+ * anything else.  rstd (FP32 [tokens][heads_q + heads_kv], or NULL) receives r
+ * when there are weights.  A head's sum of squares must be finite in FP32.
+ * Errors: heads, head_dim and rotary_dim PURO_ERR_SHAPE, interleaved other than
+ * 0 or 1 PURO_ERR_ENUM, eps and rope_scale PURO_ERR_VALUE, one weight of the two
+ * PURO_ERR_NULL.
+ */
+#define PURO_MAX_HEADS 1024
+typedef struct {
+    int heads_q, heads_kv, head_dim;
+    int rotary_dim, interleaved;
+    int64_t tokens;
+    const int32_t *positions;
+    const float *inv_freq;
+    float rope_scale;
+    const void *wq, *wk;
+    puro_dtype_t wdt;
+    float eps;
+} puro_qk_norm_rope_t;
+puro_status_t puro_fp8_qk_norm_rope(const puro_qk_norm_rope_t *shape, const void *q, int64_t ldq, const void *k,
+                                    int64_t ldk, void *qo, int64_t ldqo, void *ko, int64_t ldko, float *rstd,
+                                    hipStream_t stream);
+
+/*
+ * Its gradient, quantised as the output gradient of the joint q/k/v product.
+ * For dq and dk, the gradients of qo and ko, and dv (BF16 [tokens][heads head_dim]
+ * each, heads_kv of them for dv), with g the gradient of n (the rotation's
+ * transpose applied to dq or dk) and xh = x r, r the forward's rstd:
+ *     dx = r (w g - xh mean( w g xh ))      (dx = g without weights)
+ *     dwq[d], dwk[d] = (accumulate ? dw[d] : 0) + sum over tokens and heads of g xh
+ * The FP32 values of dx for q, then for k, and dv are the columns of a tensor of
+ * cols = (heads_q + 2 heads_kv) head_dim columns that is quantised unrounded both
+ * ways as puro_fp8_quant_dual would, and stored as BF16 in dx (stride lddx) unless
+ * dx is NULL.  q, k and rstd are read only with weights, and may be NULL without;
+ * so may dwq and dwk (FP32 [head_dim], tokens added in a fixed order).  tokens = 0
+ * leaves dwq and dwk zero, or as they were with accumulate.  The products are
+ * formed in that order, x r first; they, the sums and dx must be finite in FP32.
+ * workspace: at least puro_fp8_qk_norm_rope_bwd_workspace_size(shape) bytes (0
+ * for invalid shapes; pointers are not looked at but for wq) of device memory,
+ * 256-byte aligned, not used by other work in flight.
+ */
+size_t puro_fp8_qk_norm_rope_bwd_workspace_size(const puro_qk_norm_rope_t *shape);
+puro_status_t puro_fp8_qk_norm_rope_bwd_quant_dual(const puro_qk_norm_rope_t *shape, const void *dq, int64_t lddq,
+                                                   const void *dk, int64_t lddk, const void *dv, int64_t lddv,
+                                                   const void *q, int64_t ldq, const void *k, int64_t ldk,
+                                                   const float *rstd, void *dx, int64_t lddx, float *dwq, float *dwk,
+                                                   int accumulate, uint8_t *q_row, int64_t ldq_row, float *s_row,
+                                                   int transpose_out, uint8_t *q_tok, int64_t ldq_tok, float *s_tok,
+                                                   void *workspace, size_t ws_bytes, hipStream_t stream);
+puro_status_t puro_fp8_qk_norm_rope_bwd_quant_dual_pow2(const puro_qk_norm_rope_t *shape, const void *dq,
+                                                        int64_t lddq, const void *dk, int64_t lddk, const void *dv,
+                                                        int64_t lddv, const void *q, int64_t ldq, const void *k,
+                                                        int64_t ldk, const float *rstd, void *dx, int64_t lddx,
+                                                        float *dwq, float *dwk, int accumulate, uint8_t *q_row,
+                                                        int64_t ldq_row, float *s_row, int transpose_out,
+                                                        uint8_t *q_tok, int64_t ldq_tok, float *s_tok, void *workspace,
+                                                        size_t ws_bytes, hipStream_t stream);
+
+/*
+ * Attention of packed sequences with grouped heads.
+ * Passage: the model card's configuration table (16 query heads on 8 key/value
+ * heads, causal) and its setup paragraph: attention is not among the FP8 GEMMs,
+ * so its products run on the BF16 matrix cores with FP32 accumulation.  For
+ * sequence s with n query rows and m key rows, query head h and key head
+ * h / (heads_q / heads_kv):
+ *     S[i][j] = scale q_i . k_j for the keys j that query i sees: all m, or,
+ *               causal, j <= i + m - n (the last query sees every key)
+ *     lse[i] = log sum_j exp S[i][j],   o_i = sum_j exp(S[i][j] - lse[i]) v_j
+ * A row that sees no key gets o = 0 and lse = -infinity.  So whole prompts (n = m),
+ * a chunk of new tokens after earlier ones (n < m) and single tokens (n = 1) are
+ * one call.
+ *   heads_q      a multiple of heads_kv, at most PURO_MAX_HEADS
+ *   head_dim     64 or 128
+ *   sequences    0 or more
+ *   q_offsets    int32 device array: sequence s starts at row q_offsets[s] and has
+ *                q_offsets[s + 1] - q_offsets[s] rows, or q_lengths[s] when
+ *                q_lengths is not NULL (q_offsets then needs no last entry):
+ *                packed rows, or the used part of padded ones.  k_offsets and
+ *                k_lengths the same for keys and values.
+ *   tokens_q, tokens_k   rows of q and o, and of k and v
+ *   max_q, max_k the most rows of one sequence.  Rows past a maximum or past the
+ *                tensor are left out, so the arrays may change between replays
+ *                of a captured call.  Smaller maxima cost less.
+ *   scale        finite and > 0, else PURO_ERR_VALUE
+ * shape is a HOST structure, read before the call returns.  q BF16 [tokens_q]
+ * [heads_q head_dim], k and v BF16 [tokens_k][heads_kv head_dim], o as q; row
+ * strides ldq, ldk, ldv, ldo.  lse FP32 [heads_q][tokens_q], or NULL.  Rows of
+ * o and lse outside every sequence are left as they were, rows of k and v outside
+ * are not read into any result.  Query rows of two sequences must not overlap; key
+ * rows may.  Every |S| must stay below 2^96.
+ * Precision: exp(S - its row's running maximum) enters the second product as BF16,
+ * within 2^-8 of itself per key; sums, maxima and results before their rounding
+ * to BF16 are FP32.  Equal calls give equal bits.
+ * workspace: puro_fp8_attention_workspace_size(shape) bytes (often 0; only the
+ * numbers and head counts are read; 0 for invalid shapes) of device memory, 256-byte
+ * aligned, not used by other work in flight.
+ */
+typedef struct {
+    int heads_q, heads_kv, head_dim;
+    int sequences, causal;
+    int64_t tokens_q, tokens_k, max_q, max_k;
+    const int32_t *q_offsets, *q_lengths, *k_offsets, *k_lengths;
+    float scale;
+} puro_attention_t;
+size_t puro_fp8_attention_workspace_size(const puro_attention_t *shape);
+puro_status_t puro_fp8_attention(const puro_attention_t *shape, const void *q, int64_t ldq, const void *k, int64_t ldk,
+                                 const void *v, int64_t ldv, void *o, int64_t ldo, float *lse, void *workspace,
+                                 size_t ws_bytes, hipStream_t stream);
+
+/*
+ * Gradient of attention: for dout (the gradient of o, BF16 as o) and the
+ * forward's q, k, v, o and lse, with P = exp(S - lse), dP = dout_i . v_j and
+ * D_i = dout_i . o_i:
+ *     dS = P (dP - D),  dv = P^T dout,  dq = scale dS k,  dk = scale dS^T q
+ * dk and dv are summed over the query heads of their key head.  P and dS enter
+ * their products as BF16; everything else is FP32 until the results are rounded
+ * to BF16.  No sum is formed in memory: equal calls give equal bits.  Rows of dq
+ * outside every sequence of queries, and of dk and dv outside every sequence
+ * of keys, are left as they were.  Neither query nor key rows of two sequences
+ * may overlap.  dq, dk and dv may lie in one tensor (the joint gradient's columns).
+ * workspace: puro_fp8_attention_bwd_workspace_size(shape) bytes (0 for invalid
+ * shapes) of device memory, 256-byte aligned, not used by other work in flight.
+ */
+size_t puro_fp8_attention_bwd_workspace_size(const puro_attention_t *shape);
+puro_status_t puro_fp8_attention_bwd(const puro_attention_t *shape, const void *dout, int64_t lddout, const void *q,
+                                     int64_t ldq, const void *k, int64_t ldk, const void *v, int64_t ldv,
+                                     const void *o, int64_t ldo, const float *lse, void *dq, int64_t lddq, void *dk,
+                                     int64_t lddk, void *dv, int64_t lddv, void *workspace, size_t ws_bytes,
+                                     hipStream_t stream);
+
+/*
  * puro_fp8_gemm without a workspace argument, for callers that cannot
  * allocate device memory (code under HIP graph capture, tight serving loops,
  * harnesses that forbid hipMalloc).  Arguments, validation, result and
