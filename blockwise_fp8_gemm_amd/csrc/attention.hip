@@ -59,56 +59,68 @@ __device__ __forceinline__ void copy4(const void *base, uint32_t off, void *lds_
 template <int N> __device__ __forceinline__ void wait_copies() { asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory"); }
 
 // ---------------------------------------------------------------------------
-// Tiles of BF16 rows in LDS.  16-byte segment s of row r sits at s ^ swz(r): any
-// 16 consecutive rows hold one segment column on 16 different banks' places
-// (row reads), and the four rows x 64 bytes of a transposing read lie on
-// different banks too.
+// Tiles of BF16 rows in LDS.  A tile is made of 1 KB pieces of 1024 / ROW rows,
+// each filled by one copy of a wave (lane l's 16 bytes at 16 l) and followed by a
+// little padding.  Within a piece, segment 4 x + y (16 bytes) of row r lies at
+// 256 x + 64 (r % 4) + 16 y; with heads of 64 rows r % 8 >= 4 follow 512 bytes
+// behind, their y with the low bit flipped.  So 16 consecutive rows hold one
+// segment on 16 different places of the 256 bytes that the banks span (row
+// reads), and a transposing read's four rows x 64 bytes lie side by side; and
+// both addresses are one register a lane plus constants.
 // ---------------------------------------------------------------------------
 template <int D> struct Tile {
-    static constexpr int ROW = 2 * D, SEGS = D / 8, SLICES = D / 16, BLOCKS = D / 32;
-    static constexpr int ROWS_PER_KB = 1024 / ROW;
-
-    __device__ __forceinline__ static int swz(int row)
-    {
-        return D == 128 ? ((row & 3) << 2) | ((row >> 2) & 3) : (((row >> 1) & 1) << 2) | ((row >> 2) & 3);
-    }
+    static constexpr int SEGS = D / 8, SLICES = D / 16, BLOCKS = D / 32;
+    static constexpr int PIECE = 64 / SEGS;                       // rows of a piece: 4 or 8
+    static constexpr int STRIDE = 1024 + (D == 128 ? 16 : 32);    // bytes from piece to piece
+    static constexpr int bytes(int rows) { return rows / PIECE * STRIDE; }
 
     // This wave's share of a tile of ROWS rows from g on (row stride ld bytes); rows past `last` are
     // copies of it, so that nothing behind a sequence is read.
     template <int ROWS, int NW>
     __device__ __forceinline__ static void stage(uint8_t *t, const uint16_t *g, uint32_t ld, int last, int wave, int lane)
     {
-        constexpr int CHUNKS = ROWS / ROWS_PER_KB;
-        static_assert(CHUNKS % NW == 0, "whole 1 KB pieces per wave");
+        constexpr int PIECES = ROWS / PIECE;
+        static_assert(PIECES % NW == 0, "whole pieces per wave");
+        const int sub = D == 128 ? 0 : lane >> 5, x = D == 128 ? lane >> 4 : (lane >> 4) & 1;
+        const int row = 4 * sub + ((lane >> 2) & 3), seg = 4 * x + ((lane & 3) ^ sub);
 #pragma unroll
-        for (int it = 0; it < CHUNKS / NW; it++) {
-            const int c = wave + NW * it, row = c * ROWS_PER_KB + lane / SEGS;
-            const int seg = (lane % SEGS) ^ swz(row);
-            copy16(g, (uint32_t)min(row, last) * ld + (uint32_t)(seg * 16), t + c * 1024);
+        for (int it = 0; it < PIECES / NW; it++) {
+            const int c = wave + NW * it;
+            copy16(g, (uint32_t)min(PIECE * c + row, last) * ld + (uint32_t)(seg * 16), t + c * STRIDE);
         }
     }
 
-    // Rows row0 + lane % 32 (row0 a multiple of 32), elements 16 s + 8 (lane / 32) .. +7.
-    __device__ __forceinline__ static v8bf rows(const uint8_t *t, int row0, int s, int lane)
+    // Where the lane's part of a row read and of a column read begins.
+    __device__ __forceinline__ static int row_base(int lane)
     {
-        const int r = lane & 31;
+        const int r = lane & 31, h = lane >> 5;
+        return D == 128 ? (r >> 2) * STRIDE + (r & 3) * 64 + h * 16
+                        : (r >> 3) * STRIDE + ((r >> 2) & 1) * 512 + (r & 3) * 64 + ((h ^ (r >> 2)) & 1) * 16;
+    }
+    __device__ __forceinline__ static int col_base(int lane)
+    {
+        const int h = lane >> 5, i = lane & 15, y = 2 * ((lane >> 4) & 1) + ((i & 3) >> 1);
+        return D == 128 ? h * STRIDE + (i >> 2) * 64 + y * 16 + 8 * (i & 1)
+                        : h * 512 + (i >> 2) * 64 + (y ^ h) * 16 + 8 * (i & 1);
+    }
+
+    // Rows row0 + lane % 32 (row0 a multiple of 32), elements 16 s + 8 (lane / 32) .. +7; t: the tile plus row_base.
+    __device__ __forceinline__ static v8bf rows(const uint8_t *t, int row0, int s)
+    {
         return __builtin_bit_cast(v8bf, *reinterpret_cast<const v4u *>(
-                                            t + (row0 + r) * ROW + (((2 * s + (lane >> 5)) ^ swz(r)) << 4)));
+                                            t + row0 / PIECE * STRIDE + (s >> 1) * 256 + (s & 1) * 32));
     }
 
     // Column 32 b + lane % 32 of the 16 rows from row0 on (a multiple of 16): rows 4 h .. 4 h + 3 and
-    // 8 + 4 h .. 8 + 4 h + 3, h = lane / 32, which is the order of an accumulator's 8 values.
-    __device__ __forceinline__ static v8bf cols(const uint8_t *t, int row0, int b, int lane)
+    // 8 + 4 h .. 8 + 4 h + 3, h = lane / 32, which is the order of an accumulator's 8 values; t: the tile plus
+    // col_base.
+    __device__ __forceinline__ static v8bf cols(const uint8_t *t, int row0, int b)
     {
         typedef __attribute__((address_space(3))) v4s lds_v4s;
-        const int i = lane & 15, seg = 4 * b + 2 * ((lane >> 4) & 1) + ((i & 3) >> 1);
         v4s q[2];
 #pragma unroll
-        for (int j = 0; j < 2; j++) {
-            const int r = 8 * j + 4 * (lane >> 5) + (i >> 2);
-            q[j] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                (lds_v4s *)(t + (row0 + r) * ROW + ((seg ^ swz(r)) << 4) + 8 * (i & 1)));
-        }
+        for (int j = 0; j < 2; j++)
+            q[j] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s *)(t + (row0 + 8 * j) / PIECE * STRIDE + b * 256));
         return __builtin_bit_cast(v8bf, __builtin_shufflevector(q[0], q[1], 0, 1, 2, 3, 4, 5, 6, 7));
     }
 
@@ -195,13 +207,14 @@ template <int D> struct Softmax {
     __device__ __forceinline__ void step(const uint8_t *kt, const uint8_t *vt, const v8bf (&q)[D / 16], float c2,
                                          int first, int lim, bool masked, int lane)
     {
+        const uint8_t *kr = kt + Tile<D>::row_base(lane), *vc = vt + Tile<D>::col_base(lane);
         v16f s[N];
 #pragma unroll
         for (int n = 0; n < N; n++) {
             s[n] = splat(0.0f);
 #pragma unroll
             for (int k = 0; k < D / 16; k++)
-                s[n] = mfma(Tile<D>::rows(kt, 32 * n, k, lane), q[k], s[n]);
+                s[n] = mfma(Tile<D>::rows(kr, 32 * n, k), q[k], s[n]);
         }
         if (masked) {
 #pragma unroll
@@ -239,7 +252,7 @@ template <int D> struct Softmax {
                 const v8bf p = operand(s[n], k);
 #pragma unroll
                 for (int b = 0; b < D / 32; b++)
-                    o[b] = mfma(Tile<D>::cols(vt, 32 * n + 16 * k, b, lane), p, o[b]);
+                    o[b] = mfma(Tile<D>::cols(vc, 32 * n + 16 * k, b), p, o[b]);
             }
     }
 };
@@ -281,7 +294,7 @@ constexpr int KT = 64;
 template <int D, int NW>
 __global__ __launch_bounds__(64 * NW) void attn_fwd_kernel(AttnFwd a)
 {
-    constexpr int R = 32 * NW, TILE = KT * 2 * D;
+    constexpr int R = 32 * NW, TILE = Tile<D>::bytes(KT);
     __shared__ __attribute__((aligned(16))) uint8_t lds[2][2][TILE];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     // blocks of later rows, which see more keys, first; a sequence's key head on one XCD where their
@@ -333,7 +346,7 @@ __global__ __launch_bounds__(64 * NW) void attn_fwd_kernel(AttnFwd a)
 template <int D>
 __global__ __launch_bounds__(256) void attn_rows_kernel(AttnFwd a)
 {
-    constexpr int NW = 4, KW = 32, TILE = KW * 2 * D, S = 2, WAVE = S * 2 * TILE;
+    constexpr int NW = 4, KW = 32, TILE = Tile<D>::bytes(KW), S = 2, WAVE = S * 2 * TILE;
     static_assert(WAVE >= 32 * (D + 4) * 4, "a wave's results take its tiles' place");
     __shared__ __attribute__((aligned(16))) uint8_t lds[NW][WAVE];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -354,7 +367,7 @@ __global__ __launch_bounds__(256) void attn_rows_kernel(AttnFwd a)
         Tile<D>::template stage<KW, 1>(dst, kp + (int64_t)t * KW * a.ldk, (uint32_t)a.ldk * 2, last, 0, lane);
         Tile<D>::template stage<KW, 1>(dst + TILE, vp + (int64_t)t * KW * a.ldv, (uint32_t)a.ldv * 2, last, 0, lane);
     };
-    constexpr int COPIES = 2 * TILE / 1024;
+    constexpr int COPIES = 2 * KW / Tile<D>::PIECE;
     const int c = min(lane & 31, cols - 1), i = c / group, head = kh * group + c % group;
     v8bf qf[D / 16];
     Tile<D>::load(a.q + (int64_t)(q.start + i) * a.ldq + head * D, lane, qf);
@@ -498,7 +511,7 @@ __global__ __launch_bounds__(256) void attn_bwd_rows_kernel(AttnBwd a)
 template <int D, int NW>
 __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2, 2))) void attn_bwd_k_kernel(AttnBwd a)
 {
-    constexpr int R = 32 * NW, QT = 64, TILE = QT * 2 * D;
+    constexpr int R = 32 * NW, QT = 64, TILE = Tile<D>::bytes(QT);
     __shared__ __attribute__((aligned(16))) uint8_t lds[2][2 * TILE + 2 * QT * 4];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int units = a.s.seqs * a.s.hk, group = a.s.hq / a.s.hk;
@@ -532,6 +545,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2, 2)))
     const int from = a.s.causal ? j - shift : 0;              // the lane's first query
     const int wfirst = a.s.causal ? w0 - shift : 0, wlast = a.s.causal ? w0 + 31 - shift : 0;
 
+    const int rb = Tile<D>::row_base(lane), cb = Tile<D>::col_base(lane);
     v16f dk[D / 32], dv[D / 32];
 #pragma unroll
     for (int b = 0; b < D / 32; b++)
@@ -559,10 +573,10 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2, 2)))
             }
 #pragma unroll
             for (int x = 0; x < D / 16; x++)
-                s = mfma(Tile<D>::rows(qt, 32 * u, x, lane), kf[x], s);
+                s = mfma(Tile<D>::rows(qt + rb, 32 * u, x), kf[x], s);
 #pragma unroll
             for (int x = 0; x < D / 16; x++)
-                dp = mfma(Tile<D>::rows(dt, 32 * u, x, lane), vf[x], dp);
+                dp = mfma(Tile<D>::rows(dt + rb, 32 * u, x), vf[x], dp);
             if (i1 < wlast || i1 + 32 > q.len) {
 #pragma unroll
                 for (int e = 0; e < 16; e++) {
@@ -580,8 +594,8 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2, 2)))
                 const v8bf p = operand(s, x), ds = operand(dp, x);
 #pragma unroll
                 for (int b = 0; b < D / 32; b++) {
-                    dv[b] = mfma(Tile<D>::cols(dt, 32 * u + 16 * x, b, lane), p, dv[b]);
-                    dk[b] = mfma(Tile<D>::cols(qt, 32 * u + 16 * x, b, lane), ds, dk[b]);
+                    dv[b] = mfma(Tile<D>::cols(dt + cb, 32 * u + 16 * x, b), p, dv[b]);
+                    dk[b] = mfma(Tile<D>::cols(qt + cb, 32 * u + 16 * x, b), ds, dk[b]);
                 }
             }
         }
@@ -596,7 +610,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2, 2)))
 template <int D, int NW>
 __global__ __launch_bounds__(64 * NW) void attn_bwd_q_kernel(AttnBwd a)
 {
-    constexpr int R = 32 * NW, TILE = KT * 2 * D;
+    constexpr int R = 32 * NW, TILE = Tile<D>::bytes(KT);
     __shared__ __attribute__((aligned(16))) uint8_t lds[2][2][TILE];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int units = a.s.seqs * a.s.hk, group = a.s.hq / a.s.hk;
@@ -627,6 +641,7 @@ __global__ __launch_bounds__(64 * NW) void attn_bwd_q_kernel(AttnBwd a)
     const int low = a.s.causal ? min(k.len - 1, w0 + shift) : k.len - 1;
     const int high = a.s.causal ? min(k.len - 1, w0 + 31 + shift) : k.len - 1;
 
+    const int rb = Tile<D>::row_base(lane), cb = Tile<D>::col_base(lane);
     v16f dq[D / 32];
 #pragma unroll
     for (int b = 0; b < D / 32; b++)
@@ -645,10 +660,10 @@ __global__ __launch_bounds__(64 * NW) void attn_bwd_q_kernel(AttnBwd a)
             v16f s = splat(0.0f), dp = splat(nd);
 #pragma unroll
             for (int e = 0; e < D / 16; e++)
-                s = mfma(Tile<D>::rows(kt, 32 * u, e, lane), qf[e], s);
+                s = mfma(Tile<D>::rows(kt + rb, 32 * u, e), qf[e], s);
 #pragma unroll
             for (int e = 0; e < D / 16; e++)
-                dp = mfma(Tile<D>::rows(vt, 32 * u, e, lane), df[e], dp);
+                dp = mfma(Tile<D>::rows(vt + rb, 32 * u, e), df[e], dp);
             if (j0 + 31 > low) {
 #pragma unroll
                 for (int e = 0; e < 16; e++)
@@ -662,7 +677,7 @@ __global__ __launch_bounds__(64 * NW) void attn_bwd_q_kernel(AttnBwd a)
                 const v8bf ds = operand(dp, e);
 #pragma unroll
                 for (int b = 0; b < D / 32; b++)
-                    dq[b] = mfma(Tile<D>::cols(kt, 32 * u + 16 * e, b, lane), ds, dq[b]);
+                    dq[b] = mfma(Tile<D>::cols(kt + cb, 32 * u + 16 * e, b), ds, dq[b]);
             }
         }
     }
