@@ -74,21 +74,38 @@ template <int D> struct Tile {
     static constexpr int STRIDE = 1024 + (D == 128 ? 16 : 32);    // bytes from piece to piece
     static constexpr int bytes(int rows) { return rows / PIECE * STRIDE; }
 
-    // This wave's share of a tile of ROWS rows from g on (row stride ld bytes); rows past `last` are
-    // copies of it, so that nothing behind a sequence is read.
-    template <int ROWS, int NW>
-    __device__ __forceinline__ static void stage(uint8_t *t, const uint16_t *g, uint32_t ld, int last, int wave, int lane)
-    {
-        constexpr int PIECES = ROWS / PIECE;
-        static_assert(PIECES % NW == 0, "whole pieces per wave");
-        const int sub = D == 128 ? 0 : lane >> 5, x = D == 128 ? lane >> 4 : (lane >> 4) & 1;
-        const int row = 4 * sub + ((lane >> 2) & 3), seg = 4 * x + ((lane & 3) ^ sub);
+    // A wave's share of tiles of ROWS rows: the lane's offsets from the first row, of row stride ld bytes.
+    template <int ROWS, int NW> struct Stage {
+        static constexpr int N = ROWS / PIECE / NW;
+        static_assert(ROWS / PIECE % NW == 0, "whole pieces per wave");
+        uint32_t ld, off[N];
+        int row, seg;
+
+        __device__ __forceinline__ Stage(int64_t stride, int wave, int lane) : ld((uint32_t)stride * 2)
+        {
+            const int sub = D == 128 ? 0 : lane >> 5, x = D == 128 ? lane >> 4 : (lane >> 4) & 1;
+            row = PIECE * wave + 4 * sub + ((lane >> 2) & 3);
+            seg = (4 * x + ((lane & 3) ^ sub)) * 16;
 #pragma unroll
-        for (int it = 0; it < PIECES / NW; it++) {
-            const int c = wave + NW * it;
-            copy16(g, (uint32_t)min(PIECE * c + row, last) * ld + (uint32_t)(seg * 16), t + c * STRIDE);
+            for (int i = 0; i < N; i++)
+                off[i] = (uint32_t)(row + PIECE * NW * i) * ld + (uint32_t)seg;
         }
-    }
+
+        // The tile that begins at g to t.  Rows past `last` are copies of it, so that nothing behind a
+        // sequence is read.
+        __device__ __forceinline__ void operator()(uint8_t *t, const uint16_t *g, int last, int wave) const
+        {
+            if (last >= ROWS - 1) {
+#pragma unroll
+                for (int i = 0; i < N; i++)
+                    copy16(g, off[i], t + (wave + NW * i) * STRIDE);
+            } else {
+#pragma unroll
+                for (int i = 0; i < N; i++)
+                    copy16(g, (uint32_t)min(row + PIECE * NW * i, last) * ld + (uint32_t)seg, t + (wave + NW * i) * STRIDE);
+            }
+        }
+    };
 
     // Where the lane's part of a row read and of a column read begins.
     __device__ __forceinline__ static int row_base(int lane)
@@ -140,6 +157,44 @@ __device__ __forceinline__ v16f splat(float x) { return v16f{x, x, x, x, x, x, x
 // Row of an accumulator's value i in this lane.
 __device__ __forceinline__ int acc_row(int i, int lane) { return 8 * (i >> 2) + 4 * (lane >> 5) + (i & 3); }
 
+// f(0) .. f(N - 1) with constant arguments.
+template <int N, class F> __device__ __forceinline__ void each(F f)
+{
+    if constexpr (N > 0) {
+        each<N - 1>(f);
+        f(std::integral_constant<int, N - 1>{});
+    }
+}
+
+// N products: use(i, load(i)) in order, with the next AHEAD operands' reads from LDS in flight.  The scheduling
+// barriers hold every read at its place: left alone the compiler puts each in front of its product, which then
+// waits for it.
+template <int N, int AHEAD = 6, class L, class U> __device__ __forceinline__ void feed(L load, U use)
+{
+    constexpr int RING = N < AHEAD ? N : AHEAD;
+    v8bf f[RING];
+    each<RING>([&](auto I) { f[I] = load(I); });
+    each<N>([&](auto I) {
+        constexpr int i = decltype(I)::value;
+        __builtin_amdgcn_sched_barrier(0);
+        use(I, f[i % RING]);
+        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (i + RING < N)
+            f[i % RING] = load(std::integral_constant<int, i + RING>{});
+    });
+}
+
+// Holds an operand in registers from here on, its load from memory waited for.
+template <int N> __device__ __forceinline__ void pin(v8bf (&f)[N])
+{
+#pragma unroll
+    for (int i = 0; i < N; i++) {
+        v4u w = __builtin_bit_cast(v4u, f[i]);
+        asm volatile("" : "+v"(w));
+        f[i] = __builtin_bit_cast(v8bf, w);
+    }
+}
+
 // Values 8 s .. 8 s + 7 of an accumulator as an operand.
 __device__ __forceinline__ v8bf operand(const v16f &v, int s)
 {
@@ -155,6 +210,9 @@ __device__ __forceinline__ float other_half(float x)
     return __uint_as_float((threadIdx.x & 32) ? r[0] : r[1]);
 }
 
+// A value that is the same in every lane, in a scalar register.
+__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
+
 // A sequence's rows, held inside the tensor and the announced maximum whatever the arrays say.
 struct Rows {
     int start, len;
@@ -168,6 +226,7 @@ __device__ __forceinline__ Rows rows_of(const int32_t *off, const int32_t *len, 
     n = n < most ? n : most;
     return Rows{(int)start, (int)(n < 0 ? 0 : n)};
 }
+__device__ __forceinline__ Rows uniform(const Rows &r) { return Rows{uniform(r.start), uniform(r.len)}; }
 __device__ __forceinline__ Rows q_rows(const AttnShape &a, int s) { return rows_of(a.q_off, a.q_len, s, a.tokens_q, a.max_q); }
 __device__ __forceinline__ Rows k_rows(const AttnShape &a, int s) { return rows_of(a.k_off, a.k_len, s, a.tokens_k, a.max_k); }
 
@@ -201,21 +260,41 @@ template <int D> struct Softmax {
             o[b] = splat(0.0f);
     }
 
-    // N blocks of 32 keys: scores (transposed) of rows kt, then P v of rows vt.  first .. : the blocks' first
-    // key; lim: the lane's last visible key; masked: whether some key of the blocks may be hidden.
-    template <int N>
-    __device__ __forceinline__ void step(const uint8_t *kt, const uint8_t *vt, const v8bf (&q)[D / 16], float c2,
-                                         int first, int lim, bool masked, int lane)
+    // The matrix cores' part: ADD: the P v of the last N blocks of 32 keys (tile rows vt); NEW: the scores,
+    // transposed, of the next ones (tile rows kt).
+    template <int N, bool ADD, bool NEW>
+    __device__ __forceinline__ void products(const uint8_t *vt, const v8bf (&p)[2 * N], const uint8_t *kt,
+                                             const v8bf (&q)[D / 16], v16f (&s)[N], int lane)
     {
+        constexpr int B = D / 32, A = ADD ? 2 * N * B : 0, T = A + (NEW ? N * D / 16 : 0);
         const uint8_t *kr = kt + Tile<D>::row_base(lane), *vc = vt + Tile<D>::col_base(lane);
-        v16f s[N];
+        if (NEW) {
 #pragma unroll
-        for (int n = 0; n < N; n++) {
-            s[n] = splat(0.0f);
-#pragma unroll
-            for (int k = 0; k < D / 16; k++)
-                s[n] = mfma(Tile<D>::rows(kr, 32 * n, k), q[k], s[n]);
+            for (int n = 0; n < N; n++)
+                s[n] = splat(0.0f);
         }
+        feed<T>(
+            [&](auto I) {
+                constexpr int i = decltype(I)::value;
+                if constexpr (i < A)
+                    return Tile<D>::cols(vc, 16 * (i / B), i % B);
+                else
+                    return Tile<D>::rows(kr, 32 * ((i - A) % N), (i - A) / N);
+            },
+            [&](auto I, const v8bf &f) {
+                constexpr int i = decltype(I)::value;
+                if constexpr (i < A)
+                    o[i % B] = mfma(f, p[i / B], o[i % B]);
+                else
+                    s[(i - A) % N] = mfma(f, q[(i - A) / N], s[(i - A) % N]);
+            });
+    }
+
+    // Their exponentials as the next product's operand.  first: the blocks' first key; lim: the lane's last
+    // visible key; masked: whether some key of the blocks may be hidden.
+    template <int N>
+    __device__ __forceinline__ void weigh(v16f (&s)[N], v8bf (&p)[2 * N], float c2, int first, int lim, bool masked, int lane)
+    {
         if (masked) {
 #pragma unroll
             for (int n = 0; n < N; n++)
@@ -246,19 +325,16 @@ template <int D> struct Softmax {
                 l += s[n][i];
             }
 #pragma unroll
-        for (int n = 0; n < N; n++)
-#pragma unroll
-            for (int k = 0; k < 2; k++) {
-                const v8bf p = operand(s[n], k);
-#pragma unroll
-                for (int b = 0; b < D / 32; b++)
-                    o[b] = mfma(Tile<D>::cols(vc, 32 * n + 16 * k, b), p, o[b]);
-            }
+        for (int n = 0; n < N; n++) {
+            p[2 * n] = operand(s[n], 0);
+            p[2 * n + 1] = operand(s[n], 1);
+        }
+        pin(p);   // formed here, not where the products want them
     }
 };
 
-// Share `split` of n tiles.
-__device__ __forceinline__ int share(int n, int split, int splits) { return (int)((int64_t)n * split / splits); }
+// Share `split` of n tiles (at most 2^18, in at most 2^8 shares).
+__device__ __forceinline__ int share(int n, int split, int splits) { return uniform(n * split / splits); }
 
 // Where row t's partial results of a split go: [split][head][row].
 __device__ __forceinline__ int64_t part_row(const AttnFwd &a, int split, int head, int t)
@@ -289,21 +365,20 @@ __device__ __forceinline__ void put_row(const AttnFwd &a, Softmax<D> &x, int spl
         a.stat[p] = make_float2(x.m, l);
 }
 
-// Many rows: NW waves of 32 queries of one head, 64 keys at a time through LDS.
-constexpr int KT = 64;
+// Many rows: NW waves of 32 queries of one head, 64 keys (128 of narrow heads) at a time through LDS.
 template <int D, int NW>
 __global__ __launch_bounds__(64 * NW) void attn_fwd_kernel(AttnFwd a)
 {
-    constexpr int R = 32 * NW, TILE = Tile<D>::bytes(KT);
+    constexpr int R = 32 * NW, KT = 8192 / D, TILE = Tile<D>::bytes(KT);
     __shared__ __attribute__((aligned(16))) uint8_t lds[2][2][TILE];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     // blocks of later rows, which see more keys, first; a sequence's key head on one XCD where their
     // number is a multiple of 8 (workgroups go round the XCDs)
     const int units = a.s.seqs * a.s.hk, group = a.s.hq / a.s.hk;
-    const int x = (int)blockIdx.x / (units * group), y = (int)blockIdx.x % (units * group);
-    const int unit = y % units, seq = unit / a.s.hk, kh = unit % a.s.hk, head = kh * group + y / units;
-    const int split = x % a.splits, block = a.blocks - 1 - x / a.splits;
-    const Rows q = q_rows(a.s, seq), k = k_rows(a.s, seq);
+    const int x = uniform((int)blockIdx.x / (units * group)), y = (int)blockIdx.x - x * units * group;
+    const int g = uniform(y / units), unit = y - g * units, seq = uniform(unit / a.s.hk), kh = unit - seq * a.s.hk;
+    const int head = kh * group + g, later = uniform(x / a.splits), split = x - later * a.splits, block = a.blocks - 1 - later;
+    const Rows q = uniform(q_rows(a.s, seq)), k = uniform(k_rows(a.s, seq));
     const int q0 = block * R;
     if (q0 >= q.len)
         return;
@@ -312,29 +387,71 @@ __global__ __launch_bounds__(64 * NW) void attn_fwd_kernel(AttnFwd a)
     const int tiles = (seen + KT - 1) / KT, t0 = share(tiles, split, a.splits), t1 = share(tiles, split + 1, a.splits);
 
     const uint16_t *kp = a.k + (int64_t)k.start * a.ldk + kh * D, *vp = a.v + (int64_t)k.start * a.ldv + kh * D;
-    auto stage = [&](int t) {
-        uint8_t *dst = lds[t & 1][0];
-        const int last = k.len - 1 - t * KT;
-        Tile<D>::template stage<KT, NW>(dst, kp + (int64_t)t * KT * a.ldk, (uint32_t)a.ldk * 2, last, wave, lane);
-        Tile<D>::template stage<KT, NW>(dst + TILE, vp + (int64_t)t * KT * a.ldv, (uint32_t)a.ldv * 2, last, wave, lane);
+    const typename Tile<D>::template Stage<KT, NW> copy_k(a.ldk, wave, lane), copy_v(a.ldv, wave, lane);
+    auto stage_k = [&](int t) {
+        if (t < t1)
+            copy_k(lds[0][t & 1], kp + (int64_t)t * KT * a.ldk, k.len - 1 - t * KT, wave);
     };
-    if (t0 < t1)
-        stage(t0);
+    auto stage_v = [&](int t) {
+        if (t < t1)
+            copy_v(lds[1][t & 1], vp + (int64_t)t * KT * a.ldv, k.len - 1 - t * KT, wave);
+    };
+    auto turn = [] {
+        __builtin_amdgcn_sched_barrier(0);
+        __syncthreads();
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    stage_k(t0);
     const int w0 = q0 + 32 * wave, i = w0 + (lane & 31), row = q.start + min(i, q.len - 1);
     v8bf qf[D / 16];
     Tile<D>::load(a.q + (int64_t)row * a.ldq + head * D, lane, qf);
     const int lim = a.s.causal ? min(k.len - 1, i + shift) : k.len - 1;
     const int low = a.s.causal ? min(k.len - 1, w0 + shift) : k.len - 1;           // the wave's first row's
-    const int high = a.s.causal ? min(k.len - 1, w0 + 31 + shift) : k.len - 1;     // and its last one's
 
+    // The two waves of a SIMD take turns on its matrix cores: one forms the next tile's scores and adds up the
+    // last one's P v while the other takes the exponentials of its own.
+    const bool late = wave >= NW / 2;
     Softmax<D> st;
-    for (int t = t0; t < t1; t++) {
-        wait_copies<0>();
-        __syncthreads();
-        if (t + 1 < t1)
-            stage(t + 1);
-        if (t * KT <= high)
-            st.template step<KT / 32>(lds[t & 1][0], lds[t & 1][1], qf, a.c2, t * KT, lim, t * KT + KT - 1 > low, lane);
+    constexpr int N = KT / 32;
+    v16f s[N];
+    v8bf p[2 * N];
+    pin(qf);
+    wait_copies<0>();
+    turn();
+    if (t0 < t1) {
+        stage_k(t0 + 1);
+        stage_v(t0);
+        if (late)
+            turn();
+        st.template products<N, false, true>(lds[1][0], p, lds[0][t0 & 1], qf, s, lane);
+        if (late)
+            wait_copies<0>();
+        turn();
+        for (int t = t0; t < t1 - 1; t++) {
+            if (late) {
+                stage_k(t + 2);
+                stage_v(t + 1);
+            }
+            st.template weigh<N>(s, p, a.c2, t * KT, lim, t * KT + KT - 1 > low, lane);
+            if (!late)
+                wait_copies<0>();
+            turn();
+            if (!late) {
+                stage_k(t + 2);
+                stage_v(t + 1);
+            }
+            st.template products<N, true, true>(lds[1][t & 1], p, lds[0][(t + 1) & 1], qf, s, lane);
+            if (late)
+                wait_copies<0>();
+            turn();
+        }
+        st.template weigh<N>(s, p, a.c2, (t1 - 1) * KT, lim, t1 * KT - 1 > low, lane);
+        if (!late)
+            wait_copies<0>();
+        turn();
+        if (!late)
+            turn();   // as many as the others
+        st.template products<N, true, false>(lds[1][(t1 - 1) & 1], p, lds[0][0], qf, s, lane);
     }
     if (i < q.len)
         put_row<D>(a, st, split, head, q.start + i, lane);
@@ -351,8 +468,9 @@ __global__ __launch_bounds__(256) void attn_rows_kernel(AttnFwd a)
     __shared__ __attribute__((aligned(16))) uint8_t lds[NW][WAVE];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int units = a.s.seqs * a.s.hk, group = a.s.hq / a.s.hk;
-    const int unit = (int)blockIdx.x % units, split = (int)blockIdx.x / units, seq = unit / a.s.hk, kh = unit % a.s.hk;
-    const Rows q = q_rows(a.s, seq), k = k_rows(a.s, seq);
+    const int split = uniform((int)blockIdx.x / units), unit = (int)blockIdx.x - split * units;
+    const int seq = uniform(unit / a.s.hk), kh = unit - seq * a.s.hk;
+    const Rows q = uniform(q_rows(a.s, seq)), k = uniform(k_rows(a.s, seq));
     const int cols = q.len * group;
     if (cols == 0)
         return;
@@ -361,11 +479,12 @@ __global__ __launch_bounds__(256) void attn_rows_kernel(AttnFwd a)
     const int t0 = share(tiles, part, parts), t1 = share(tiles, part + 1, parts);
 
     const uint16_t *kp = a.k + (int64_t)k.start * a.ldk + kh * D, *vp = a.v + (int64_t)k.start * a.ldv + kh * D;
+    const typename Tile<D>::template Stage<KW, 1> copy_k(a.ldk, 0, lane), copy_v(a.ldv, 0, lane);
     auto stage = [&](int t) {
         uint8_t *dst = lds[wave] + (t & 1) * 2 * TILE;
         const int last = k.len - 1 - t * KW;
-        Tile<D>::template stage<KW, 1>(dst, kp + (int64_t)t * KW * a.ldk, (uint32_t)a.ldk * 2, last, 0, lane);
-        Tile<D>::template stage<KW, 1>(dst + TILE, vp + (int64_t)t * KW * a.ldv, (uint32_t)a.ldv * 2, last, 0, lane);
+        copy_k(dst, kp + (int64_t)t * KW * a.ldk, last, 0);
+        copy_v(dst + TILE, vp + (int64_t)t * KW * a.ldv, last, 0);
     };
     constexpr int COPIES = 2 * KW / Tile<D>::PIECE;
     const int c = min(lane & 31, cols - 1), i = c / group, head = kh * group + c % group;
@@ -385,8 +504,12 @@ __global__ __launch_bounds__(256) void attn_rows_kernel(AttnFwd a)
         } else {
             wait_copies<0>();
         }
-        st.template step<1>(lds[wave] + (t & 1) * 2 * TILE, lds[wave] + (t & 1) * 2 * TILE + TILE, qf, a.c2, t * KW, lim,
-                            t * KW + KW - 1 > low, lane);
+        v16f s[1];
+        v8bf p[2];
+        const uint8_t *tile = lds[wave] + (t & 1) * 2 * TILE;
+        st.template products<1, false, true>(tile, p, tile, qf, s, lane);
+        st.template weigh<1>(s, p, a.c2, t * KW, lim, t * KW + KW - 1 > low, lane);
+        st.template products<1, true, false>(tile + TILE, p, tile, qf, s, lane);
         __builtin_amdgcn_s_waitcnt(0xc07f);   // lgkmcnt(0): the tile is read before copies go over it
     }
     // the waves' results: [column][D + 4] floats, output then maximum and sum
@@ -515,21 +638,23 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2, 2)))
     __shared__ __attribute__((aligned(16))) uint8_t lds[2][2 * TILE + 2 * QT * 4];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int units = a.s.seqs * a.s.hk, group = a.s.hq / a.s.hk;
-    const int block = (int)blockIdx.x / units, unit = (int)blockIdx.x % units;   // earlier keys, seen by more, first
-    const int seq = unit / a.s.hk, kh = unit % a.s.hk;
-    const Rows q = q_rows(a.s, seq), k = k_rows(a.s, seq);
+    const int x0 = uniform((int)blockIdx.x / units), unit = (int)blockIdx.x - x0 * units, half = (a.k_blocks + 1) / 2;
+    const int block = a.fold && x0 >= half ? a.k_blocks - 1 - (x0 - half) : x0;   // earlier keys, seen by more, first
+    const int seq = uniform(unit / a.s.hk), kh = unit - seq * a.s.hk;
+    const Rows q = uniform(q_rows(a.s, seq)), k = uniform(k_rows(a.s, seq));
     const int k0 = block * R;
     if (k0 >= k.len)
         return;
     const int shift = k.len - q.len, tiles = (q.len + QT - 1) / QT;
     const int t0 = a.s.causal ? min(tiles, max(0, k0 - shift) / QT) : 0, per = tiles - t0, steps = per * group;
 
+    const typename Tile<D>::template Stage<QT, NW> copy_q(a.ldq, wave, lane), copy_d(a.lddo, wave, lane);
     auto stage = [&](int n) {
         const int h = kh * group + n / per, t = t0 + n % per, last = q.len - 1 - t * QT;
         const int64_t row = (int64_t)q.start + t * QT;
         uint8_t *dst = lds[n & 1];
-        Tile<D>::template stage<QT, NW>(dst, a.q + row * a.ldq + h * D, (uint32_t)a.ldq * 2, last, wave, lane);
-        Tile<D>::template stage<QT, NW>(dst + TILE, a.dout + row * a.lddo + h * D, (uint32_t)a.lddo * 2, last, wave, lane);
+        copy_q(dst, a.q + row * a.ldq + h * D, last, wave);
+        copy_d(dst + TILE, a.dout + row * a.lddo + h * D, last, wave);
         if (wave == 0) {
             const uint32_t off = (uint32_t)min(lane, last) * 4;
             copy4(a.nl + (int64_t)h * a.s.tokens_q + row, off, dst + 2 * TILE);
@@ -606,17 +731,18 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2, 2)))
     }
 }
 
-// Queries' gradients: NW waves of 32 queries of one head, 64 keys at a time.
+// Queries' gradients: NW waves of 32 queries of one head, 64 keys at a time through LDS, 32 in a step.
 template <int D, int NW>
 __global__ __launch_bounds__(64 * NW) void attn_bwd_q_kernel(AttnBwd a)
 {
-    constexpr int R = 32 * NW, TILE = Tile<D>::bytes(KT);
-    __shared__ __attribute__((aligned(16))) uint8_t lds[2][2][TILE];
+    constexpr int R = 32 * NW, KT = 64, TILE = Tile<D>::bytes(KT), B = D / 32, S = D / 16;
+    __shared__ __attribute__((aligned(16))) uint8_t lds_k[3][TILE], lds_v[2][TILE];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int units = a.s.seqs * a.s.hk, group = a.s.hq / a.s.hk;
-    const int x = (int)blockIdx.x / (units * group), y = (int)blockIdx.x % (units * group);
-    const int unit = y % units, seq = unit / a.s.hk, kh = unit % a.s.hk, head = kh * group + y / units;
-    const Rows q = q_rows(a.s, seq), k = k_rows(a.s, seq);
+    const int x = uniform((int)blockIdx.x / (units * group)), y = (int)blockIdx.x - x * units * group;
+    const int g = uniform(y / units), unit = y - g * units, seq = uniform(unit / a.s.hk), kh = unit - seq * a.s.hk;
+    const int head = kh * group + g;
+    const Rows q = uniform(q_rows(a.s, seq)), k = uniform(k_rows(a.s, seq));
     const int q0 = (a.q_blocks - 1 - x) * R;
     if (q0 >= q.len)
         return;
@@ -625,62 +751,91 @@ __global__ __launch_bounds__(64 * NW) void attn_bwd_q_kernel(AttnBwd a)
     const int tiles = (seen + KT - 1) / KT;
 
     const uint16_t *kp = a.k + (int64_t)k.start * a.ldk + kh * D, *vp = a.v + (int64_t)k.start * a.ldv + kh * D;
-    auto stage = [&](int t) {
+    const typename Tile<D>::template Stage<KT, NW> copy_k(a.ldk, wave, lane), copy_v(a.ldv, wave, lane);
+    int at = 0;   // the K tile's place among three: the last tile's is read for one step into the next
+    auto stage = [&](int t, int place) {
         const int last = k.len - 1 - t * KT;
-        Tile<D>::template stage<KT, NW>(lds[t & 1][0], kp + (int64_t)t * KT * a.ldk, (uint32_t)a.ldk * 2, last, wave, lane);
-        Tile<D>::template stage<KT, NW>(lds[t & 1][1], vp + (int64_t)t * KT * a.ldv, (uint32_t)a.ldv * 2, last, wave, lane);
+        copy_k(lds_k[place], kp + (int64_t)t * KT * a.ldk, last, wave);
+        copy_v(lds_v[t & 1], vp + (int64_t)t * KT * a.ldv, last, wave);
     };
     if (tiles > 0)
-        stage(0);
+        stage(0, 0);
     const int w0 = q0 + 32 * wave, i = w0 + (lane & 31), row = q.start + min(i, q.len - 1);
-    v8bf qf[D / 16], df[D / 16];
+    v8bf qf[S], df[S];
     Tile<D>::load(a.q + (int64_t)row * a.ldq + head * D, lane, qf);
     Tile<D>::load(a.dout + (int64_t)row * a.lddo + head * D, lane, df);
+    pin(qf);
+    pin(df);
     const float nl = a.nl[(int64_t)head * a.s.tokens_q + row] * a.c2, nd = a.nd[(int64_t)head * a.s.tokens_q + row];
     const int lim = a.s.causal ? min(k.len - 1, i + shift) : k.len - 1;
     const int low = a.s.causal ? min(k.len - 1, w0 + shift) : k.len - 1;
     const int high = a.s.causal ? min(k.len - 1, w0 + 31 + shift) : k.len - 1;
-
     const int rb = Tile<D>::row_base(lane), cb = Tile<D>::col_base(lane);
-    v16f dq[D / 32];
+
+    v16f dq[B];
+    v8bf ds[2];
 #pragma unroll
-    for (int b = 0; b < D / 32; b++)
+    for (int b = 0; b < B; b++)
         dq[b] = splat(0.0f);
+    ds[0] = ds[1] = __builtin_bit_cast(v8bf, v4u{0, 0, 0, 0});
+    // a step: the last step's dS k (rows kc; zeros before the first one), and 32 keys' scores and dP
+    auto add = [&](const uint8_t *kc) {
+        feed<2 * B>([&](auto I) { return Tile<D>::cols(kc, 16 * (I / B), I % B); },
+                    [&](auto I, const v8bf &f) { dq[I % B] = mfma(f, ds[I / B], dq[I % B]); });
+    };
+    auto step = [&](const uint8_t *kc, const uint8_t *kr, const uint8_t *vr, int j0) {
+        v16f s = splat(0.0f), dp = splat(nd);
+        feed<2 * B + 2 * S>(
+            [&](auto I) {
+                constexpr int n = decltype(I)::value;
+                if constexpr (n < 2 * B)
+                    return Tile<D>::cols(kc, 16 * (n / B), n % B);
+                else if constexpr (n % 2 == 0)
+                    return Tile<D>::rows(kr, 0, (n - 2 * B) / 2);
+                else
+                    return Tile<D>::rows(vr, 0, (n - 2 * B) / 2);
+            },
+            [&](auto I, const v8bf &f) {
+                constexpr int n = decltype(I)::value;
+                if constexpr (n < 2 * B)
+                    dq[n % B] = mfma(f, ds[n / B], dq[n % B]);
+                else if constexpr (n % 2 == 0)
+                    s = mfma(f, qf[(n - 2 * B) / 2], s);
+                else
+                    dp = mfma(f, df[(n - 2 * B) / 2], dp);
+            });
+        if (j0 + 31 > low) {
+#pragma unroll
+            for (int e = 0; e < 16; e++)
+                s[e] = j0 + acc_row(e, lane) > lim ? -INFINITY : s[e];
+        }
+#pragma unroll
+        for (int e = 0; e < 16; e++)
+            dp[e] *= __builtin_amdgcn_exp2f(fmaf(s[e], a.c2, nl));
+        ds[0] = operand(dp, 0);
+        ds[1] = operand(dp, 1);
+    };
+    constexpr int HALF = Tile<D>::bytes(32);
+    const uint8_t *kc = lds_k[0] + cb;
     for (int t = 0; t < tiles; t++) {
         wait_copies<0>();
         __syncthreads();
+        const int next = at == 2 ? 0 : at + 1;
         if (t + 1 < tiles)
-            stage(t + 1);
-        const uint8_t *kt = lds[t & 1][0], *vt = lds[t & 1][1];
-#pragma unroll
-        for (int u = 0; u < KT / 32; u++) {
+            stage(t + 1, next);
+#pragma unroll 1
+        for (int u = 0; u < 2; u++) {
+            // one step past the wave's last visible key: it adds the step before and leaves zeros
             const int j0 = t * KT + 32 * u;
-            if (j0 > high)
-                continue;
-            v16f s = splat(0.0f), dp = splat(nd);
-#pragma unroll
-            for (int e = 0; e < D / 16; e++)
-                s = mfma(Tile<D>::rows(kt + rb, 32 * u, e), qf[e], s);
-#pragma unroll
-            for (int e = 0; e < D / 16; e++)
-                dp = mfma(Tile<D>::rows(vt + rb, 32 * u, e), df[e], dp);
-            if (j0 + 31 > low) {
-#pragma unroll
-                for (int e = 0; e < 16; e++)
-                    s[e] = j0 + acc_row(e, lane) > lim ? -INFINITY : s[e];
-            }
-#pragma unroll
-            for (int e = 0; e < 16; e++)
-                dp[e] *= __builtin_amdgcn_exp2f(fmaf(s[e], a.c2, nl));
-#pragma unroll
-            for (int e = 0; e < 2; e++) {
-                const v8bf ds = operand(dp, e);
-#pragma unroll
-                for (int b = 0; b < D / 32; b++)
-                    dq[b] = mfma(Tile<D>::cols(kt + cb, 32 * u + 16 * e, b), ds, dq[b]);
-            }
+            const uint8_t *kt = lds_k[at] + u * HALF;
+            if (j0 - 32 <= high)
+                step(kc, kt + rb, lds_v[t & 1] + u * HALF + rb, j0);
+            kc = kt + cb;
         }
+        at = next;
     }
+    if (tiles > 0)
+        add(kc);
     if (i < q.len)
         store_row<D>(a.dq + (int64_t)row * a.lddq + head * D, dq, a.scale, lane);
 }
@@ -784,6 +939,9 @@ hipError_t launch_attn_bwd(AttnBwd b, void *workspace, hipStream_t st)
 {
     b.c2 = b.scale * kLog2e;
     b.q_blocks = (int)blocks_of(b.s.max_q, 32 * BWD_Q_WAVES);
+    b.k_blocks = (int)blocks_of(b.s.max_k, 32 * BWD_K_WAVES);
+    const int64_t groups = (int64_t)b.s.seqs * b.s.hk * b.k_blocks;
+    b.fold = b.s.causal && groups > 256 && groups <= 512;
     b.nl = (float *)workspace;
     b.nd = (float *)((char *)workspace + attn_bwd_workspace_bytes(b.s) / 2);
     return b.s.dim == 64 ? bwd<64>(b, st) : bwd<128>(b, st);
