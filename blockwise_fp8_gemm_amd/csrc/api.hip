@@ -1232,8 +1232,8 @@ puro_status_t puro_fp8_attention_bwd(const puro_attention_t *shape, const void *
         const puro::AttnBwd b{s, static_cast<const uint16_t *>(dout), lddout, static_cast<const uint16_t *>(q), ldq,
                               static_cast<const uint16_t *>(k), ldk, static_cast<const uint16_t *>(v), ldv,
                               static_cast<const uint16_t *>(o), ldo, lse, shape->scale, static_cast<uint16_t *>(dq),
-                              lddq, static_cast<uint16_t *>(dk), lddk, static_cast<uint16_t *>(dv), lddv, 0.0f, 0, 0,
-                              false, nullptr, nullptr};
+                              lddq, static_cast<uint16_t *>(dk), lddk, static_cast<uint16_t *>(dv), lddv, 0.0f, 0,
+                              nullptr, nullptr};
         return from_hip(puro::launch_attn_bwd(b, workspace, stream));
     } catch (...) {
         return PURO_ERR_INTERNAL;

@@ -365,7 +365,7 @@ __device__ __forceinline__ void put_row(const AttnFwd &a, Softmax<D> &x, int spl
         a.stat[p] = make_float2(x.m, l);
 }
 
-// Many rows: NW waves of 32 queries of one head, 64 keys (128 of narrow heads) at a time through LDS.
+// Many rows: NW waves of 32 rows, a query of one head each, 64 keys (128 of narrow heads) at a time through LDS.
 template <int D, int NW>
 __global__ __launch_bounds__(64 * NW) void attn_fwd_kernel(AttnFwd a)
 {
@@ -373,17 +373,17 @@ __global__ __launch_bounds__(64 * NW) void attn_fwd_kernel(AttnFwd a)
     __shared__ __attribute__((aligned(16))) uint8_t lds[2][2][TILE];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     // blocks of later rows, which see more keys, first; a sequence's key head on one XCD where their
-    // number is a multiple of 8 (workgroups go round the XCDs)
+    // number is a multiple of 8 (workgroups go round the XCDs).  The query heads of a key head share its tiles.
     const int units = a.s.seqs * a.s.hk, group = a.s.hq / a.s.hk;
-    const int x = uniform((int)blockIdx.x / (units * group)), y = (int)blockIdx.x - x * units * group;
-    const int g = uniform(y / units), unit = y - g * units, seq = uniform(unit / a.s.hk), kh = unit - seq * a.s.hk;
-    const int head = kh * group + g, later = uniform(x / a.splits), split = x - later * a.splits, block = a.blocks - 1 - later;
+    const int x = uniform((int)blockIdx.x / units), unit = (int)blockIdx.x - x * units;
+    const int seq = uniform(unit / a.s.hk), kh = unit - seq * a.s.hk;
+    const int later = uniform(x / a.splits), split = x - later * a.splits, r0 = (a.blocks - 1 - later) * R;
     const Rows q = uniform(q_rows(a.s, seq)), k = uniform(k_rows(a.s, seq));
-    const int q0 = block * R;
-    if (q0 >= q.len)
+    const int rows = q.len * group;   // (query, head) pairs, a query's heads side by side
+    if (r0 >= rows)
         return;
-    const int shift = k.len - q.len;
-    const int seen = a.s.causal ? max(0, min(k.len, min(q0 + R, q.len) + shift)) : k.len;
+    const int shift = k.len - q.len, last = uniform((min(r0 + R, rows) - 1) / group);
+    const int seen = a.s.causal ? max(0, min(k.len, last + 1 + shift)) : k.len;
     const int tiles = (seen + KT - 1) / KT, t0 = share(tiles, split, a.splits), t1 = share(tiles, split + 1, a.splits);
 
     const uint16_t *kp = a.k + (int64_t)k.start * a.ldk + kh * D, *vp = a.v + (int64_t)k.start * a.ldv + kh * D;
@@ -402,11 +402,12 @@ __global__ __launch_bounds__(64 * NW) void attn_fwd_kernel(AttnFwd a)
         __builtin_amdgcn_sched_barrier(0);
     };
     stage_k(t0);
-    const int w0 = q0 + 32 * wave, i = w0 + (lane & 31), row = q.start + min(i, q.len - 1);
+    const int w0 = r0 + 32 * wave, r = w0 + (lane & 31), rc = min(r, rows - 1);
+    const int i = rc / group, head = kh * group + (rc - i * group), row = q.start + i;
     v8bf qf[D / 16];
     Tile<D>::load(a.q + (int64_t)row * a.ldq + head * D, lane, qf);
     const int lim = a.s.causal ? min(k.len - 1, i + shift) : k.len - 1;
-    const int low = a.s.causal ? min(k.len - 1, w0 + shift) : k.len - 1;           // the wave's first row's
+    const int low = a.s.causal ? min(k.len - 1, uniform(w0 / group) + shift) : k.len - 1;   // the wave's first row's
 
     // The two waves of a SIMD take turns on its matrix cores: one forms the next tile's scores and adds up the
     // last one's P v while the other takes the exponentials of its own.
@@ -453,8 +454,8 @@ __global__ __launch_bounds__(64 * NW) void attn_fwd_kernel(AttnFwd a)
             turn();   // as many as the others
         st.template products<N, true, false>(lds[1][(t1 - 1) & 1], p, lds[0][0], qf, s, lane);
     }
-    if (i < q.len)
-        put_row<D>(a, st, split, head, q.start + i, lane);
+    if (r < rows)
+        put_row<D>(a, st, split, head, row, lane);
 }
 
 // Few rows (at most 32 of a key head's queries over all its query heads): a wave
@@ -630,51 +631,63 @@ __global__ __launch_bounds__(256) void attn_bwd_rows_kernel(AttnBwd a)
     }
 }
 
-// Keys' and values' gradients: NW waves of 32 keys, 64 queries of one head at a time.
+// Keys' and values' gradients: NW waves of 32 keys, twice; 64 queries (128 of narrow heads) of one head at a time
+// through LDS.  The
+// two waves of the same keys lie on one SIMD and take the even and the odd runs of 32 queries; their sums meet
+// at the end.
 template <int D, int NW>
-__global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2, 2))) void attn_bwd_k_kernel(AttnBwd a)
+__global__ __launch_bounds__(128 * NW) void attn_bwd_k_kernel(AttnBwd a)
 {
-    constexpr int R = 32 * NW, QT = 64, TILE = Tile<D>::bytes(QT);
-    __shared__ __attribute__((aligned(16))) uint8_t lds[2][2 * TILE + 2 * QT * 4];
+    constexpr int R = 32 * NW, QT = 8192 / D, TILE = Tile<D>::bytes(QT), STAGE = 2 * TILE + 2 * QT * 4, B = D / 32;
+    static_assert(2 * STAGE >= NW * 16 * B * 256, "one of the sums takes the tiles' place");
+    __shared__ __attribute__((aligned(16))) uint8_t lds[2][STAGE];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int kw = wave % NW, half = wave / NW;
     const int units = a.s.seqs * a.s.hk, group = a.s.hq / a.s.hk;
-    const int x0 = uniform((int)blockIdx.x / units), unit = (int)blockIdx.x - x0 * units, half = (a.k_blocks + 1) / 2;
-    const int block = a.fold && x0 >= half ? a.k_blocks - 1 - (x0 - half) : x0;   // earlier keys, seen by more, first
+    const int block = uniform((int)blockIdx.x / units), unit = (int)blockIdx.x - block * units;   // earlier keys, seen by more, first
     const int seq = uniform(unit / a.s.hk), kh = unit - seq * a.s.hk;
     const Rows q = uniform(q_rows(a.s, seq)), k = uniform(k_rows(a.s, seq));
     const int k0 = block * R;
     if (k0 >= k.len)
         return;
     const int shift = k.len - q.len, tiles = (q.len + QT - 1) / QT;
-    const int t0 = a.s.causal ? min(tiles, max(0, k0 - shift) / QT) : 0, per = tiles - t0, steps = per * group;
+    const int t0 = a.s.causal ? min(tiles, max(0, k0 - shift) / QT) : 0, steps = (tiles - t0) * group;
 
-    const typename Tile<D>::template Stage<QT, NW> copy_q(a.ldq, wave, lane), copy_d(a.lddo, wave, lane);
+    const typename Tile<D>::template Stage<QT, 2 * NW> copy_q(a.ldq, wave, lane), copy_d(a.lddo, wave, lane);
+    int sh = kh * group, st = t0;   // the next tile to be copied: its head and its place
     auto stage = [&](int n) {
-        const int h = kh * group + n / per, t = t0 + n % per, last = q.len - 1 - t * QT;
-        const int64_t row = (int64_t)q.start + t * QT;
+        const int last = q.len - 1 - st * QT;
+        const int64_t row = (int64_t)q.start + st * QT;
         uint8_t *dst = lds[n & 1];
-        copy_q(dst, a.q + row * a.ldq + h * D, last, wave);
-        copy_d(dst + TILE, a.dout + row * a.lddo + h * D, last, wave);
-        if (wave == 0) {
-            const uint32_t off = (uint32_t)min(lane, last) * 4;
-            copy4(a.nl + (int64_t)h * a.s.tokens_q + row, off, dst + 2 * TILE);
-            copy4(a.nd + (int64_t)h * a.s.tokens_q + row, off, dst + 2 * TILE + QT * 4);
+        copy_q(dst, a.q + row * a.ldq + sh * D, last, wave);
+        copy_d(dst + TILE, a.dout + row * a.lddo + sh * D, last, wave);
+        if (wave < QT / 64) {
+            const uint32_t off = (uint32_t)min(64 * wave + lane, last) * 4;
+            copy4(a.nl + (int64_t)sh * a.s.tokens_q + row, off, dst + 2 * TILE + 256 * wave);
+            copy4(a.nd + (int64_t)sh * a.s.tokens_q + row, off, dst + 2 * TILE + QT * 4 + 256 * wave);
+        }
+        if (++st == tiles) {
+            st = t0;
+            sh++;
         }
     };
     if (steps > 0)
         stage(0);
-    const int w0 = k0 + 32 * wave, j = w0 + (lane & 31), row = k.start + min(j, k.len - 1);
+    const int w0 = k0 + 32 * kw, j = w0 + (lane & 31), row = k.start + min(j, k.len - 1);
     v8bf kf[D / 16], vf[D / 16];
     Tile<D>::load(a.k + (int64_t)row * a.ldk + kh * D, lane, kf);
     Tile<D>::load(a.v + (int64_t)row * a.ldv + kh * D, lane, vf);
+    pin(kf);
+    pin(vf);
     const int from = a.s.causal ? j - shift : 0;              // the lane's first query
     const int wfirst = a.s.causal ? w0 - shift : 0, wlast = a.s.causal ? w0 + 31 - shift : 0;
-
     const int rb = Tile<D>::row_base(lane), cb = Tile<D>::col_base(lane);
-    v16f dk[D / 32], dv[D / 32];
+
+    v16f dk[B], dv[B];
 #pragma unroll
-    for (int b = 0; b < D / 32; b++)
+    for (int b = 0; b < B; b++)
         dk[b] = dv[b] = splat(0.0f);
+    int t = t0;
     for (int n = 0; n < steps; n++) {
         wait_copies<0>();
         __syncthreads();
@@ -682,12 +695,14 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2, 2)))
             stage(n + 1);
         const uint8_t *qt = lds[n & 1], *dt = qt + TILE;
         const float *nl = reinterpret_cast<const float *>(qt + 2 * TILE), *nd = nl + QT;
-        const int i0 = (t0 + n % per) * QT;
-#pragma unroll
-        for (int u = 0; u < QT / 32; u++) {
+        const int i0 = t * QT;
+        t = t + 1 == tiles ? t0 : t + 1;
+#pragma unroll 1
+        for (int u = half; u < QT / 32; u += 2) {
             const int i1 = i0 + 32 * u;
             if (i1 + 31 < wfirst || i1 >= q.len)
                 continue;
+            const uint8_t *qu = qt + u * Tile<D>::bytes(32), *du = dt + u * Tile<D>::bytes(32);
             v16f s, dp;
 #pragma unroll
             for (int g = 0; g < 4; g++) {
@@ -698,10 +713,10 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2, 2)))
             }
 #pragma unroll
             for (int x = 0; x < D / 16; x++)
-                s = mfma(Tile<D>::rows(qt + rb, 32 * u, x), kf[x], s);
+                s = mfma(Tile<D>::rows(qu + rb, 0, x), kf[x], s);
 #pragma unroll
             for (int x = 0; x < D / 16; x++)
-                dp = mfma(Tile<D>::rows(dt + rb, 32 * u, x), vf[x], dp);
+                dp = mfma(Tile<D>::rows(du + rb, 0, x), vf[x], dp);
             if (i1 < wlast || i1 + 32 > q.len) {
 #pragma unroll
                 for (int e = 0; e < 16; e++) {
@@ -718,20 +733,50 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2, 2)))
             for (int x = 0; x < 2; x++) {
                 const v8bf p = operand(s, x), ds = operand(dp, x);
 #pragma unroll
-                for (int b = 0; b < D / 32; b++) {
-                    dv[b] = mfma(Tile<D>::cols(dt + cb, 32 * u + 16 * x, b), p, dv[b]);
-                    dk[b] = mfma(Tile<D>::cols(qt + cb, 32 * u + 16 * x, b), ds, dk[b]);
+                for (int b = 0; b < B; b++) {
+                    dv[b] = mfma(Tile<D>::cols(du + cb, 16 * x, b), p, dv[b]);
+                    dk[b] = mfma(Tile<D>::cols(qu + cb, 16 * x, b), ds, dk[b]);
                 }
             }
         }
     }
+    // the odd runs' dk go to the even ones' waves, and the even runs' dv to the odd ones'
+    float *x = reinterpret_cast<float *>(lds[0]) + kw * 16 * B * 64 + lane;
+    auto put = [&](const v16f (&v)[B]) {
+#pragma unroll
+        for (int b = 0; b < B; b++)
+#pragma unroll
+            for (int e = 0; e < 16; e++)
+                x[(16 * b + e) * 64] = v[b][e];
+    };
+    auto take = [&](v16f (&v)[B]) {
+#pragma unroll
+        for (int b = 0; b < B; b++)
+#pragma unroll
+            for (int e = 0; e < 16; e++)
+                v[b][e] += x[(16 * b + e) * 64];
+    };
+    __syncthreads();
+    if (half == 1)
+        put(dk);
+    __syncthreads();
+    if (half == 0)
+        take(dk);
+    __syncthreads();
+    if (half == 0)
+        put(dv);
+    __syncthreads();
+    if (half == 1)
+        take(dv);
     if (j < k.len) {
-        store_row<D>(a.dk + (int64_t)row * a.lddk + kh * D, dk, a.scale, lane);
-        store_row<D>(a.dv + (int64_t)row * a.lddv + kh * D, dv, 1.0f, lane);
+        if (half == 0)
+            store_row<D>(a.dk + (int64_t)row * a.lddk + kh * D, dk, a.scale, lane);
+        else
+            store_row<D>(a.dv + (int64_t)row * a.lddv + kh * D, dv, 1.0f, lane);
     }
 }
 
-// Queries' gradients: NW waves of 32 queries of one head, 64 keys at a time through LDS, 32 in a step.
+// Queries' gradients: NW waves of 32 rows (as in the forward), 64 keys at a time through LDS, 32 in a step.
 template <int D, int NW>
 __global__ __launch_bounds__(64 * NW) void attn_bwd_q_kernel(AttnBwd a)
 {
@@ -739,15 +784,15 @@ __global__ __launch_bounds__(64 * NW) void attn_bwd_q_kernel(AttnBwd a)
     __shared__ __attribute__((aligned(16))) uint8_t lds_k[3][TILE], lds_v[2][TILE];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int units = a.s.seqs * a.s.hk, group = a.s.hq / a.s.hk;
-    const int x = uniform((int)blockIdx.x / (units * group)), y = (int)blockIdx.x - x * units * group;
-    const int g = uniform(y / units), unit = y - g * units, seq = uniform(unit / a.s.hk), kh = unit - seq * a.s.hk;
-    const int head = kh * group + g;
+    const int x = uniform((int)blockIdx.x / units), unit = (int)blockIdx.x - x * units;
+    const int seq = uniform(unit / a.s.hk), kh = unit - seq * a.s.hk;
     const Rows q = uniform(q_rows(a.s, seq)), k = uniform(k_rows(a.s, seq));
-    const int q0 = (a.q_blocks - 1 - x) * R;
-    if (q0 >= q.len)
+    const int r0 = (a.q_blocks - 1 - x) * R;
+    const int rows = q.len * group;   // (query, head) pairs, a query's heads side by side
+    if (r0 >= rows)
         return;
-    const int shift = k.len - q.len;
-    const int seen = a.s.causal ? max(0, min(k.len, min(q0 + R, q.len) + shift)) : k.len;
+    const int shift = k.len - q.len, last = uniform((min(r0 + R, rows) - 1) / group);
+    const int seen = a.s.causal ? max(0, min(k.len, last + 1 + shift)) : k.len;
     const int tiles = (seen + KT - 1) / KT;
 
     const uint16_t *kp = a.k + (int64_t)k.start * a.ldk + kh * D, *vp = a.v + (int64_t)k.start * a.ldv + kh * D;
@@ -760,7 +805,8 @@ __global__ __launch_bounds__(64 * NW) void attn_bwd_q_kernel(AttnBwd a)
     };
     if (tiles > 0)
         stage(0, 0);
-    const int w0 = q0 + 32 * wave, i = w0 + (lane & 31), row = q.start + min(i, q.len - 1);
+    const int w0 = r0 + 32 * wave, r = w0 + (lane & 31), rc = min(r, rows - 1);
+    const int i = rc / group, head = kh * group + (rc - i * group), row = q.start + i;
     v8bf qf[S], df[S];
     Tile<D>::load(a.q + (int64_t)row * a.ldq + head * D, lane, qf);
     Tile<D>::load(a.dout + (int64_t)row * a.lddo + head * D, lane, df);
@@ -768,8 +814,9 @@ __global__ __launch_bounds__(64 * NW) void attn_bwd_q_kernel(AttnBwd a)
     pin(df);
     const float nl = a.nl[(int64_t)head * a.s.tokens_q + row] * a.c2, nd = a.nd[(int64_t)head * a.s.tokens_q + row];
     const int lim = a.s.causal ? min(k.len - 1, i + shift) : k.len - 1;
-    const int low = a.s.causal ? min(k.len - 1, w0 + shift) : k.len - 1;
-    const int high = a.s.causal ? min(k.len - 1, w0 + 31 + shift) : k.len - 1;
+    // what the wave's first and last rows see
+    const int low = a.s.causal ? min(k.len - 1, uniform(w0 / group) + shift) : k.len - 1;
+    const int high = a.s.causal ? min(k.len - 1, uniform((w0 + 31) / group) + shift) : k.len - 1;
     const int rb = Tile<D>::row_base(lane), cb = Tile<D>::col_base(lane);
 
     v16f dq[B];
@@ -836,7 +883,7 @@ __global__ __launch_bounds__(64 * NW) void attn_bwd_q_kernel(AttnBwd a)
     }
     if (tiles > 0)
         add(kc);
-    if (i < q.len)
+    if (r < rows)
         store_row<D>(a.dq + (int64_t)row * a.lddq + head * D, dq, a.scale, lane);
 }
 
@@ -844,8 +891,11 @@ constexpr int FWD_WAVES = 8, BWD_K_WAVES = 4, BWD_Q_WAVES = 8;
 
 int64_t blocks_of(int64_t n, int64_t per) { return (n + per - 1) / per; }
 
-// Whether a key head's queries of every sequence fit one wave.
-bool few_rows(const AttnShape &s) { return (int64_t)s.max_q * (s.hq / s.hk) <= 32; }
+// Rows of a key head: its queries of every query head.
+int64_t rows_most(const AttnShape &s) { return (int64_t)s.max_q * (s.hq / s.hk); }
+
+// Whether a key head's rows of every sequence fit one wave.
+bool few_rows(const AttnShape &s) { return rows_most(s) <= 32; }
 
 // Shares of the key axis: where workgroups are fewer than two rounds of the 256 CUs, up to one share for each
 // 256 keys.
@@ -854,7 +904,7 @@ int splits_of(const AttnShape &s)
     if (s.seqs == 0 || s.max_q == 0)
         return 1;
     const int64_t units = (int64_t)s.seqs * s.hk;
-    const int64_t groups = few_rows(s) ? units : units * (s.hq / s.hk) * blocks_of(s.max_q, 32 * FWD_WAVES);
+    const int64_t groups = few_rows(s) ? units : units * blocks_of(rows_most(s), 32 * FWD_WAVES);
     int64_t want = groups ? 512 / groups : 1;
     const int64_t most = s.max_k / (few_rows(s) ? 512 : 1024);
     want = want < most ? want : most;
@@ -871,8 +921,8 @@ template <int D> hipError_t fwd(AttnFwd a, hipStream_t st)
     if (few_rows(a.s)) {
         hipLaunchKernelGGL((attn_rows_kernel<D>), dim3((unsigned)(units * a.splits)), dim3(256), 0, st, a);
     } else {
-        a.blocks = (int)blocks_of(a.s.max_q, 32 * FWD_WAVES);
-        hipLaunchKernelGGL((attn_fwd_kernel<D, FWD_WAVES>), dim3((unsigned)(units * (a.s.hq / a.s.hk) * a.splits * a.blocks)),
+        a.blocks = (int)blocks_of(rows_most(a.s), 32 * FWD_WAVES);
+        hipLaunchKernelGGL((attn_fwd_kernel<D, FWD_WAVES>), dim3((unsigned)(units * a.splits * a.blocks)),
                            dim3(64 * FWD_WAVES), 0, st, a);
     }
     hipError_t e = hipGetLastError();
@@ -894,11 +944,11 @@ template <int D> hipError_t bwd(const AttnBwd &b, hipStream_t st)
     }
     if (e == hipSuccess && b.s.max_k > 0 && b.s.tokens_k > 0) {
         hipLaunchKernelGGL((attn_bwd_k_kernel<D, BWD_K_WAVES>),
-                           dim3((unsigned)(units * blocks_of(b.s.max_k, 32 * BWD_K_WAVES))), dim3(64 * BWD_K_WAVES), 0, st, b);
+                           dim3((unsigned)(units * blocks_of(b.s.max_k, 32 * BWD_K_WAVES))), dim3(128 * BWD_K_WAVES), 0, st, b);
         e = hipGetLastError();
     }
     if (e == hipSuccess && b.s.max_q > 0 && b.s.tokens_q > 0) {
-        hipLaunchKernelGGL((attn_bwd_q_kernel<D, BWD_Q_WAVES>), dim3((unsigned)(units * (b.s.hq / b.s.hk) * b.q_blocks)),
+        hipLaunchKernelGGL((attn_bwd_q_kernel<D, BWD_Q_WAVES>), dim3((unsigned)(units * b.q_blocks)),
                            dim3(64 * BWD_Q_WAVES), 0, st, b);
         e = hipGetLastError();
     }
@@ -910,11 +960,13 @@ template <int D> hipError_t bwd(const AttnBwd &b, hipStream_t st)
 bool attn_fits(const AttnShape &s, bool backward)
 {
     const double units = (double)s.seqs * s.hk, heads = (double)s.seqs * s.hq, most = 4294967295.0;
+    if (rows_most(s) > 1 << 30)
+        return false;
     if (backward)
         return (double)s.tokens_q * s.hq * (s.dim / 8) + 256 <= most &&
-               units * (double)blocks_of(s.max_k, 32 * BWD_K_WAVES) * 64 * BWD_K_WAVES <= most &&
-               heads * (double)blocks_of(s.max_q, 32 * BWD_Q_WAVES) * 64 * BWD_Q_WAVES <= most;
-    const double groups = few_rows(s) ? units * 256 : heads * (double)blocks_of(s.max_q, 32 * FWD_WAVES) * 64 * FWD_WAVES;
+               units * (double)blocks_of(s.max_k, 32 * BWD_K_WAVES) * 128 * BWD_K_WAVES <= most &&
+               units * (double)blocks_of(rows_most(s), 32 * BWD_Q_WAVES) * 64 * BWD_Q_WAVES <= most;
+    const double groups = few_rows(s) ? units * 256 : units * (double)blocks_of(rows_most(s), 32 * FWD_WAVES) * 64 * FWD_WAVES;
     return groups * splits_of(s) <= most && heads * s.max_q * (s.dim / 4) + 256 <= most;
 }
 
@@ -938,10 +990,7 @@ size_t attn_bwd_workspace_bytes(const AttnShape &s) { return 2 * pad256((size_t)
 hipError_t launch_attn_bwd(AttnBwd b, void *workspace, hipStream_t st)
 {
     b.c2 = b.scale * kLog2e;
-    b.q_blocks = (int)blocks_of(b.s.max_q, 32 * BWD_Q_WAVES);
-    b.k_blocks = (int)blocks_of(b.s.max_k, 32 * BWD_K_WAVES);
-    const int64_t groups = (int64_t)b.s.seqs * b.s.hk * b.k_blocks;
-    b.fold = b.s.causal && groups > 256 && groups <= 512;
+    b.q_blocks = (int)blocks_of(rows_most(b.s), 32 * BWD_Q_WAVES);
     b.nl = (float *)workspace;
     b.nd = (float *)((char *)workspace + attn_bwd_workspace_bytes(b.s) / 2);
     return b.s.dim == 64 ? bwd<64>(b, st) : bwd<128>(b, st);

@@ -226,8 +226,7 @@ struct AttnBwd {
     uint16_t *dv;
     int64_t lddv;
     float c2;
-    int q_blocks, k_blocks;
-    bool fold;
+    int q_blocks;
     float *nl, *nd;    // [hq][tokens_q]: -lse / scale, -sum of do o
 };
 size_t attn_bwd_workspace_bytes(const AttnShape &s);
