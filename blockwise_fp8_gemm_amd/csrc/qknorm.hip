@@ -14,6 +14,8 @@
 #include "kernels.h"
 #include "tile.h"
 
+#include <type_traits>
+
 namespace puro {
 
 namespace {
@@ -148,97 +150,126 @@ __global__ __launch_bounds__(256) void rope_turn_kernel(RopeShape r, float2 *__r
         turn[n] = rotation(r.pos[n / half], r.freq[n % half], r.mscale);
 }
 
-template <int D, bool FULL, bool TR, bool INTER>
-__device__ __forceinline__ void rope_bwd_tile(const RopeBwd &b, const Place &p, const QuantOut &ro, const QuantOut &to,
+// How a tile's threads hold the pairs.  PAIRS: whole heads rotated in the half layout: a thread has both members of
+// four pairs, in two runs.  INTER: four neighbouring pairs.  APART (part of a head in the half layout, or none of it):
+// eight columns, whose other members it loads beside its own.
+enum { PAIRS, INTER, APART };
+
+template <int D, bool FULL, bool TR, int MODE, class P>
+__device__ __forceinline__ void rope_bwd_tile(const RopeBwd &b, const P &p, const QuantOut &ro, const QuantOut &to,
                                               int pow2, TileShared &sh, float (*red)[128])
 {
     constexpr int L = D / 8;
     const int H = b.r.hq + b.r.hk, R = b.r.rotary;
-    const int64_t c0 = p.c0();
-    const int h = (int)(c0 / D), d0 = (int)(c0 % D);
-    const bool in = FULL || c0 < p.cols, norm = in && h < H && b.r.wq, rot = in && h < H && d0 < R;
-    const uint16_t *dy, *x = nullptr;
-    int64_t lddy, ldx = 0;
-    if (h < b.r.hq) {
-        dy = b.dq + h * D + d0;
-        lddy = b.lddq;
-        x = b.r.q + h * D + d0;
-        ldx = b.r.ldq;
-    } else if (h < H) {
-        dy = b.dk + (h - b.r.hq) * D + d0;
-        lddy = b.lddk;
-        x = b.r.k + (h - b.r.hq) * D + d0;
-        ldx = b.r.ldk;
-    } else {
-        dy = b.dv + (h - H) * D + d0;
-        lddy = b.lddv;
-    }
+    const int64_t c0 = p.col0 + p.col(0);
+    const bool in = FULL || c0 < p.cols;
+    const int h = in ? (int)(c0 / D) : 0, d0 = (int)(c0 % D), up = p.col(4) - p.col(0);   // the second run's distance
+    // whether the tile has query or key heads at all (the same in every lane), and this thread's columns are of one
+    const bool heads = p.col0 < (int64_t)H * D, own = h < H, norm = heads && b.r.wq, rot = own && (MODE == PAIRS || d0 < R);
+    const uint16_t *dy = h < b.r.hq ? b.dq + h * D : own ? b.dk + (h - b.r.hq) * D : b.dv + (h - H) * D;
+    const int64_t lddy = h < b.r.hq ? b.lddq : own ? b.lddk : b.lddv;
+    const uint16_t *x = h < b.r.hq ? b.r.q + h * D : own ? b.r.k + (h - b.r.hq) * D : dy;   // not used for values
+    const int64_t ldx = h < b.r.hq ? b.r.ldq : own ? b.r.ldk : lddy;
     // in the half layout the other member of a pair is R / 2 elements away
     const bool low = d0 < R / 2;
-    const int other = INTER ? 0 : low ? R / 2 : -(R / 2), f0 = INTER ? d0 / 2 : low ? d0 : d0 - R / 2;
-    float w[8], dw[8], v[RT][8];
+    const int other = !rot ? 0 : low ? R / 2 : -(R / 2), f0 = !rot ? 0 : MODE == INTER ? d0 / 2 : low ? d0 : d0 - R / 2;
+    auto load8 = [&](const uint16_t *row) {
+        if constexpr (MODE == PAIRS) {
+            const uint2 a = *reinterpret_cast<const uint2 *>(row + d0), c = *reinterpret_cast<const uint2 *>(row + d0 + D / 2);
+            return make_uint4(a.x, a.y, c.x, c.y);
+        } else {
+            return *reinterpret_cast<const uint4 *>(row + d0);
+        }
+    };
+    // Every load comes before any arithmetic, without a branch that lanes take differently: rows past the last
+    // token and columns past the last head read what is there and are left out below.
+    constexpr int TURNS = MODE == APART ? 4 : 2;
+    uint4 ya[RT], yb[RT], xa[RT];
+    float rs[RT], w[8], dw[8], v[RT][8];
+    float4 turn[RT][TURNS];
+    auto load_turn = [&](int i, int64_t t) {
+#pragma unroll
+        for (int j = 0; j < TURNS; j++)
+            turn[i][j] = *reinterpret_cast<const float4 *>(b.turn + t * (R / 2) + f0 + 2 * j);
+    };
+#pragma unroll
+    for (int i = 0; i < RT; i++) {
+        const int64_t t = FULL ? p.tk(i) : min(p.tk(i), p.tokens - 1);
+        ya[i] = load8(dy + t * lddy);
+        if (heads && R > 0) {
+            if (MODE == APART)
+                yb[i] = load8(dy + t * lddy + other);
+            else
+                load_turn(i, t);   // eight of them apart: there are no registers for all at once
+        }
+        if (norm) {
+            xa[i] = load8(x + t * ldx);
+            rs[i] = b.rstd[t * H + (own ? h : 0)];
+        }
+    }
 #pragma unroll
     for (int j = 0; j < 8; j++)
         dw[j] = w[j] = 0.0f;
-    if (norm)
-        load8_weight(h < b.r.hq ? b.r.wq : b.r.wk, b.r.wbf16, d0, D, w);
+    if (norm) {
+        const void *wp = h < b.r.hq ? b.r.wq : b.r.wk;
+        load4_weight(wp, b.r.wbf16, d0, w);
+        load4_weight(wp, b.r.wbf16, d0 + up, w + 4);
+    }
 #pragma unroll
     for (int i = 0; i < RT; i++) {
-        const int64_t t = p.tk(i);
-#pragma unroll
-        for (int j = 0; j < 8; j++)
-            v[i][j] = 0.0f;
-        if (!in || (!FULL && t >= p.tokens))
-            continue;
+        const bool here = in && (FULL || p.tk(i) < p.tokens);
         float g[8];
-        unpack8(*reinterpret_cast<const uint4 *>(dy + t * lddy), g);
-        if (rot) {
-            const float4 *turn = reinterpret_cast<const float4 *>(b.turn + t * (R / 2) + f0);
-            if (INTER) {
-#pragma unroll
-                for (int j = 0; j < 2; j++) {
-                    const float4 c = turn[j];
-                    const float a0 = g[4 * j], b0 = g[4 * j + 1], a1 = g[4 * j + 2], b1 = g[4 * j + 3];
-                    g[4 * j] = fmaf(a0, c.x, b0 * c.y);
-                    g[4 * j + 1] = fmaf(b0, c.x, -(a0 * c.y));
-                    g[4 * j + 2] = fmaf(a1, c.z, b1 * c.w);
-                    g[4 * j + 3] = fmaf(b1, c.z, -(a1 * c.w));
-                }
-            } else {
-                float o[8];
-                unpack8(*reinterpret_cast<const uint4 *>(dy + t * lddy + other), o);
-#pragma unroll
-                for (int j = 0; j < 4; j++) {
-                    const float4 c = turn[j];
-                    g[2 * j] = fmaf(g[2 * j], c.x, low ? o[2 * j] * c.y : -(o[2 * j] * c.y));
-                    g[2 * j + 1] = fmaf(g[2 * j + 1], c.z, low ? o[2 * j + 1] * c.w : -(o[2 * j + 1] * c.w));
-                }
+        unpack8(ya[i], g);
+        if (heads && R > 0) {
+            float o[8];
+            if (MODE == APART) {
+                unpack8(yb[i], o);
+                load_turn(i, FULL ? p.tk(i) : min(p.tk(i), p.tokens - 1));
+                __builtin_amdgcn_sched_barrier(0);
             }
+#pragma unroll
+            for (int j = 0; j < TURNS; j++)
+#pragma unroll
+                for (int e = 0; e < 2; e++) {   // rotation 2 j + e of the thread's
+                    const float4 c = turn[i][j];
+                    const float cs = rot ? e ? c.z : c.x : 1.0f, sn = rot ? e ? c.w : c.y : 0.0f;
+                    const int n = 2 * j + e;
+                    if constexpr (MODE == APART) {
+                        g[n] = fmaf(g[n], cs, low ? o[n] * sn : -(o[n] * sn));
+                    } else {
+                        const int m0 = MODE == INTER ? 2 * n : n, m1 = MODE == INTER ? 2 * n + 1 : n + 4;
+                        const float u = g[m0], y = g[m1];
+                        g[m0] = fmaf(u, cs, y * sn);
+                        g[m1] = fmaf(y, cs, -(u * sn));
+                    }
+                }
         }
         if (norm) {
-            const float r = b.rstd[t * H + h];
-            float xh[8], s = 0.0f;
-            unpack8(*reinterpret_cast<const uint4 *>(x + t * ldx), xh);
+            const float r = rs[i];
+            float xh[8], n[8], s = 0.0f;
+            unpack8(xa[i], xh);
 #pragma unroll
             for (int j = 0; j < 8; j++) {
                 xh[j] *= r;
-                dw[j] = fmaf(g[j], xh[j], dw[j]);
-                g[j] *= w[j];
-                s = fmaf(g[j], xh[j], s);
+                n[j] = g[j] * w[j];
+                s = fmaf(n[j], xh[j], s);
             }
             s = sum_lanes<L>(s) * (1.0f / D);
 #pragma unroll
-            for (int j = 0; j < 8; j++)
-                g[j] = r * fmaf(-xh[j], s, g[j]);
+            for (int j = 0; j < 8; j++) {
+                dw[j] = own && here ? fmaf(g[j], xh[j], dw[j]) : dw[j];
+                n[j] = r * fmaf(-xh[j], s, n[j]);
+                g[j] = own ? n[j] : g[j];
+            }
         }
 #pragma unroll
         for (int j = 0; j < 8; j++)
-            v[i][j] = g[j];
+            v[i][j] = here ? g[j] : 0.0f;
     }
     pin(v);
     if (b.r.wq) {
         const int t = threadIdx.x, lane = t & 63;
-        *reinterpret_cast<float2 *>(&red[t >> 6][8 * p.cc + first_of(lane)]) =
+        *reinterpret_cast<float2 *>(&red[t >> 6][p.col(first_of(lane))]) =
             cross4(dw, [](float a, float c) { return a + c; });
         __syncthreads();
         if (t < 128 && p.col0 + t < (int64_t)H * D) {
@@ -254,21 +285,22 @@ __device__ __forceinline__ void rope_bwd_tile(const RopeBwd &b, const Place &p, 
     quant_tile<FULL, TR, true>(v, ro, to, p, pow2, sh);
 }
 
-template <int D, bool TR, bool INTER>
+template <int D, bool TR, int MODE>
 __global__ __launch_bounds__(TILE_THREADS) __attribute__((amdgpu_waves_per_eu(4)))
 void rope_bwd_kernel(RopeBwd b, QuantOut ro, QuantOut to, int pow2)
 {
     __shared__ TileShared sh;
     __shared__ float red[TileShared::WAVES][128];
-    const auto p = place(blockIdx.y, blockIdx.x, b.r.tokens, (int64_t)(b.r.hq + 2 * b.r.hk) * D);
+    typedef typename std::conditional<MODE == PAIRS, PairPlace<D>, Place>::type P;
+    const P p = place(blockIdx.y, blockIdx.x, b.r.tokens, (int64_t)(b.r.hq + 2 * b.r.hk) * D);
     if (full_tile(p))
-        rope_bwd_tile<D, true, TR, INTER>(b, p, ro, to, pow2, sh, red);
+        rope_bwd_tile<D, true, TR, MODE>(b, p, ro, to, pow2, sh, red);
     else
-        rope_bwd_tile<D, false, TR, INTER>(b, p, ro, to, pow2, sh, red);
+        rope_bwd_tile<D, false, TR, MODE>(b, p, ro, to, pow2, sh, red);
 }
 
-// dw of 32 elements of the queries' (then the keys') weight: 16 threads each add every 16th of the (token tile,
-// head) shares, and their sums are added in a fixed order.
+// dw of 32 elements of the queries' (then the keys') weight: 16 threads each add some of the (token tile, head)
+// shares, and their sums are added in a fixed order.
 __global__ __launch_bounds__(512) void rope_dw_kernel(RopeBwd b, int ntb)
 {
     __shared__ float red[16][32];
@@ -276,11 +308,16 @@ __global__ __launch_bounds__(512) void rope_dw_kernel(RopeBwd b, int ntb)
     const bool keys = (int)blockIdx.x >= per;
     const int d = ((int)blockIdx.x - (keys ? per : 0)) * 32 + x, heads = keys ? b.r.hk : b.r.hq, H = b.r.hq + b.r.hk;
     const float *part = b.part + (keys ? b.r.hq * D : 0) + d;
+    // as many threads over the heads as fit (a power of two), the others over the tiles
+    int hs = 16;
+    while (hs > heads)
+        hs >>= 1;
     float s = 0.0f;
-    const int64_t n = (int64_t)ntb * heads;
+    for (int h = y & (hs - 1); h < heads; h += hs) {
 #pragma unroll 8
-    for (int64_t i = y; i < n; i += 16)
-        s += part[(i / heads) * ((int64_t)H * D) + (i % heads) * D];
+        for (int tb = y / hs; tb < ntb; tb += 16 / hs)
+            s += part[(int64_t)tb * H * D + h * D];
+    }
     red[y][x] = s;
     for (int m = 8; m > 0; m >>= 1) {
         __syncthreads();
@@ -295,16 +332,21 @@ __global__ __launch_bounds__(512) void rope_dw_kernel(RopeBwd b, int ntb)
 size_t pad256(size_t n) { return (n + 255) / 256 * 256; }
 int64_t turn_count(const RopeShape &r) { return r.tokens * (r.rotary / 2); }
 
-template <int D, bool TR, bool INTER> void bwd_tiles(const RopeBwd &b, const QuantOut &ro, const QuantOut &to, int pow2, hipStream_t st)
+template <int D, bool TR, int MODE> void bwd_tiles(const RopeBwd &b, const QuantOut &ro, const QuantOut &to, int pow2, hipStream_t st)
 {
     const int64_t cols = (int64_t)(b.r.hq + 2 * b.r.hk) * D;
-    hipLaunchKernelGGL((rope_bwd_kernel<D, TR, INTER>), dim3((unsigned)((cols + 127) / 128), (unsigned)((b.r.tokens + 127) / 128)),
+    hipLaunchKernelGGL((rope_bwd_kernel<D, TR, MODE>), dim3((unsigned)((cols + 127) / 128), (unsigned)((b.r.tokens + 127) / 128)),
                        dim3(TILE_THREADS), 0, st, b, ro, to, pow2);
 }
 
 template <int D, bool TR> void bwd_tiles(const RopeBwd &b, const QuantOut &ro, const QuantOut &to, int pow2, hipStream_t st)
 {
-    b.r.interleaved ? bwd_tiles<D, TR, true>(b, ro, to, pow2, st) : bwd_tiles<D, TR, false>(b, ro, to, pow2, st);
+    if (b.r.interleaved)
+        bwd_tiles<D, TR, INTER>(b, ro, to, pow2, st);
+    else if (b.r.rotary == D)
+        bwd_tiles<D, TR, PAIRS>(b, ro, to, pow2, st);
+    else
+        bwd_tiles<D, TR, APART>(b, ro, to, pow2, st);
 }
 
 } // namespace

@@ -248,10 +248,20 @@ __device__ __forceinline__ void pin(float (&v)[RT][8])
 
 // This thread's place in a tile.
 struct Place {
+    static constexpr bool SPLIT = false;
     int64_t tok0, col0, tokens, cols;
     int cc, rq;
+    __device__ __forceinline__ int col(int j) const { return 8 * cc + j; }   // column j of the thread's eight, in the tile
     __device__ __forceinline__ int64_t tk(int i) const { return tok0 + RT * rq + i; }
     __device__ __forceinline__ int64_t c0() const { return col0 + 8 * cc; }
+};
+// The same with a thread's columns in two runs of four, which are the two members of four pairs (j, j + D / 2) of a
+// head of D.
+template <int D> struct PairPlace : Place {
+    static constexpr bool SPLIT = true;
+    __device__ __forceinline__ PairPlace(const Place &p) : Place(p) {}
+    __device__ __forceinline__ int low() const { return D == 128 ? 4 * cc : 64 * (cc >> 3) + 4 * (cc & 7); }
+    __device__ __forceinline__ int col(int j) const { return low() + (j < 4 ? j : D / 2 + j - 4); }
 };
 // Tiles are taken row by row (measured against eight neighbours per XCD, which
 // saves partial sectors of the row scales: 5 to 8% slower).
@@ -286,27 +296,40 @@ template <int I> __device__ __forceinline__ Scale row_scale(const Scale &own)
     return Scale{dpp_f<0x150 + I>(own.s), dpp_f<0x150 + I>(own.r), dpp_f<0x150 + I>(own.rl)};
 }
 
-template <bool SLOW, bool FULL, bool TR, bool ROWS>
+// A thread's eight codes of one token, at `row` (the tensor's).
+template <bool FULL, class P> __device__ __forceinline__ void store_codes(uint8_t *row, const P &p, uint32_t lo, uint32_t hi)
+{
+    if constexpr (P::SPLIT) {   // whole heads lie inside or outside the tensor
+        if (FULL || p.col0 + p.col(0) < p.cols) {
+            __builtin_nontemporal_store(lo, reinterpret_cast<uint32_t *>(row + p.col0 + p.col(0)));
+            __builtin_nontemporal_store(hi, reinterpret_cast<uint32_t *>(row + p.col0 + p.col(4)));
+        }
+    } else if (FULL) {
+        store_nt(row + p.c0(), lo, hi);
+    } else {
+        store8_codes(row, p.c0(), p.cols, lo, hi);
+    }
+}
+
+template <bool SLOW, bool FULL, bool TR, bool ROWS, class P>
 __device__ __forceinline__ void tile_codes(const float (&v)[RT][8], const Scale &own, const QuantOut &ro,
-                                           const QuantOut &to, const Place &p, TileShared &sh)
+                                           const QuantOut &to, const P &p, TileShared &sh)
 {
     if constexpr (ROWS) {
         const Scale sr[RT] = {row_scale<0>(own), row_scale<1>(own), row_scale<2>(own), row_scale<3>(own)};
-        uint8_t *qr = ro.q + p.tk(0) * ro.ldq + (FULL ? p.c0() : 0);
+        uint8_t *qr = ro.q + p.tk(0) * ro.ldq;
 #pragma unroll
         for (int i = 0; i < RT; i++) {
             const uint32_t lo = codes4<SLOW>(v[i][0], v[i][1], v[i][2], v[i][3], sr[i]);
             const uint32_t hi = codes4<SLOW>(v[i][4], v[i][5], v[i][6], v[i][7], sr[i]);
-            if (FULL)
-                store_nt(qr + i * ro.ldq, lo, hi);
-            else if (p.tk(i) < p.tokens)
-                store8_codes(qr + i * ro.ldq, p.c0(), p.cols, lo, hi);
+            if (FULL || p.tk(i) < p.tokens)
+                store_codes<FULL>(qr + i * ro.ldq, p, lo, hi);
         }
     }
     uint32_t word[8];   // RT codes of a column, a byte each
 #pragma unroll
     for (int j = 0; j < 8; j++) {
-        const Scale c{SLOW ? sh.scl[8 * p.cc + j] : 0.0f, sh.rcl[8 * p.cc + j], sh.rll[8 * p.cc + j]};
+        const Scale c{SLOW ? sh.scl[p.col(j)] : 0.0f, sh.rcl[p.col(j)], sh.rll[p.col(j)]};
         word[j] = codes4<SLOW>(v[0][j], v[1][j], v[2][j], v[3][j], c);
         if (SLOW)
             __builtin_amdgcn_sched_barrier(0);   // a column at a time: the wide form's temporaries do not fit several
@@ -321,18 +344,18 @@ __device__ __forceinline__ void tile_codes(const float (&v)[RT][8], const Scale 
             const uint32_t lo = b[0] | (b[1] << 8) | (b[2] << 16) | (b[3] << 24);
             const uint32_t hi = b[4] | (b[5] << 8) | (b[6] << 16) | (b[7] << 24);
             if (p.tk(i) < p.tokens)
-                store8_codes(to.q + p.tk(i) * to.ldq, p.c0(), p.cols, lo, hi);
+                store_codes<false>(to.q + p.tk(i) * to.ldq, p, lo, hi);
         }
         return;
     }
 #pragma unroll
     for (int j = 0; j < 8; j++)
-        *reinterpret_cast<uint32_t *>(&sh.tile[8 * p.cc + j][RT * p.rq]) = word[j];
+        *reinterpret_cast<uint32_t *>(&sh.tile[p.col(j)][RT * p.rq]) = word[j];
 }
 
-template <bool FULL, bool TR, bool ROWS>
+template <bool FULL, bool TR, bool ROWS, class P>
 __device__ __forceinline__ void quant_tile(const float (&v)[RT][8], const QuantOut &ro, const QuantOut &to,
-                                           const Place &p, int pow2, TileShared &sh)
+                                           const P &p, int pow2, TileShared &sh)
 {
     constexpr int WAVES = TileShared::WAVES;
     const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
@@ -342,7 +365,7 @@ __device__ __forceinline__ void quant_tile(const float (&v)[RT][8], const QuantO
 #pragma unroll
     for (int j = 0; j < 8; j++)
         m[j] = absmax3(v[2][j], v[3][j], absmax3(v[0][j], v[1][j], 0.0f));
-    *reinterpret_cast<float2 *>(&sh.red[wave][8 * p.cc + first_of(lane)]) =
+    *reinterpret_cast<float2 *>(&sh.red[wave][p.col(first_of(lane))]) =
         cross4(m, [](float a, float b) { return absmax3(a, b, 0.0f); });
     Scale own{0.0f, 0.0f, 0.0f};
     uint32_t slow = 0;
@@ -419,17 +442,24 @@ __device__ __forceinline__ void load_tile(const uint16_t *x, int64_t ldx, const 
     }
 }
 
-template <bool FULL>
-__device__ __forceinline__ void store_tile(uint16_t *x, int64_t ldx, const Place &p, const float (&v)[RT][8])
+template <bool FULL, class P>
+__device__ __forceinline__ void store_tile(uint16_t *x, int64_t ldx, const P &p, const float (&v)[RT][8])
 {
 #pragma unroll
     for (int i = 0; i < RT; i++) {
         const uint32_t o[4] = {to_bf16x2(v[i][0], v[i][1]), to_bf16x2(v[i][2], v[i][3]), to_bf16x2(v[i][4], v[i][5]),
                                to_bf16x2(v[i][6], v[i][7])};
-        if (FULL)
-            store_nt(x + p.tk(i) * ldx + p.c0(), o[0], o[1], o[2], o[3]);
-        else if (p.tk(i) < p.tokens)
-            store8_bf16(x + p.tk(i) * ldx, p.c0(), p.cols, o);
+        uint16_t *row = x + p.tk(i) * ldx;
+        if constexpr (P::SPLIT) {
+            if (FULL || (p.tk(i) < p.tokens && p.col0 + p.col(0) < p.cols)) {
+                store_nt(row + p.col0 + p.col(0), o[0], o[1]);
+                store_nt(row + p.col0 + p.col(4), o[2], o[3]);
+            }
+        } else if (FULL) {
+            store_nt(row + p.c0(), o[0], o[1], o[2], o[3]);
+        } else if (p.tk(i) < p.tokens) {
+            store8_bf16(row, p.c0(), p.cols, o);
+        }
     }
 }
 
