@@ -459,18 +459,21 @@ __global__ __launch_bounds__(64 * NW) void attn_fwd_kernel(AttnFwd a)
 }
 
 // Few rows (at most 32 of a key head's queries over all its query heads): a wave
-// holds them all and the workgroup's four waves take keys of their own, 32 at a
+// holds them all and the workgroup's two waves take keys of their own, 32 at a
 // time through LDS of their own; their results are added up at the end.
+constexpr int ROW_WAVES = 2;
 template <int D>
-__global__ __launch_bounds__(256) void attn_rows_kernel(AttnFwd a)
+__global__ __launch_bounds__(64 * ROW_WAVES) void attn_rows_kernel(AttnFwd a)
 {
-    constexpr int NW = 4, KW = 32, TILE = Tile<D>::bytes(KW), S = 2, WAVE = S * 2 * TILE;
+    constexpr int NW = ROW_WAVES, KW = 32, TILE = Tile<D>::bytes(KW), S = 2, WAVE = S * 2 * TILE;
     static_assert(WAVE >= 32 * (D + 4) * 4, "a wave's results take its tiles' place");
     __shared__ __attribute__((aligned(16))) uint8_t lds[NW][WAVE];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int units = a.s.seqs * a.s.hk, group = a.s.hq / a.s.hk;
+    // heads change places from sequence to sequence and share to share: with as many as XCDs each would read one
+    // head's 256 bytes of every row
     const int split = uniform((int)blockIdx.x / units), unit = (int)blockIdx.x - split * units;
-    const int seq = uniform(unit / a.s.hk), kh = unit - seq * a.s.hk;
+    const int seq = uniform(unit / a.s.hk), kh = uniform((unit - seq * a.s.hk + seq + split) % a.s.hk);
     const Rows q = uniform(q_rows(a.s, seq)), k = uniform(k_rows(a.s, seq));
     const int cols = q.len * group;
     if (cols == 0)
@@ -481,37 +484,47 @@ __global__ __launch_bounds__(256) void attn_rows_kernel(AttnFwd a)
 
     const uint16_t *kp = a.k + (int64_t)k.start * a.ldk + kh * D, *vp = a.v + (int64_t)k.start * a.ldv + kh * D;
     const typename Tile<D>::template Stage<KW, 1> copy_k(a.ldk, 0, lane), copy_v(a.ldv, 0, lane);
-    auto stage = [&](int t) {
-        uint8_t *dst = lds[wave] + (t & 1) * 2 * TILE;
-        const int last = k.len - 1 - t * KW;
-        copy_k(dst, kp + (int64_t)t * KW * a.ldk, last, 0);
-        copy_v(dst + TILE, vp + (int64_t)t * KW * a.ldv, last, 0);
+    uint8_t *const kt = lds[wave], *const vt = lds[wave] + 2 * TILE;
+    auto stage_k = [&](int t) {
+        if (t < t1)
+            copy_k(kt + (t & 1) * TILE, kp + (int64_t)t * KW * a.ldk, k.len - 1 - t * KW, 0);
     };
-    constexpr int COPIES = 2 * KW / Tile<D>::PIECE;
+    auto stage_v = [&](int t) {
+        if (t < t1)
+            copy_v(vt + (t & 1) * TILE, vp + (int64_t)t * KW * a.ldv, k.len - 1 - t * KW, 0);
+    };
+    stage_k(t0);
+    stage_v(t0);
+    stage_k(t0 + 1);
+    stage_v(t0 + 1);
     const int c = min(lane & 31, cols - 1), i = c / group, head = kh * group + c % group;
     v8bf qf[D / 16];
     Tile<D>::load(a.q + (int64_t)(q.start + i) * a.ldq + head * D, lane, qf);
     const int lim = a.s.causal ? min(k.len - 1, i + shift) : k.len - 1;
     const int low = a.s.causal ? min(k.len - 1, shift) : k.len - 1;
+    pin(qf);
 
+    // A tile's place is filled again as soon as it is read: of a wave's four tiles in LDS three or more are on
+    // their way at any time.  (Two of four: 4.2 TB/s of keys and values.)
+    constexpr int C = KW / Tile<D>::PIECE;   // copies of a tile
     Softmax<D> st;
-    if (t0 < t1)
-        stage(t0);
     for (int t = t0; t < t1; t++) {
-        // the tile after this one, or this one again in its place's other half, so that the count in flight is the same
-        if (t + 1 < t1) {
-            stage(t + 1);
-            wait_copies<COPIES>();
-        } else {
-            wait_copies<0>();
-        }
         v16f s[1];
         v8bf p[2];
-        const uint8_t *tile = lds[wave] + (t & 1) * 2 * TILE;
-        st.template products<1, false, true>(tile, p, tile, qf, s, lane);
-        st.template weigh<1>(s, p, a.c2, t * KW, lim, t * KW + KW - 1 > low, lane);
-        st.template products<1, true, false>(tile + TILE, p, tile, qf, s, lane);
+        const bool more = t + 2 < t1;
+        if (more)
+            wait_copies<3 * C>();
+        else
+            wait_copies<0>();
+        st.template products<1, false, true>(vt, p, kt + (t & 1) * TILE, qf, s, lane);
         __builtin_amdgcn_s_waitcnt(0xc07f);   // lgkmcnt(0): the tile is read before copies go over it
+        stage_k(t + 2);
+        st.template weigh<1>(s, p, a.c2, t * KW, lim, t * KW + KW - 1 > low, lane);
+        if (more)
+            wait_copies<3 * C>();
+        st.template products<1, true, false>(vt + (t & 1) * TILE, p, kt, qf, s, lane);
+        __builtin_amdgcn_s_waitcnt(0xc07f);
+        stage_v(t + 2);
     }
     // the waves' results: [column][D + 4] floats, output then maximum and sum
     constexpr int LD = D + 4;
@@ -526,7 +539,7 @@ __global__ __launch_bounds__(256) void attn_rows_kernel(AttnFwd a)
     if (lane < 32)
         *reinterpret_cast<float2 *>(mine + D) = make_float2(st.m, l);
     __syncthreads();
-    constexpr int RUN = 8, PER = 256 / (D / RUN);   // columns at a time, 8 elements a thread
+    constexpr int RUN = 8, PER = 64 * NW / (D / RUN);   // columns at a time, 8 elements a thread
     for (int cc = threadIdx.x / (D / RUN); cc < cols; cc += PER) {
         const int d = (threadIdx.x % (D / RUN)) * RUN;
         float m = kNoMax, sum = 0.0f, v[RUN];
@@ -897,15 +910,14 @@ int64_t rows_most(const AttnShape &s) { return (int64_t)s.max_q * (s.hq / s.hk);
 // Whether a key head's rows of every sequence fit one wave.
 bool few_rows(const AttnShape &s) { return rows_most(s) <= 32; }
 
-// Shares of the key axis: where workgroups are fewer than two rounds of the 256 CUs, up to one share for each
-// 256 keys.
+// Shares of the key axis, as many as the 256 CUs take at once
 int splits_of(const AttnShape &s)
 {
     if (s.seqs == 0 || s.max_q == 0)
         return 1;
     const int64_t units = (int64_t)s.seqs * s.hk;
     const int64_t groups = few_rows(s) ? units : units * blocks_of(rows_most(s), 32 * FWD_WAVES);
-    int64_t want = groups ? 512 / groups : 1;
+    int64_t want = groups ? (few_rows(s) ? 1024 : 256) / groups : 1;
     const int64_t most = s.max_k / (few_rows(s) ? 512 : 1024);
     want = want < most ? want : most;
     return (int)(want < 1 ? 1 : want > 64 ? 64 : want);
@@ -919,7 +931,7 @@ template <int D> hipError_t fwd(AttnFwd a, hipStream_t st)
 {
     const int64_t units = (int64_t)a.s.seqs * a.s.hk;
     if (few_rows(a.s)) {
-        hipLaunchKernelGGL((attn_rows_kernel<D>), dim3((unsigned)(units * a.splits)), dim3(256), 0, st, a);
+        hipLaunchKernelGGL((attn_rows_kernel<D>), dim3((unsigned)(units * a.splits)), dim3(64 * ROW_WAVES), 0, st, a);
     } else {
         a.blocks = (int)blocks_of(rows_most(a.s), 32 * FWD_WAVES);
         hipLaunchKernelGGL((attn_fwd_kernel<D, FWD_WAVES>), dim3((unsigned)(units * a.splits * a.blocks)),
@@ -966,7 +978,7 @@ bool attn_fits(const AttnShape &s, bool backward)
         return (double)s.tokens_q * s.hq * (s.dim / 8) + 256 <= most &&
                units * (double)blocks_of(s.max_k, 32 * BWD_K_WAVES) * 128 * BWD_K_WAVES <= most &&
                units * (double)blocks_of(rows_most(s), 32 * BWD_Q_WAVES) * 64 * BWD_Q_WAVES <= most;
-    const double groups = few_rows(s) ? units * 256 : units * (double)blocks_of(rows_most(s), 32 * FWD_WAVES) * 64 * FWD_WAVES;
+    const double groups = few_rows(s) ? units * 64 * ROW_WAVES : units * (double)blocks_of(rows_most(s), 32 * FWD_WAVES) * 64 * FWD_WAVES;
     return groups * splits_of(s) <= most && heads * s.max_q * (s.dim / 4) + 256 <= most;
 }
 
