@@ -168,20 +168,32 @@ template <int N, class F> __device__ __forceinline__ void each(F f)
 
 // N products: use(i, load(i)) in order, with the next AHEAD operands' reads from LDS in flight.  The scheduling
 // barriers hold every read at its place: left alone the compiler puts each in front of its product, which then
-// waits for it.
-template <int N, int AHEAD = 6, class L, class U> __device__ __forceinline__ void feed(L load, U use)
+// waits for it.  The first reads may be made earlier, by first().
+template <int N, int AHEAD = 6, class T = v8bf> struct Feed {
+    static constexpr int RING = N < AHEAD ? N : AHEAD;
+    T f[RING];
+
+    template <class L> __device__ __forceinline__ void first(L load)
+    {
+        each<RING>([&](auto I) { f[I] = load(I); });
+    }
+    template <class L, class U> __device__ __forceinline__ void run(L load, U use)
+    {
+        each<N>([&](auto I) {
+            constexpr int i = decltype(I)::value;
+            __builtin_amdgcn_sched_barrier(0);
+            use(I, f[i % RING]);
+            __builtin_amdgcn_sched_barrier(0);
+            if constexpr (i + RING < N)
+                f[i % RING] = load(std::integral_constant<int, i + RING>{});
+        });
+    }
+};
+template <int N, class L, class U> __device__ __forceinline__ void feed(L load, U use)
 {
-    constexpr int RING = N < AHEAD ? N : AHEAD;
-    v8bf f[RING];
-    each<RING>([&](auto I) { f[I] = load(I); });
-    each<N>([&](auto I) {
-        constexpr int i = decltype(I)::value;
-        __builtin_amdgcn_sched_barrier(0);
-        use(I, f[i % RING]);
-        __builtin_amdgcn_sched_barrier(0);
-        if constexpr (i + RING < N)
-            f[i % RING] = load(std::integral_constant<int, i + RING>{});
-    });
+    Feed<N> f;
+    f.first(load);
+    f.run(load, use);
 }
 
 // Holds an operand in registers from here on, its load from memory waited for.
@@ -396,10 +408,14 @@ __global__ __launch_bounds__(64 * NW) void attn_fwd_kernel(AttnFwd a)
         if (t < t1)
             copy_v(lds[1][t & 1], vp + (int64_t)t * KT * a.ldv, k.len - 1 - t * KT, wave);
     };
-    auto turn = [] {
+    // everyone's copies of K tile t and V tile t - 1 have landed and the places of the ones before are free
+    auto turn = [&](int t) {
+        wait_copies<0>();
         __builtin_amdgcn_sched_barrier(0);
         __syncthreads();
         __builtin_amdgcn_sched_barrier(0);
+        stage_k(t + 1);
+        stage_v(t);
     };
     stage_k(t0);
     const int w0 = r0 + 32 * wave, r = w0 + (lane & 31), rc = min(r, rows - 1);
@@ -409,49 +425,31 @@ __global__ __launch_bounds__(64 * NW) void attn_fwd_kernel(AttnFwd a)
     const int lim = a.s.causal ? min(k.len - 1, i + shift) : k.len - 1;
     const int low = a.s.causal ? min(k.len - 1, uniform(w0 / group) + shift) : k.len - 1;   // the wave's first row's
 
-    // The two waves of a SIMD take turns on its matrix cores: one forms the next tile's scores and adds up the
-    // last one's P v while the other takes the exponentials of its own.
+    // Between two barriers a wave has the matrix cores' part of a tile (the last one's P v, the next scores) and
+    // the exponentials of one: the early half of the waves in that order, the late half, which is on the same
+    // SIMDs, the other way round, so that one's products run beside the other's exponentials.
     const bool late = wave >= NW / 2;
     Softmax<D> st;
     constexpr int N = KT / 32;
     v16f s[N];
     v8bf p[2 * N];
     pin(qf);
-    wait_copies<0>();
-    turn();
     if (t0 < t1) {
-        stage_k(t0 + 1);
-        stage_v(t0);
-        if (late)
-            turn();
+        turn(t0);
         st.template products<N, false, true>(lds[1][0], p, lds[0][t0 & 1], qf, s, lane);
-        if (late)
-            wait_copies<0>();
-        turn();
         for (int t = t0; t < t1 - 1; t++) {
-            if (late) {
-                stage_k(t + 2);
-                stage_v(t + 1);
-            }
+            if (late)
+                turn(t + 1);
             st.template weigh<N>(s, p, a.c2, t * KT, lim, t * KT + KT - 1 > low, lane);
             if (!late)
-                wait_copies<0>();
-            turn();
-            if (!late) {
-                stage_k(t + 2);
-                stage_v(t + 1);
-            }
+                turn(t + 1);
             st.template products<N, true, true>(lds[1][t & 1], p, lds[0][(t + 1) & 1], qf, s, lane);
-            if (late)
-                wait_copies<0>();
-            turn();
         }
+        if (late)
+            turn(t1);
         st.template weigh<N>(s, p, a.c2, (t1 - 1) * KT, lim, t1 * KT - 1 > low, lane);
         if (!late)
-            wait_copies<0>();
-        turn();
-        if (!late)
-            turn();   // as many as the others
+            turn(t1);
         st.template products<N, true, false>(lds[1][(t1 - 1) & 1], p, lds[0][0], qf, s, lane);
     }
     if (r < rows)
@@ -651,9 +649,9 @@ __global__ __launch_bounds__(256) void attn_bwd_rows_kernel(AttnBwd a)
 template <int D, int NW>
 __global__ __launch_bounds__(128 * NW) void attn_bwd_k_kernel(AttnBwd a)
 {
-    constexpr int R = 32 * NW, QT = 8192 / D, TILE = Tile<D>::bytes(QT), STAGE = 2 * TILE + 2 * QT * 4, B = D / 32;
+    constexpr int A1 = 4, A2 = 4, R = 32 * NW, QT = 8192 / D, TILE = Tile<D>::bytes(QT), STAGE = 2 * TILE + 2 * QT * 4, B = D / 32;
     static_assert(2 * STAGE >= NW * 16 * B * 256, "one of the sums takes the tiles' place");
-    __shared__ __attribute__((aligned(16))) uint8_t lds[2][STAGE];
+    __shared__ __attribute__((aligned(16))) uint8_t lds[2][STAGE], lds_k[Tile<D>::bytes(R)];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int kw = wave % NW, half = wave / NW;
     const int units = a.s.seqs * a.s.hk, group = a.s.hq / a.s.hk;
@@ -687,10 +685,12 @@ __global__ __launch_bounds__(128 * NW) void attn_bwd_k_kernel(AttnBwd a)
     if (steps > 0)
         stage(0);
     const int w0 = k0 + 32 * kw, j = w0 + (lane & 31), row = k.start + min(j, k.len - 1);
-    v8bf kf[D / 16], vf[D / 16];
-    Tile<D>::load(a.k + (int64_t)row * a.ldk + kh * D, lane, kf);
+    // the values' operand stays in registers; the keys' is read from LDS again, which leaves registers for the reads
+    // ahead
+    const typename Tile<D>::template Stage<R, 2 * NW> copy_k(a.ldk, wave, lane);
+    copy_k(lds_k, a.k + (int64_t)(k.start + k0) * a.ldk + kh * D, k.len - 1 - k0, wave);
+    v8bf vf[D / 16];
     Tile<D>::load(a.v + (int64_t)row * a.ldv + kh * D, lane, vf);
-    pin(kf);
     pin(vf);
     const int from = a.s.causal ? j - shift : 0;              // the lane's first query
     const int wfirst = a.s.causal ? w0 - shift : 0, wlast = a.s.causal ? w0 + 31 - shift : 0;
@@ -700,6 +700,7 @@ __global__ __launch_bounds__(128 * NW) void attn_bwd_k_kernel(AttnBwd a)
 #pragma unroll
     for (int b = 0; b < B; b++)
         dk[b] = dv[b] = splat(0.0f);
+    wait_copies<0>();   // where there are no steps, no copy outlives the workgroup
     int t = t0;
     for (int n = 0; n < steps; n++) {
         wait_copies<0>();
@@ -724,12 +725,36 @@ __global__ __launch_bounds__(128 * NW) void attn_bwd_k_kernel(AttnBwd a)
                 s[4 * g] = x.x; s[4 * g + 1] = x.y; s[4 * g + 2] = x.z; s[4 * g + 3] = x.w;
                 dp[4 * g] = y.x; dp[4 * g + 1] = y.y; dp[4 * g + 2] = y.z; dp[4 * g + 3] = y.w;
             }
-#pragma unroll
-            for (int x = 0; x < D / 16; x++)
-                s = mfma(Tile<D>::rows(qu + rb, 0, x), kf[x], s);
-#pragma unroll
-            for (int x = 0; x < D / 16; x++)
-                dp = mfma(Tile<D>::rows(du + rb, 0, x), vf[x], dp);
+            struct Two {
+                v8bf a, k;
+            };
+            constexpr int S = D / 16;
+            Feed<2 * S, A1, Two> in;
+            auto load_in = [&](auto I) {
+                constexpr int n = decltype(I)::value;
+                Two t;
+                if constexpr (n % 2 == 0) {
+                    t.a = Tile<D>::rows(qu + rb, 0, n / 2);
+                    t.k = Tile<D>::rows(lds_k + kw * Tile<D>::bytes(32) + rb, 0, n / 2);
+                } else {
+                    t.a = t.k = Tile<D>::rows(du + rb, 0, n / 2);
+                }
+                return t;
+            };
+            in.first(load_in);
+            in.run(load_in, [&](auto I, const Two &t) {
+                constexpr int n = decltype(I)::value;
+                if constexpr (n % 2 == 0)
+                    s = mfma(t.a, t.k, s);
+                else
+                    dp = mfma(t.a, vf[n / 2], dp);
+            });
+            Feed<4 * B, A2> out;
+            auto load_out = [&](auto I) {
+                constexpr int n = decltype(I)::value;   // dv and dk in turn, block by block of both runs of 16 queries
+                return Tile<D>::cols((n % 2 == 0 ? du : qu) + cb, 16 * (n / (2 * B)), n / 2 % B);
+            };
+            out.first(load_out);
             if (i1 < wlast || i1 + 32 > q.len) {
 #pragma unroll
                 for (int e = 0; e < 16; e++) {
@@ -737,20 +762,24 @@ __global__ __launch_bounds__(128 * NW) void attn_bwd_k_kernel(AttnBwd a)
                     s[e] = i < from || i >= q.len ? -INFINITY : s[e];
                 }
             }
-#pragma unroll
-            for (int e = 0; e < 16; e++) {
-                s[e] = __builtin_amdgcn_exp2f(s[e] * a.c2);
-                dp[e] *= s[e];
-            }
+            v8bf p[2], ds[2];
 #pragma unroll
             for (int x = 0; x < 2; x++) {
-                const v8bf p = operand(s, x), ds = operand(dp, x);
 #pragma unroll
-                for (int b = 0; b < B; b++) {
-                    dv[b] = mfma(Tile<D>::cols(du + cb, 16 * x, b), p, dv[b]);
-                    dk[b] = mfma(Tile<D>::cols(qu + cb, 16 * x, b), ds, dk[b]);
+                for (int e = 8 * x; e < 8 * x + 8; e++) {
+                    s[e] = __builtin_amdgcn_exp2f(s[e] * a.c2);
+                    dp[e] *= s[e];
                 }
+                p[x] = operand(s, x);
+                ds[x] = operand(dp, x);
             }
+            out.run(load_out, [&](auto I, const v8bf &x) {
+                constexpr int n = decltype(I)::value, b = n / 2 % B, h = n / (2 * B);
+                if constexpr (n % 2 == 0)
+                    dv[b] = mfma(x, p[h], dv[b]);
+                else
+                    dk[b] = mfma(x, ds[h], dk[b]);
+            });
         }
     }
     // the odd runs' dk go to the even ones' waves, and the even runs' dv to the odd ones'
