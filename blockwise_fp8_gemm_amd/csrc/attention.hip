@@ -642,18 +642,17 @@ __global__ __launch_bounds__(256) void attn_bwd_rows_kernel(AttnBwd a)
     }
 }
 
-// Keys' and values' gradients: NW waves of 32 keys, twice; 64 queries (128 of narrow heads) of one head at a time
-// through LDS.  The
-// two waves of the same keys lie on one SIMD and take the even and the odd runs of 32 queries; their sums meet
-// at the end.
-template <int D, int NW>
-__global__ __launch_bounds__(128 * NW) void attn_bwd_k_kernel(AttnBwd a)
+// Keys' and values' gradients: NW waves of 32 keys, HV times.  QT queries of one head at a time go through LDS; the
+// HV waves of the same keys take every HV-th run of 32 of them, and their sums meet at the end.  Four waves of keys,
+// twice, read a tile least often; where that makes too few workgroups for the 256 CUs it is two waves, four times.
+template <int D, int NW, int HV>
+__global__ __launch_bounds__(64 * NW * HV) void attn_bwd_k_kernel(AttnBwd a)
 {
-    constexpr int A1 = 4, A2 = 4, R = 32 * NW, QT = 8192 / D, TILE = Tile<D>::bytes(QT), STAGE = 2 * TILE + 2 * QT * 4, B = D / 32;
-    static_assert(2 * STAGE >= NW * 16 * B * 256, "one of the sums takes the tiles' place");
+    constexpr int A1 = 4, A2 = 4, R = 32 * NW, QT = HV == 4 ? 128 : 8192 / D, TILE = Tile<D>::bytes(QT), STAGE = 2 * TILE + 2 * QT * 4, B = D / 32;
+    static_assert(2 * STAGE >= HV / 2 * NW * 16 * B * 256, "half of one of the sums takes the tiles' place");
     __shared__ __attribute__((aligned(16))) uint8_t lds[2][STAGE], lds_k[Tile<D>::bytes(R)];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int kw = wave % NW, half = wave / NW;
+    const int kw = wave % NW, part = wave / NW;
     const int units = a.s.seqs * a.s.hk, group = a.s.hq / a.s.hk;
     const int block = uniform((int)blockIdx.x / units), unit = (int)blockIdx.x - block * units;   // earlier keys, seen by more, first
     const int seq = uniform(unit / a.s.hk), kh = unit - seq * a.s.hk;
@@ -664,7 +663,7 @@ __global__ __launch_bounds__(128 * NW) void attn_bwd_k_kernel(AttnBwd a)
     const int shift = k.len - q.len, tiles = (q.len + QT - 1) / QT;
     const int t0 = a.s.causal ? min(tiles, max(0, k0 - shift) / QT) : 0, steps = (tiles - t0) * group;
 
-    const typename Tile<D>::template Stage<QT, 2 * NW> copy_q(a.ldq, wave, lane), copy_d(a.lddo, wave, lane);
+    const typename Tile<D>::template Stage<QT, HV * NW> copy_q(a.ldq, wave, lane), copy_d(a.lddo, wave, lane);
     int sh = kh * group, st = t0;   // the next tile to be copied: its head and its place
     auto stage = [&](int n) {
         const int last = q.len - 1 - st * QT;
@@ -687,7 +686,7 @@ __global__ __launch_bounds__(128 * NW) void attn_bwd_k_kernel(AttnBwd a)
     const int w0 = k0 + 32 * kw, j = w0 + (lane & 31), row = k.start + min(j, k.len - 1);
     // the values' operand stays in registers; the keys' is read from LDS again, which leaves registers for the reads
     // ahead
-    const typename Tile<D>::template Stage<R, 2 * NW> copy_k(a.ldk, wave, lane);
+    const typename Tile<D>::template Stage<R, HV * NW> copy_k(a.ldk, wave, lane);
     copy_k(lds_k, a.k + (int64_t)(k.start + k0) * a.ldk + kh * D, k.len - 1 - k0, wave);
     v8bf vf[D / 16];
     Tile<D>::load(a.v + (int64_t)row * a.ldv + kh * D, lane, vf);
@@ -712,7 +711,7 @@ __global__ __launch_bounds__(128 * NW) void attn_bwd_k_kernel(AttnBwd a)
         const int i0 = t * QT;
         t = t + 1 == tiles ? t0 : t + 1;
 #pragma unroll 1
-        for (int u = half; u < QT / 32; u += 2) {
+        for (int u = part; u < QT / 32; u += HV) {
             const int i1 = i0 + 32 * u;
             if (i1 + 31 < wfirst || i1 >= q.len)
                 continue;
@@ -782,38 +781,36 @@ __global__ __launch_bounds__(128 * NW) void attn_bwd_k_kernel(AttnBwd a)
             });
         }
     }
-    // the odd runs' dk go to the even ones' waves, and the even runs' dv to the odd ones'
-    float *x = reinterpret_cast<float *>(lds[0]) + kw * 16 * B * 64 + lane;
-    auto put = [&](const v16f (&v)[B]) {
+    // dk is added up towards the first part, dv towards the last one
+    float *const sums = reinterpret_cast<float *>(lds[0]) + lane;
+    auto meet = [&](v16f (&v)[B], int place, int h) {
+        float *x = sums + ((place < h ? place : place - h) * NW + kw) * 16 * B * 64;
+        __syncthreads();
+        if (place >= h && place < 2 * h) {
 #pragma unroll
-        for (int b = 0; b < B; b++)
+            for (int b = 0; b < B; b++)
 #pragma unroll
-            for (int e = 0; e < 16; e++)
-                x[(16 * b + e) * 64] = v[b][e];
+                for (int e = 0; e < 16; e++)
+                    x[(16 * b + e) * 64] = v[b][e];
+        }
+        __syncthreads();
+        if (place < h) {
+#pragma unroll
+            for (int b = 0; b < B; b++)
+#pragma unroll
+                for (int e = 0; e < 16; e++)
+                    v[b][e] += x[(16 * b + e) * 64];
+        }
     };
-    auto take = [&](v16f (&v)[B]) {
 #pragma unroll
-        for (int b = 0; b < B; b++)
-#pragma unroll
-            for (int e = 0; e < 16; e++)
-                v[b][e] += x[(16 * b + e) * 64];
-    };
-    __syncthreads();
-    if (half == 1)
-        put(dk);
-    __syncthreads();
-    if (half == 0)
-        take(dk);
-    __syncthreads();
-    if (half == 0)
-        put(dv);
-    __syncthreads();
-    if (half == 1)
-        take(dv);
+    for (int h = HV / 2; h > 0; h /= 2) {
+        meet(dk, part, h);
+        meet(dv, HV - 1 - part, h);
+    }
     if (j < k.len) {
-        if (half == 0)
+        if (part == 0)
             store_row<D>(a.dk + (int64_t)row * a.lddk + kh * D, dk, a.scale, lane);
-        else
+        if (part == HV - 1)
             store_row<D>(a.dv + (int64_t)row * a.lddv + kh * D, dv, 1.0f, lane);
     }
 }
@@ -929,7 +926,7 @@ __global__ __launch_bounds__(64 * NW) void attn_bwd_q_kernel(AttnBwd a)
         store_row<D>(a.dq + (int64_t)row * a.lddq + head * D, dq, a.scale, lane);
 }
 
-constexpr int FWD_WAVES = 8, BWD_K_WAVES = 4, BWD_Q_WAVES = 8;
+constexpr int FWD_WAVES = 8, BWD_Q_WAVES = 8;
 
 int64_t blocks_of(int64_t n, int64_t per) { return (n + per - 1) / per; }
 
@@ -950,6 +947,14 @@ int splits_of(const AttnShape &s)
     const int64_t most = s.max_k / (few_rows(s) ? 512 : 1024);
     want = want < most ? want : most;
     return (int)(want < 1 ? 1 : want > 64 ? 64 : want);
+}
+
+// Waves of 32 keys of the keys' gradients: four, or two where four would make fewer workgroups than there are CUs
+// (by the longest sequence, or by the rows there are).
+int bwd_k_waves(const AttnShape &s)
+{
+    const int64_t longest = (int64_t)s.seqs * s.hk * blocks_of(s.max_k, 128), rows = s.hk * (s.tokens_k / 128 + s.seqs);
+    return (longest < rows ? longest : rows) < 256 ? 2 : 4;
 }
 
 size_t pad256(size_t n) { return (n + 255) / 256 * 256; }
@@ -984,8 +989,9 @@ template <int D> hipError_t bwd(const AttnBwd &b, hipStream_t st)
         e = hipGetLastError();
     }
     if (e == hipSuccess && b.s.max_k > 0 && b.s.tokens_k > 0) {
-        hipLaunchKernelGGL((attn_bwd_k_kernel<D, BWD_K_WAVES>),
-                           dim3((unsigned)(units * blocks_of(b.s.max_k, 32 * BWD_K_WAVES))), dim3(128 * BWD_K_WAVES), 0, st, b);
+        const int waves = bwd_k_waves(b.s);
+        hipLaunchKernelGGL((waves == 4 ? attn_bwd_k_kernel<D, 4, 2> : attn_bwd_k_kernel<D, 2, 4>),
+                           dim3((unsigned)(units * blocks_of(b.s.max_k, 32 * waves))), dim3(512), 0, st, b);
         e = hipGetLastError();
     }
     if (e == hipSuccess && b.s.max_q > 0 && b.s.tokens_q > 0) {
@@ -1005,7 +1011,7 @@ bool attn_fits(const AttnShape &s, bool backward)
         return false;
     if (backward)
         return (double)s.tokens_q * s.hq * (s.dim / 8) + 256 <= most &&
-               units * (double)blocks_of(s.max_k, 32 * BWD_K_WAVES) * 128 * BWD_K_WAVES <= most &&
+               units * (double)blocks_of(s.max_k, 64) * 512 <= most &&
                units * (double)blocks_of(rows_most(s), 32 * BWD_Q_WAVES) * 64 * BWD_Q_WAVES <= most;
     const double groups = few_rows(s) ? units * 64 * ROW_WAVES : units * (double)blocks_of(rows_most(s), 32 * FWD_WAVES) * 64 * FWD_WAVES;
     return groups * splits_of(s) <= most && heads * s.max_q * (s.dim / 4) + 256 <= most;
