@@ -302,18 +302,29 @@ template <int D> struct Softmax {
             });
     }
 
-    // Their exponentials as the next product's operand.  first: the blocks' first key; lim: the lane's last
-    // visible key; masked: whether some key of the blocks may be hidden.
-    template <int N>
-    __device__ __forceinline__ void weigh(v16f (&s)[N], v8bf (&p)[2 * N], float c2, int first, int lim, bool masked, int lane)
+    // 2^(c2 s - m) as the next product's operand, and their sum over the lane.
+    template <int N> __device__ __forceinline__ float exponentials(const v16f (&s)[N], v8bf (&p)[2 * N], float c2) const
     {
-        if (masked) {
+        float sum = 0.0f;
 #pragma unroll
-            for (int n = 0; n < N; n++)
+        for (int n = 0; n < N; n++)
 #pragma unroll
-                for (int i = 0; i < 16; i++)
-                    s[n][i] = first + 32 * n + acc_row(i, lane) > lim ? -INFINITY : s[n][i];
-        }
+            for (int k = 0; k < 2; k++) {
+                float e[8];
+#pragma unroll
+                for (int i = 0; i < 8; i++) {
+                    e[i] = __builtin_amdgcn_exp2f(fmaf(s[n][8 * k + i], c2, -m));
+                    sum += e[i];
+                }
+                const v4u w = {to_bf16x2(e[0], e[1]), to_bf16x2(e[2], e[3]), to_bf16x2(e[4], e[5]), to_bf16x2(e[6], e[7])};
+                p[2 * n + k] = __builtin_bit_cast(v8bf, w);
+            }
+        return sum;
+    }
+
+    // The running maximum up to the scores, where one lies more than 2^8 above it.
+    template <int N> __device__ __forceinline__ void raise(const v16f (&s)[N], float c2)
+    {
         float top = s[0][0];
 #pragma unroll
         for (int n = 0; n < N; n++)
@@ -329,18 +340,31 @@ template <int D> struct Softmax {
             for (int b = 0; b < D / 32; b++)
                 o[b] *= f;
         }
+    }
+
+    // P of the blocks, and their share of the sum.  first: the blocks' first key; start: that of all of them; lim: the
+    // lane's last visible key; masked: whether some key of the blocks may be hidden.  With heads of 128 the maximum is
+    // looked for only among the first keys and where P's sum shows that a score has left it behind (2 x 4096 causal
+    // 125 us, and 127.5 with a search in every tile; heads of 64: 82 and 80.5).
+    template <int N>
+    __device__ __forceinline__ void weigh(v16f (&s)[N], v8bf (&p)[2 * N], float c2, int first, int start, int lim, bool masked,
+                                          int lane)
+    {
+        if (masked) {
 #pragma unroll
-        for (int n = 0; n < N; n++)
+            for (int n = 0; n < N; n++)
 #pragma unroll
-            for (int i = 0; i < 16; i++) {
-                s[n][i] = __builtin_amdgcn_exp2f(fmaf(s[n][i], c2, -m));
-                l += s[n][i];
-            }
-#pragma unroll
-        for (int n = 0; n < N; n++) {
-            p[2 * n] = operand(s[n], 0);
-            p[2 * n + 1] = operand(s[n], 1);
+                for (int i = 0; i < 16; i++)
+                    s[n][i] = first + 32 * n + acc_row(i, lane) > lim ? -INFINITY : s[n][i];
         }
+        float sum = INFINITY;
+        if (D == 128 && first != start)
+            sum = exponentials<N>(s, p, c2);
+        if (D != 128 || __any(!(sum <= 1024.0f))) {
+            raise<N>(s, c2);
+            sum = exponentials<N>(s, p, c2);
+        }
+        l += sum;
         pin(p);   // formed here, not where the products want them
     }
 };
@@ -440,14 +464,14 @@ __global__ __launch_bounds__(64 * NW) void attn_fwd_kernel(AttnFwd a)
         for (int t = t0; t < t1 - 1; t++) {
             if (late)
                 turn(t + 1);
-            st.template weigh<N>(s, p, a.c2, t * KT, lim, t * KT + KT - 1 > low, lane);
+            st.template weigh<N>(s, p, a.c2, t * KT, t0 * KT, lim, t * KT + KT - 1 > low, lane);
             if (!late)
                 turn(t + 1);
             st.template products<N, true, true>(lds[1][t & 1], p, lds[0][(t + 1) & 1], qf, s, lane);
         }
         if (late)
             turn(t1);
-        st.template weigh<N>(s, p, a.c2, (t1 - 1) * KT, lim, t1 * KT - 1 > low, lane);
+        st.template weigh<N>(s, p, a.c2, (t1 - 1) * KT, t0 * KT, lim, t1 * KT - 1 > low, lane);
         if (!late)
             turn(t1);
         st.template products<N, true, false>(lds[1][(t1 - 1) & 1], p, lds[0][0], qf, s, lane);
@@ -517,7 +541,7 @@ __global__ __launch_bounds__(64 * ROW_WAVES) void attn_rows_kernel(AttnFwd a)
         st.template products<1, false, true>(vt, p, kt + (t & 1) * TILE, qf, s, lane);
         __builtin_amdgcn_s_waitcnt(0xc07f);   // lgkmcnt(0): the tile is read before copies go over it
         stage_k(t + 2);
-        st.template weigh<1>(s, p, a.c2, t * KW, lim, t * KW + KW - 1 > low, lane);
+        st.template weigh<1>(s, p, a.c2, t * KW, t0 * KW, lim, t * KW + KW - 1 > low, lane);
         if (more)
             wait_copies<3 * C>();
         st.template products<1, true, false>(vt + (t & 1) * TILE, p, kt, qf, s, lane);
