@@ -509,7 +509,7 @@ def _refuse(t, shape, dtypes, name, device):
 
 def _mat(t, shape, dtype, name, device):
     """(address, row stride) of a checked 2-D tensor; the address of an empty one is 0."""
-    if t.shape != shape or t.dtype is not dtype or not t.is_cuda or t.device != device:
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != device.index:   # -1 and None on the host
         _refuse(t, shape, (dtype,), name, device)
     rows, cols = shape
     if not rows or not cols:
@@ -526,7 +526,7 @@ def _opt_mat(t, shape, dtype, name, device):
 
 def _dense(t, shape, dtypes, name, device):
     """Address of a checked dense tensor (0 for an empty one)."""
-    if t.shape != shape or t.dtype not in dtypes or not t.is_cuda or t.device != device:
+    if t.shape != shape or t.dtype not in dtypes or t.get_device() != device.index:
         _refuse(t, shape, dtypes, name, device)
     if not t.is_contiguous():
         raise ValueError("%s must be dense (contiguous)" % name)
@@ -735,33 +735,44 @@ def puro_fp8_swiglu_bwd_quant_dual(dh, gate, up, transpose_out=True, joined=Fals
     return res
 
 
-def _rope(q, k, head_dim, positions, inv_freq, q_weight, k_weight, eps, rope_scale, interleaved):
-    """Checked QkNormRope for query heads q and key heads k (shapes and devices of tensors), with its device."""
-    dev = q.device
-    for t, name in ((q, "q"), (k, "k")):
-        if len(t.shape) != 2:
-            raise ValueError("%s: expected a 2-D tensor, got shape %s" % (name, tuple(t.shape)))
-    if head_dim not in (64, 128):
+def _heads(t, head_dim, name):
+    """Heads of a [tokens][heads * head_dim] tensor's columns."""
+    if t.dim() != 2:
+        raise ValueError("%s: expected a 2-D tensor, got shape %s" % (name, tuple(t.shape)))
+    if head_dim != 128 and head_dim != 64:
         raise ValueError("head_dim is 64 or 128, got %r" % (head_dim,))
-    tokens, rotary = q.shape[0], 0 if inv_freq is None else 2 * inv_freq.numel()
-    for t, name in ((q, "q"), (k, "k")):
-        if t.shape[1] % head_dim or not t.shape[1]:
-            raise ValueError("%s: %d columns are no whole heads of %d" % (name, t.shape[1], head_dim))
-    pos = freq = wqp = wkp = 0
+    heads, rest = divmod(t.shape[1], head_dim)
+    if rest or not heads:
+        raise ValueError("%s: %d columns are no whole heads of %d" % (name, t.shape[1], head_dim))
+    return heads
+
+
+_I32S, _F32S, _WEIGHTS = (torch.int32,), (_F32,), (_F32, _BF16)
+
+
+def _rope(q, k, head_dim, positions, inv_freq, q_weight, k_weight, eps, rope_scale, interleaved):
+    """Checked QkNormRope for query heads q and key heads k (shapes of tensors that are checked elsewhere)."""
+    dev, heads_q, heads_kv, tokens = q.device, _heads(q, head_dim, "q"), _heads(k, head_dim, "k"), q.shape[0]
+    rotary = pos = freq = wqp = wkp = 0
     wdt = PURO_F32
-    if rotary:
-        if positions is None:
+    if inv_freq is not None:
+        half = inv_freq.numel()
+        if half and positions is None:
             raise ValueError("positions are needed with inv_freq")
-        pos = _dense(positions, (tokens,), (torch.int32,), "positions", dev)
-        freq = _dense(inv_freq, (rotary // 2,), (_F32,), "inv_freq", dev)
-    if (q_weight is None) != (k_weight is None):
-        raise ValueError("q_weight and k_weight: both or neither")
+        if half:
+            rotary = 2 * half
+            pos = _dense(positions, (tokens,), _I32S, "positions", dev)
+            freq = _dense(inv_freq, (half,), _F32S, "inv_freq", dev)
     if q_weight is not None:
-        wqp = _dense(q_weight, (head_dim,), (_F32, _BF16), "q_weight", dev)
+        if k_weight is None:
+            raise ValueError("q_weight and k_weight: both or neither")
+        wqp = _dense(q_weight, (head_dim,), _WEIGHTS, "q_weight", dev)
         wkp = _dense(k_weight, (head_dim,), (q_weight.dtype,), "k_weight", dev)
         wdt = PURO_BF16 if q_weight.dtype is _BF16 else PURO_F32
-    return QkNormRope(q.shape[1] // head_dim, k.shape[1] // head_dim, head_dim, rotary, 1 if interleaved else 0,
-                      tokens, pos, freq, rope_scale, wqp, wkp, wdt, eps)
+    elif k_weight is not None:
+        raise ValueError("q_weight and k_weight: both or neither")
+    return QkNormRope(heads_q, heads_kv, head_dim, rotary, 1 if interleaved else 0, tokens, pos, freq, rope_scale, wqp, wkp,
+                      wdt, eps)
 
 
 @_on_device
@@ -775,26 +786,29 @@ def puro_fp8_qk_norm_rope(q, k, head_dim, positions=None, inv_freq=None, q_weigh
     be q and k themselves.  Returns (q_out, k_out, rstd [tokens][heads_q + heads_kv]; None without weights or
     store_rstd)."""
     r, dev = _rope(q, k, head_dim, positions, inv_freq, q_weight, k_weight, eps, rope_scale, interleaved), q.device
-    shapes = (r.tokens, q.shape[1]), (r.tokens, k.shape[1])
-    ins = (*_mat(q, shapes[0], _BF16, "q", dev), *_mat(k, shapes[1], _BF16, "k", dev))
-    outs, args = [], []
-    for t, shape, name in ((q_out, shapes[0], "q_out"), (k_out, shapes[1], "k_out")):
-        if t is None:
-            t, p, ld = _new(*shape, _BF16, dev)
-        else:
-            p, ld = _mat(t, shape, _BF16, name, dev)
-        outs.append(t)
-        args += [p, ld]
-    rp, heads = 0, (r.tokens, r.heads_q + r.heads_kv)
+    tokens = r.tokens
+    sq, sk = (tokens, q.shape[1]), (tokens, k.shape[1])
+    qp, ldq = _mat(q, sq, _BF16, "q", dev)
+    kp, ldk = _mat(k, sk, _BF16, "k", dev)
+    if q_out is None:
+        q_out, qop, ldqo = _new(*sq, _BF16, dev)
+    else:
+        qop, ldqo = _mat(q_out, sq, _BF16, "q_out", dev)
+    if k_out is None:
+        k_out, kop, ldko = _new(*sk, _BF16, dev)
+    else:
+        kop, ldko = _mat(k_out, sk, _BF16, "k_out", dev)
+    rp = 0
     if q_weight is None or not (store_rstd or rstd is not None):
         rstd = None
     elif rstd is None:
-        rstd = torch.empty(heads, dtype=_F32, device=dev)
+        rstd = torch.empty((tokens, r.heads_q + r.heads_kv), dtype=_F32, device=dev)
         rp = rstd.data_ptr()
     else:
-        rp = _dense(rstd, heads, (_F32,), "rstd", dev)
-    _check(lib().puro_fp8_qk_norm_rope(r, *ins, *args, rp, _raw_stream(stream, dev)), "puro_fp8_qk_norm_rope")
-    return outs[0], outs[1], rstd
+        rp = _dense(rstd, (tokens, r.heads_q + r.heads_kv), _F32S, "rstd", dev)
+    _check(lib().puro_fp8_qk_norm_rope(r, qp, ldq, kp, ldk, qop, ldqo, kop, ldko, rp, _raw_stream(stream, dev)),
+           "puro_fp8_qk_norm_rope")
+    return q_out, k_out, rstd
 
 
 @_on_device
@@ -843,33 +857,28 @@ def puro_fp8_qk_norm_rope_bwd_quant_dual(dq, dk, dv, q, k, head_dim, positions=N
 
 def _sequences(off, lengths, name, dev):
     """(addresses of a checked offset and length array, the number of sequences)."""
-    if off.dim() != 1 or off.numel() < 1:
+    n = off.numel()
+    if off.dim() != 1 or n < 1:
         raise ValueError("%s_offsets: expected one int32 per sequence and one more, got shape %s" % (name, tuple(off.shape)))
-    p = _dense(off, off.shape, (torch.int32,), name + "_offsets", dev)
+    p = _dense(off, (n,), _I32S, name + "_offsets", dev)
     if lengths is None:
-        return p, 0, off.numel() - 1
-    n = lengths.numel()
-    if off.numel() not in (n, n + 1):
-        raise ValueError("%s_offsets: %d entries for %d lengths" % (name, off.numel(), n))
-    return p, _dense(lengths, (n,), (torch.int32,), name + "_lengths", dev), n
+        return p, 0, n - 1
+    m = lengths.numel()
+    if n != m and n != m + 1:
+        raise ValueError("%s_offsets: %d entries for %d lengths" % (name, n, m))
+    return p, _dense(lengths, (m,), _I32S, name + "_lengths", dev), m
 
 
 def _attention(q, k, v, head_dim, q_offsets, k_offsets, max_q, max_k, q_lengths, k_lengths, causal, scale):
     """Checked Attention and the addresses and strides of q, k and v."""
-    dev = q.device
-    for t, name in ((q, "q"), (k, "k")):
-        if len(t.shape) != 2:
-            raise ValueError("%s: expected a 2-D tensor, got shape %s" % (name, tuple(t.shape)))
-        if head_dim not in (64, 128) or t.shape[1] % head_dim or not t.shape[1]:
-            raise ValueError("%s: %d columns are no whole heads of %r (64 or 128)" % (name, t.shape[1], head_dim))
-    ins = (*_mat(q, q.shape, _BF16, "q", dev), *_mat(k, k.shape, _BF16, "k", dev), *_mat(v, k.shape, _BF16, "v", dev))
+    dev, heads_q, heads_kv, sq, sk = q.device, _heads(q, head_dim, "q"), _heads(k, head_dim, "k"), q.shape, k.shape
+    ins = (*_mat(q, sq, _BF16, "q", dev), *_mat(k, sk, _BF16, "k", dev), *_mat(v, sk, _BF16, "v", dev))
     qo, ql, n = _sequences(q_offsets, q_lengths, "q", dev)
     ko, kl, m = _sequences(k_offsets, k_lengths, "k", dev)
     if n != m:
         raise ValueError("%d sequences of queries and %d of keys" % (n, m))
-    a = Attention(q.shape[1] // head_dim, k.shape[1] // head_dim, head_dim, n, 1 if causal else 0, q.shape[0],
-                  k.shape[0], max_q, max_k, qo, ql, ko, kl, head_dim ** -0.5 if scale is None else scale)
-    return a, ins
+    return Attention(heads_q, heads_kv, head_dim, n, 1 if causal else 0, sq[0], sk[0], max_q, max_k, qo, ql, ko, kl,
+                     head_dim ** -0.5 if scale is None else scale), ins
 
 
 @_on_device

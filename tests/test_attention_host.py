@@ -163,7 +163,7 @@ def test_binding_refusals():
             call()
     with pytest.raises(ValueError, match="whole heads"):
         pf.puro_fp8_attention(bf(4, 100), bf(4, 64), bf(4, 64), 64, off, off, 4, 4)
-    with pytest.raises(ValueError, match="head"):
+    with pytest.raises(ValueError, match="head_dim"):
         pf.puro_fp8_attention(bf(4, 96), bf(4, 96), bf(4, 96), 96, off, off, 4, 4)
     with pytest.raises(ValueError, match="2-D"):
         pf.puro_fp8_attention(torch.zeros((4,), dtype=torch.bfloat16), bf(4, 64), bf(4, 64), 64, off, off, 4, 4)
