@@ -33,13 +33,19 @@ template <int N> __device__ __forceinline__ float sum_lanes(float v)
 
 // (cos, sin) of position * frequency, times m.  The frequency in turns and the
 // product are off by 2^-53 of themselves each: for |position * frequency| < 2^31,
-// below 2^-20 radians, and for less than 2^20, below 2^-31.
+// below 2^-20 radians, and for less than 2^20, below 2^-31.  What is left of whole
+// turns and quarters, at most an eighth either way, becomes an FP32 number (2^-25
+// radians off at most), whose cosine and sine change places and signs by the quarter.
 __device__ __forceinline__ float2 rotation(int32_t position, float frequency, float m)
 {
-    const double turns = (double)position * ((double)frequency * 0.15915494309189533577);
+    double turns = (double)position * ((double)frequency * 0.15915494309189533577);
+    turns -= rint(turns);
+    const double quarters = rint(4.0 * turns);
     float s, c;
-    sincospif(2.0f * (float)(turns - rint(turns)), &s, &c);
-    return make_float2(c * m, s * m);
+    sincospif(2.0f * (float)(turns - 0.25 * quarters), &s, &c);
+    const int n = (int)quarters;
+    const float x = n & 1 ? s : c, y = n & 1 ? c : s;
+    return make_float2((n + 1) & 2 ? -(x * m) : x * m, n & 2 ? -(y * m) : y * m);
 }
 
 __device__ __forceinline__ void unpack4(const uint2 &a, float v[4])
