@@ -15,7 +15,7 @@
 // the order of a product's contraction is free, so that the transposing reads
 // take their rows in the accumulator's order instead of moving P between lanes.
 //
-// P and dS enter their products as BF16 numbers (each rounded once, 2^-9 of
+// P and dS enter their products as BF16 numbers (each rounded once, 2^-8 of
 // itself; the results are BF16 too, and the roundings of a row's many terms
 // average out); scores, statistics and every sum are FP32.
 #include "common.h"
@@ -631,7 +631,7 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnFwd a)
 }
 
 // ---------------------------------------------------------------------------
-// Gradient.  A first pass forms -L / c and -D of every row and head, with which
+// Gradient.  A first pass forms -L / c and -D of every row of a sequence and head, with which
 // the two products S and dP start their accumulators: P is then 2^(c log2(e) S')
 // and dS is P dP'.  Two kernels follow: keys' gradients (a workgroup owns keys and
 // goes through the queries of the key head's group) and queries' gradients (it
@@ -639,30 +639,75 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnFwd a)
 // products instead of five, so that no sum is added up in memory: results do not
 // depend on the order workgroups run in.
 // ---------------------------------------------------------------------------
-template <int D>
-__global__ __launch_bounds__(256) void attn_bwd_rows_kernel(AttnBwd a)
+// A wave takes 32 rows of one head.  D is sum P dP, and do o the same number with o's rounding to BF16 in it (half a
+// step, 2^-8 of each term at most).  Rows that see many keys do not notice; where few keys share the weight it would
+// double dq's and dk's error, so that rows that see at most FEW keys form the sum itself, from one tile of S and dP
+// (lanes that walk over such a row's keys cost 8 us more at 2 x 4096 queries).  The rest is one read of o and do: 18 us
+// for the 67 MB of 2 x 4096 queries, 16 heads of 128 (3.7 TB/s; a pass without the tile took 17).
+constexpr int FEW = 32;
+template <int D> __global__ __launch_bounds__(256) void attn_bwd_rows_kernel(AttnBwd a)
 {
-    constexpr int PER = 256 / (D / 8);
-    const int64_t n = (int64_t)blockIdx.x * PER + threadIdx.x / (D / 8);
-    const int64_t t = n / a.s.hq;
-    const int head = (int)(n % a.s.hq), d = (threadIdx.x % (D / 8)) * 8;
-    float sum = 0.0f;
-    if (t < a.s.tokens_q) {
-        float x[8], y[8];
-        Elem<uint16_t>::load8(a.o + t * a.ldo + head * D + d, x);
-        Elem<uint16_t>::load8(a.dout + t * a.lddo + head * D + d, y);
+    using Lds = Tile<D>;
+    constexpr int L = D / 8, R = 64 / L;   // lanes of a row, rows of a load
+    const int lane = threadIdx.x & 63, wave = uniform((int)threadIdx.x >> 6);
+    const int heads = (a.s.hq + 3) / 4, seq = uniform((int)blockIdx.x % a.s.seqs), block = uniform((int)blockIdx.x / a.s.seqs);
+    const int head = block % heads * 4 + wave, i0 = block / heads * 32;
+    const Rows q = uniform(q_rows(a.s, seq)), k = uniform(k_rows(a.s, seq));
+    if (head >= a.s.hq || i0 >= q.len)
+        return;
+    // Rows few .. most - 1 see 1 to FEW keys.
+    const int shift = k.len - q.len;
+    const int few = a.s.causal ? max(0, -shift) : 0, most = a.s.causal ? min(q.len, FEW - shift) : k.len > FEW ? 0 : q.len;
+    const int own = min(i0 + (lane & 31), q.len - 1);
+    const int64_t at = (int64_t)head * a.s.tokens_q + q.start;
+    const float lse = a.lse[at + own];
+    const bool sees = fabsf(lse) < INFINITY;   // rows that see nothing are masked everywhere
+    if (i0 + lane == own)
+        a.nl[at + own] = sees ? -lse / a.scale : 0.0f;
+    if (k.len > 0 && i0 < most && i0 + 32 > few) {
+        const int64_t t = q.start + own, j = k.start + min(lane & 31, k.len - 1);
+        const int kv = head / (a.s.hq / a.s.hk);
+        v16f s = splat(0.0f), dp = splat(0.0f);
+        v8bf x[Lds::SLICES], y[Lds::SLICES];
+        Lds::load(a.k + j * a.ldk + kv * D, lane, x);
+        Lds::load(a.q + t * a.ldq + head * D, lane, y);
+#pragma unroll
+        for (int n = 0; n < Lds::SLICES; n++)
+            s = mfma(x[n], y[n], s);
+        Lds::load(a.v + j * a.ldv + kv * D, lane, x);
+        Lds::load(a.dout + t * a.lddo + head * D, lane, y);
+#pragma unroll
+        for (int n = 0; n < Lds::SLICES; n++)
+            dp = mfma(x[n], y[n], dp);
+        const int lim = a.s.causal ? min(k.len - 1, own + shift) : k.len - 1;
+        float sum = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 16; e++) {
+            const float p = __builtin_amdgcn_exp2f(fmaf(s[e], a.c2, -lse * kLog2e)) * dp[e];
+            sum += acc_row(e, lane) > lim ? 0.0f : p;
+        }
+        sum += __shfl_xor(sum, 32, 64);
+        if (i0 + lane == own && own >= few && own < most)
+            a.nd[at + own] = sees ? -sum : 0.0f;
+    }
+    if (i0 >= few && i0 + 31 < most)
+        return;
+    const int64_t first = (int64_t)q.start * a.lddo + head * D + lane % L * 8;
+    const int64_t first_o = (int64_t)q.start * a.ldo + head * D + lane % L * 8;
+#pragma unroll
+    for (int n = 0; n < 32; n += R) {
+        const int i = i0 + n + lane / L, row = min(i, q.len - 1);
+        float x[8], y[8], sum = 0.0f;
+        Elem<uint16_t>::load8(a.o + first_o + row * a.ldo, x);
+        Elem<uint16_t>::load8(a.dout + first + row * a.lddo, y);
 #pragma unroll
         for (int e = 0; e < 8; e++)
             sum = fmaf(x[e], y[e], sum);
-    }
 #pragma unroll
-    for (int w = 1; w < D / 8; w <<= 1)
-        sum += __shfl_xor(sum, w, 64);
-    if (t < a.s.tokens_q && d == 0) {
-        const int64_t r = (int64_t)head * a.s.tokens_q + t;
-        const float lse = a.lse[r];
-        a.nl[r] = fabsf(lse) < INFINITY ? -lse / a.scale : 0.0f;   // rows that see nothing are masked everywhere
-        a.nd[r] = -sum;
+        for (int w = 1; w < L; w <<= 1)
+            sum += __shfl_xor(sum, w, 64);
+        if (lane % L == 0 && i < q.len && (i < few || i >= most))
+            a.nd[at + i] = -sum;
     }
 }
 
@@ -981,6 +1026,9 @@ int bwd_k_waves(const AttnShape &s)
     return (longest < rows ? longest : rows) < 256 ? 2 : 4;
 }
 
+// Workgroups of the gradient's first pass: four heads' 32 rows each.
+int64_t bwd_row_groups(const AttnShape &s) { return s.seqs * blocks_of(s.max_q, 32) * blocks_of(s.hq, 4); }
+
 size_t pad256(size_t n) { return (n + 255) / 256 * 256; }
 
 size_t part_bytes(const AttnShape &s, int splits) { return pad256((size_t)splits * s.hq * s.tokens_q * s.dim * 4); }
@@ -1007,18 +1055,17 @@ template <int D> hipError_t bwd(const AttnBwd &b, hipStream_t st)
 {
     const int64_t units = (int64_t)b.s.seqs * b.s.hk;
     hipError_t e = hipSuccess;
-    if (b.s.tokens_q > 0) {
-        hipLaunchKernelGGL((attn_bwd_rows_kernel<D>), dim3((unsigned)blocks_of(b.s.tokens_q * b.s.hq, 256 / (D / 8))),
-                           dim3(256), 0, st, b);
+    if (b.s.max_q > 0) {
+        hipLaunchKernelGGL((attn_bwd_rows_kernel<D>), dim3((unsigned)bwd_row_groups(b.s)), dim3(256), 0, st, b);
         e = hipGetLastError();
     }
-    if (e == hipSuccess && b.s.max_k > 0 && b.s.tokens_k > 0) {
+    if (e == hipSuccess && b.s.max_k > 0) {
         const int waves = bwd_k_waves(b.s);
         hipLaunchKernelGGL((waves == 4 ? attn_bwd_k_kernel<D, 4, 2> : attn_bwd_k_kernel<D, 2, 4>),
                            dim3((unsigned)(units * blocks_of(b.s.max_k, 32 * waves))), dim3(512), 0, st, b);
         e = hipGetLastError();
     }
-    if (e == hipSuccess && b.s.max_q > 0 && b.s.tokens_q > 0) {
+    if (e == hipSuccess && b.s.max_q > 0) {
         hipLaunchKernelGGL((attn_bwd_q_kernel<D, BWD_Q_WAVES>), dim3((unsigned)(units * b.q_blocks)),
                            dim3(64 * BWD_Q_WAVES), 0, st, b);
         e = hipGetLastError();
@@ -1034,7 +1081,7 @@ bool attn_fits(const AttnShape &s, bool backward)
     if (rows_most(s) > 1 << 30)
         return false;
     if (backward)
-        return (double)s.tokens_q * s.hq * (s.dim / 8) + 256 <= most &&
+        return (double)bwd_row_groups(s) * 256 <= most &&
                units * (double)blocks_of(s.max_k, 64) * 512 <= most &&
                units * (double)blocks_of(rows_most(s), 32 * BWD_Q_WAVES) * 64 * BWD_Q_WAVES <= most;
     const double groups = few_rows(s) ? units * 64 * ROW_WAVES : units * (double)blocks_of(rows_most(s), 32 * FWD_WAVES) * 64 * FWD_WAVES;

@@ -700,7 +700,8 @@ puro_status_t puro_fp8_attention(const puro_attention_t *shape, const void *q, i
 /*
  * Gradient of attention: for dout (the gradient of o, BF16 as o) and the
  * forward's q, k, v, o and lse, with P = exp(S - lse), dP = dout_i . v_j and
- * D_i = dout_i . o_i:
+ * D_i = dout_i . o_i (for rows that see at most 32 keys sum_j P dP, the same
+ * number without o's rounding in it):
  *     dS = P (dP - D),  dv = P^T dout,  dq = scale dS k,  dk = scale dS^T q
  * dk and dv are summed over the query heads of their key head.  P and dS enter
  * their products as BF16; everything else is FP32 until the results are rounded

@@ -136,7 +136,13 @@ def head_bwd(q, k, v, do, o, lse, scale, causal):
     top = torch.where(hide, 0.0, scale * (q.abs() @ k.abs().t())).amax(1, keepdim=True)
     ep = (2 * d + 8) * U * (top + base.abs()) + 8 * U
     dp, dd = do @ v.t(), (do * o).sum(1, keepdim=True)
-    edp = 2 * d * U * (do.abs() @ v.abs().t() + (do * o).abs().sum(1, keepdim=True) + dd.abs())
+    edd = 2 * d * U * (do * o).abs().sum(1, keepdim=True)
+    # rows that see at most 32 keys: D from P dP itself, 32 more additions and P's own error
+    few = (~hide).sum(1, keepdim=True) <= 32
+    own = (p * dp).sum(1, keepdim=True)
+    eown = (p * (2 * (d + 40) * U + ep) * (do.abs() @ v.abs().t())).sum(1, keepdim=True)
+    dd, edd = torch.where(few, own, dd), torch.where(few, eown, edd)
+    edp = 2 * d * U * (do.abs() @ v.abs().t() + dd.abs()) + edd
     ds = p * (dp - dd)
     eds = ds.abs() * (B + ep + 4 * U) + p * edp * (1 + B) + TINY * (1 + (dp - dd).abs() + edp)
     aq, ak = (m + 16) * 2 * U, (n + 16) * 2 * U
