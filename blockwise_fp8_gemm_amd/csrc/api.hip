@@ -1135,7 +1135,7 @@ static puro_status_t check_attention(const puro_attention_t &a, bool backward)
         return PURO_ERR_NULL;
     if (!aligned(a.q_offsets, 4) || !aligned(a.q_lengths, 4) || !aligned(a.k_offsets, 4) || !aligned(a.k_lengths, 4))
         return PURO_ERR_ALIGN;
-    if (!(a.scale > 0.0f) || !std::isfinite(a.scale))
+    if (!(a.scale >= 0x1p-64f && a.scale <= 0x1p64f))
         return PURO_ERR_VALUE;
     return PURO_OK;
 }

@@ -369,8 +369,12 @@ template <int D> struct Softmax {
     }
 };
 
-// Share `split` of n tiles (at most 2^18, in at most 2^8 shares).
+// Share `split` of n tiles (at most 2^18: of 32 keys, of 2^23; in at most 2^7 shares).
 __device__ __forceinline__ int share(int n, int split, int splits) { return uniform(n * split / splits); }
+
+// 1 / l of a row's sum, and its lse.  0 is a row that sees nothing; NaN stays NaN.
+__device__ __forceinline__ float reciprocal(float l) { return l == 0.0f ? 0.0f : 1.0f / l; }
+__device__ __forceinline__ float log_sum(float m, float l) { return l == 0.0f ? -INFINITY : (m + __log2f(l)) * kLn2; }
 
 // Where row t's partial results of a split go: [split][head][row].
 __device__ __forceinline__ int64_t part_row(const AttnFwd &a, int split, int head, int t)
@@ -384,9 +388,9 @@ __device__ __forceinline__ void put_row(const AttnFwd &a, Softmax<D> &x, int spl
 {
     const float l = x.l + other_half(x.l);
     if (a.splits == 1) {
-        store_row<D>(a.o + (int64_t)t * a.ldo + head * D, x.o, l > 0.0f ? 1.0f / l : 0.0f, lane);
+        store_row<D>(a.o + (int64_t)t * a.ldo + head * D, x.o, reciprocal(l), lane);
         if (a.lse && lane < 32)
-            a.lse[(int64_t)head * a.s.tokens_q + t] = l > 0.0f ? (x.m + __log2f(l)) * kLn2 : -INFINITY;
+            a.lse[(int64_t)head * a.s.tokens_q + t] = log_sum(x.m, l);
         return;
     }
     const int64_t p = part_row(a, split, head, t);
@@ -582,12 +586,12 @@ __global__ __launch_bounds__(64 * ROW_WAVES) void attn_rows_kernel(AttnFwd a)
         }
         const int t = q.start + cc / group, hd = kh * group + cc % group;
         if (a.splits == 1) {
-            const float f = sum > 0.0f ? 1.0f / sum : 0.0f;
+            const float f = reciprocal(sum);
             *reinterpret_cast<uint4 *>(a.o + (int64_t)t * a.ldo + hd * D + d) =
                 make_uint4(to_bf16x2(v[0] * f, v[1] * f), to_bf16x2(v[2] * f, v[3] * f), to_bf16x2(v[4] * f, v[5] * f),
                            to_bf16x2(v[6] * f, v[7] * f));
             if (a.lse && d == 0)
-                a.lse[(int64_t)hd * a.s.tokens_q + t] = sum > 0.0f ? (m + __log2f(sum)) * kLn2 : -INFINITY;
+                a.lse[(int64_t)hd * a.s.tokens_q + t] = log_sum(m, sum);
         } else {
             const int64_t p = part_row(a, split, hd, t);
             *reinterpret_cast<float4 *>(a.part + p * D + d) = make_float4(v[0], v[1], v[2], v[3]);
@@ -623,11 +627,11 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnFwd a)
         sum = fmaf(f, st.y, sum);
         v = make_float4(fmaf(f, o.x, v.x), fmaf(f, o.y, v.y), fmaf(f, o.z, v.z), fmaf(f, o.w, v.w));
     }
-    const float f = sum > 0.0f ? 1.0f / sum : 0.0f;
+    const float f = reciprocal(sum);
     *reinterpret_cast<uint2 *>(a.o + (int64_t)t * a.ldo + head * D + d) =
         make_uint2(to_bf16x2(v.x * f, v.y * f), to_bf16x2(v.z * f, v.w * f));
     if (a.lse && d == 0)
-        a.lse[(int64_t)head * a.s.tokens_q + t] = sum > 0.0f ? (m + __log2f(sum)) * kLn2 : -INFINITY;
+        a.lse[(int64_t)head * a.s.tokens_q + t] = log_sum(m, sum);
 }
 
 // ---------------------------------------------------------------------------
@@ -661,7 +665,7 @@ template <int D> __global__ __launch_bounds__(256) void attn_bwd_rows_kernel(Att
     const int own = min(i0 + (lane & 31), q.len - 1);
     const int64_t at = (int64_t)head * a.s.tokens_q + q.start;
     const float lse = a.lse[at + own];
-    const bool sees = fabsf(lse) < INFINITY;   // rows that see nothing are masked everywhere
+    const bool sees = lse != -INFINITY;   // rows that see nothing are masked everywhere
     if (i0 + lane == own)
         a.nl[at + own] = sees ? -lse / a.scale : 0.0f;
     if (k.len > 0 && i0 < most && i0 + 32 > few) {

@@ -671,13 +671,16 @@ puro_status_t puro_fp8_qk_norm_rope_bwd_quant_dual_pow2(const puro_qk_norm_rope_
  *   max_q, max_k the most rows of one sequence.  Rows past a maximum or past the
  *                tensor are left out, so the arrays may change between replays
  *                of a captured call.  Smaller maxima cost less.
- *   scale        finite and > 0, else PURO_ERR_VALUE
+ *   scale        2^-64 .. 2^64, else PURO_ERR_VALUE
  * shape is a HOST structure, read before the call returns.  q BF16 [tokens_q]
  * [heads_q head_dim], k and v BF16 [tokens_k][heads_kv head_dim], o as q; row
  * strides ldq, ldk, ldv, ldo.  lse FP32 [heads_q][tokens_q], or NULL.  Rows of
  * o and lse outside every sequence are left as they were, rows of k and v outside
  * are not read into any result.  Query rows of two sequences must not overlap; key
- * rows may.  Every |S| must stay below 2^96.
+ * rows may.  Every |S| and |q_i . k_j| must stay below 2^96, and a sequence's
+ * elements be finite.  A NaN reaches all that the formulas say; one in a key or value
+ * row, or in the gradients in any row, may reach rows of its sequence that do not
+ * see it, too.
  * Precision: exp(S - its row's running maximum) enters the second product as BF16,
  * within 2^-8 of itself per key; sums, maxima and results before their rounding
  * to BF16 are FP32.  Equal calls give equal bits.

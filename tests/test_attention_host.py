@@ -98,7 +98,7 @@ ATTN_BAD = [(dict(heads_q=0), SHAPE), (dict(heads_kv=0), SHAPE), (dict(heads_q=5
             (dict(causal=-1), ENUM), (dict(q_offsets=0), NULL), (dict(k_offsets=0), NULL), (dict(q_offsets=PTR + 2), ALIGN),
             (dict(k_offsets=PTR + 1), ALIGN), (dict(q_lengths=PTR + 2), ALIGN), (dict(k_lengths=PTR + 2), ALIGN),
             (dict(scale=0.0), VALUE), (dict(scale=-1.0), VALUE), (dict(scale=float("nan")), VALUE),
-            (dict(scale=float("inf")), VALUE),
+            (dict(scale=float("inf")), VALUE), (dict(scale=2.0 ** -65), VALUE), (dict(scale=2.0 ** 65), VALUE),
             # more work items than a grid has
             (dict(sequences=2 ** 31 - 1, tokens_q=2 ** 23, tokens_k=2 ** 23, max_q=2 ** 23, max_k=2 ** 23), SHAPE),
             (dict(heads_q=1024, heads_kv=1, tokens_q=2 ** 23, max_q=2 ** 23), SHAPE)]

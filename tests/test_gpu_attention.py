@@ -184,3 +184,23 @@ def test_nothing_to_do(dev):
     o, lse = pf.puro_fp8_attention(q, k, k, 64, ref.i32([0, 5], dev), ref.i32([0, 0], dev), 5, 0)
     torch.cuda.synchronize()
     assert not o.any() and bool((lse == -torch.inf).all())
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("n,m", [(300, 300), (4, 40), (1, 3000), (2, 9000), (40, 9000)])
+def test_a_row_of_nan_is_its_own(dev, n, m, dim):
+    """NaN in one query row: its o and lse are NaN, the other rows' are what they are without it."""
+    gen = torch.Generator().manual_seed(n + m)
+    q, k = ref.bf16(gen, n, 4 * dim, 1.0, 0, dev), ref.bf16(gen, m, 2 * dim, 1.0, 0, dev)
+    v = ref.bf16(gen, m, 2 * dim, 1.0, 0, dev)
+    plan = (dim, ref.i32([0, n], dev), ref.i32([0, m], dev), n, m)
+    o0, l0 = pf.puro_fp8_attention(q, k, v, *plan)
+    bad = n // 2
+    q[bad, 5] = float("nan")      # of the first head
+    o1, l1 = pf.puro_fp8_attention(q, k, v, *plan)
+    torch.cuda.synchronize()
+    assert bool(torch.isnan(o1[bad, :dim]).all()) and bool(torch.isnan(l1[0, bad]))
+    o1[bad, :dim], l1[0, bad] = o0[bad, :dim], l0[0, bad]
+    # the maximum is looked for again in the tiles of a wave with a NaN: P may round differently, twice B of sum P |v|
+    assert bool(torch.isfinite(o1).all()) and bool(torch.isfinite(l1).all())
+    assert float((o1.float() - o0.float()).abs().max()) <= 4 * ref.B * float(v.float().abs().max())

@@ -127,3 +127,27 @@ def test_nothing_to_do(dev):
     dq, dk, dv = pf.puro_fp8_attention_bwd(q, q, kk, kk, q, lse, 64, ref.i32([0, 0], dev), ref.i32([0, 70], dev), 0, 70)
     torch.cuda.synchronize()
     assert not dk.any() and not dv.any()
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("n", [20, 300])
+def test_nan_is_not_hidden(dev, n, dim):
+    """A row whose lse is NaN has a NaN dq, and so have dk and dv of the keys that it sees."""
+    args, kw, _, _ = case(dev, 2, 2, dim, [n], [n], True, seed=n)
+    lse, row = args[5], n // 2
+    lse[0, row] = float("nan")
+    dq, dk, dv = pf.puro_fp8_attention_bwd(*args, **kw)
+    torch.cuda.synchronize()
+    assert bool(torch.isnan(dq[row, :dim]).all())
+    assert bool(torch.isnan(dk[:row + 1, :dim]).all()) and bool(torch.isnan(dv[:row + 1, :dim]).all())
+    others = torch.ones(n, dtype=torch.bool)
+    others[row] = False
+    assert bool(torch.isfinite(dq[others.to(dev)]).all()) and bool(torch.isfinite(dk[:, dim:]).all())
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("q,k", [(100, 70), (70, 100), (40, 32), (200, 20), (33, 65), (5, 31), (300, 33)])
+def test_rows_that_see_few_keys(dev, q, k, causal, dim):
+    """Both sides of the 32 keys where D's form changes, inside a wave's 32 rows and between them."""
+    run(dev, 6, 2, dim, [q, 3, q], [k, k, 4], causal, seed=q + k)
