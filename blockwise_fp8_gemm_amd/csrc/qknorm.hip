@@ -305,27 +305,28 @@ void rope_bwd_kernel(RopeBwd b, QuantOut ro, QuantOut to, int pow2)
         rope_bwd_tile<D, false, TR, MODE>(b, p, ro, to, pow2, sh, red);
 }
 
-// dw of 32 elements of the queries' (then the keys') weight: 16 threads each add some of the (token tile, head)
-// shares, and their sums are added in a fixed order.
-__global__ __launch_bounds__(512) void rope_dw_kernel(RopeBwd b, int ntb)
+// dw of 16 elements of the queries' (then the keys') weight: 64 threads each add some of the (token tile, head)
+// shares, eight loads at a time, and their sums are added in a fixed order.
+constexpr int DW_COLS = 16, DW_ROWS = 64;
+__global__ __launch_bounds__(DW_COLS *DW_ROWS) void rope_dw_kernel(RopeBwd b, int ntb)
 {
-    __shared__ float red[16][32];
-    const int x = threadIdx.x % 32, y = threadIdx.x / 32, D = b.r.dim, per = D / 32;
+    __shared__ float red[DW_ROWS][DW_COLS];
+    const int x = threadIdx.x % DW_COLS, y = threadIdx.x / DW_COLS, D = b.r.dim, per = D / DW_COLS;
     const bool keys = (int)blockIdx.x >= per;
-    const int d = ((int)blockIdx.x - (keys ? per : 0)) * 32 + x, heads = keys ? b.r.hk : b.r.hq, H = b.r.hq + b.r.hk;
+    const int d = ((int)blockIdx.x - (keys ? per : 0)) * DW_COLS + x, heads = keys ? b.r.hk : b.r.hq, H = b.r.hq + b.r.hk;
     const float *part = b.part + (keys ? b.r.hq * D : 0) + d;
     // as many threads over the heads as fit (a power of two), the others over the tiles
-    int hs = 16;
+    int hs = DW_ROWS;
     while (hs > heads)
         hs >>= 1;
     float s = 0.0f;
     for (int h = y & (hs - 1); h < heads; h += hs) {
 #pragma unroll 8
-        for (int tb = y / hs; tb < ntb; tb += 16 / hs)
+        for (int tb = y / hs; tb < ntb; tb += DW_ROWS / hs)
             s += part[(int64_t)tb * H * D + h * D];
     }
     red[y][x] = s;
-    for (int m = 8; m > 0; m >>= 1) {
+    for (int m = DW_ROWS / 2; m > 0; m >>= 1) {
         __syncthreads();
         if (y < m)
             red[y][x] += red[y + m][x];
@@ -399,7 +400,8 @@ hipError_t launch_rope_bwd(RopeBwd b, uint8_t *qr, int64_t ldqr, float *sr, bool
         e = hipGetLastError();
     }
     if (e == hipSuccess && b.r.wq) {
-        hipLaunchKernelGGL(rope_dw_kernel, dim3((unsigned)(2 * b.r.dim / 32)), dim3(512), 0, st, b, (int)ntb);
+        hipLaunchKernelGGL(rope_dw_kernel, dim3((unsigned)(2 * b.r.dim / DW_COLS)), dim3(DW_COLS * DW_ROWS), 0,
+                           st, b, (int)ntb);
         e = hipGetLastError();
     }
     return e;
