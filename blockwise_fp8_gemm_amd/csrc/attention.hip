@@ -405,13 +405,15 @@ __device__ __forceinline__ void put_row(const AttnFwd &a, Softmax<D> &x, int spl
         a.stat[p] = make_float2(x.m, l);
 }
 
-// Many rows: NW waves of 32 rows, a query of one head each, 64 keys (128 of narrow heads) at a time through LDS.
-template <int D, int NW>
-__global__ __launch_bounds__(64 * NW) void attn_fwd_kernel(AttnFwd a)
+// Many rows: NW waves of 32 rows, a query of one head each, HV times; 64 keys (128 of narrow heads) at a time through
+// LDS.  The HV waves of the same rows take every HV-th tile, and their results meet at the end.
+template <int D, int NW, int HV>
+__global__ __launch_bounds__(64 * NW * HV, 2) void attn_fwd_kernel(AttnFwd a)
 {
-    constexpr int R = 32 * NW, KT = 8192 / D, TILE = Tile<D>::bytes(KT);
-    __shared__ __attribute__((aligned(16))) uint8_t lds[2][2][TILE];
+    constexpr int R = 32 * NW, KT = 8192 / D, TILE = Tile<D>::bytes(KT), N = KT / 32;
+    __shared__ __attribute__((aligned(16))) uint8_t lds[2][2][HV][TILE];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int rw = wave % NW, part = wave / NW;
     // blocks of later rows, which see more keys, first; a sequence's key head on one XCD where their
     // number is a multiple of 8 (workgroups go round the XCDs).  The query heads of a key head share its tiles.
     const int units = a.s.seqs * a.s.hk, group = a.s.hq / a.s.hk;
@@ -425,60 +427,98 @@ __global__ __launch_bounds__(64 * NW) void attn_fwd_kernel(AttnFwd a)
     const int shift = k.len - q.len, last = uniform((min(r0 + R, rows) - 1) / group);
     const int seen = a.s.causal ? max(0, min(k.len, last + 1 + shift)) : k.len;
     const int tiles = (seen + KT - 1) / KT, t0 = share(tiles, split, a.splits), t1 = share(tiles, split + 1, a.splits);
+    const int rounds = (t1 - t0 + HV - 1) / HV;
 
     const uint16_t *kp = a.k + (int64_t)k.start * a.ldk + kh * D, *vp = a.v + (int64_t)k.start * a.ldv + kh * D;
-    const typename Tile<D>::template Stage<KT, NW> copy_k(a.ldk, wave, lane), copy_v(a.ldv, wave, lane);
-    auto stage_k = [&](int t) {
-        if (t < t1)
-            copy_k(lds[0][t & 1], kp + (int64_t)t * KT * a.ldk, k.len - 1 - t * KT, wave);
+    const typename Tile<D>::template Stage<KT, NW * HV> copy_k(a.ldk, wave, lane), copy_v(a.ldv, wave, lane);
+    // a round's tiles; places past the last tile hold it again, and its keys are hidden there
+    auto stage_k = [&](int n) {
+        if (n < rounds)
+#pragma unroll
+            for (int h = 0; h < HV; h++) {
+                const int j = min(t0 + HV * n + h, t1 - 1) * KT;
+                copy_k(lds[0][n & 1][h], kp + (int64_t)j * a.ldk, k.len - 1 - j, wave);
+            }
     };
-    auto stage_v = [&](int t) {
-        if (t < t1)
-            copy_v(lds[1][t & 1], vp + (int64_t)t * KT * a.ldv, k.len - 1 - t * KT, wave);
+    auto stage_v = [&](int n) {
+        if (n < rounds)
+#pragma unroll
+            for (int h = 0; h < HV; h++) {
+                const int j = min(t0 + HV * n + h, t1 - 1) * KT;
+                copy_v(lds[1][n & 1][h], vp + (int64_t)j * a.ldv, k.len - 1 - j, wave);
+            }
     };
-    // everyone's copies of K tile t and V tile t - 1 have landed and the places of the ones before are free
-    auto turn = [&](int t) {
+    // everyone's copies of round n's K tiles and the last one's V tiles have landed and the places of the ones before
+    // are free
+    auto turn = [&](int n) {
         wait_copies<0>();
         __builtin_amdgcn_sched_barrier(0);
         __syncthreads();
         __builtin_amdgcn_sched_barrier(0);
-        stage_k(t + 1);
-        stage_v(t);
+        stage_k(n + 1);
+        stage_v(n);
     };
-    stage_k(t0);
-    const int w0 = r0 + 32 * wave, r = w0 + (lane & 31), rc = min(r, rows - 1);
+    stage_k(0);
+    const int w0 = r0 + 32 * rw, r = w0 + (lane & 31), rc = min(r, rows - 1);
     const int i = rc / group, head = kh * group + (rc - i * group), row = q.start + i;
     v8bf qf[D / 16];
     Tile<D>::load(a.q + (int64_t)row * a.ldq + head * D, lane, qf);
-    const int lim = a.s.causal ? min(k.len - 1, i + shift) : k.len - 1;
-    const int low = a.s.causal ? min(k.len - 1, uniform(w0 / group) + shift) : k.len - 1;   // the wave's first row's
+    const int lim = min(t1 * KT - 1, a.s.causal ? min(k.len - 1, i + shift) : k.len - 1);
+    // the wave's first row's
+    const int low = min(t1 * KT - 1, a.s.causal ? min(k.len - 1, uniform(w0 / group) + shift) : k.len - 1);
 
     // Between two barriers a wave has the matrix cores' part of a tile (the last one's P v, the next scores) and
     // the exponentials of one: the early half of the waves in that order, the late half, which is on the same
     // SIMDs, the other way round, so that one's products run beside the other's exponentials.
-    const bool late = wave >= NW / 2;
+    const bool late = wave >= NW * HV / 2;
     Softmax<D> st;
-    constexpr int N = KT / 32;
     v16f s[N];
     v8bf p[2 * N];
     pin(qf);
-    if (t0 < t1) {
-        turn(t0);
-        st.template products<N, false, true>(lds[1][0], p, lds[0][t0 & 1], qf, s, lane);
-        for (int t = t0; t < t1 - 1; t++) {
+    if (rounds > 0) {
+        auto weigh = [&](int n) {
+            const int j = (t0 + HV * n + part) * KT;
+            st.template weigh<N>(s, p, a.c2, j, (t0 + part) * KT, lim, j + KT - 1 > low, lane);
+        };
+        turn(0);
+        st.template products<N, false, true>(lds[1][0][part], p, lds[0][0][part], qf, s, lane);
+        for (int n = 0; n < rounds - 1; n++) {
             if (late)
-                turn(t + 1);
-            st.template weigh<N>(s, p, a.c2, t * KT, t0 * KT, lim, t * KT + KT - 1 > low, lane);
+                turn(n + 1);
+            weigh(n);
             if (!late)
-                turn(t + 1);
-            st.template products<N, true, true>(lds[1][t & 1], p, lds[0][(t + 1) & 1], qf, s, lane);
+                turn(n + 1);
+            st.template products<N, true, true>(lds[1][n & 1][part], p, lds[0][(n + 1) & 1][part], qf, s, lane);
         }
         if (late)
-            turn(t1);
-        st.template weigh<N>(s, p, a.c2, (t1 - 1) * KT, t0 * KT, lim, t1 * KT - 1 > low, lane);
+            turn(rounds);
+        weigh(rounds - 1);
         if (!late)
-            turn(t1);
-        st.template products<N, true, false>(lds[1][(t1 - 1) & 1], p, lds[0][0], qf, s, lane);
+            turn(rounds);
+        st.template products<N, true, false>(lds[1][(rounds - 1) & 1][part], p, lds[0][0][part], qf, s, lane);
+    }
+    if constexpr (HV == 2) {
+        constexpr int V = D / 2;   // a lane's values of o
+        static_assert(NW * (V + 2) * 256 <= (int)sizeof(lds), "a half's results take the tiles' place");
+        float *x = reinterpret_cast<float *>(lds) + rw * (V + 2) * 64 + lane;
+        __syncthreads();
+        if (part == 1) {
+#pragma unroll
+            for (int e = 0; e < V; e++)
+                x[e * 64] = st.o[e / 16][e % 16];
+            x[V * 64] = st.m;
+            x[(V + 1) * 64] = st.l;
+        }
+        __syncthreads();
+        if (part == 1)
+            return;
+        const float m = fmaxf(st.m, x[V * 64]);
+        const float f = __builtin_amdgcn_exp2f(st.m - m), g = __builtin_amdgcn_exp2f(x[V * 64] - m);
+        st.m = m;
+        st.l = fmaf(g, x[(V + 1) * 64], f * st.l);
+#pragma unroll
+        for (int e = 0; e < V; e++)
+            st.o[e / 16][e % 16] = fmaf(g, x[e * 64], f * st.o[e / 16][e % 16]);
     }
     if (r < rows)
         put_row<D>(a, st, split, head, row, lane);
@@ -999,7 +1039,7 @@ __global__ __launch_bounds__(64 * NW) void attn_bwd_q_kernel(AttnBwd a)
         store_row<D>(a.dq + (int64_t)row * a.lddq + head * D, dq, a.scale, lane);
 }
 
-constexpr int FWD_WAVES = 8, BWD_Q_WAVES = 8;
+constexpr int BWD_Q_WAVES = 8;
 
 int64_t blocks_of(int64_t n, int64_t per) { return (n + per - 1) / per; }
 
@@ -1009,17 +1049,45 @@ int64_t rows_most(const AttnShape &s) { return (int64_t)s.max_q * (s.hq / s.hk);
 // Whether a key head's rows of every sequence fit one wave.
 bool few_rows(const AttnShape &s) { return rows_most(s) <= 32; }
 
-// Shares of the key axis, as many as the 256 CUs take at once
+// Workgroups of 128 rows of the forward: by the longest sequence, or by the rows there are.
+int64_t fwd_groups(const AttnShape &s)
+{
+    const int64_t longest = (int64_t)s.seqs * s.hk * blocks_of(rows_most(s), 128);
+    const int64_t rows = s.hk * (s.tokens_q * (s.hq / s.hk) / 128 + s.seqs);
+    return longest < rows ? longest : rows;
+}
+
+// Shares of the key axis.  Few rows: as many as make 1024 workgroups (four a CU), of 512 keys or more.  Many rows: as
+// many as make 256 workgroups of eight waves, one a CU, of 1024 keys or more (777 queries over 20000 keys, heads of
+// 128: 135 us, unsplit 283, twice as many shares 157), but none where workgroups of 128 rows fill most CUs and the keys
+// are not much longer than those workgroups' work (192 groups or more: 2048 x 2048 33 us, split 45; over 8192 keys 120
+// either way; 1500 x 17500 220, split 201), and none of up to 2048 keys (512 x 2048 32 us, split 35.5).
 int splits_of(const AttnShape &s)
 {
     if (s.seqs == 0 || s.max_q == 0)
         return 1;
     const int64_t units = (int64_t)s.seqs * s.hk;
-    const int64_t groups = few_rows(s) ? units : units * blocks_of(rows_most(s), 32 * FWD_WAVES);
+    if (!few_rows(s) && (s.max_k <= 2048 || (s.max_k <= 8192 && fwd_groups(s) >= 192)))
+        return 1;
+    const int64_t groups = few_rows(s) ? units : units * blocks_of(rows_most(s), 256);
     int64_t want = groups ? (few_rows(s) ? 1024 : 256) / groups : 1;
     const int64_t most = s.max_k / (few_rows(s) ? 512 : 1024);
     want = want < most ? want : most;
     return (int)(want < 1 ? 1 : want > 64 ? 64 : want);
+}
+
+// Form of the forward's workgroups, NW x HV waves.  8 x 1 reads a tile for the most rows, and fills the card from some
+// 640 workgroups of 128 rows on (2 x 3000 queries, heads of 128: 77 us, 4 x 1 78.6; 2 x 4096: 126, 141).  Below, smaller
+// ones spread the rows over more CUs.  4 x 2 has a CU to itself and halves the way along the keys: for as many
+// workgroups as CUs (1024 queries: 20 us, 4 x 1 23, 8 x 1 28), or twice as many where that way is long (4096: 73, 84 and
+// 91).  4 x 1, two to a CU, for the rest (packed lengths 1 to 1500, heads of 64: 24.9 us, 4 x 2 30, 8 x 1 28.8).
+enum Form { EIGHT, FOUR, FOUR_TWICE };
+Form form_of(const AttnShape &s)
+{
+    const int64_t groups = fwd_groups(s);
+    if (splits_of(s) > 1 || groups > 640)
+        return EIGHT;
+    return groups <= 256 || (groups <= 512 && s.max_k >= 2048) ? FOUR_TWICE : FOUR;
 }
 
 // Waves of 32 keys of the keys' gradients: four, or two where four would make fewer workgroups than there are CUs
@@ -1043,9 +1111,10 @@ template <int D> hipError_t fwd(AttnFwd a, hipStream_t st)
     if (few_rows(a.s)) {
         hipLaunchKernelGGL((attn_rows_kernel<D>), dim3((unsigned)(units * a.splits)), dim3(64 * ROW_WAVES), 0, st, a);
     } else {
-        a.blocks = (int)blocks_of(rows_most(a.s), 32 * FWD_WAVES);
-        hipLaunchKernelGGL((attn_fwd_kernel<D, FWD_WAVES>), dim3((unsigned)(units * a.splits * a.blocks)),
-                           dim3(64 * FWD_WAVES), 0, st, a);
+        const Form form = form_of(a.s);
+        auto *kernel = form == EIGHT ? attn_fwd_kernel<D, 8, 1> : form == FOUR ? attn_fwd_kernel<D, 4, 1> : attn_fwd_kernel<D, 4, 2>;
+        a.blocks = (int)blocks_of(rows_most(a.s), form == EIGHT ? 256 : 128);
+        hipLaunchKernelGGL(kernel, dim3((unsigned)(units * a.splits * a.blocks)), dim3(form == FOUR ? 256 : 512), 0, st, a);
     }
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.splits == 1)
@@ -1088,7 +1157,7 @@ bool attn_fits(const AttnShape &s, bool backward)
         return (double)bwd_row_groups(s) * 256 <= most &&
                units * (double)blocks_of(s.max_k, 64) * 512 <= most &&
                units * (double)blocks_of(rows_most(s), 32 * BWD_Q_WAVES) * 64 * BWD_Q_WAVES <= most;
-    const double groups = few_rows(s) ? units * 64 * ROW_WAVES : units * (double)blocks_of(rows_most(s), 32 * FWD_WAVES) * 64 * FWD_WAVES;
+    const double groups = few_rows(s) ? units * 64 * ROW_WAVES : units * (double)blocks_of(rows_most(s), 128) * 512;
     return groups * splits_of(s) <= most && heads * s.max_q * (s.dim / 4) + 256 <= most;
 }
 
