@@ -757,7 +757,7 @@ template <int D> __global__ __launch_bounds__(256) void attn_bwd_rows_kernel(Att
 
 // Keys' and values' gradients: NW waves of 32 keys, HV times.  QT queries of one head at a time go through LDS; the
 // HV waves of the same keys take every HV-th run of 32 of them, and their sums meet at the end.  Four waves of keys,
-// twice, read a tile least often; where that makes too few workgroups for the 256 CUs it is two waves, four times.
+// twice, read a tile least often; where that makes few workgroups it is two waves, four times (bwd_k_waves).
 template <int D, int NW, int HV>
 __global__ __launch_bounds__(64 * NW * HV) void attn_bwd_k_kernel(AttnBwd a)
 {
@@ -928,13 +928,16 @@ __global__ __launch_bounds__(64 * NW * HV) void attn_bwd_k_kernel(AttnBwd a)
     }
 }
 
-// Queries' gradients: NW waves of 32 rows (as in the forward), 64 keys at a time through LDS, 32 in a step.
-template <int D, int NW>
-__global__ __launch_bounds__(64 * NW) void attn_bwd_q_kernel(AttnBwd a)
+// Queries' gradients: NW waves of 32 rows (as in the forward), HV times, 64 keys at a time through LDS, 32 in a step.
+// The two waves of the same rows take a half of every tile each, and their sums meet at the end.
+template <int D, int NW, int HV>
+__global__ __launch_bounds__(64 * NW * HV) void attn_bwd_q_kernel(AttnBwd a)
 {
     constexpr int R = 32 * NW, KT = 64, TILE = Tile<D>::bytes(KT), B = D / 32, S = D / 16;
-    __shared__ __attribute__((aligned(16))) uint8_t lds_k[3][TILE], lds_v[2][TILE];
+    __shared__ __attribute__((aligned(16))) uint8_t lds[5][TILE];
+    uint8_t(*const lds_k)[TILE] = lds, (*const lds_v)[TILE] = lds + 3;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int rw = wave % NW, part = wave / NW;
     const int units = a.s.seqs * a.s.hk, group = a.s.hq / a.s.hk;
     const int x = uniform((int)blockIdx.x / units), unit = (int)blockIdx.x - x * units;
     const int seq = uniform(unit / a.s.hk), kh = unit - seq * a.s.hk;
@@ -948,7 +951,7 @@ __global__ __launch_bounds__(64 * NW) void attn_bwd_q_kernel(AttnBwd a)
     const int tiles = (seen + KT - 1) / KT;
 
     const uint16_t *kp = a.k + (int64_t)k.start * a.ldk + kh * D, *vp = a.v + (int64_t)k.start * a.ldv + kh * D;
-    const typename Tile<D>::template Stage<KT, NW> copy_k(a.ldk, wave, lane), copy_v(a.ldv, wave, lane);
+    const typename Tile<D>::template Stage<KT, NW * HV> copy_k(a.ldk, wave, lane), copy_v(a.ldv, wave, lane);
     int at = 0;   // the K tile's place among three: the last tile's is read for one step into the next
     auto stage = [&](int t, int place) {
         const int last = k.len - 1 - t * KT;
@@ -957,7 +960,7 @@ __global__ __launch_bounds__(64 * NW) void attn_bwd_q_kernel(AttnBwd a)
     };
     if (tiles > 0)
         stage(0, 0);
-    const int w0 = r0 + 32 * wave, r = w0 + (lane & 31), rc = min(r, rows - 1);
+    const int w0 = r0 + 32 * rw, r = w0 + (lane & 31), rc = min(r, rows - 1);
     const int i = rc / group, head = kh * group + (rc - i * group), row = q.start + i;
     v8bf qf[S], df[S];
     Tile<D>::load(a.q + (int64_t)row * a.ldq + head * D, lane, qf);
@@ -1023,11 +1026,11 @@ __global__ __launch_bounds__(64 * NW) void attn_bwd_q_kernel(AttnBwd a)
         if (t + 1 < tiles)
             stage(t + 1, next);
 #pragma unroll 1
-        for (int u = 0; u < 2; u++) {
+        for (int u = part; u < 2; u += HV) {
             // one step past the wave's last visible key: it adds the step before and leaves zeros
             const int j0 = t * KT + 32 * u;
             const uint8_t *kt = lds_k[at] + u * HALF;
-            if (j0 - 32 <= high)
+            if (j0 - 32 * HV <= high)
                 step(kc, kt + rb, lds_v[t & 1] + u * HALF + rb, j0);
             kc = kt + cb;
         }
@@ -1035,11 +1038,26 @@ __global__ __launch_bounds__(64 * NW) void attn_bwd_q_kernel(AttnBwd a)
     }
     if (tiles > 0)
         add(kc);
+    if constexpr (HV == 2) {
+        constexpr int V = D / 2;   // a lane's values of dq
+        static_assert(NW * V * 256 <= (int)sizeof(lds), "a half's sums take the tiles' place");
+        float *x = reinterpret_cast<float *>(lds) + rw * V * 64 + lane;
+        __syncthreads();
+        if (part == 1) {
+#pragma unroll
+            for (int e = 0; e < V; e++)
+                x[e * 64] = dq[e / 16][e % 16];
+        }
+        __syncthreads();
+        if (part == 1)
+            return;
+#pragma unroll
+        for (int e = 0; e < V; e++)
+            dq[e / 16][e % 16] += x[e * 64];
+    }
     if (r < rows)
         store_row<D>(a.dq + (int64_t)row * a.lddq + head * D, dq, a.scale, lane);
 }
-
-constexpr int BWD_Q_WAVES = 8;
 
 int64_t blocks_of(int64_t n, int64_t per) { return (n + per - 1) / per; }
 
@@ -1090,12 +1108,23 @@ Form form_of(const AttnShape &s)
     return groups <= 256 || (groups <= 512 && s.max_k >= 2048) ? FOUR_TWICE : FOUR;
 }
 
-// Waves of 32 keys of the keys' gradients: four, or two where four would make fewer workgroups than there are CUs
-// (by the longest sequence, or by the rows there are).
+// Whether the queries' gradients take 128 rows a workgroup, every row's keys on two waves, instead of 256 (one CU each
+// either way): where that leaves no more than one and a half workgroups a CU, or two with many keys.  The whole gradient,
+// heads of 128: 1024 queries 83 -> 69 us, 4096 345 -> 306, 3 x 1024 94 -> 86; but 3 x 1500 155 -> 157, and packed
+// lengths of 1 to 1500 (472 workgroups, heads of 64) 104 -> 111.
+bool bwd_q_twice(const AttnShape &s)
+{
+    const int64_t groups = fwd_groups(s);
+    return groups <= 384 || (groups <= 512 && s.max_k >= 2048);
+}
+
+// Waves of 32 keys of the keys' gradients: four, or two where four would make fewer workgroups (one a CU) than go over
+// the CUs twice, by the longest sequence or by the rows there are.  The whole gradient with two and with four, heads of
+// 128: 1024 queries 69 and 89 us, 4096 252 and 305, 2 x 4096 (512 workgroups) 481 and 456, 8 x 1024 189 and 169.
 int bwd_k_waves(const AttnShape &s)
 {
     const int64_t longest = (int64_t)s.seqs * s.hk * blocks_of(s.max_k, 128), rows = s.hk * (s.tokens_k / 128 + s.seqs);
-    return (longest < rows ? longest : rows) < 256 ? 2 : 4;
+    return (longest < rows ? longest : rows) < 512 ? 2 : 4;
 }
 
 // Workgroups of the gradient's first pass: four heads' 32 rows each.
@@ -1124,7 +1153,7 @@ template <int D> hipError_t fwd(AttnFwd a, hipStream_t st)
     return hipGetLastError();
 }
 
-template <int D> hipError_t bwd(const AttnBwd &b, hipStream_t st)
+template <int D> hipError_t bwd(AttnBwd b, hipStream_t st)
 {
     const int64_t units = (int64_t)b.s.seqs * b.s.hk;
     hipError_t e = hipSuccess;
@@ -1139,8 +1168,10 @@ template <int D> hipError_t bwd(const AttnBwd &b, hipStream_t st)
         e = hipGetLastError();
     }
     if (e == hipSuccess && b.s.max_q > 0) {
-        hipLaunchKernelGGL((attn_bwd_q_kernel<D, BWD_Q_WAVES>), dim3((unsigned)(units * b.q_blocks)),
-                           dim3(64 * BWD_Q_WAVES), 0, st, b);
+        const bool twice = bwd_q_twice(b.s);
+        b.q_blocks = (int)blocks_of(rows_most(b.s), twice ? 128 : 256);
+        hipLaunchKernelGGL((twice ? attn_bwd_q_kernel<D, 4, 2> : attn_bwd_q_kernel<D, 8, 1>),
+                           dim3((unsigned)(units * b.q_blocks)), dim3(512), 0, st, b);
         e = hipGetLastError();
     }
     return e;
@@ -1156,7 +1187,7 @@ bool attn_fits(const AttnShape &s, bool backward)
     if (backward)
         return (double)bwd_row_groups(s) * 256 <= most &&
                units * (double)blocks_of(s.max_k, 64) * 512 <= most &&
-               units * (double)blocks_of(rows_most(s), 32 * BWD_Q_WAVES) * 64 * BWD_Q_WAVES <= most;
+               units * (double)blocks_of(rows_most(s), 128) * 512 <= most;
     const double groups = few_rows(s) ? units * 64 * ROW_WAVES : units * (double)blocks_of(rows_most(s), 128) * 512;
     return groups * splits_of(s) <= most && heads * s.max_q * (s.dim / 4) + 256 <= most;
 }
@@ -1181,7 +1212,6 @@ size_t attn_bwd_workspace_bytes(const AttnShape &s) { return 2 * pad256((size_t)
 hipError_t launch_attn_bwd(AttnBwd b, void *workspace, hipStream_t st)
 {
     b.c2 = b.scale * kLog2e;
-    b.q_blocks = (int)blocks_of(rows_most(b.s), 32 * BWD_Q_WAVES);
     b.nl = (float *)workspace;
     b.nd = (float *)((char *)workspace + attn_bwd_workspace_bytes(b.s) / 2);
     return b.s.dim == 64 ? bwd<64>(b, st) : bwd<128>(b, st);
