@@ -204,3 +204,19 @@ def test_a_row_of_nan_is_its_own(dev, n, m, dim):
     # the maximum is looked for again in the tiles of a wave with a NaN: P may round differently, twice B of sum P |v|
     assert bool(torch.isfinite(o1).all()) and bool(torch.isfinite(l1).all())
     assert float((o1.float() - o0.float()).abs().max()) <= 4 * ref.B * float(v.float().abs().max())
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("times", [2, 3, 6])
+def test_many_packed_rows(dev, times, causal, dim):
+    """About 240, 360 and 720 workgroups of 128 rows: every form of the forward's workgroups."""
+    lens = [300, 299, 257, 300, 129] * times
+    run(dev, 8, 8, dim, lens, lens, causal, seed=times, gap=2)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("q,k", [(1700, 1700), (200, 2049), (130, 4097), (2100, 2100)])
+def test_long_rows(dev, q, k, dim):
+    """Both sides of 2048 keys, from which on the keys are split over workgroups."""
+    run(dev, 2, 1, dim, [q], [k], True, seed=q)

@@ -151,3 +151,18 @@ def test_nan_is_not_hidden(dev, n, dim):
 def test_rows_that_see_few_keys(dev, q, k, causal, dim):
     """Both sides of the 32 keys where D's form changes, inside a wave's 32 rows and between them."""
     run(dev, 6, 2, dim, [q, 3, q], [k, k, 4], causal, seed=q + k)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("times", [2, 3, 6])
+def test_many_packed_rows(dev, times, causal, dim):
+    """About 240, 360 and 720 workgroups of 128 rows or keys: every form of both kernels' workgroups."""
+    lens = [300, 299, 257, 300, 129] * times
+    run(dev, 8, 8, dim, lens, lens, causal, seed=times, gap=2)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("q,k", [(1700, 1700), (130, 2049), (2100, 300)])
+def test_long_rows(dev, q, k, dim):
+    run(dev, 2, 1, dim, [q], [k], True, seed=q)

@@ -64,7 +64,7 @@ def test_a_sequence_past_4_gb(dev):
 @pytest.mark.parametrize("dim", [64, 128])
 @pytest.mark.parametrize("causal", [True, False])
 def test_backward_with_many_workgroups(dev, dim, causal):
-    """Enough blocks of 128 keys for the four-wave form of the keys' gradients."""
+    """More workgroups of 128 keys, and of 256 rows, than there are CUs."""
     bwd.run(dev, 64, 64, dim, [520], [520], causal, seed=3)
     bwd.run(dev, 33, 33, dim, [1100], [1037], causal, seed=4)
 
