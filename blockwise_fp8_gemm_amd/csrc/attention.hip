@@ -406,7 +406,10 @@ __device__ __forceinline__ void put_row(const AttnFwd &a, Softmax<D> &x, int spl
 }
 
 // Many rows: NW waves of 32 rows, a query of one head each, HV times; 64 keys (128 of narrow heads) at a time through
-// LDS.  The HV waves of the same rows take every HV-th tile, and their results meet at the end.
+// LDS.  The HV waves of the same rows take every HV-th tile, and their results meet at the end.  Bound by the matrix
+// cores and the exponentials, which hardly overlap: 2 x 4096 causal queries, 16 heads of 128, 137 GFLOP in 125 us (1.1
+// PFLOP/s), matrix cores busy 0.6 of the time, no bank conflicts, 82 MB fetched.  128 keys a tile with heads of 128 took
+// 177 us against 132, 64 keys with heads of 64 37 against 29.5 (packed lengths of 1 to 1500).
 template <int D, int NW, int HV>
 __global__ __launch_bounds__(64 * NW * HV, 2) void attn_fwd_kernel(AttnFwd a)
 {
@@ -526,7 +529,10 @@ __global__ __launch_bounds__(64 * NW * HV, 2) void attn_fwd_kernel(AttnFwd a)
 
 // Few rows (at most 32 of a key head's queries over all its query heads): a wave
 // holds them all and the workgroup's two waves take keys of their own, 32 at a
-// time through LDS of their own; their results are added up at the end.
+// time through LDS of their own; their results are added up at the end.  Bound by
+// reading the keys and values once: 16 sequences of 64 to 16384 keys, 500 MB in 101 us
+// (4.9 TB/s; a copy reaches 5.0).  Two waves a workgroup let every wave go on
+// without a barrier; four, without the heads changing places, took 123.5 us against 113.
 constexpr int ROW_WAVES = 2;
 template <int D>
 __global__ __launch_bounds__(64 * ROW_WAVES) void attn_rows_kernel(AttnFwd a)
@@ -642,7 +648,8 @@ __global__ __launch_bounds__(64 * ROW_WAVES) void attn_rows_kernel(AttnFwd a)
     }
 }
 
-// The splits' shares of a row and head: o = sum 2^(m_s - m) o_s / sum 2^(m_s - m) l_s.
+// The splits' shares of a row and head: o = sum 2^(m_s - m) o_s / sum 2^(m_s - m) l_s, eight shares' loads at a time
+// (8 shares of 16 rows of 16 heads: 4.5 us; one share after the other 8.1).
 template <int D>
 __global__ __launch_bounds__(256) void attn_join_kernel(AttnFwd a)
 {
@@ -655,17 +662,32 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnFwd a)
     if (i >= q.len)
         return;
     const int t = q.start + i;
+    constexpr int AT = 8;
     float m = kNoMax, sum = 0.0f;
-    for (int s = 0; s < a.splits; s++)
-        m = fmaxf(m, a.stat[part_row(a, s, head, t)].x);
     float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    for (int s = 0; s < a.splits; s++) {
-        const int64_t p = part_row(a, s, head, t);
-        const float2 st = a.stat[p];
-        const float f = __builtin_amdgcn_exp2f(st.x - m);
-        const float4 o = *reinterpret_cast<const float4 *>(a.part + p * D + d);
-        sum = fmaf(f, st.y, sum);
-        v = make_float4(fmaf(f, o.x, v.x), fmaf(f, o.y, v.y), fmaf(f, o.z, v.z), fmaf(f, o.w, v.w));
+    for (int s0 = 0; s0 < a.splits; s0 += AT) {
+        float2 st[AT];
+        float4 o[AT];
+#pragma unroll
+        for (int u = 0; u < AT; u++) {
+            const int64_t p = part_row(a, min(s0 + u, a.splits - 1), head, t);
+            st[u] = a.stat[p];
+            o[u] = *reinterpret_cast<const float4 *>(a.part + p * D + d);
+        }
+        float now = m;
+#pragma unroll
+        for (int u = 0; u < AT; u++)
+            now = fmaxf(now, st[u].x);
+        const float f = __builtin_amdgcn_exp2f(m - now);
+        m = now;
+        sum *= f;
+        v = make_float4(v.x * f, v.y * f, v.z * f, v.w * f);
+#pragma unroll
+        for (int u = 0; u < AT; u++) {
+            const float g = s0 + u < a.splits ? __builtin_amdgcn_exp2f(st[u].x - m) : 0.0f;
+            sum = fmaf(g, st[u].y, sum);
+            v = make_float4(fmaf(g, o[u].x, v.x), fmaf(g, o[u].y, v.y), fmaf(g, o[u].z, v.z), fmaf(g, o[u].w, v.w));
+        }
     }
     const float f = reciprocal(sum);
     *reinterpret_cast<uint2 *>(a.o + (int64_t)t * a.ldo + head * D + d) =
@@ -757,7 +779,10 @@ template <int D> __global__ __launch_bounds__(256) void attn_bwd_rows_kernel(Att
 
 // Keys' and values' gradients: NW waves of 32 keys, HV times.  QT queries of one head at a time go through LDS; the
 // HV waves of the same keys take every HV-th run of 32 of them, and their sums meet at the end.  Four waves of keys,
-// twice, read a tile least often; where that makes few workgroups it is two waves, four times (bwd_k_waves).
+// twice, read a tile least often; where that makes few workgroups it is two waves, four times (bwd_k_waves).  2 x 4096 causal queries, 16 heads of 128:
+// 255 to 285 us for four products (275 GFLOP, 1.0 PFLOP/s), matrix cores busy 0.55 of the time, waits 0.31 of the waves'.
+// Registers bound it: with K read from LDS and two waves a SIMD all 256 are in use, so that a third tile on its way or
+// the exponentials beside the products' next run found no room (472 against 456 us in all; 302 against 255 alone).
 template <int D, int NW, int HV>
 __global__ __launch_bounds__(64 * NW * HV) void attn_bwd_k_kernel(AttnBwd a)
 {
@@ -929,7 +954,9 @@ __global__ __launch_bounds__(64 * NW * HV) void attn_bwd_k_kernel(AttnBwd a)
 }
 
 // Queries' gradients: NW waves of 32 rows (as in the forward), HV times, 64 keys at a time through LDS, 32 in a step.
-// The two waves of the same rows take a half of every tile each, and their sums meet at the end.
+// The two waves of the same rows take a half of every tile each, and their sums meet at the end.  2 x 4096 causal
+// queries, 16 heads of 128: 185 to 210 us for three products (206 GFLOP, 1.05 PFLOP/s), matrix cores busy 0.57 of the
+// time.  Two barriers a tile with a SIMD's waves in turns, which helps the forward, took 211 us against 189.
 template <int D, int NW, int HV>
 __global__ __launch_bounds__(64 * NW * HV) void attn_bwd_q_kernel(AttnBwd a)
 {
@@ -1064,7 +1091,7 @@ int64_t blocks_of(int64_t n, int64_t per) { return (n + per - 1) / per; }
 // Rows of a key head: its queries of every query head.
 int64_t rows_most(const AttnShape &s) { return (int64_t)s.max_q * (s.hq / s.hk); }
 
-// Whether a key head's rows of every sequence fit one wave.
+// Whether a key head's rows of every sequence fit one wave.  Then there is less to compute than to read.
 bool few_rows(const AttnShape &s) { return rows_most(s) <= 32; }
 
 // Workgroups of 128 rows of the forward: by the longest sequence, or by the rows there are.
