@@ -1206,17 +1206,22 @@ template <int D> hipError_t bwd(AttnBwd b, hipStream_t st)
 
 } // namespace
 
+// Whether every launch stays below 2^32 threads.
 bool attn_fits(const AttnShape &s, bool backward)
 {
-    const double units = (double)s.seqs * s.hk, heads = (double)s.seqs * s.hq, most = 4294967295.0;
-    if (rows_most(s) > 1 << 30)
+    const double units = (double)s.seqs * s.hk, most = 4294967295.0;
+    if (rows_most(s) > 1 << 30 || units > most)
         return false;
+    auto threads = [&](int64_t blocks, int each) { return units * (double)blocks * each; };
     if (backward)
-        return (double)bwd_row_groups(s) * 256 <= most &&
-               units * (double)blocks_of(s.max_k, 64) * 512 <= most &&
-               units * (double)blocks_of(rows_most(s), 128) * 512 <= most;
-    const double groups = few_rows(s) ? units * 64 * ROW_WAVES : units * (double)blocks_of(rows_most(s), 128) * 512;
-    return groups * splits_of(s) <= most && heads * s.max_q * (s.dim / 4) + 256 <= most;
+        return (double)bwd_row_groups(s) * 256 <= most && threads(blocks_of(s.max_k, 32 * bwd_k_waves(s)), 512) <= most &&
+               threads(blocks_of(rows_most(s), bwd_q_twice(s) ? 128 : 256), 512) <= most;
+    const int splits = splits_of(s);
+    const double join = splits == 1 ? 0.0 : (double)s.seqs * s.hq * s.max_q * (s.dim / 4) + 256;
+    if (few_rows(s))
+        return threads(splits, 64 * ROW_WAVES) <= most && join <= most;
+    const Form form = form_of(s);
+    return threads(blocks_of(rows_most(s), form == EIGHT ? 256 : 128) * splits, form == FOUR ? 256 : 512) <= most && join <= most;
 }
 
 size_t attn_workspace_bytes(const AttnShape &s)

@@ -661,7 +661,9 @@ puro_status_t puro_fp8_qk_norm_rope_bwd_quant_dual_pow2(const puro_qk_norm_rope_
  * one call.
  *   heads_q      a multiple of heads_kv, at most PURO_MAX_HEADS
  *   head_dim     64 or 128
- *   sequences    0 or more
+ *   sequences    0 or more, such that no launch has 2^32 threads, else PURO_ERR_SHAPE: sequences x
+ *                heads_kv x ceil(n / 64) below 2^23 is enough, n the larger of max_k and
+ *                r = max_q heads_q / heads_kv.  r may not pass 2^30
  *   q_offsets    int32 device array: sequence s starts at row q_offsets[s] and has
  *                q_offsets[s + 1] - q_offsets[s] rows, or q_lengths[s] when
  *                q_lengths is not NULL (q_offsets then needs no last entry):

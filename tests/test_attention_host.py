@@ -101,7 +101,25 @@ ATTN_BAD = [(dict(heads_q=0), SHAPE), (dict(heads_kv=0), SHAPE), (dict(heads_q=5
             (dict(scale=float("inf")), VALUE), (dict(scale=2.0 ** -65), VALUE), (dict(scale=2.0 ** 65), VALUE),
             # more work items than a grid has
             (dict(sequences=2 ** 31 - 1, tokens_q=2 ** 23, tokens_k=2 ** 23, max_q=2 ** 23, max_k=2 ** 23), SHAPE),
-            (dict(heads_q=1024, heads_kv=1, tokens_q=2 ** 23, max_q=2 ** 23), SHAPE)]
+            (dict(heads_q=1024, heads_kv=1, tokens_q=2 ** 23, max_q=2 ** 23), SHAPE),
+            (dict(sequences=2 ** 31 - 1, max_q=1, max_k=1), SHAPE)]
+
+# the most that is promised: sequences x heads_kv x ceil(n / 64) just below 2^23
+ATTN_MANY = [dict(sequences=2 ** 14 - 1, heads_q=8, heads_kv=8, max_q=4096), dict(sequences=2 ** 14 - 1, heads_q=1, heads_kv=1, max_q=2 ** 15),
+             dict(sequences=2 ** 22 - 1, heads_q=4, heads_kv=2, max_q=1), dict(sequences=2 ** 14 - 1, heads_q=64, heads_kv=8, max_q=512),
+             dict(sequences=1, heads_q=127, heads_kv=127, max_q=2 ** 22), dict(sequences=2 ** 21 - 1, heads_q=20, heads_kv=4, max_q=12),
+             dict(sequences=1, heads_q=128, heads_kv=1, max_q=2 ** 22), dict(sequences=63, heads_q=1, heads_kv=1, max_q=2 ** 23)]
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("tokens", [2 ** 23, 1 << 16])
+@pytest.mark.parametrize("fields", ATTN_MANY)
+def test_attention_sizes_that_are_promised(fields, tokens, dim):
+    for max_k in (64, 64 * (fields["max_q"] * (fields["heads_q"] // fields["heads_kv"]) // 64)):
+        shape = attn(tokens_q=tokens, tokens_k=tokens, head_dim=dim, **dict(fields, max_k=min(max_k, 2 ** 23)))
+        assert pf.lib().puro_fp8_attention_bwd_workspace_size(shape) > 0
+        # one that fits is told from one that does not by the check that comes next
+        assert _fwd(shape, ldq=2 ** 22, ldk=2 ** 22, ldv=2 ** 22, ldo=2 ** 22, lse=TWO) == ALIGN
 
 
 def _fwd(shape=None, q=P, ldq=256, k=P, ldk=128, v=P, ldv=128, o=P, ldo=256, lse=P, ws=NUL, n=0):

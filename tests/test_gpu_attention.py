@@ -9,8 +9,9 @@ import attn_ref as ref
 pytestmark = pytest.mark.gpu
 
 
-def run(dev, hq, hk, dim, q_lens, k_lens, causal, seed=0, scale=None, pad=0, std=1.0, gap=0):
-    """One call on packed sequences (gap: unused rows behind each); o and lse start as NaN."""
+def run(dev, hq, hk, dim, q_lens, k_lens, causal, seed=0, scale=None, pad=0, std=1.0, gap=0, loose=0):
+    """One call on packed sequences (gap: unused rows behind each; loose: how far the maxima lie above the longest);
+    o and lse start as NaN."""
     gen = torch.Generator().manual_seed(seed)
     qo, ko = [sum(q_lens[:i]) + gap * i for i in range(len(q_lens) + 1)], [sum(k_lens[:i]) + gap * i for i in range(len(k_lens) + 1)]
     q = ref.bf16(gen, qo[-1], hq * dim, std, pad, dev)
@@ -24,7 +25,8 @@ def run(dev, hq, hk, dim, q_lens, k_lens, causal, seed=0, scale=None, pad=0, std
     o = torch.full((qo[-1], (hq * dim + 15) // 16 * 16 + pad), float("nan"), dtype=torch.bfloat16, device=dev)[:, :hq * dim]
     lse = torch.full((hq, qo[-1]), float("nan"), device=dev)
     kw = {"q_lengths": ref.i32(q_lens, dev), "k_lengths": ref.i32(k_lens, dev)} if gap else {}
-    got = pf.puro_fp8_attention(q, k, v, dim, ref.i32(qo, dev), ref.i32(ko, dev), max(q_lens), max(k_lens), causal=causal,
+    got = pf.puro_fp8_attention(q, k, v, dim, ref.i32(qo, dev), ref.i32(ko, dev), max(q_lens) + loose,
+                                max(k_lens) + loose, causal=causal,
                                 scale=scale, o=o, lse=lse, **kw)
     torch.cuda.synchronize()
     assert got[0].data_ptr() == o.data_ptr() and got[1].data_ptr() == lse.data_ptr()

@@ -8,7 +8,7 @@ import attn_ref as ref
 pytestmark = pytest.mark.gpu
 
 
-def case(dev, hq, hk, dim, q_lens, k_lens, causal, seed=0, scale=None, pad=0, std=1.0, gap=0):
+def case(dev, hq, hk, dim, q_lens, k_lens, causal, seed=0, scale=None, pad=0, std=1.0, gap=0, loose=0):
     gen = torch.Generator().manual_seed(seed)
     scale = scale or dim ** -0.5
     qo, ko = [sum(q_lens[:i]) + gap * i for i in range(len(q_lens) + 1)], [sum(k_lens[:i]) + gap * i for i in range(len(k_lens) + 1)]
@@ -24,7 +24,8 @@ def case(dev, hq, hk, dim, q_lens, k_lens, causal, seed=0, scale=None, pad=0, st
                 t[s.stop:end] = float("nan")
     kw = {"q_lengths": ref.i32(q_lens, dev), "k_lengths": ref.i32(k_lens, dev)} if gap else {}
     kw |= {"causal": causal, "scale": scale}
-    return (do, q, k, v, o, lse, dim, ref.i32(qo, dev), ref.i32(ko, dev), max(q_lens), max(k_lens)), kw, qs, ks
+    return (do, q, k, v, o, lse, dim, ref.i32(qo, dev), ref.i32(ko, dev), max(q_lens) + loose,
+            max(k_lens) + loose), kw, qs, ks
 
 
 def nan_like(t, pad=0):

@@ -106,3 +106,10 @@ def test_rope_rows_past_4_gb(dev):
     want = torch.cat([p[0].flatten(1) for p in parts] + [ref.f64(few[2])], 1)
     tol = torch.cat([p[1].flatten(1) for p in parts] + [torch.zeros((200, dim), dtype=torch.float64)], 1)
     check_blocks(want, tol, qr[at], sr[at], "codes")
+
+
+def test_many_sequences_with_loose_maxima(dev):
+    """Maxima far above the lengths: most workgroups find nothing to do."""
+    lens = [(7 * i) % 90 for i in range(320)]
+    fwd.run(dev, 8, 4, 128, lens, lens, True, seed=9, gap=180, loose=1 << 16)
+    bwd.run(dev, 8, 4, 128, lens, lens, True, seed=9, gap=180, loose=1 << 16)
