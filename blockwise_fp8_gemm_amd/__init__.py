@@ -536,10 +536,15 @@ def _dense(t, shape, dtypes, name, device):
 def _workspace(workspace, need, device):
     """(tensor, address, bytes) of the caller's checked workspace, or of a new one of need() bytes."""
     if workspace is None:
-        workspace = torch.empty((need(),), dtype=_U8, device=device)
+        workspace = _empty(1, need(), _U8, device)
     elif not workspace.is_cuda or workspace.device != device or not workspace.is_contiguous():
         raise ValueError("workspace: expected a contiguous tensor on %s, got one on %s" % (device, workspace.device))
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def _empty(rows, cols, dtype, device):
+    """Uninitialised dense [rows][cols] (torch.empty takes 1.6 us on the host, this 1.3)."""
+    return torch.empty_strided((rows, cols), (cols, 1), dtype=dtype, device=device)
 
 
 def _new(rows, cols, dtype, device):
@@ -563,7 +568,7 @@ def _codes(tokens, cols, device, q, s, tok=False, transpose_out=True):
     else:
         qp, ld = _mat(q, qs, _U8, "q_tok" if tok else "q", device)
     if s is None:
-        s = torch.empty(ss, dtype=_F32, device=device)
+        s = _empty(*ss, _F32, device)
         return q, s, qp, ld, s.data_ptr()
     return q, s, qp, ld, _dense(s, ss, (_F32,), "s_tok" if tok else "s", device)
 
@@ -802,7 +807,7 @@ def puro_fp8_qk_norm_rope(q, k, head_dim, positions=None, inv_freq=None, q_weigh
     if q_weight is None or not (store_rstd or rstd is not None):
         rstd = None
     elif rstd is None:
-        rstd = torch.empty((tokens, r.heads_q + r.heads_kv), dtype=_F32, device=dev)
+        rstd = _empty(tokens, r.heads_q + r.heads_kv, _F32, dev)
         rp = rstd.data_ptr()
     else:
         rp = _dense(rstd, (tokens, r.heads_q + r.heads_kv), _F32S, "rstd", dev)
@@ -898,7 +903,7 @@ def puro_fp8_attention(q, k, v, head_dim, q_offsets, k_offsets, max_q, max_k, q_
     else:
         op, ldo = _mat(o, q.shape, _BF16, "o", dev)
     if lse is None:
-        lse = torch.empty((a.heads_q, a.tokens_q), dtype=_F32, device=dev)
+        lse = _empty(a.heads_q, a.tokens_q, _F32, dev)
         lp = lse.data_ptr()
     else:
         lp = _dense(lse, (a.heads_q, a.tokens_q), (_F32,), "lse", dev)
