@@ -779,14 +779,15 @@ template <int D> __global__ __launch_bounds__(256) void attn_bwd_rows_kernel(Att
 
 // Keys' and values' gradients: NW waves of 32 keys, HV times.  QT queries of one head at a time go through LDS; the
 // HV waves of the same keys take every HV-th run of 32 of them, and their sums meet at the end.  Four waves of keys,
-// twice, read a tile least often; where that makes few workgroups it is two waves, four times (bwd_k_waves).  2 x 4096 causal queries, 16 heads of 128:
+// twice, read a tile least often; where that makes few workgroups it is two waves, four times, or one, eight times
+// (bwd_k_waves).  2 x 4096 causal queries, 16 heads of 128:
 // 255 to 285 us for four products (275 GFLOP, 1.0 PFLOP/s), matrix cores busy 0.55 of the time, waits 0.31 of the waves'.
 // Registers bound it: with K read from LDS and two waves a SIMD all 256 are in use, so that a third tile on its way or
 // the exponentials beside the products' next run found no room (472 against 456 us in all; 302 against 255 alone).
 template <int D, int NW, int HV>
 __global__ __launch_bounds__(64 * NW * HV) void attn_bwd_k_kernel(AttnBwd a)
 {
-    constexpr int A1 = 4, A2 = 4, R = 32 * NW, QT = HV == 4 ? 128 : 8192 / D, TILE = Tile<D>::bytes(QT), STAGE = 2 * TILE + 2 * QT * 4, B = D / 32;
+    constexpr int A1 = 4, A2 = 4, R = 32 * NW, QT = HV == 8 ? 256 : HV == 4 ? 128 : 8192 / D, TILE = Tile<D>::bytes(QT), STAGE = 2 * TILE + 2 * QT * 4, B = D / 32;
     static_assert(2 * STAGE >= HV / 2 * NW * 16 * B * 256, "half of one of the sums takes the tiles' place");
     __shared__ __attribute__((aligned(16))) uint8_t lds[2][STAGE], lds_k[Tile<D>::bytes(R)];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -824,8 +825,10 @@ __global__ __launch_bounds__(64 * NW * HV) void attn_bwd_k_kernel(AttnBwd a)
     const int w0 = k0 + 32 * kw, j = w0 + (lane & 31), row = k.start + min(j, k.len - 1);
     // the values' operand stays in registers; the keys' is read from LDS again, which leaves registers for the reads
     // ahead
-    const typename Tile<D>::template Stage<R, HV * NW> copy_k(a.ldk, wave, lane);
-    copy_k(lds_k, a.k + (int64_t)(k.start + k0) * a.ldk + kh * D, k.len - 1 - k0, wave);
+    constexpr int KW = R / Tile<D>::PIECE < HV * NW ? R / Tile<D>::PIECE : HV * NW;   // waves that copy K
+    const typename Tile<D>::template Stage<R, KW> copy_k(a.ldk, wave, lane);
+    if (wave < KW)
+        copy_k(lds_k, a.k + (int64_t)(k.start + k0) * a.ldk + kh * D, k.len - 1 - k0, wave);
     v8bf vf[D / 16];
     Tile<D>::load(a.v + (int64_t)row * a.ldv + kh * D, lane, vf);
     pin(vf);
@@ -1148,10 +1151,14 @@ bool bwd_q_twice(const AttnShape &s)
 // Waves of 32 keys of the keys' gradients: four, or two where four would make fewer workgroups (one a CU) than go over
 // the CUs twice, by the longest sequence or by the rows there are.  The whole gradient with two and with four, heads of
 // 128: 1024 queries 69 and 89 us, 4096 252 and 305, 2 x 4096 (512 workgroups) 481 and 456, 8 x 1024 189 and 169.
+// One, eight times, where heads of 64 leave LDS for 256 queries a tile and it makes no more than two workgroups a CU: 12
+// heads on 4 of 64, one and two: 1024 queries 43 and 52 us, 4096 133 and 157, 8192 445 and 409 (16 on 8: 3 x 1024 62
+// and 53).
 int bwd_k_waves(const AttnShape &s)
 {
     const int64_t longest = (int64_t)s.seqs * s.hk * blocks_of(s.max_k, 128), rows = s.hk * (s.tokens_k / 128 + s.seqs);
-    return (longest < rows ? longest : rows) < 512 ? 2 : 4;
+    const int64_t groups = longest < rows ? longest : rows;
+    return groups >= 512 ? 4 : s.dim == 64 && groups <= 128 && longest < 1 << 20 ? 1 : 2;
 }
 
 // Workgroups of the gradient's first pass: four heads' 32 rows each.
@@ -1190,7 +1197,10 @@ template <int D> hipError_t bwd(AttnBwd b, hipStream_t st)
     }
     if (e == hipSuccess && b.s.max_k > 0) {
         const int waves = bwd_k_waves(b.s);
-        hipLaunchKernelGGL((waves == 4 ? attn_bwd_k_kernel<D, 4, 2> : attn_bwd_k_kernel<D, 2, 4>),
+        auto *kernel = waves == 4 ? attn_bwd_k_kernel<D, 4, 2> : attn_bwd_k_kernel<D, 2, 4>;
+        if constexpr (D == 64)
+            kernel = waves == 1 ? attn_bwd_k_kernel<D, 1, 8> : kernel;
+        hipLaunchKernelGGL(kernel,
                            dim3((unsigned)(units * blocks_of(b.s.max_k, 32 * waves))), dim3(512), 0, st, b);
         e = hipGetLastError();
     }
