@@ -716,7 +716,10 @@ template <int D> __global__ __launch_bounds__(256) void attn_bwd_rows_kernel(Att
     using Lds = Tile<D>;
     constexpr int L = D / 8, R = 64 / L;   // lanes of a row, rows of a load
     const int lane = threadIdx.x & 63, wave = uniform((int)threadIdx.x >> 6);
-    const int heads = (a.s.hq + 3) / 4, seq = uniform((int)blockIdx.x % a.s.seqs), block = uniform((int)blockIdx.x / a.s.seqs);
+    // sequences first, then heads, then rows; the grid's second dimension keeps the first one's threads below 2^32 where
+    // sequences and query heads are many
+    const unsigned at_grid = blockIdx.y * gridDim.x + blockIdx.x, seqs = (unsigned)a.s.seqs;
+    const int heads = (int)gridDim.y, seq = uniform((int)(at_grid % seqs)), block = uniform((int)(at_grid / seqs));
     const int head = block % heads * 4 + wave, i0 = block / heads * 32;
     const Rows q = uniform(q_rows(a.s, seq)), k = uniform(k_rows(a.s, seq));
     if (head >= a.s.hq || i0 >= q.len)
@@ -1161,8 +1164,8 @@ int bwd_k_waves(const AttnShape &s)
     return groups >= 512 ? 4 : s.dim == 64 && groups <= 128 && longest < 1 << 20 ? 1 : 2;
 }
 
-// Workgroups of the gradient's first pass: four heads' 32 rows each.
-int64_t bwd_row_groups(const AttnShape &s) { return s.seqs * blocks_of(s.max_q, 32) * blocks_of(s.hq, 4); }
+// Workgroups of the gradient's first pass for four heads, of 32 rows each.
+int64_t bwd_row_groups(const AttnShape &s) { return s.seqs * blocks_of(s.max_q, 32); }
 
 size_t pad256(size_t n) { return (n + 255) / 256 * 256; }
 
@@ -1192,7 +1195,8 @@ template <int D> hipError_t bwd(AttnBwd b, hipStream_t st)
     const int64_t units = (int64_t)b.s.seqs * b.s.hk;
     hipError_t e = hipSuccess;
     if (b.s.max_q > 0) {
-        hipLaunchKernelGGL((attn_bwd_rows_kernel<D>), dim3((unsigned)bwd_row_groups(b.s)), dim3(256), 0, st, b);
+        hipLaunchKernelGGL((attn_bwd_rows_kernel<D>), dim3((unsigned)bwd_row_groups(b.s), (unsigned)blocks_of(b.s.hq, 4)),
+                           dim3(256), 0, st, b);
         e = hipGetLastError();
     }
     if (e == hipSuccess && b.s.max_k > 0) {
@@ -1216,7 +1220,7 @@ template <int D> hipError_t bwd(AttnBwd b, hipStream_t st)
 
 } // namespace
 
-// Whether every launch stays below 2^32 threads.
+// Whether every launch stays below 2^32 threads along the grid's first dimension.
 bool attn_fits(const AttnShape &s, bool backward)
 {
     const double units = (double)s.seqs * s.hk, most = 4294967295.0;
