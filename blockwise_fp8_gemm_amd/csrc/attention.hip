@@ -258,8 +258,9 @@ template <int D> __device__ __forceinline__ void store_row(uint16_t *row, const 
 // Forward.  Running state of 32 queries of a wave (one per lane and half):
 // maximum m in log2 units, this half's share of the sum, the transposed output.
 // The maximum only moves, and sum and output are only rescaled, when a score
-// passes it by more than 8 (2^8): P stays below 2^8 and keeps its relative
-// precision, and most tiles need no rescaling.
+// passes it by more than 8 (2^8), or with heads of 128 when the sum of a lane's
+// scores of a tile does: P stays below 2^8 and keeps its relative precision, and
+// most tiles need no rescaling.
 // ---------------------------------------------------------------------------
 template <int D> struct Softmax {
     float m = kNoMax, l = 0.0f;
@@ -322,8 +323,8 @@ template <int D> struct Softmax {
         return sum;
     }
 
-    // The running maximum up to the scores, where one lies more than 2^8 above it.
-    template <int N> __device__ __forceinline__ void raise(const v16f (&s)[N], float c2)
+    // The running maximum up to the scores, where one lies more than 2^SLACK above it.
+    template <int N, int SLACK> __device__ __forceinline__ void raise(const v16f (&s)[N], float c2)
     {
         float top = s[0][0];
 #pragma unroll
@@ -332,7 +333,7 @@ template <int D> struct Softmax {
             for (int i = 0; i < 16; i++)
                 top = fmaxf(top, s[n][i]);
         top = fmaxf(top, other_half(top)) * c2;
-        if (__any(top > m + 8.0f)) {
+        if (__any(top > m + (float)SLACK)) {
             const float now = fmaxf(m, top), f = __builtin_amdgcn_exp2f(m - now);
             m = now;
             l *= f;
@@ -344,8 +345,10 @@ template <int D> struct Softmax {
 
     // P of the blocks, and their share of the sum.  first: the blocks' first key; start: that of all of them; lim: the
     // lane's last visible key; masked: whether some key of the blocks may be hidden.  With heads of 128 the maximum is
-    // looked for only among the first keys and where P's sum shows that a score has left it behind (2 x 4096 causal
-    // 125 us, and 127.5 with a search in every tile; heads of 64: 82 and 80.5).
+    // looked for only among the first keys and where P's sum shows that scores have left it behind (2 x 4096 causal
+    // 125 us, and 127.5 with a search in every tile; heads of 64: 82 and 80.5).  It then goes up to the highest of them, so
+    // that a sum is at most the number of its keys again: with 2^8 left between them, many scores a little below that
+    // would have every later tile searched and formed twice.
     template <int N>
     __device__ __forceinline__ void weigh(v16f (&s)[N], v8bf (&p)[2 * N], float c2, int first, int start, int lim, bool masked,
                                           int lane)
@@ -360,8 +363,8 @@ template <int D> struct Softmax {
         float sum = INFINITY;
         if (D == 128 && first != start)
             sum = exponentials<N>(s, p, c2);
-        if (D != 128 || __any(!(sum <= 1024.0f))) {
-            raise<N>(s, c2);
+        if (D != 128 || __any(!(sum <= 256.0f))) {
+            raise<N, D == 128 ? 0 : 8>(s, c2);
             sum = exponentials<N>(s, p, c2);
         }
         l += sum;
