@@ -4,7 +4,7 @@
 //   dP = do v^T,  dS = P (dP - D),  D = sum over the head of do o
 //   dv = P^T do,  dq = c dS k,  dk = c dS^T q
 //
-// Query i of n sees keys 0 .. m - 1, or 0 .. i + m - n with a causal mask.
+// Query i of n sees keys 0 .. m - 1, or those of them up to i + m - n with a causal mask.
 // Products run on the BF16 matrix cores (32x32x16) with FP32 accumulation.
 // Every operand tile is a [rows][D] run of BF16 rows in LDS, copied there
 // straight from memory, and read in two ways: rows (a lane takes 8 consecutive
@@ -225,22 +225,29 @@ __device__ __forceinline__ float other_half(float x)
 // A value that is the same in every lane, in a scalar register.
 __device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
 
-// A sequence's rows, held inside the tensor and the announced maximum whatever the arrays say.
+// A sequence's rows, held inside the tensor and the announced maximum whatever the arrays say, and how many the arrays
+// give it (up to 2^30).
 struct Rows {
-    int start, len;
+    int start, len, whole;
 };
 __device__ __forceinline__ Rows rows_of(const int32_t *off, const int32_t *len, int s, int64_t tokens, int most)
 {
     const int64_t total = tokens, a = off[s];
     const int64_t start = a < 0 ? 0 : a > total ? total : a;
     int64_t n = len ? (int64_t)len[s] : (int64_t)off[s + 1] - a;
+    n = n < 0 ? 0 : n < 1 << 30 ? n : 1 << 30;
+    const int whole = (int)n;
     n = n < total - start ? n : total - start;
     n = n < most ? n : most;
-    return Rows{(int)start, (int)(n < 0 ? 0 : n)};
+    return Rows{(int)start, (int)n, whole};
 }
-__device__ __forceinline__ Rows uniform(const Rows &r) { return Rows{uniform(r.start), uniform(r.len)}; }
+__device__ __forceinline__ Rows uniform(const Rows &r) { return Rows{uniform(r.start), uniform(r.len), uniform(r.whole)}; }
 __device__ __forceinline__ Rows q_rows(const AttnShape &a, int s) { return rows_of(a.q_off, a.q_len, s, a.tokens_q, a.max_q); }
 __device__ __forceinline__ Rows k_rows(const AttnShape &a, int s) { return rows_of(a.k_off, a.k_len, s, a.tokens_k, a.max_k); }
+
+// Causal: query i sees the keys up to i + shift.  By the whole sequences, so that rows that are kept see no other keys
+// when rows behind them are left out.
+__device__ __forceinline__ int shift_of(const Rows &q, const Rows &k) { return k.whole - q.whole; }
 
 // A lane's 4 D / 32 runs of four values of one row (acc_row's order), times f, as BF16.
 template <int D> __device__ __forceinline__ void store_row(uint16_t *row, const v16f (&acc)[D / 32], float f, int lane)
@@ -430,7 +437,7 @@ __global__ __launch_bounds__(64 * NW * HV, 2) void attn_fwd_kernel(AttnFwd a)
     const int rows = q.len * group;   // (query, head) pairs, a query's heads side by side
     if (r0 >= rows)
         return;
-    const int shift = k.len - q.len, last = uniform((min(r0 + R, rows) - 1) / group);
+    const int shift = shift_of(q, k), last = uniform((min(r0 + R, rows) - 1) / group);
     const int seen = a.s.causal ? max(0, min(k.len, last + 1 + shift)) : k.len;
     const int tiles = (seen + KT - 1) / KT, t0 = share(tiles, split, a.splits), t1 = share(tiles, split + 1, a.splits);
     const int rounds = (t1 - t0 + HV - 1) / HV;
@@ -553,7 +560,7 @@ __global__ __launch_bounds__(64 * ROW_WAVES) void attn_rows_kernel(AttnFwd a)
     const int cols = q.len * group;
     if (cols == 0)
         return;
-    const int shift = k.len - q.len, seen = k.len;
+    const int shift = shift_of(q, k), seen = k.len;
     const int tiles = (seen + KW - 1) / KW, parts = a.splits * NW, part = split * NW + wave;
     const int t0 = share(tiles, part, parts), t1 = share(tiles, part + 1, parts);
 
@@ -728,8 +735,9 @@ template <int D> __global__ __launch_bounds__(256) void attn_bwd_rows_kernel(Att
     if (head >= a.s.hq || i0 >= q.len)
         return;
     // Rows few .. most - 1 see 1 to FEW keys.
-    const int shift = k.len - q.len;
-    const int few = a.s.causal ? max(0, -shift) : 0, most = a.s.causal ? min(q.len, FEW - shift) : k.len > FEW ? 0 : q.len;
+    const int shift = shift_of(q, k);
+    const int few = a.s.causal ? max(0, -shift) : 0;
+    const int most = k.len <= FEW ? q.len : a.s.causal ? min(q.len, FEW - shift) : 0;
     const int own = min(i0 + (lane & 31), q.len - 1);
     const int64_t at = (int64_t)head * a.s.tokens_q + q.start;
     const float lse = a.lse[at + own];
@@ -805,7 +813,7 @@ __global__ __launch_bounds__(64 * NW * HV) void attn_bwd_k_kernel(AttnBwd a)
     const int k0 = block * R;
     if (k0 >= k.len)
         return;
-    const int shift = k.len - q.len, tiles = (q.len + QT - 1) / QT;
+    const int shift = shift_of(q, k), tiles = (q.len + QT - 1) / QT;
     const int t0 = a.s.causal ? min(tiles, max(0, k0 - shift) / QT) : 0, steps = (tiles - t0) * group;
 
     const typename Tile<D>::template Stage<QT, HV * NW> copy_q(a.ldq, wave, lane), copy_d(a.lddo, wave, lane);
@@ -982,7 +990,7 @@ __global__ __launch_bounds__(64 * NW * HV) void attn_bwd_q_kernel(AttnBwd a)
     const int rows = q.len * group;   // (query, head) pairs, a query's heads side by side
     if (r0 >= rows)
         return;
-    const int shift = k.len - q.len, last = uniform((min(r0 + R, rows) - 1) / group);
+    const int shift = shift_of(q, k), last = uniform((min(r0 + R, rows) - 1) / group);
     const int seen = a.s.causal ? max(0, min(k.len, last + 1 + shift)) : k.len;
     const int tiles = (seen + KT - 1) / KT;
 

@@ -672,7 +672,9 @@ puro_status_t puro_fp8_qk_norm_rope_bwd_quant_dual_pow2(const puro_qk_norm_rope_
  *   tokens_q, tokens_k   rows of q and o, and of k and v
  *   max_q, max_k the most rows of one sequence.  Rows past a maximum or past the
  *                tensor are left out, so the arrays may change between replays
- *                of a captured call.  Smaller maxima cost less.
+ *                of a captured call.  n and m of the causal mask are the arrays'
+ *                own: rows that are kept see no other keys for those left out.
+ *                Smaller maxima cost less.
  *   scale        2^-64 .. 2^64, else PURO_ERR_VALUE
  * shape is a HOST structure, read before the call returns.  q BF16 [tokens_q]
  * [heads_q head_dim], k and v BF16 [tokens_k][heads_kv head_dim], o as q; row
