@@ -225,15 +225,15 @@ __device__ __forceinline__ float other_half(float x)
 // A value that is the same in every lane, in a scalar register.
 __device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
 
-// A sequence's rows, held inside the tensor and the announced maximum whatever the arrays say, and how many the arrays
-// give it (up to 2^30).
+// A sequence's rows, held inside the tensor and the announced maximum whatever the arrays say (none where it starts before
+// row 0), and how many the arrays give it (up to 2^30).
 struct Rows {
     int start, len, whole;
 };
 __device__ __forceinline__ Rows rows_of(const int32_t *off, const int32_t *len, int s, int64_t tokens, int most)
 {
     const int64_t total = tokens, a = off[s];
-    const int64_t start = a < 0 ? 0 : a > total ? total : a;
+    const int64_t start = a < 0 || a > total ? total : a;
     int64_t n = len ? (int64_t)len[s] : (int64_t)off[s + 1] - a;
     n = n < 0 ? 0 : n < 1 << 30 ? n : 1 << 30;
     const int whole = (int)n;

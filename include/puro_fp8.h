@@ -668,7 +668,9 @@ puro_status_t puro_fp8_qk_norm_rope_bwd_quant_dual_pow2(const puro_qk_norm_rope_
  *                q_offsets[s + 1] - q_offsets[s] rows, or q_lengths[s] when
  *                q_lengths is not NULL (q_offsets then needs no last entry):
  *                packed rows, or the used part of padded ones.  k_offsets and
- *                k_lengths the same for keys and values.
+ *                k_lengths the same for keys and values.  A sequence that starts
+ *                before row 0 or past the last row, or of a negative number of
+ *                rows, has none.
  *   tokens_q, tokens_k   rows of q and o, and of k and v
  *   max_q, max_k the most rows of one sequence.  Rows past a maximum or past the
  *                tensor are left out, so the arrays may change between replays
