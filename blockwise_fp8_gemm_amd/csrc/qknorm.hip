@@ -175,7 +175,9 @@ __device__ __forceinline__ void rope_bwd_tile(const RopeBwd &b, const P &p, cons
     const bool in = FULL || c0 < p.cols;
     const int h = in ? (int)(c0 / D) : 0, d0 = (int)(c0 % D), up = p.col(4) - p.col(0);   // the second run's distance
     // whether the tile has query or key heads at all (the same in every lane), and this thread's columns are of one
-    const bool heads = p.col0 < (int64_t)H * D, own = h < H, norm = heads && b.r.wq, rot = own && (MODE == PAIRS || d0 < R);
+    const bool heads = p.col0 < (int64_t)H * D, own = h < H, norm = heads && b.r.wq;
+    // whether these columns are turned, in a tile that has heads; one of 128-wide heads is one head
+    const bool rot = (D == 128 && MODE == PAIRS) || (own && (MODE == PAIRS || d0 < R));
     const uint16_t *dy = h < b.r.hq ? b.dq + h * D : own ? b.dk + (h - b.r.hq) * D : b.dv + (h - H) * D;
     const int64_t lddy = h < b.r.hq ? b.lddq : own ? b.lddk : b.lddv;
     const uint16_t *x = h < b.r.hq ? b.r.q + h * D : own ? b.r.k + (h - b.r.hq) * D : dy;   // not used for values
@@ -240,17 +242,17 @@ __device__ __forceinline__ void rope_bwd_tile(const RopeBwd &b, const P &p, cons
 #pragma unroll
             for (int j = 0; j < TURNS; j++)
 #pragma unroll
-                for (int e = 0; e < 2; e++) {   // rotation 2 j + e of the thread's
+                for (int e = 0; e < 2; e++) {   // rotation 2 j + e of the thread's; what is not turned keeps its bits
                     const float4 c = turn[i][j];
-                    const float cs = rot ? e ? c.z : c.x : 1.0f, sn = rot ? e ? c.w : c.y : 0.0f;
+                    const float cs = e ? c.z : c.x, sn = e ? c.w : c.y;
                     const int n = 2 * j + e;
                     if constexpr (MODE == APART) {
-                        g[n] = fmaf(g[n], cs, low ? o[n] * sn : -(o[n] * sn));
+                        g[n] = rot ? fmaf(g[n], cs, low ? o[n] * sn : -(o[n] * sn)) : g[n];
                     } else {
                         const int m0 = MODE == INTER ? 2 * n : n, m1 = MODE == INTER ? 2 * n + 1 : n + 4;
                         const float u = g[m0], y = g[m1];
-                        g[m0] = fmaf(u, cs, y * sn);
-                        g[m1] = fmaf(y, cs, -(u * sn));
+                        g[m0] = rot ? fmaf(u, cs, y * sn) : u;
+                        g[m1] = rot ? fmaf(y, cs, -(u * sn)) : y;
                     }
                 }
         }
