@@ -716,10 +716,13 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnFwd a)
 // depend on the order workgroups run in.
 // ---------------------------------------------------------------------------
 // A wave takes 32 rows of one head.  D is sum P dP, and do o the same number with o's rounding to BF16 in it (half a
-// step, 2^-8 of each term at most).  Rows that see many keys do not notice; where few keys share the weight it would
-// double dq's and dk's error, so that rows that see at most FEW keys form the sum itself, from one tile of S and dP
-// (lanes that walk over such a row's keys cost 8 us more at 2 x 4096 queries).  The rest is one read of o and do: 18 us
-// for the 67 MB of 2 x 4096 queries, 16 heads of 128 (3.7 TB/s; a pass without the tile took 17).
+// step, 2^-8 of each term at most).  Where the weight is spread over many keys dq and dk do not notice (300 rows of
+// normal q and k: 2.3e-3 off); where few keys share it, dP and D nearly cancel, and it is most of their error.  Rows that
+// see at most FEW keys form the sum itself, from one tile of S and dP (lanes that walk over such a row's keys cost 8 us
+// more at 2 x 4096 queries).  Longer rows keep it, also when their weight lies on a few keys: with q and k three and six
+// times as large dq and dk are 4.4e-3 to 1.2e-2 off.  The sum itself would need every score once more here.  The rest is
+// one read of o and do: 18 us for the 67 MB of 2 x 4096 queries, 16 heads of 128 (3.7 TB/s; a pass without the tile took
+// 17).
 constexpr int FEW = 32;
 template <int D> __global__ __launch_bounds__(256) void attn_bwd_rows_kernel(AttnBwd a)
 {

@@ -712,6 +712,8 @@ puro_status_t puro_fp8_attention(const puro_attention_t *shape, const void *q, i
  * D_i = dout_i . o_i (for rows that see at most 32 keys sum_j P dP, the same
  * number without o's rounding in it):
  *     dS = P (dP - D),  dv = P^T dout,  dq = scale dS k,  dk = scale dS^T q
+ * (in longer rows whose weight lies on a few keys, where dP and D nearly cancel,
+ * that rounding, 2^-8 of each term of D at most, is most of dq's and dk's error).
  * dk and dv are summed over the query heads of their key head.  P and dS enter
  * their products as BF16; everything else is FP32 until the results are rounded
  * to BF16.  No sum is formed in memory: equal calls give equal bits.  Rows of dq
