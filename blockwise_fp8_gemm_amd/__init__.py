@@ -893,7 +893,8 @@ def puro_fp8_attention(q, k, v, head_dim, q_offsets, k_offsets, max_q, max_k, q_
     keys and values rows k_offsets[s] .. of k and v (with q_lengths / k_lengths only the first so many of them,
     as in padded caches).  A query sees every key, or with causal those up to its place from the end.
     q: bfloat16 [tokens_q][heads_q * head_dim], k and v: [tokens_k][heads_kv * head_dim]; offsets and lengths:
-    int32 on the GPU; max_q, max_k: the longest sequence's rows (upper bounds); scale: head_dim^-0.5 by default.
+    int32 on the GPU; max_q, max_k: the longest sequence's rows (rows past them are left out; the others see what they
+    would in the whole sequence, of the keys that are left); scale: head_dim^-0.5 by default.
     Returns (o as q, lse float32 [heads_q][tokens_q], the rows' log-sums); rows outside every sequence are
     left as they were."""
     a, ins = _attention(q, k, v, head_dim, q_offsets, k_offsets, max_q, max_k, q_lengths, k_lengths, causal, scale)

@@ -540,7 +540,7 @@ __global__ __launch_bounds__(64 * NW * HV, 2) void attn_fwd_kernel(AttnFwd a)
 // Few rows (at most 32 of a key head's queries over all its query heads): a wave
 // holds them all and the workgroup's two waves take keys of their own, 32 at a
 // time through LDS of their own; their results are added up at the end.  Bound by
-// reading the keys and values once: 16 sequences of 64 to 16384 keys, 500 MB in 101 us
+// reading the keys and values once: 16 sequences of up to 16384 keys, 500 MB in 101 us
 // (4.9 TB/s; a copy reaches 5.0).  Two waves a workgroup let every wave go on
 // without a barrier; four, without the heads changing places, took 123.5 us against 113.
 constexpr int ROW_WAVES = 2;
@@ -1122,11 +1122,13 @@ int64_t fwd_groups(const AttnShape &s)
     return longest < rows ? longest : rows;
 }
 
-// Shares of the key axis.  Few rows: as many as make 1024 workgroups (four a CU), of 512 keys or more.  Many rows: as
-// many as make 256 workgroups of eight waves, one a CU, of 1024 keys or more (777 queries over 20000 keys, heads of
-// 128: 135 us, unsplit 283, twice as many shares 157), but none where workgroups of 128 rows fill most CUs and the keys
-// are not much longer than those workgroups' work (192 groups or more: 2048 x 2048 33 us, split 45; over 8192 keys 120
-// either way; 1500 x 17500 220, split 201), and none of up to 2048 keys (512 x 2048 32 us, split 35.5).
+// Shares of the key axis.  Few rows: as many as make 1024 workgroups (four a CU), of 512 keys or more (at least 256, 512
+// and 1024 keys, 16 heads on 8 of 128: one sequence of 1000 keys 16, 18 and 18 us, of 4000 16, 16 and 25, eight of 4000
+// 37.5, 36 and 36, one of 16000 23.5, 22 and 23.5; so a few sequences of up to 1023 keys are 2 us slower than they would
+// be in shares).  Many rows: as many as make 256 workgroups of eight waves, one a CU, of 1024 keys or more (777 queries over
+// 20000 keys, heads of 128: 135 us, unsplit 283, twice as many shares 157), but none where workgroups of 128 rows fill most
+// CUs and the keys are not much longer than those workgroups' work (192 groups or more: 2048 x 2048 33 us, split 45; over
+// 8192 keys 120 either way; 1500 x 17500 220, split 201), and none of up to 2048 keys (512 x 2048 32 us, split 35.5).
 int splits_of(const AttnShape &s)
 {
     if (s.seqs == 0 || s.max_q == 0)
@@ -1142,7 +1144,10 @@ int splits_of(const AttnShape &s)
 }
 
 // Form of the forward's workgroups, NW x HV waves.  8 x 1 reads a tile for the most rows, and fills the card from some
-// 640 workgroups of 128 rows on (2 x 3000 queries, heads of 128: 77 us, 4 x 1 78.6; 2 x 4096: 126, 141).  Below, smaller
+// 640 workgroups of 128 rows on (2 x 3000 queries, heads of 128: 77 us, 4 x 1 78.6; 2 x 4096: 126, 141).  It is taken for
+// keys in shares too: 777 queries over 20000 keys, 16 heads on 8: 135 us, 4 x 1 151, 4 x 2 158; 300 over 9000: 40, 43 and
+// 51.  Where one block holds a key head's rows the others would be faster (100 queries over 9000 keys: 34, 30 and 27; 16
+// times 5 over 9000, 16 heads on 2, 40 rows and six waves of copies of the last one: 41, 36 and 36).  Elsewhere below 640, smaller
 // ones spread the rows over more CUs.  4 x 2 has a CU to itself and halves the way along the keys: for as many
 // workgroups as CUs (1024 queries: 20 us, 4 x 1 23, 8 x 1 28), or twice as many where that way is long (4096: 73, 84 and
 // 91).  4 x 1, two to a CU, for the rest (packed lengths 1 to 1500, heads of 64: 24.9 us, 4 x 2 30, 8 x 1 28.8).

@@ -227,7 +227,7 @@ struct AttnBwd {
     int64_t lddv;
     float c2;
     int q_blocks;
-    float *nl, *nd;    // [hq][tokens_q]: -lse / scale, -sum of do o
+    float *nl, *nd;    // [hq][tokens_q]: -lse / scale, -D (sum of do o, or of P dP for rows that see few keys)
 };
 size_t attn_bwd_workspace_bytes(const AttnShape &s);
 hipError_t launch_attn_bwd(AttnBwd b, void *workspace, hipStream_t st);

@@ -692,7 +692,9 @@ puro_status_t puro_fp8_qk_norm_rope_bwd_quant_dual_pow2(const puro_qk_norm_rope_
  * to BF16 are FP32.  Equal calls give equal bits.
  * workspace: puro_fp8_attention_workspace_size(shape) bytes (often 0; only the
  * numbers and head counts are read; 0 for invalid shapes) of device memory, 256-byte
- * aligned, not used by other work in flight.
+ * aligned, not used by other work in flight.  Where the key axis is split it holds a
+ * share's results for every row of q, also those of no sequence: for few sequences in
+ * a long buffer, pass the rows that are in use as tokens_q.
  */
 typedef struct {
     int heads_q, heads_kv, head_dim;
